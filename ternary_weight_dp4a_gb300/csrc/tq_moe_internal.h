@@ -1,0 +1,73 @@
+// tq_moe_internal.h -- what the translation units of the mixture-of-experts layer share:
+// workspace layout and the launch functions behind the C ABI (include/tq_moe.h).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "tq.h"
+#include "tq_moe.h"
+#include "tq_workspace.h"
+
+namespace tq {
+
+// Workspace: err u32 | operand (the tile kernel's copy of a product's input:
+// 2 bytes per value, max of gate/up's m rows and down's slots) | hist (the sort's
+// counts per block of slots) | offsets | rows | pos | h | hq | hs | y.
+struct MoeWorkspace {
+    size_t err, operand, hist, offsets, rows, pos, h, hq, hs, y, total;
+};
+
+// slots sorted by one CTA of the plan kernels
+constexpr int kPlanChunk = 1024;
+
+constexpr MoeWorkspace moe_layout(int64_t m, int64_t topk, int64_t experts, int64_t hidden, int64_t inter) {
+    MoeWorkspace w{};
+    const int64_t slots = m * topk;
+    const int64_t in_a = m * hidden, in_b = slots * inter;
+    size_t off = 0;
+    w.err = off; off = ws_round(off + 4);
+    w.operand = off; off = ws_round(off + static_cast<size_t>(2 * (in_a > in_b ? in_a : in_b)));
+    w.hist = off; off = ws_round(off + static_cast<size_t>(ws_cdiv(slots, kPlanChunk) * experts * 4));
+    w.offsets = off; off = ws_round(off + static_cast<size_t>((experts + 1) * 4));
+    w.rows = off; off = ws_round(off + static_cast<size_t>(slots * 4));
+    w.pos = off; off = ws_round(off + static_cast<size_t>(slots * 4));
+    w.h = off; off = ws_round(off + static_cast<size_t>(slots * inter * 2));
+    w.hq = off; off = ws_round(off + static_cast<size_t>(slots * inter));
+    w.hs = off; off = ws_round(off + static_cast<size_t>(slots * (inter / 128) * 4));
+    w.y = off; off = ws_round(off + static_cast<size_t>(slots * hidden * 4));
+    w.total = off;
+    return w;
+}
+
+// What a product alone needs: the error word and its input's operand copy.
+constexpr size_t moe_product_bytes(int64_t m, int64_t k) { return ws_round(4) + static_cast<size_t>(2 * m * k); }
+
+// One grouped product (up == nullptr: y; else gate and up into h).
+struct MoeProduct {
+    const uint8_t *codes[2];
+    const uint16_t *scales[2];
+    int experts, n, k, fmt;
+    const int8_t *q;
+    const float *s;
+    int m;                  // rows of q
+    const int *rows;        // activation row of each sorted slot, or nullptr
+    const int *offsets;     // [experts + 1]
+    int slots;
+    float *y;
+    uint16_t *h;
+    int max_rows;           // most rows that an expert can be expected to have
+};
+
+cudaError_t moe_stream_launch(const MoeProduct &p, cudaStream_t stream);
+
+cudaError_t moe_norm_launch(const void *res, bool res_bf16, const void *delta, bool delta_bf16, const uint16_t *gamma,
+                            int m, int n, float eps, void *res_out, uint16_t *x_out, int8_t *q, float *s,
+                            cudaStream_t stream);
+cudaError_t moe_combine_launch(const float *y, const int *pos, const float *weights, int m, int topk, int slots, int n,
+                               void *out, bool out_bf16, cudaStream_t stream);
+cudaError_t moe_route_launch(const void *logits, bool bf16, int m, int experts, int topk, bool renorm, int *ids,
+                             float *weights, cudaStream_t stream);
+cudaError_t moe_plan_launch(const int *ids, int m, int topk, int experts, int *offsets, int *rows, int *pos, int *hist,
+                            cudaStream_t stream);
+
+}  // namespace tq

@@ -1,4 +1,4 @@
-"""ctypes binding of libtq (include/tq.h).  Argument marshalling only.
+"""ctypes binding of libtq (include/tq.h, include/tq_moe.h).  Argument marshalling only.
 
 Every function takes torch CUDA tensors (PyTorch provides device memory and
 streams), passes raw device pointers to the C ABI and raises ``TQError`` on a
@@ -23,7 +23,7 @@ TQ_ERR_TIMEOUT = 6
 BLOCK = 128
 MAX_ROWS = 64
 
-# every entry point include/tq.h and include/tq_lifecycle.h declare
+# every entry point include/tq.h, include/tq_moe.h and include/tq_lifecycle.h declare
 EXPORTS = ("tq_status_string", "tq_last_cuda_error", "tq_set_engine", "tq_get_engine",
            "tq_error_status", "tq_read_error_word", "tq_workspace_init", "tq_pack_weights",
            "tq_rotate_quant", "tq_gemv_workspace_bytes", "tq_gemv", "tq_ffn_gateup",
@@ -31,6 +31,8 @@ EXPORTS = ("tq_status_string", "tq_last_cuda_error", "tq_set_engine", "tq_get_en
            "tq_ffn_step", "tq_ffn_stage_input", "tq_ffn_stage_gateup", "tq_ffn_stage_down",
            "tq_ffn_stack", "tq_ffn_static_workspace_bytes", "tq_ffn_step_static",
            "tq_rmsnorm_bf16",
+           "tq_add_rmsnorm_rotq", "tq_moe_route", "tq_moe_workspace_bytes", "tq_moe_plan",
+           "tq_moe_gemv", "tq_moe_gateup", "tq_moe_combine", "tq_moe_ffn",
            "tq_lifecycle_init", "tq_lifecycle_load", "tq_lifecycle_copy", "tq_lifecycle_alloc",
            "tq_lifecycle_free", "tq_lifecycle_poll", "tq_lifecycle_release", "tq_lifecycle_destroy")
 
@@ -49,6 +51,11 @@ class TQError(RuntimeError):
 
 class _Weight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("fmt", ctypes.c_int32)]
+
+
+class _Experts(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("experts", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("fmt", ctypes.c_int32)]
 
 
@@ -118,6 +125,16 @@ def load():
             L.tq_ffn_static_workspace_bytes.argtypes = []
             L.tq_ffn_static_workspace_bytes.restype = sz
             L.tq_ffn_step_static.argtypes = [W, W, W, vp, i32, vp, vp]
+            X = ctypes.POINTER(_Experts)
+            L.tq_add_rmsnorm_rotq.argtypes = [vp, i32, vp, i32, vp, i32, i32, f32, vp, vp, vp, vp, vp]
+            L.tq_moe_route.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp]
+            L.tq_moe_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+            L.tq_moe_workspace_bytes.restype = sz
+            L.tq_moe_plan.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+            L.tq_moe_gemv.argtypes = [X, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp]
+            L.tq_moe_gateup.argtypes = [X, X, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp]
+            L.tq_moe_combine.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i32, vp]
+            L.tq_moe_ffn.argtypes = [X, X, X, vp, vp, vp, vp, i32, i32, vp, i32, vp, sz, vp]
             LC = ctypes.POINTER(_Lifecycle)
             L.tq_lifecycle_init.argtypes = [LC, ctypes.POINTER(_LcConfig), ctypes.POINTER(_LcHooks)]
             L.tq_lifecycle_load.argtypes = [LC]
@@ -134,7 +151,7 @@ def load():
             L.tq_lifecycle_destroy.restype = None
             for name in EXPORTS:
                 if name not in ("tq_status_string", "tq_last_cuda_error", "tq_ffn_workspace_bytes",
-                                "tq_gemv_workspace_bytes",
+                                "tq_gemv_workspace_bytes", "tq_moe_workspace_bytes",
                                 "tq_ffn_workspace_error_offset", "tq_ffn_static_workspace_bytes", "tq_lifecycle_copy", "tq_lifecycle_alloc",
                                 "tq_lifecycle_free", "tq_lifecycle_release", "tq_lifecycle_destroy"):
                     getattr(L, name).restype = ctypes.c_int
@@ -358,6 +375,261 @@ def rmsnorm_bf16(y, eps: float = 1e-6, x_out=None, stream=None):
     _check("tq_rmsnorm_bf16", load().tq_rmsnorm_bf16(_ptr(y), m, n, eps, _ptr(x_out),
                                                      _stream(stream)))
     return x_out
+
+
+# ---------------------------------------------------------------------------
+# mixture-of-experts layer (include/tq_moe.h)
+# ---------------------------------------------------------------------------
+
+@dataclass
+class PackedExperts:
+    """The packed weights of all experts on the device: codes
+    [experts][n][k/4] (2-bit) or [experts][n][k/8] (1-bit) uint8, scales
+    [experts][n][k/128] float16."""
+    codes: "object"
+    scales: "object"
+    experts: int
+    n: int
+    k: int
+    fmt: int
+
+    def __post_init__(self):
+        import torch
+        per = 4 if self.fmt == FMT_TERNARY2 else 8
+        _tensor("codes", self.codes, torch.uint8, (self.experts, self.n, self.k // per))
+        _tensor("scales", self.scales, torch.float16, (self.experts, self.n, self.k // BLOCK))
+
+    def c_struct(self) -> _Experts:
+        return _Experts(self.codes.data_ptr(), self.scales.data_ptr(), self.experts, self.n, self.k, self.fmt)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 2 * self.scales.numel()
+
+
+@dataclass
+class MoePlan:
+    """The slots (token, choice) sorted by expert (tq_moe_plan): offsets int32
+    [experts + 1], rows int32 [m * topk] (flat or of pos's shape), pos int32 [m][topk]."""
+    offsets: "object"
+    rows: "object"
+    pos: "object"
+
+    @property
+    def slots(self) -> int:
+        return self.rows.numel()
+
+
+def _tensor(name: str, t, dtype, shape=None):
+    """Check a tensor argument of a mixture-of-experts call: the kernels read raw
+    contiguous device memory of one type."""
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    if not t.is_cuda or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} is "
+                         f"needed, got {t.dtype} on {t.device}, strides {tuple(t.stride())}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+    return t
+
+
+def _dtype_code(t) -> int:
+    import torch
+    return 1 if t.dtype == torch.bfloat16 else 0
+
+
+def pack_experts(codes, fmt: int, scales, stream=None) -> PackedExperts:
+    """codes: uint8 CUDA tensor [experts][n][k] (as pack_weights); scales: float16
+    CUDA tensor [experts][n][k/128]."""
+    import torch
+    _tensor("codes", codes, torch.uint8)
+    experts, n, k = codes.shape
+    packed = torch.empty((experts, n, k // (4 if fmt == FMT_TERNARY2 else 8)), dtype=torch.uint8,
+                         device=codes.device)
+    _check("tq_pack_weights", load().tq_pack_weights(_ptr(codes), experts * n, k, fmt, _ptr(packed),
+                                                      _stream(stream)))
+    return PackedExperts(packed, scales.contiguous(), experts, n, k, fmt)
+
+
+def add_rmsnorm_rotq(residual, delta=None, gamma=None, eps: float = 1e-6, residual_out=None,
+                     x_out=None, q=None, s=None, stream=None):
+    """residual (+ delta) float32 or bf16 [m][n] -> (residual_out, q int8 [m][n],
+    s float32 [m][n/128]): the sum, its RMS norm (times gamma, bf16 [n]), rotated
+    and quantised.  residual_out may be residual itself; a bf16 x_out also
+    receives the norm before the rotation."""
+    import torch
+    floats = (torch.float32, torch.bfloat16)
+    _tensor("residual", residual, floats)
+    m, n = residual.shape
+    if delta is not None:
+        _tensor("delta", delta, floats, (m, n))
+    if gamma is not None:
+        _tensor("gamma", gamma, torch.bfloat16, (n,))
+    if x_out is not None:
+        _tensor("x_out", x_out, torch.bfloat16, (m, n))
+    if residual_out is None:
+        residual_out = torch.empty_like(residual)
+    if q is None:
+        q = torch.empty((m, n), dtype=torch.int8, device=residual.device)
+    if s is None:
+        s = torch.empty((m, n // BLOCK), dtype=torch.float32, device=residual.device)
+    _tensor("residual_out", residual_out, residual.dtype, (m, n))
+    _tensor("q", q, torch.int8, (m, n))
+    _tensor("s", s, torch.float32, (m, n // BLOCK))
+    _check("tq_add_rmsnorm_rotq", load().tq_add_rmsnorm_rotq(
+        _ptr(residual), _dtype_code(residual), _ptr(delta), 0 if delta is None else _dtype_code(delta),
+        _ptr(gamma), m, n, eps, _ptr(residual_out), _ptr(x_out), _ptr(q), _ptr(s), _stream(stream)))
+    return residual_out, q, s
+
+
+def moe_route(logits, topk: int, renormalize: bool = True, ids=None, weights=None, stream=None):
+    """logits float32 or bf16 [m][experts] -> (ids int32 [m][topk], weights
+    float32 [m][topk]); -1 and 0 where a token has no expert left."""
+    import torch
+    _tensor("logits", logits, (torch.float32, torch.bfloat16))
+    m, experts = logits.shape
+    if ids is None:
+        ids = torch.empty((m, topk), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((m, topk), dtype=torch.float32, device=logits.device)
+    _tensor("ids", ids, torch.int32, (m, topk))
+    _tensor("weights", weights, torch.float32, (m, topk))
+    _check("tq_moe_route", load().tq_moe_route(_ptr(logits), _dtype_code(logits), m, experts, topk,
+                                               int(renormalize), _ptr(ids), _ptr(weights), _stream(stream)))
+    return ids, weights
+
+
+def moe_workspace_bytes(m: int, topk: int, experts: int, hidden: int = 0, inter: int = 0) -> int:
+    return int(load().tq_moe_workspace_bytes(m, topk, experts, hidden, inter))
+
+
+def moe_workspace(m: int, topk: int, experts: int, hidden: int = 0, inter: int = 0, device="cuda"):
+    """A zero-filled workspace for the moe_* calls with up to m tokens (its first
+    4 bytes are the error word); keep it between calls."""
+    import torch
+    nbytes = moe_workspace_bytes(m, topk, experts, hidden, inter)
+    if nbytes == 0:
+        raise ValueError(f"moe_workspace: sizes out of range (m {m}, topk {topk}, experts {experts}, "
+                         f"hidden {hidden}, inter {inter})")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def _moe_product_workspace(workspace, q):
+    import torch
+    if workspace is None:
+        return torch.zeros(256 + 2 * q.numel(), dtype=torch.uint8, device=q.device)
+    return _tensor("workspace", workspace, torch.uint8)
+
+
+def moe_plan(ids, experts: int, plan: MoePlan = None, workspace=None, stream=None) -> MoePlan:
+    """ids int32 [m][topk] -> MoePlan; an id outside 0 .. experts-1 leaves its slot out."""
+    import torch
+    _tensor("ids", ids, torch.int32)
+    m, topk = ids.shape
+    if plan is None:
+        plan = MoePlan(*(torch.empty(n, dtype=torch.int32, device=ids.device)
+                         for n in (experts + 1, m * topk, (m, topk))))
+    _tensor("offsets", plan.offsets, torch.int32, (experts + 1,))
+    for name, t in (("rows", plan.rows), ("pos", plan.pos)):
+        if _tensor(name, t, torch.int32).numel() != m * topk:
+            raise ValueError(f"{name}: {m * topk} entries are needed, got {t.numel()}")
+    if workspace is None:
+        workspace = moe_workspace(m, topk, experts, device=ids.device)
+    _check("tq_moe_plan", load().tq_moe_plan(_ptr(ids), m, topk, experts, _ptr(plan.offsets), _ptr(plan.rows),
+                                             _ptr(plan.pos), _ptr(workspace), workspace.numel(),
+                                             _stream(stream)))
+    return plan
+
+
+def _moe_inputs(w: PackedExperts, q, s, plan: MoePlan):
+    import torch
+    _tensor("q", q, torch.int8)
+    m, k = q.shape
+    if k != w.k:
+        raise ValueError(f"q: rows of {w.k} codes are needed, got {k}")
+    _tensor("s", s, torch.float32, (m, k // BLOCK))
+    _tensor("offsets", plan.offsets, torch.int32, (w.experts + 1,))
+    _tensor("rows", plan.rows, torch.int32)
+    return m
+
+
+def moe_gemv(w: PackedExperts, q, s, plan: MoePlan, gather: bool = False, y=None, workspace=None,
+             stream=None):
+    """y float32 [slots][n], one row per sorted slot.  q int8, s float32: one row
+    per sorted slot, or with ``gather`` one per token, picked by plan.rows."""
+    import torch
+    m = _moe_inputs(w, q, s, plan)
+    if y is None:
+        y = torch.empty((plan.slots, w.n), dtype=torch.float32, device=q.device)
+    _tensor("y", y, torch.float32, (plan.slots, w.n))
+    workspace = _moe_product_workspace(workspace, q)
+    ws = w.c_struct()
+    _check("tq_moe_gemv", load().tq_moe_gemv(
+        ctypes.byref(ws), _ptr(q), _ptr(s), m, _ptr(plan.rows if gather else None), _ptr(plan.offsets),
+        plan.slots, _ptr(y), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return y
+
+
+def moe_gateup(gate: PackedExperts, up: PackedExperts, q, s, plan: MoePlan, gather: bool = True, h=None,
+               workspace=None, stream=None):
+    """SiLU(gate) * up as bf16 [slots][n], one row per sorted slot.  q int8, s
+    float32: one row per token, picked by plan.rows (``gather``), or one per
+    sorted slot."""
+    import torch
+    m = _moe_inputs(gate, q, s, plan)
+    if h is None:
+        h = torch.empty((plan.slots, gate.n), dtype=torch.bfloat16, device=q.device)
+    _tensor("h", h, torch.bfloat16, (plan.slots, gate.n))
+    workspace = _moe_product_workspace(workspace, q)
+    g, u = gate.c_struct(), up.c_struct()
+    _check("tq_moe_gateup", load().tq_moe_gateup(
+        ctypes.byref(g), ctypes.byref(u), _ptr(q), _ptr(s), m, _ptr(plan.rows if gather else None),
+        _ptr(plan.offsets), plan.slots, _ptr(h), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return h
+
+
+def moe_combine(y, plan: MoePlan, weights, out=None, dtype=None, stream=None):
+    """y float32 [slots][n], weights float32 [m][topk] -> the weighted sum over each
+    token's experts [m][n] (float32 unless dtype or out says bf16)."""
+    import torch
+    _tensor("y", y, torch.float32)
+    _tensor("weights", weights, torch.float32)
+    m, topk = weights.shape
+    if _tensor("pos", plan.pos, torch.int32).numel() != m * topk:
+        raise ValueError(f"pos: {m * topk} entries are needed, got {plan.pos.numel()}")
+    if out is None:
+        out = torch.empty((m, y.shape[1]), dtype=dtype or torch.float32, device=y.device)
+    _tensor("out", out, (torch.float32, torch.bfloat16), (m, y.shape[1]))
+    _check("tq_moe_combine", load().tq_moe_combine(
+        _ptr(y), _ptr(plan.pos), _ptr(weights), m, topk, y.shape[0], y.shape[1], _ptr(out), _dtype_code(out),
+        _stream(stream)))
+    return out
+
+
+def moe_ffn(gate: PackedExperts, up: PackedExperts, down: PackedExperts, q, s, ids, weights, out=None,
+            dtype=None, workspace=None, stream=None):
+    """The FFN of a mixture-of-experts layer: q int8 [m][hidden], s float32
+    [m][hidden/128], ids int32 and weights float32 [m][topk] -> [m][hidden]
+    (float32 unless dtype or out says bf16)."""
+    import torch
+    _tensor("q", q, torch.int8)
+    m, hidden = q.shape
+    _tensor("s", s, torch.float32, (m, hidden // BLOCK))
+    _tensor("ids", ids, torch.int32)
+    topk = ids.shape[1]
+    _tensor("ids", ids, torch.int32, (m, topk))
+    _tensor("weights", weights, torch.float32, (m, topk))
+    if hidden != gate.k:
+        raise ValueError(f"q: rows of {gate.k} codes are needed, got {hidden}")
+    if out is None:
+        out = torch.empty((m, hidden), dtype=dtype or torch.float32, device=q.device)
+    _tensor("out", out, (torch.float32, torch.bfloat16), (m, hidden))
+    if workspace is None:
+        workspace = moe_workspace(m, topk, gate.experts, hidden, gate.n, q.device)
+    g, u, d = gate.c_struct(), up.c_struct(), down.c_struct()
+    _check("tq_moe_ffn", load().tq_moe_ffn(
+        ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), _ptr(q), _ptr(s), _ptr(ids), _ptr(weights), m, topk,
+        _ptr(out), _dtype_code(out), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return out
 
 
 # ---------------------------------------------------------------------------
