@@ -78,8 +78,19 @@ tq::MoeProduct product(const tq_experts *w, const tq_experts *up, const int8_t *
     return p;
 }
 
-tq_status run_product(const tq::MoeProduct &p, cudaStream_t stream) {
-    return cuda_status(tq::moe_stream_launch(p, stream));
+// Experts with more rows than this run on the tile kernel, the others on the
+// stream kernel; the bits are the same.
+constexpr int kTileAbove = 64;
+
+tq_status run_product(const tq::MoeProduct &p, void *workspace, cudaStream_t stream) {
+    const tq::MoeWorkspace L = tq::moe_layout(1, 1, 1, 0, 0);      // err and operand come first
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    cudaError_t e = cudaSuccess;
+    const bool tiles = p.max_rows > kTileAbove;
+    if (tiles)
+        e = tq::moe_tile_launch(p, kTileAbove, ws + L.operand, reinterpret_cast<unsigned *>(ws + L.err), stream);
+    if (e == cudaSuccess) e = tq::moe_stream_launch(p, tiles ? kTileAbove : p.slots, stream);
+    return cuda_status(e);
 }
 
 }  // namespace
@@ -145,7 +156,7 @@ tq_status tq_moe_gemv(const tq_experts *w, const int8_t *q, const float *s, int3
     tq::MoeProduct p = product(w, nullptr, q, s, m, rows, offsets, slots);
     p.y = y;
     p.max_rows = slots;
-    return run_product(p, reinterpret_cast<cudaStream_t>(stream));
+    return run_product(p, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 tq_status tq_moe_gateup(const tq_experts *gate, const tq_experts *up, const int8_t *q,
@@ -162,7 +173,7 @@ tq_status tq_moe_gateup(const tq_experts *gate, const tq_experts *up, const int8
     tq::MoeProduct p = product(gate, up, q, s, m, rows, offsets, slots);
     p.h = h;
     p.max_rows = rows != nullptr && m < slots ? m : slots;
-    return run_product(p, reinterpret_cast<cudaStream_t>(stream));
+    return run_product(p, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 tq_status tq_moe_combine(const float *y, const int32_t *pos, const float *weights, int32_t m,
@@ -210,12 +221,12 @@ tq_status tq_moe_ffn(const tq_experts *gate, const tq_experts *up, const tq_expe
     tq::MoeProduct a = product(gate, up, q, s, m, rows, offsets, slots);
     a.h = h;
     a.max_rows = m;
-    if ((st = run_product(a, str)) != TQ_OK) return st;
+    if ((st = run_product(a, workspace, str)) != TQ_OK) return st;
     if ((st = tq_rotate_quant(h, slots, inter, hq, hs, stream)) != TQ_OK) return st;
     tq::MoeProduct b = product(down, nullptr, hq, hs, slots, nullptr, offsets, slots);
     b.y = y;
     b.max_rows = m;
-    if ((st = run_product(b, str)) != TQ_OK) return st;
+    if ((st = run_product(b, workspace, str)) != TQ_OK) return st;
     return cuda_status(tq::moe_combine_launch(y, pos, weights, m, topk, slots, hidden, out, out_type == TQ_BF16, str));
 }
 

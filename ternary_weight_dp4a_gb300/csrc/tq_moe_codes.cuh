@@ -1,0 +1,90 @@
+// tq_moe_codes.cuh -- codes to e4m3, for the grouped products: int8 activations as two
+// exact e4m3 numbers, and the order in which decoded weights meet them.
+#pragma once
+
+#include "tq_device.cuh"
+
+namespace tq {
+
+// Four int8 codes -> the e4m3 bytes of L * 2^-9 and of 16 H * 2^-9.
+__device__ __forceinline__ void split4(uint32_t w, uint32_t &hi, uint32_t &lo) {
+    const uint32_t sign = w & 0x80808080u;
+    const uint32_t mask = prmt(w, w, 0xba98u);                              // 0xff where negative
+    const uint32_t a = (w ^ mask) + (mask & 0x01010101u);                   // |q|, no carry between bytes
+    lo = (a & 0x0f0f0f0fu) | sign;
+    uint32_t sel = (a >> 4) & 0x07070707u;                                  // H per byte -> one nibble each
+    sel = (sel | (sel >> 4)) & 0x00ff00ffu;
+    sel = sel | (sel >> 8);
+    // 16 H * 2^-9 = H * 2^-5: e4m3 patterns of 0, 1, 2, 3 | 4, 5, 6, 7 times 2^-5
+    hi = prmt(0x1c181000u, 0x26242220u, sel) | sign;
+}
+
+// 32 consecutive codes (8 words) in the order in which the decoded weights meet
+// them (tq_dp4a.cuh, staged_pos).
+template <int FMT>
+__device__ __forceinline__ void stage_order(const uint32_t (&w)[8], uint32_t (&o)[8]) {
+    if (FMT == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            o[4 * h + 0] = prmt(w[4 * h], w[4 * h + 1], 0x6420u);
+            o[4 * h + 1] = prmt(w[4 * h + 2], w[4 * h + 3], 0x6420u);
+            o[4 * h + 2] = prmt(w[4 * h], w[4 * h + 1], 0x7531u);
+            o[4 * h + 3] = prmt(w[4 * h + 2], w[4 * h + 3], 0x7531u);
+        }
+    } else {
+        // o[s] byte k = element 8k + s = byte s & 3 of word 2k + (s >> 2)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t a = prmt(w[h], w[2 + h], 0x5140u), b = prmt(w[4 + h], w[6 + h], 0x5140u);
+            const uint32_t c = prmt(w[h], w[2 + h], 0x7362u), d = prmt(w[4 + h], w[6 + h], 0x7362u);
+            o[4 * h + 0] = prmt(a, b, 0x5410u);
+            o[4 * h + 1] = prmt(a, b, 0x7632u);
+            o[4 * h + 2] = prmt(c, d, 0x5410u);
+            o[4 * h + 3] = prmt(c, d, 0x7632u);
+        }
+    }
+}
+
+// Four int8 codes -> the e4m3 numbers 16 H and L themselves, |q| = 16 H + L.
+__device__ __forceinline__ void split4_whole(uint32_t w, uint32_t &hi, uint32_t &lo) {
+    const uint32_t sign = w & 0x80808080u;
+    const uint32_t mask = prmt(w, w, 0xba98u);
+    const uint32_t a = (w ^ mask) + (mask & 0x01010101u);
+    uint32_t sel = (a >> 4) & 0x07070707u;
+    sel = (sel | (sel >> 4)) & 0x00ff00ffu;
+    sel = sel | (sel >> 8);
+    hi = prmt(0x64605800u, 0x6e6c6a68u, sel) | sign;            // 0, 16, 32, 48 | 64, 80, 96, 112
+    uint32_t low = a & 0x07070707u;
+    low = (low | (low >> 4)) & 0x00ff00ffu;
+    low = low | (low >> 8);
+    const uint32_t small = prmt(0x44403800u, 0x4e4c4a48u, low); // 0 .. 7
+    const uint32_t large = (a & 0x07070707u) | 0x50505050u;     // 8 .. 15: one binade, linear
+    const uint32_t pick = prmt((a & 0x08080808u) << 4, 0u, 0xba98u);
+    lo = ((small & ~pick) | (large & pick)) | sign;
+}
+
+// One row's 128 weights (32 or 16 bytes of codes) -> 32 registers of four e4m3
+// numbers -1, 0, +1 each, in staged order.
+template <int FMT>
+__device__ __forceinline__ void decode_block(const uint4 *c, uint32_t (&v)[32]) {
+    if (FMT == 0) {
+        constexpr uint32_t kTable = 0x00b83800u;                // codes 0, 1, 2 -> 0, +1, -1
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = i & 2 ? (i & 1 ? c[i >> 2].w : c[i >> 2].z) : (i & 1 ? c[i >> 2].y : c[i >> 2].x);
+            const uint32_t even = w & 0x33333333u, odd = (w >> 2) & 0x33333333u;
+            v[4 * i + 0] = prmt(kTable, 0u, even);
+            v[4 * i + 1] = prmt(kTable, 0u, even >> 16);
+            v[4 * i + 2] = prmt(kTable, 0u, odd);
+            v[4 * i + 3] = prmt(kTable, 0u, odd >> 16);
+        }
+    } else {
+        const uint32_t w[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < 8; ++s) v[8 * i + s] = ((w[i] << (7 - s)) & 0x80808080u) ^ 0xb8b8b8b8u;
+    }
+}
+
+}  // namespace tq

@@ -58,7 +58,10 @@ struct MoeProduct {
     int max_rows;           // most rows that an expert can be expected to have
 };
 
-cudaError_t moe_stream_launch(const MoeProduct &p, cudaStream_t stream);
+// The experts with at most `limit` rows, and those with more than `above`
+// (operand: 2 * m * k bytes of workspace for the laid-out input).
+cudaError_t moe_stream_launch(const MoeProduct &p, int limit, cudaStream_t stream);
+cudaError_t moe_tile_launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *err, cudaStream_t stream);
 
 cudaError_t moe_norm_launch(const void *res, bool res_bf16, const void *delta, bool delta_bf16, const uint16_t *gamma,
                             int m, int n, float eps, void *res_out, uint16_t *x_out, int8_t *q, float *s,

@@ -20,6 +20,7 @@
 #include "tq_device.cuh"
 #include "tq_dp4a.cuh"
 #include "tq_launch.h"
+#include "tq_moe_codes.cuh"
 #include "tq_moe_internal.h"
 
 namespace tq {
@@ -41,45 +42,6 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four int8 codes -> the e4m3 bytes of L * 2^-9 and of 16 H * 2^-9.
-__device__ __forceinline__ void split4(uint32_t w, uint32_t &hi, uint32_t &lo) {
-    const uint32_t sign = w & 0x80808080u;
-    const uint32_t mask = prmt(w, w, 0xba98u);                              // 0xff where negative
-    const uint32_t a = (w ^ mask) + (mask & 0x01010101u);                   // |q|, no carry between bytes
-    lo = (a & 0x0f0f0f0fu) | sign;
-    uint32_t sel = (a >> 4) & 0x07070707u;                                  // H per byte -> one nibble each
-    sel = (sel | (sel >> 4)) & 0x00ff00ffu;
-    sel = sel | (sel >> 8);
-    // 16 H * 2^-9 = H * 2^-5: e4m3 patterns of 0, 1, 2, 3 | 4, 5, 6, 7 times 2^-5
-    hi = prmt(0x1c181000u, 0x26242220u, sel) | sign;
-}
-
-// 32 consecutive codes (8 words) in the order in which the decoded weights meet
-// them (tq_dp4a.cuh, staged_pos).
-template <int FMT>
-__device__ __forceinline__ void stage_order(const uint32_t (&w)[8], uint32_t (&o)[8]) {
-    if (FMT == 0) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            o[4 * h + 0] = prmt(w[4 * h], w[4 * h + 1], 0x6420u);
-            o[4 * h + 1] = prmt(w[4 * h + 2], w[4 * h + 3], 0x6420u);
-            o[4 * h + 2] = prmt(w[4 * h], w[4 * h + 1], 0x7531u);
-            o[4 * h + 3] = prmt(w[4 * h + 2], w[4 * h + 3], 0x7531u);
-        }
-    } else {
-        // o[s] byte k = element 8k + s = byte s & 3 of word 2k + (s >> 2)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t a = prmt(w[h], w[2 + h], 0x5140u), b = prmt(w[4 + h], w[6 + h], 0x5140u);
-            const uint32_t c = prmt(w[h], w[2 + h], 0x7362u), d = prmt(w[4 + h], w[6 + h], 0x7362u);
-            o[4 * h + 0] = prmt(a, b, 0x5410u);
-            o[4 * h + 1] = prmt(a, b, 0x7632u);
-            o[4 * h + 2] = prmt(c, d, 0x5410u);
-            o[4 * h + 3] = prmt(c, d, 0x7632u);
-        }
-    }
 }
 
 // The weights of one row that a lane holds per block: 32 of them, 8 bytes (2-bit) or 4 (1-bit).
@@ -116,11 +78,12 @@ __device__ __forceinline__ void decode(const Codes<FMT> &c, uint32_t (&r)[8]) {
 struct StreamArgs {
     MoeProduct p;
     int chunk;      // rows of an expert per CTA, at most kCols
+    int limit;      // experts with more rows are another kernel's
 };
 
 // One warp looks for the pair'th (expert, chunk of its rows); false behind the last.
-__device__ __forceinline__ bool find_chunk(const int *offsets, int experts, int slots, int chunk, int pair, int &expert,
-                                           int &row0, int &rows) {
+__device__ __forceinline__ bool find_chunk(const int *offsets, int experts, int slots, int chunk, int limit, int pair,
+                                           int &expert, int &row0, int &rows) {
     const int lane = threadIdx.x & 31;
     int base = 0;
     for (int e0 = 0; e0 < experts; e0 += 32) {
@@ -130,7 +93,7 @@ __device__ __forceinline__ bool find_chunk(const int *offsets, int experts, int 
             lo = min(max(offsets[e], 0), slots);
             n = max(min(max(offsets[e + 1], 0), slots) - lo, 0);
         }
-        const int c = (n + chunk - 1) / chunk;
+        const int c = n <= limit ? (n + chunk - 1) / chunk : 0;
         int incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -160,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) stream_kernel(const __grid_constant_
     pdl_launch_dependents();
     pdl_wait();
     int expert, row0, rows;
-    if (!find_chunk(p.offsets, p.experts, p.slots, args.chunk, blockIdx.x, expert, row0, rows)) return;
+    if (!find_chunk(p.offsets, p.experts, p.slots, args.chunk, args.limit, blockIdx.x, expert, row0, rows)) return;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int nb = p.k / kBlock;
@@ -311,8 +274,8 @@ size_t stream_smem(int chunk, int nb) {
 }
 
 template <int FMT, bool GATEUP>
-cudaError_t launch(const MoeProduct &p, cudaStream_t stream) {
-    StreamArgs a{p, 0};
+cudaError_t launch(const MoeProduct &p, int limit, cudaStream_t stream) {
+    StreamArgs a{p, 0, limit};
     const int nb = p.k / kBlock;
     // as many rows per CTA as fit in shared memory, at most 8 and no more than an expert has
     int chunk = p.max_rows < kCols ? p.max_rows : kCols;
@@ -334,9 +297,9 @@ cudaError_t launch(const MoeProduct &p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t moe_stream_launch(const MoeProduct &p, cudaStream_t stream) {
-    if (p.h != nullptr) return p.fmt == TQ_FMT_TERNARY2 ? launch<0, true>(p, stream) : launch<1, true>(p, stream);
-    return p.fmt == TQ_FMT_TERNARY2 ? launch<0, false>(p, stream) : launch<1, false>(p, stream);
+cudaError_t moe_stream_launch(const MoeProduct &p, int limit, cudaStream_t stream) {
+    if (p.h != nullptr) return p.fmt == TQ_FMT_TERNARY2 ? launch<0, true>(p, limit, stream) : launch<1, true>(p, limit, stream);
+    return p.fmt == TQ_FMT_TERNARY2 ? launch<0, false>(p, limit, stream) : launch<1, false>(p, limit, stream);
 }
 
 }  // namespace tq
