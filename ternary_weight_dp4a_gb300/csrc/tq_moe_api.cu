@@ -152,7 +152,7 @@ tq_status tq_moe_gemv(const tq_experts *w, const int8_t *q, const float *s, int3
     if (y == nullptr) return TQ_ERR_INVALID_ARG;
     if ((st = check_rows(q, s, m, rows, offsets, slots)) != TQ_OK) return st;
     if (!aligned(y, 4)) return TQ_ERR_ALIGNMENT;
-    if ((st = check_ws(workspace, workspace_bytes, tq::moe_product_bytes(m, w->k))) != TQ_OK) return st;
+    if ((st = check_ws(workspace, workspace_bytes, tq::moe_product_bytes(slots, w->k))) != TQ_OK) return st;
     tq::MoeProduct p = product(w, nullptr, q, s, m, rows, offsets, slots);
     p.y = y;
     p.max_rows = slots;
@@ -169,7 +169,7 @@ tq_status tq_moe_gateup(const tq_experts *gate, const tq_experts *up, const int8
     if (!same_shape(gate, up) || h == nullptr) return TQ_ERR_INVALID_ARG;
     if ((st = check_rows(q, s, m, rows, offsets, slots)) != TQ_OK) return st;
     if (!aligned(h, 2)) return TQ_ERR_ALIGNMENT;
-    if ((st = check_ws(workspace, workspace_bytes, tq::moe_product_bytes(m, gate->k))) != TQ_OK) return st;
+    if ((st = check_ws(workspace, workspace_bytes, tq::moe_product_bytes(slots, gate->k))) != TQ_OK) return st;
     tq::MoeProduct p = product(gate, up, q, s, m, rows, offsets, slots);
     p.h = h;
     p.max_rows = rows != nullptr && m < slots ? m : slots;

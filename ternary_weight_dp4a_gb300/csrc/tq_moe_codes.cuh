@@ -87,4 +87,42 @@ __device__ __forceinline__ void decode_block(const uint4 *c, uint32_t (&v)[32]) 
     }
 }
 
+// SiLU of N gates, g / (1 + exp(-g)), the division correctly rounded.  For 2^-80 <= |g| < 64
+// or g = 0 without a branch: tq_expf's polynomial with 2^n put in at once (2^n is a normal
+// number there), a reciprocal refined by one Newton step, and the quotient corrected with its
+// exact remainder (P. Markstein, "IA-64 and Elementary Functions", 2000, chapter 8).  Other
+// arguments take tq_silu; the results are the same bits.
+template <int N>
+__device__ __forceinline__ void moe_silu(const float (&g)[N], float (&s)[N]) {
+    bool other = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float z = -g[i], a = fabsf(g[i]);
+        other |= !(a < 64.0f) || (a < 8.2718061e-25f && a != 0.0f);
+        const float t = __fadd_rn(__fmul_rn(z, __uint_as_float(0x3fb8aa3bu)), 12582912.0f);
+        const float n = __fsub_rn(t, 12582912.0f);
+        float r = __fmaf_rn(-n, __uint_as_float(0x3f317000u), z);
+        r = __fmaf_rn(-n, __uint_as_float(0x3805fdf4u), r);
+        float p = __uint_as_float(0x39500d01u);
+        p = __fmaf_rn(p, r, __uint_as_float(0x3ab60b61u));
+        p = __fmaf_rn(p, r, __uint_as_float(0x3c088889u));
+        p = __fmaf_rn(p, r, __uint_as_float(0x3d2aaaabu));
+        p = __fmaf_rn(p, r, __uint_as_float(0x3e2aaaabu));
+        p = __fmaf_rn(p, r, 0.5f);
+        p = __fmaf_rn(p, r, 1.0f);
+        p = __fmaf_rn(p, r, 1.0f);
+        const float e = __int_as_float(__float_as_int(p) + ((__float_as_int(t) - 0x4b400000) << 23));
+        const float d = __fadd_rn(1.0f, e);
+        float y;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+        y = __fmaf_rn(__fmaf_rn(-d, y, 1.0f), y, y);
+        const float q = __fmul_rn(g[i], y);
+        s[i] = __fmaf_rn(__fmaf_rn(-d, q, g[i]), y, q);
+    }
+    if (other) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = tq_silu(g[i]);
+    }
+}
+
 }  // namespace tq

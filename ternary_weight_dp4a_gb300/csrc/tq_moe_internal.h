@@ -11,7 +11,7 @@
 namespace tq {
 
 // Workspace: err u32 | operand (the tile kernel's copy of a product's input:
-// 2 bytes per value, max of gate/up's m rows and down's slots) | hist (the sort's
+// 2 bytes per value and slot) | hist (the sort's
 // counts per block of slots) | offsets | rows | pos | h | hq | hs | y.
 struct MoeWorkspace {
     size_t err, operand, hist, offsets, rows, pos, h, hq, hs, y, total;
@@ -23,10 +23,10 @@ constexpr int kPlanChunk = 1024;
 constexpr MoeWorkspace moe_layout(int64_t m, int64_t topk, int64_t experts, int64_t hidden, int64_t inter) {
     MoeWorkspace w{};
     const int64_t slots = m * topk;
-    const int64_t in_a = m * hidden, in_b = slots * inter;
+    const int64_t in = slots * (hidden > inter ? hidden : inter);
     size_t off = 0;
     w.err = off; off = ws_round(off + 4);
-    w.operand = off; off = ws_round(off + static_cast<size_t>(2 * (in_a > in_b ? in_a : in_b)));
+    w.operand = off; off = ws_round(off + static_cast<size_t>(2 * in));
     w.hist = off; off = ws_round(off + static_cast<size_t>(ws_cdiv(slots, kPlanChunk) * experts * 4));
     w.offsets = off; off = ws_round(off + static_cast<size_t>((experts + 1) * 4));
     w.rows = off; off = ws_round(off + static_cast<size_t>(slots * 4));
@@ -40,7 +40,7 @@ constexpr MoeWorkspace moe_layout(int64_t m, int64_t topk, int64_t experts, int6
 }
 
 // What a product alone needs: the error word and its input's operand copy.
-constexpr size_t moe_product_bytes(int64_t m, int64_t k) { return ws_round(4) + static_cast<size_t>(2 * m * k); }
+constexpr size_t moe_product_bytes(int64_t slots, int64_t k) { return ws_round(4) + static_cast<size_t>(2 * slots * k); }
 
 // One grouped product (up == nullptr: y; else gate and up into h).
 struct MoeProduct {
@@ -59,7 +59,7 @@ struct MoeProduct {
 };
 
 // The experts with at most `limit` rows, and those with more than `above`
-// (operand: 2 * m * k bytes of workspace for the laid-out input).
+// (operand: 2 * slots * k bytes of workspace for the laid-out input).
 cudaError_t moe_stream_launch(const MoeProduct &p, int limit, cudaStream_t stream);
 cudaError_t moe_tile_launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *err, cudaStream_t stream);
 

@@ -18,8 +18,8 @@
 // of the code: 3580 int8 x ternary MACs.  224 columns also leave room for
 // two accumulators (448 of 512 columns) and two blocks of A (64 columns).
 //
-// Warps: 0-3 decode weights, 4 issues MMAs, 5-7 copy activation rows (cp.async,
-// gathered by plan), 8-15 fold (a quarter of the lanes and half of the columns
+// Warps: 0-3 decode weights, 4 issues MMAs, 5 copies activation rows (TMA),
+// 6-7 their scales, 8-15 fold (a quarter of the lanes and half of the columns
 // each).  The fold's 112 accumulators per thread need more than an even share of
 // the registers, so the roles resize theirs.
 #include <cuda_runtime.h>
@@ -29,15 +29,17 @@
 #include "tq_moe_codes.cuh"
 #include "tq_moe_internal.h"
 #include "tq_tcgen05.cuh"
+#include "tq_tmap.h"
 
 namespace tq {
 namespace {
 
 constexpr int kCols = 224;                          // most activation rows per tile
 constexpr int kStages = 3;
+constexpr int kBoxRows = 32;                        // rows per TMA copy
 constexpr int kScaleSlots = 8;
 constexpr int kThreads = 512;
-constexpr int kCopyThreads = 96;                    // warps 5-7
+constexpr int kScaleThreads = 64;                   // warps 6 and 7
 constexpr uint32_t kHalf = kCols * 128;             // bytes of one part of a stage
 constexpr uint32_t kStageBytes = 2 * kHalf;
 constexpr uint32_t kTmemA = 2 * kCols;              // first column of the A buffers
@@ -49,7 +51,6 @@ constexpr int kRegsDecode = 96, kRegsIssue = 48, kRegsFold = 184;
 struct __align__(1024) TileSmem {
     uint8_t b[kStages][kStageBytes];
     float as[kScaleSlots][kCols];
-    int row[3][kCols];                              // per copy warp
     uint64_t b_full[kStages], b_empty[kStages], a_full[2], a_empty[2], d_full[2], d_empty[2], s_full[kScaleSlots], drain;
     uint32_t tmem;
     uint32_t dead;                                  // a bounded wait ran out
@@ -57,7 +58,7 @@ struct __align__(1024) TileSmem {
 
 struct TileArgs {
     MoeProduct p;
-    const uint8_t *operand;     // [m][k/128][16 h: 128 | l: 128]
+    CUtensorMap map;            // the operand, [slots][k/128][16 h: 128 | l: 128] bytes, boxes of kBoxRows x 128
     unsigned *err;
     int above;                  // experts with more rows than this are this kernel's
 };
@@ -107,8 +108,12 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
     return d;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// kBoxRows rows of 128 bytes at (byte x, row y) of the operand; counted on `bar`.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -140,6 +145,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+
+// tcgen05.wait::ld; the registers pass through it, so nothing reads them before.
+__device__ __forceinline__ void wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 
 // A bounded wait; once one ran out every later wait of the CTA gives up at once.
@@ -175,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sm.b_full[i]), kCopyThreads);
+            mbar_init(smem_u32(&sm.b_full[i]), 1);
             mbar_init(smem_u32(&sm.b_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -184,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             mbar_init(smem_u32(&sm.d_full[i]), 1);
             mbar_init(smem_u32(&sm.d_empty[i]), 8);
         }
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&sm.s_full[i]), kCopyThreads);
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&sm.s_full[i]), kScaleThreads);
         mbar_init(smem_u32(&sm.drain), 1);
         sm.dead = 0;
         mbar_init_fence();
@@ -282,43 +296,56 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp < 8) {
-        // ---- copy: 16 threads per row (16 bytes each of a block's 256), six rows at a time ----
-        const int ct = tid - 160, chunk = ct & 15, sub = ct >> 4;
-        const uint32_t b_base = smem_u32(sm.b[0]) + (chunk >> 3) * kHalf;
-        int *row = sm.row[warp - 5];
-        bool ok = true;
-        for (int item = blockIdx.x; ok && find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
-            __syncwarp();
-            for (int i = lane; i < cols; i += 32) {
-                const int a = p.rows != nullptr ? p.rows[row0 + i] : row0 + i;
-                row[i] = min(max(a, 0), p.m - 1);
-            }
-            __syncwarp();
-            for (int b = 0; b < nb; ++b) {
-                const int st = it % kStages;
-                ok = warp_wait(sm, sm.b_empty[st], ((it / kStages) & 1) ^ 1, args.err, 1u << 5);
-                if (!ok) break;
-                const uint8_t *src = args.operand + static_cast<int64_t>(b) * 256 + chunk * 16;
-                const uint32_t dst = b_base + st * kStageBytes;
-                for (int i = sub; i < cols; i += kCopyThreads / 16)
-                    cp_async16(dst + i * 128 + (((chunk & 7) ^ (i & 7)) << 4), src + static_cast<int64_t>(row[i]) * 2 * p.k);
-                for (int i = ct; i < cols; i += kCopyThreads)
-                    cp_async4(smem_u32(&sm.as[it % kScaleSlots][i]), p.s + static_cast<int64_t>(row[i]) * nb + b);
-                cp_async_commit();
-                if (it >= 2) {
-                    cp_async_wait<2>();             // the block before last has landed
-                    fence_proxy_async_smem();
-                    mbar_arrive(smem_u32(&sm.b_full[(it - 2) % kStages]));
-                    mbar_arrive(smem_u32(&sm.s_full[(it - 2) % kScaleSlots]));
+        // ---- copy: warp 5 brings activation rows, 32 per copy, lane i rows 32 i
+        // (i < 7) of one part and lane 8 + i of the other; warps 6 and 7 the scales ----
+        if (warp == 5) {
+            bool ok = true;
+            for (int item = blockIdx.x; ok && find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
+                const int boxes = (cols + kBoxRows - 1) / kBoxRows;
+                const int part = lane >> 3, box = lane & 7;
+                for (int b = 0; b < nb; ++b, ++it) {
+                    const int st = it % kStages;
+                    ok = warp_wait(sm, sm.b_empty[st], ((it / kStages) & 1) ^ 1, args.err, 1u << 5);
+                    if (!ok) break;
+                    const uint32_t bar = smem_u32(&sm.b_full[st]);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes) * 2 * kBoxRows * 128);
+                    __syncwarp();
+                    if (lane < 16 && box < boxes)
+                        copy_box(smem_u32(sm.b[st]) + part * kHalf + box * kBoxRows * 128, &args.map, b * 256 + part * 128,
+                                 row0 + box * kBoxRows, bar);
                 }
-                ++it;
             }
-        }
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        for (int j = it >= 2 ? it - 2 : 0; j < it; ++j) {
-            mbar_arrive(smem_u32(&sm.b_full[j % kStages]));
-            mbar_arrive(smem_u32(&sm.s_full[j % kScaleSlots]));
+            // none of this CTA's copies may be in flight when it leaves
+            for (int j = max(it - kStages, 0); j < it; ++j)
+                if (!mbar_wait(smem_u32(&sm.b_full[j % kStages]), (j / kStages) & 1)) atomicOr(args.err, 1u << 8);
+        } else {
+            const int ct = tid - 192;
+            bool ok = true;
+            for (int item = blockIdx.x; ok && find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
+                const float *src[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = row0 + min(ct + kScaleThreads * i, cols - 1);
+                    src[i] = p.s + static_cast<int64_t>(min(max(p.rows != nullptr ? p.rows[r] : r, 0), p.m - 1)) * nb;
+                }
+                for (int b = 0; b < nb; ++b) {
+                    const int st = it % kStages, slot = it % kScaleSlots;
+                    // a slot is free again long before: its block's fold came before the MMAs that freed this stage
+                    ok = warp_wait(sm, sm.b_empty[st], ((it / kStages) & 1) ^ 1, args.err, 1u << 5);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (ct + kScaleThreads * i < cols) cp_async4(smem_u32(&sm.as[slot][ct + kScaleThreads * i]), src[i] + b);
+                    cp_async_commit();
+                    if (it >= 2) {
+                        cp_async_wait<2>();         // the block before last has landed
+                        mbar_arrive(smem_u32(&sm.s_full[(it - 2) % kScaleSlots]));
+                    }
+                    ++it;
+                }
+            }
+            cp_async_wait<0>();
+            for (int j = max(it - 2, 0); j < it; ++j) mbar_arrive(smem_u32(&sm.s_full[j % kScaleSlots]));
         }
     } else {
         // ---- fold ----
@@ -345,18 +372,23 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 tc_fence_after();
                 __syncwarp();
                 const float *as = &sm.as[slot][half * kFoldCols];
+                const uint32_t dcol = lane_base + buf * kCols;
+                uint32_t d[2][16];
+                if (mine > 0) tmem_ld<16>(dcol, d[0]);
 #pragma unroll
                 for (int c = 0; c < kFoldCols; c += 16) {
                     if (c < mine) {                 // the same for the whole warp
-                        uint32_t d[16];
-                        tmem_ld<16>(lane_base + buf * kCols + c, d);
-                        tmem_wait_ld();
+                        uint32_t (&v)[16] = d[(c >> 4) & 1];
+                        ulonglong2 s4[4];           // on their way while the accumulators arrive
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s4[i] = *reinterpret_cast<const ulonglong2 *>(as + c + 4 * i);
+                        wait_ld16(v);
+                        if (c + 16 < kFoldCols && c + 16 < mine) tmem_ld<16>(dcol + c + 16, d[((c >> 4) + 1) & 1]);
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
-                            const ulonglong2 s4 = *reinterpret_cast<const ulonglong2 *>(as + c + i);
                             uint64_t &a0 = acc[(c + i) / 2], &a1 = acc[(c + i) / 2 + 1];
-                            a0 = fma2(pack2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), mul2(ws2, s4.x), a0);
-                            a1 = fma2(pack2(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])), mul2(ws2, s4.y), a1);
+                            a0 = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), mul2(ws2, s4[i >> 2].x), a0);
+                            a1 = fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), mul2(ws2, s4[i >> 2].y), a1);
                         }
                     }
                 }
@@ -365,22 +397,37 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 if (lane == 0) mbar_arrive(smem_u32(&sm.d_empty[buf]));
             }
             const int64_t first = row0 + half * kFoldCols;
+            if (GATEUP) {
+                // even lanes hold gate and take column 2i, odd lanes hold up and take 2i + 1
+                const bool odd = (lane & 1) != 0;
+                uint16_t *out = p.h + (first + (odd ? 1 : 0)) * p.n + out_r;
+                const int have = out_r < p.n ? mine - (odd ? 1 : 0) : 0;
 #pragma unroll
-            for (int i = 0; i < kFoldCols / 2; ++i) {
-                if (2 * i >= mine) break;
-                float x, y;
-                unpack2(acc[i], x, y);
-                if (GATEUP) {
-                    // even lanes hold gate and take column 2i, odd lanes hold up and take 2i + 1
-                    const bool odd = (lane & 1) != 0;
-                    const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
-                    const float g = odd ? other : x, u = odd ? y : other;
-                    const int c = 2 * i + (odd ? 1 : 0);
-                    if (c < mine && out_r < p.n)
-                        p.h[(first + c) * p.n + out_r] = f32_to_bf16_bits(__fmul_rn(tq_silu(g), u));
-                } else if (out_r < p.n) {
-                    p.y[(first + 2 * i) * p.n + out_r] = x;
-                    if (2 * i + 1 < mine) p.y[(first + 2 * i + 1) * p.n + out_r] = y;
+                for (int i0 = 0; i0 < kFoldCols / 2; i0 += 8) {
+                    if (2 * i0 >= mine) break;
+                    float g[8], u[8], s[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float x, y;
+                        unpack2(acc[i0 + i], x, y);
+                        const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+                        g[i] = odd ? other : x;
+                        u[i] = odd ? y : other;
+                    }
+                    moe_silu(g, s);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (2 * (i0 + i) < have) out[static_cast<int64_t>(2 * (i0 + i)) * p.n] = f32_to_bf16_bits(__fmul_rn(s[i], u[i]));
+                }
+            } else if (out_r < p.n) {
+                float *out = p.y + first * p.n + out_r;
+#pragma unroll
+                for (int i = 0; i < kFoldCols / 2; ++i) {
+                    if (2 * i >= mine) break;
+                    float x, y;
+                    unpack2(acc[i], x, y);
+                    out[static_cast<int64_t>(2 * i) * p.n] = x;
+                    if (2 * i + 1 < mine) out[static_cast<int64_t>(2 * i + 1) * p.n] = y;
                 }
             }
         }
@@ -394,18 +441,25 @@ done:
 }
 
 // ---------------------------------------------------------------------------
-// The operand: each row's codes in the order in which the decoded weights meet
-// them, as two e4m3 numbers each, [block][16 h: 128 bytes | l: 128 bytes].
-// One thread per 32 codes.
+// The operand: the codes of each sorted slot in the order in which the decoded
+// weights meet them, as two e4m3 numbers each, [block][16 h: 128 bytes | l: 128].
+// One thread per 32 codes.  Rows are gathered here and not by the tile kernel's
+// copies: a TMA gather of four rows runs at 13 cycles per 128-byte row
+// (measured), four times slower than the MMAs use them up.
 // ---------------------------------------------------------------------------
 template <int FMT>
-__global__ void __launch_bounds__(256) operand_kernel(const int8_t *__restrict__ q, int64_t groups,
-                                                      uint8_t *__restrict__ out) {
+__global__ void __launch_bounds__(256) operand_kernel(const int8_t *__restrict__ q, const int *__restrict__ rows,
+                                                      const int *__restrict__ offsets, int experts, int m, int slots,
+                                                      int k, uint8_t *__restrict__ out) {
     pdl_launch_dependents();
     pdl_wait();
+    const int per_row = k / 32;
+    const int64_t groups = static_cast<int64_t>(min(max(offsets[experts], 0), slots)) * per_row;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < groups;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(q + i * 32);
+        const int r = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<int64_t>(r) * per_row);
+        const int a = min(max(rows != nullptr ? rows[r] : r, 0), m - 1);
+        const uint4 *src = reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(a) * k + c * 32);
         const uint4 q0 = __ldg(src), q1 = __ldg(src + 1);
         const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
         uint32_t o[8], hi[8], lo[8];
@@ -426,15 +480,21 @@ cudaError_t launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *e
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int64_t groups = static_cast<int64_t>(p.m) * p.k / 32;
+    const int64_t groups = static_cast<int64_t>(p.slots) * p.k / 32;
     const int64_t want = (groups + 255) / 256;
     e = launch_pdl(operand_kernel<FMT>, dim3(static_cast<unsigned>(want < (1 << 20) ? want : (1 << 20))), dim3(256), 0,
-                   stream, p.q, groups, operand);
+                   stream, p.q, p.rows, p.offsets, p.experts, p.m, p.slots, p.k, operand);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = sizeof(TileSmem) + 1024;
     e = cudaFuncSetAttribute(tile_kernel<FMT, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    TileArgs a{p, operand, err, above};
+    TileArgs a{};
+    a.p = p;
+    a.err = err;
+    a.above = above;
+    e = make_tmap_2d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, operand, static_cast<uint64_t>(2) * p.k,
+                     static_cast<uint64_t>(p.slots), static_cast<uint64_t>(2) * p.k, 128, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
     return launch_pdl(tile_kernel<FMT, GATEUP>, dim3(sms), dim3(kThreads), smem, stream, a);
 }
 

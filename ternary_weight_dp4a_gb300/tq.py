@@ -513,10 +513,10 @@ def moe_workspace(m: int, topk: int, experts: int, hidden: int = 0, inter: int =
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
-def _moe_product_workspace(workspace, q):
+def _moe_product_workspace(workspace, q, slots):
     import torch
     if workspace is None:
-        return torch.zeros(256 + 2 * q.numel(), dtype=torch.uint8, device=q.device)
+        return torch.zeros(256 + 2 * slots * q.shape[1], dtype=torch.uint8, device=q.device)
     return _tensor("workspace", workspace, torch.uint8)
 
 
@@ -561,7 +561,7 @@ def moe_gemv(w: PackedExperts, q, s, plan: MoePlan, gather: bool = False, y=None
     if y is None:
         y = torch.empty((plan.slots, w.n), dtype=torch.float32, device=q.device)
     _tensor("y", y, torch.float32, (plan.slots, w.n))
-    workspace = _moe_product_workspace(workspace, q)
+    workspace = _moe_product_workspace(workspace, q, plan.slots)
     ws = w.c_struct()
     _check("tq_moe_gemv", load().tq_moe_gemv(
         ctypes.byref(ws), _ptr(q), _ptr(s), m, _ptr(plan.rows if gather else None), _ptr(plan.offsets),
@@ -579,7 +579,7 @@ def moe_gateup(gate: PackedExperts, up: PackedExperts, q, s, plan: MoePlan, gath
     if h is None:
         h = torch.empty((plan.slots, gate.n), dtype=torch.bfloat16, device=q.device)
     _tensor("h", h, torch.bfloat16, (plan.slots, gate.n))
-    workspace = _moe_product_workspace(workspace, q)
+    workspace = _moe_product_workspace(workspace, q, plan.slots)
     g, u = gate.c_struct(), up.c_struct()
     _check("tq_moe_gateup", load().tq_moe_gateup(
         ctypes.byref(g), ctypes.byref(u), _ptr(q), _ptr(s), m, _ptr(plan.rows if gather else None),
