@@ -87,37 +87,78 @@ __device__ __forceinline__ void decode_block(const uint4 *c, uint32_t (&v)[32]) 
     }
 }
 
-// SiLU of N gates, g / (1 + exp(-g)), the division correctly rounded.  For 2^-80 <= |g| < 64
-// or g = 0 without a branch: tq_expf's polynomial with 2^n put in at once (2^n is a normal
-// number there), a reciprocal refined by one Newton step, and the quotient corrected with its
-// exact remainder (P. Markstein, "IA-64 and Elementary Functions", 2000, chapter 8).  Other
-// arguments take tq_silu; the results are the same bits.
+// Two fp32 lanes per instruction, each rounded to nearest.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t both) { return pack2(__uint_as_float(both), __uint_as_float(both)); }
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
+
+// SiLU of N (even) gates, g / (1 + exp(-g)), the division correctly rounded.  For
+// 2^-80 <= |g| < 64 or g = 0 without a branch and two at a time: tq_expf's polynomial
+// with 2^n put in at once (2^n is a normal number there), a reciprocal refined by one
+// Newton step, and the quotient corrected with its exact remainder (P. Markstein,
+// "IA-64 and Elementary Functions", 2000, chapter 8).  Other arguments take tq_silu.
+// The bits are tq_silu's for every g (compared over all 2^32).
 template <int N>
 __device__ __forceinline__ void moe_silu(const float (&g)[N], float (&s)[N]) {
     bool other = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float z = -g[i], a = fabsf(g[i]);
-        other |= !(a < 64.0f) || (a < 8.2718061e-25f && a != 0.0f);
-        const float t = __fadd_rn(__fmul_rn(z, __uint_as_float(0x3fb8aa3bu)), 12582912.0f);
-        const float n = __fsub_rn(t, 12582912.0f);
-        float r = __fmaf_rn(-n, __uint_as_float(0x3f317000u), z);
-        r = __fmaf_rn(-n, __uint_as_float(0x3805fdf4u), r);
-        float p = __uint_as_float(0x39500d01u);
-        p = __fmaf_rn(p, r, __uint_as_float(0x3ab60b61u));
-        p = __fmaf_rn(p, r, __uint_as_float(0x3c088889u));
-        p = __fmaf_rn(p, r, __uint_as_float(0x3d2aaaabu));
-        p = __fmaf_rn(p, r, __uint_as_float(0x3e2aaaabu));
-        p = __fmaf_rn(p, r, 0.5f);
-        p = __fmaf_rn(p, r, 1.0f);
-        p = __fmaf_rn(p, r, 1.0f);
-        const float e = __int_as_float(__float_as_int(p) + ((__float_as_int(t) - 0x4b400000) << 23));
-        const float d = __fadd_rn(1.0f, e);
-        float y;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
-        y = __fmaf_rn(__fmaf_rn(-d, y, 1.0f), y, y);
-        const float q = __fmul_rn(g[i], y);
-        s[i] = __fmaf_rn(__fmaf_rn(-d, q, g[i]), y, q);
+    for (int i = 0; i < N; i += 2) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float a = fabsf(g[i + j]);
+            other |= !(a < 64.0f) || (a < 8.2718061e-25f && a != 0.0f);
+        }
+        const uint64_t gg = pack2(g[i], g[i + 1]), z = neg2(gg);
+        const uint64_t magic = pack2(0x4b400000u), minus = pack2(0xcb400000u);   // +-12582912
+        // (a packed product here would be fused with the addition: the product is rounded by itself)
+        const float log2e = __uint_as_float(0x3fb8aa3bu);
+        const uint64_t t = add2(pack2(__fmul_rn(-g[i], log2e), __fmul_rn(-g[i + 1], log2e)), magic);
+        const uint64_t n = neg2(add2(t, minus));
+        uint64_t r = fma2(n, pack2(0x3f317000u), z);
+        r = fma2(n, pack2(0x3805fdf4u), r);
+        uint64_t p = fma2(pack2(0x39500d01u), r, pack2(0x3ab60b61u));            // 1/7!, 1/6!
+        p = fma2(p, r, pack2(0x3c088889u));
+        p = fma2(p, r, pack2(0x3d2aaaabu));
+        p = fma2(p, r, pack2(0x3e2aaaabu));
+        p = fma2(p, r, pack2(0x3f000000u));
+        p = fma2(p, r, pack2(0x3f800000u));
+        p = fma2(p, r, pack2(0x3f800000u));
+        float p0, p1, t0, t1, d0, d1, y0, y1;
+        unpack2(p, p0, p1);
+        unpack2(t, t0, t1);
+        const uint64_t d = add2(pack2(__int_as_float(__float_as_int(p0) + ((__float_as_int(t0) - 0x4b400000) << 23)),
+                                      __int_as_float(__float_as_int(p1) + ((__float_as_int(t1) - 0x4b400000) << 23))),
+                                pack2(0x3f800000u));
+        unpack2(d, d0, d1);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(d0));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(d1));
+        uint64_t y = pack2(y0, y1);
+        const uint64_t nd = neg2(d);
+        y = fma2(fma2(nd, y, pack2(0x3f800000u)), y, y);
+        const uint64_t q = mul2(gg, y);
+        unpack2(fma2(fma2(nd, q, gg), y, q), s[i], s[i + 1]);
     }
     if (other) {
 #pragma unroll

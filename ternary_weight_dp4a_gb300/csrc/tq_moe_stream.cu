@@ -288,8 +288,10 @@ cudaError_t launch(const MoeProduct &p, int limit, cudaStream_t stream) {
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     // an upper bound of the (expert, chunk) pairs; CTAs behind the last pair leave at once
-    const int64_t pairs = static_cast<int64_t>(p.experts) + p.slots / chunk;
-    const int64_t most = pairs < p.slots ? pairs : p.slots;
+    int64_t most = static_cast<int64_t>(p.experts) + p.slots / chunk;
+    if (most > p.slots) most = p.slots;
+    const int64_t cap = static_cast<int64_t>(p.experts) * ws_cdiv(limit, chunk);
+    if (most > cap) most = cap;
     const int tile = GATEUP ? kTileM / 2 : kTileM;
     const dim3 grid(static_cast<unsigned>(most), static_cast<unsigned>((p.n + tile - 1) / tile));
     return launch_pdl(stream_kernel<FMT, GATEUP>, grid, dim3(kThreads), smem, stream, a);

@@ -37,7 +37,9 @@ namespace {
 constexpr int kCols = 224;                          // most activation rows per tile
 constexpr int kStages = 3;
 constexpr int kBoxRows = 32;                        // rows per TMA copy
-constexpr int kScaleSlots = 8;
+constexpr int kDone = 6;                            // multiple of the 3 stages and the 2 buffers
+constexpr int kGroup = 4;                           // blocks whose scales come together
+constexpr int kGroups = 3;
 constexpr int kThreads = 512;
 constexpr int kScaleThreads = 64;                   // warps 6 and 7
 constexpr uint32_t kHalf = kCols * 128;             // bytes of one part of a stage
@@ -50,8 +52,8 @@ constexpr int kRegsDecode = 96, kRegsIssue = 48, kRegsFold = 184;
 
 struct __align__(1024) TileSmem {
     uint8_t b[kStages][kStageBytes];
-    float as[kScaleSlots][kCols];
-    uint64_t b_full[kStages], b_empty[kStages], a_full[2], a_empty[2], d_full[2], d_empty[2], s_full[kScaleSlots], drain;
+    float as[kGroups][kGroup][kCols];
+    uint64_t b_full[kStages], a_full[2], d_empty[2], done[kDone], s_full[kGroups], s_empty[kGroups], drain;
     uint32_t tmem;
     uint32_t dead;                                  // a bounded wait ran out
 };
@@ -127,40 +129,27 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// (a0, a1) * (b0, b1) and fma, two fp32 lanes per instruction, each rounded to nearest
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // tcgen05.wait::ld; the registers pass through it, so nothing reads them before.
-__device__ __forceinline__ void wait_ld16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void wait_ld8(uint32_t (&r)[8]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
                  :
                  : "memory");
 }
 
 // A bounded wait; once one ran out every later wait of the CTA gives up at once.
+template <int SLEEP = 0>
 __device__ __forceinline__ bool wait_or_die(TileSmem &sm, uint64_t &bar, uint32_t parity, unsigned *err, unsigned bit) {
-    if (mbar_try_wait(smem_u32(&bar), parity)) return true;
+    const uint32_t addr = smem_u32(&bar);
+    if (mbar_try_wait(addr, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait(smem_u32(&bar), parity)) {
+    for (;;) {
+        // polls take issue slots and shared memory from the fold: few, with pauses
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+            if (mbar_try_wait(addr, parity)) return true;
+            if (SLEEP > 0) __nanosleep(SLEEP);
+        }
         if (*reinterpret_cast<volatile uint32_t *>(&sm.dead)) return false;
         if (clock64() - t0 > kWaitBudgetCycles) {
             *reinterpret_cast<volatile uint32_t *>(&sm.dead) = 1;
@@ -168,12 +157,12 @@ __device__ __forceinline__ bool wait_or_die(TileSmem &sm, uint64_t &bar, uint32_
             return false;
         }
     }
-    return true;
 }
 
 // The same for a whole warp, with one answer for all of its lanes.
+template <int SLEEP = 0>
 __device__ __forceinline__ bool warp_wait(TileSmem &sm, uint64_t &bar, uint32_t parity, unsigned *err, unsigned bit) {
-    return __all_sync(0xffffffffu, wait_or_die(sm, bar, parity, err, bit));
+    return __all_sync(0xffffffffu, wait_or_die<SLEEP>(sm, bar, parity, err, bit));
 }
 
 template <int FMT, bool GATEUP>
@@ -188,17 +177,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sm.b_full[i]), 1);
-            mbar_init(smem_u32(&sm.b_empty[i]), 1);
-        }
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sm.b_full[i]), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.a_full[i]), 4);
-            mbar_init(smem_u32(&sm.a_empty[i]), 1);
-            mbar_init(smem_u32(&sm.d_full[i]), 1);
             mbar_init(smem_u32(&sm.d_empty[i]), 8);
         }
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&sm.s_full[i]), kScaleThreads);
+        for (int i = 0; i < kDone; ++i) mbar_init(smem_u32(&sm.done[i]), 1);
+        for (int i = 0; i < kGroups; ++i) {
+            mbar_init(smem_u32(&sm.s_full[i]), kScaleThreads);
+            mbar_init(smem_u32(&sm.s_empty[i]), 8);
+        }
         mbar_init(smem_u32(&sm.drain), 1);
         sm.dead = 0;
         mbar_init_fence();
@@ -249,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     const int buf = it & 1;
                     uint32_t v[32];
                     decode_block<FMT>(&cur[j * kVec], v);
-                    if (!warp_wait(sm, sm.a_empty[buf], ((it >> 1) & 1) ^ 1, args.err, 1u << 0)) goto done;
+                    if (it >= 2 && !warp_wait<64>(sm, sm.done[(it - 2) % kDone], ((it - 2) / kDone) & 1, args.err, 1u << 0))
+                        goto done;
                     tc_fence_after();
                     __syncwarp();
                     tmem_st_x32(lane_base + buf * 32, v);
@@ -282,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         tc_mma_e4m3_ts(d, a + 8 * i, hi + 2 * i, idesc, i > 0);
                         tc_mma_e4m3_ts(d, a + 8 * i, lo + 2 * i, idesc, 1);
                     }
-                    tc_commit(smem_u32(&sm.b_empty[st]));
-                    tc_commit(smem_u32(&sm.a_empty[buf]));
-                    tc_commit(smem_u32(&sm.d_full[buf]));
+                    // one commit frees the stage and the A buffer and hands over the accumulator
+                    // (each waits for the block that it needs; none is ever six blocks behind)
+                    tc_commit(smem_u32(&sm.done[it % kDone]));
                 }
             }
             it = __shfl_sync(0xffffffffu, it, 0);
@@ -305,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 const int part = lane >> 3, box = lane & 7;
                 for (int b = 0; b < nb; ++b, ++it) {
                     const int st = it % kStages;
-                    ok = warp_wait(sm, sm.b_empty[st], ((it / kStages) & 1) ^ 1, args.err, 1u << 5);
+                    ok = it < kStages || warp_wait<64>(sm, sm.done[(it - kStages) % kDone], ((it - kStages) / kDone) & 1,
+                                                       args.err, 1u << 5);
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&sm.b_full[st]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes) * 2 * kBoxRows * 128);
@@ -328,29 +318,31 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     const int r = row0 + min(ct + kScaleThreads * i, cols - 1);
                     src[i] = p.s + static_cast<int64_t>(min(max(p.rows != nullptr ? p.rows[r] : r, 0), p.m - 1)) * nb;
                 }
-                for (int b = 0; b < nb; ++b) {
-                    const int st = it % kStages, slot = it % kScaleSlots;
-                    // a slot is free again long before: its block's fold came before the MMAs that freed this stage
-                    ok = warp_wait(sm, sm.b_empty[st], ((it / kStages) & 1) ^ 1, args.err, 1u << 5);
+                for (int b = 0; b < nb; b += kGroup, ++it) {
+                    const int slot = it % kGroups;
+                    ok = warp_wait<64>(sm, sm.s_empty[slot], ((it / kGroups) & 1) ^ 1, args.err, 1u << 6);
                     if (!ok) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (ct + kScaleThreads * i < cols) cp_async4(smem_u32(&sm.as[slot][ct + kScaleThreads * i]), src[i] + b);
+                    for (int j = 0; j < kGroup; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (b + j < nb && ct + kScaleThreads * i < cols)
+                                cp_async4(smem_u32(&sm.as[slot][j][ct + kScaleThreads * i]), src[i] + b + j);
                     cp_async_commit();
-                    if (it >= 2) {
-                        cp_async_wait<2>();         // the block before last has landed
-                        mbar_arrive(smem_u32(&sm.s_full[(it - 2) % kScaleSlots]));
+                    if (it >= 1) {
+                        cp_async_wait<1>();         // the group before has landed
+                        mbar_arrive(smem_u32(&sm.s_full[(it - 1) % kGroups]));
                     }
-                    ++it;
                 }
             }
             cp_async_wait<0>();
-            for (int j = max(it - 2, 0); j < it; ++j) mbar_arrive(smem_u32(&sm.s_full[j % kScaleSlots]));
+            if (it >= 1) mbar_arrive(smem_u32(&sm.s_full[(it - 1) % kGroups]));
         }
     } else {
         // ---- fold ----
         const int quarter = warp & 3, half = (warp - 8) >> 2;
         const int r_tile = 32 * quarter + lane;
+        int group = 0;                              // groups of scales since the start
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kFoldCols;
         for (int item = blockIdx.x; find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
             const int n0 = (item % ntiles) * kRowsPerTile;
@@ -361,40 +353,46 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             uint64_t acc[kFoldCols / 2];
 #pragma unroll
             for (int i = 0; i < kFoldCols / 2; ++i) acc[i] = 0;
-            uint16_t ws_next = ldg_u16(wsp);
+            uint16_t ws_next[2] = {ldg_u16(wsp), ldg_u16(wsp + min(1, nb - 1))};   // two blocks ahead
             for (int b = 0; b < nb; ++b, ++it) {
-                const int buf = it & 1, slot = it % kScaleSlots;
-                const float ws = f16_bits_to_f32(ws_next);
-                if (b + 1 < nb) ws_next = ldg_u16(wsp + b + 1);
+                const int buf = it & 1, slot = group % kGroups, in_group = b % kGroup;
+                const float ws = f16_bits_to_f32(ws_next[0]);
+                ws_next[0] = ws_next[1];
+                if (b + 2 < nb) ws_next[1] = ldg_u16(wsp + b + 2);
                 const uint64_t ws2 = pack2(ws, ws);
-                if (!warp_wait(sm, sm.s_full[slot], (it / kScaleSlots) & 1, args.err, 1u << 6)) goto done;
-                if (!warp_wait(sm, sm.d_full[buf], (it >> 1) & 1, args.err, 1u << 7)) goto done;
+                if (in_group == 0 && !warp_wait(sm, sm.s_full[slot], (group / kGroups) & 1, args.err, 1u << 6)) goto done;
+                if (!warp_wait(sm, sm.done[it % kDone], (it / kDone) & 1, args.err, 1u << 7)) goto done;
                 tc_fence_after();
-                __syncwarp();
-                const float *as = &sm.as[slot][half * kFoldCols];
+                const float *as = &sm.as[slot][in_group][half * kFoldCols];
                 const uint32_t dcol = lane_base + buf * kCols;
-                uint32_t d[2][16];
-                if (mine > 0) tmem_ld<16>(dcol, d[0]);
+                // all columns, whether the tile has them or not (what the others hold goes
+                // nowhere), eight at a time: while they are folded the next are on their way
+                uint32_t v[2][8];
+                ulonglong2 s4[2][2];
+                tmem_ld<8>(dcol, v[0]);
+                s4[0][0] = *reinterpret_cast<const ulonglong2 *>(as);
+                s4[0][1] = *reinterpret_cast<const ulonglong2 *>(as + 4);
 #pragma unroll
-                for (int c = 0; c < kFoldCols; c += 16) {
-                    if (c < mine) {                 // the same for the whole warp
-                        uint32_t (&v)[16] = d[(c >> 4) & 1];
-                        ulonglong2 s4[4];           // on their way while the accumulators arrive
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s4[i] = *reinterpret_cast<const ulonglong2 *>(as + c + 4 * i);
-                        wait_ld16(v);
-                        if (c + 16 < kFoldCols && c + 16 < mine) tmem_ld<16>(dcol + c + 16, d[((c >> 4) + 1) & 1]);
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            uint64_t &a0 = acc[(c + i) / 2], &a1 = acc[(c + i) / 2 + 1];
-                            a0 = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), mul2(ws2, s4[i >> 2].x), a0);
-                            a1 = fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), mul2(ws2, s4[i >> 2].y), a1);
-                        }
+                for (int c = 0; c < kFoldCols / 8; ++c) {
+                    const int x = c & 1;
+                    wait_ld8(v[x]);
+                    if (c + 1 < kFoldCols / 8) {
+                        tmem_ld<8>(dcol + 8 * c + 8, v[x ^ 1]);
+                        s4[x ^ 1][0] = *reinterpret_cast<const ulonglong2 *>(as + 8 * c + 8);
+                        s4[x ^ 1][1] = *reinterpret_cast<const ulonglong2 *>(as + 8 * c + 12);
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[4 * c + i] = fma2(pack2(__uint_as_float(v[x][2 * i]), __uint_as_float(v[x][2 * i + 1])),
+                                              mul2(ws2, i & 1 ? s4[x][i >> 1].y : s4[x][i >> 1].x), acc[4 * c + i]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.d_empty[buf]));
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sm.d_empty[buf]));
+                    if (in_group == kGroup - 1 || b + 1 == nb) mbar_arrive(smem_u32(&sm.s_empty[slot]));
+                }
+                if (in_group == kGroup - 1 || b + 1 == nb) ++group;
             }
             const int64_t first = row0 + half * kFoldCols;
             if (GATEUP) {
