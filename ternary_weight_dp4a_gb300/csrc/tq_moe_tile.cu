@@ -2,7 +2,7 @@
 // 5th-generation tensor core.
 //
 // A tile is 128 weight rows x up to 224 activation rows of one expert (gate/up:
-// 64 rows of each, interleaved, so that a pair of lanes holds both values of an
+// 64 rows of each, eight by eight, so that one lane folds both values of an
 // output).  The weights are the A operand, decoded from their codes to e4m3
 // -1, 0, +1 straight into tensor memory; the activations are the B operand in
 // shared memory, each int8 code as two exact e4m3 numbers q = 16 h + l (sign
@@ -35,6 +35,7 @@ namespace tq {
 namespace {
 
 constexpr int kCols = 224;                          // most activation rows per tile
+constexpr int kCluster = 2;                         // CTAs that share activation rows: each brings one part
 constexpr int kStages = 3;
 constexpr int kBoxRows = 32;                        // rows per TMA copy
 constexpr int kDone = 6;                            // multiple of the 3 stages and the 2 buffers
@@ -47,13 +48,17 @@ constexpr uint32_t kStageBytes = 2 * kHalf;
 constexpr uint32_t kTmemA = 2 * kCols;              // first column of the A buffers
 constexpr int kFoldCols = kCols / 2;                // columns per fold warp
 
-// register shares (launched with 128 per thread): 128 x (96 + 48 + 2 x 184) = 512 x 128
-constexpr int kRegsDecode = 96, kRegsIssue = 48, kRegsFold = 184;
+// register shares (launched with 128 per thread): 128 x (80 + 48 + 2 x 192) = 512 x 128
+constexpr int kRegsDecode = 80, kRegsIssue = 48, kRegsFold = 192;
 
 struct __align__(1024) TileSmem {
     uint8_t b[kStages][kStageBytes];
-    float as[kGroups][kGroup][kCols];
-    uint64_t b_full[kStages], a_full[2], d_empty[2], done[kDone], s_full[kGroups], s_empty[kGroups], drain;
+    float2 as[kGroups][kGroup][kCols];              // activation scales, each twice, in fold order
+    float ws[kGroups][kGroup][128];                 // weight scales, in fold order
+    int offsets[TQ_MOE_MAX_EXPERTS + 1];            // clamped to 0 .. slots
+    int tiles[TQ_MOE_MAX_EXPERTS + 1];              // column tiles of the experts before
+    int warp_sum[kThreads / 32];
+    uint64_t b_full[kStages], b_empty[kStages], a_full[2], d_empty[2], done[kDone], s_full[kGroups], s_empty[kGroups], drain;
     uint32_t tmem;
     uint32_t dead;                                  // a bounded wait ran out
 };
@@ -65,39 +70,56 @@ struct TileArgs {
     int above;                  // experts with more rows than this are this kernel's
 };
 
-// The pair'th (expert, part of its rows); false behind the last.  An expert's
-// rows are dealt to as few tiles as hold them, evenly.
-__device__ __forceinline__ bool find_tile(const MoeProduct &p, int above, int pair, int &expert, int &row0, int &cols) {
-    const int lane = threadIdx.x & 31;
+// An expert's rows are dealt to as few tiles as hold them, evenly, in multiples of 16.
+__device__ __forceinline__ int expert_tiles(int rows, int above) { return rows > above ? (rows + kCols - 1) / kCols : 0; }
+
+// Fill sm.offsets and sm.tiles (all threads).
+__device__ __forceinline__ void list_tiles(TileSmem &sm, const MoeProduct &p, int above) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e <= p.experts; e += kThreads) sm.offsets[e] = min(max(p.offsets[e], 0), p.slots);
+    __syncthreads();
     int base = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-        const int e = e0 + lane;
-        int lo = 0, n = 0;
-        if (e < p.experts) {
-            lo = min(max(p.offsets[e], 0), p.slots);
-            n = max(min(max(p.offsets[e + 1], 0), p.slots) - lo, 0);
-        }
-        const int c = n > above ? (n + kCols - 1) / kCols : 0;
+    for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
+        const int e = e0 + tid;
+        const int c = e < p.experts ? expert_tiles(sm.offsets[e + 1] - sm.offsets[e], above) : 0;
         int incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, pair < base + incl);
-        if (hit != 0) {
-            const int src = __ffs(hit) - 1;
-            const int part = pair - base - __shfl_sync(0xffffffffu, incl - c, src);
-            const int parts = __shfl_sync(0xffffffffu, c, src), rows = __shfl_sync(0xffffffffu, n, src);
-            const int each = ((rows + parts - 1) / parts + 15) / 16 * 16;    // at most kCols, a multiple of 16
-            expert = e0 + src;
-            row0 = __shfl_sync(0xffffffffu, lo, src) + part * each;
-            cols = min(each, rows - part * each);
-            return true;                             // cols may be 0 or less for the last part
+        if (lane == 31) sm.warp_sum[warp] = incl;
+        __syncthreads();
+        int all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int s = sm.warp_sum[w];
+            if (w < warp) incl += s;
+            all += s;
         }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+        if (e < p.experts) sm.tiles[e] = base + incl - c;
+        base += all;
+        __syncthreads();
     }
-    return false;
+    if (tid == 0) sm.tiles[p.experts] = base;
+    __syncthreads();
+}
+
+// The expert and rows of column tile `pair`; false behind the last.
+__device__ __forceinline__ bool find_tile(const TileSmem &sm, int experts, int pair, int &expert, int &row0, int &cols) {
+    if (pair >= sm.tiles[experts]) return false;
+    int lo = 0, hi = experts;                       // tiles[lo] <= pair < tiles[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sm.tiles[mid] <= pair) lo = mid;
+        else hi = mid;
+    }
+    const int parts = sm.tiles[lo + 1] - sm.tiles[lo], part = pair - sm.tiles[lo];
+    const int rows = sm.offsets[lo + 1] - sm.offsets[lo];
+    const int each = ((rows + parts - 1) / parts + 15) / 16 * 16;            // at most kCols
+    expert = lo;
+    row0 = sm.offsets[lo] + part * each;
+    cols = min(each, rows - part * each);           // at least 1: (parts - 1) * kCols < rows
+    return true;
 }
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
@@ -110,13 +132,30 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
     return d;
 }
 
-// kBoxRows rows of 128 bytes at (byte x, row y) of the operand; counted on `bar`.
+// kBoxRows rows of 128 bytes at (byte x, row y) of the operand, to the same place in both
+// CTAs of the cluster; counted on each one's `bar`.
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
+        "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>((1u << kCluster) - 1))
         : "memory");
 }
+// tc_commit to the barrier at this address in every CTA of the cluster.
+__device__ __forceinline__ void tc_commit_cluster(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(static_cast<uint16_t>((1u << kCluster) - 1))
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -130,10 +169,24 @@ template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // tcgen05.wait::ld; the registers pass through it, so nothing reads them before.
-__device__ __forceinline__ void wait_ld8(uint32_t (&r)[8]) {
+__device__ __forceinline__ void wait_ld16(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
+                 : "memory");
+}
+
+// 32 lanes x 16 columns in the 16x128b shape, lanes 0-15 and 16-31: register
+// 8 h + 2 n + j is row 16 h + 8 j + lane / 4, column 4 n + lane % 4.
+__device__ __forceinline__ void ld_chunk(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr + (16u << 16))
                  : "memory");
 }
 
@@ -177,14 +230,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sm.b_full[i]), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm.b_full[i]), 1);
+            mbar_init(smem_u32(&sm.b_empty[i]), kCluster);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.a_full[i]), 4);
             mbar_init(smem_u32(&sm.d_empty[i]), 8);
         }
         for (int i = 0; i < kDone; ++i) mbar_init(smem_u32(&sm.done[i]), 1);
         for (int i = 0; i < kGroups; ++i) {
-            mbar_init(smem_u32(&sm.s_full[i]), kScaleThreads);
+            mbar_init(smem_u32(&sm.s_full[i]), kScaleThreads + 4);
             mbar_init(smem_u32(&sm.s_empty[i]), 8);
         }
         mbar_init(smem_u32(&sm.drain), 1);
@@ -193,14 +249,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                                 // the other CTA's barriers are ready, too
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     pdl_launch_dependents();
     pdl_wait();
+    list_tiles(sm, p, args.above);
 
     const int nb = p.k / kBlock;
     constexpr int kRowsPerTile = GATEUP ? 64 : 128;
-    const int ntiles = (p.n + kRowsPerTile - 1) / kRowsPerTile;
+    // the CTAs of a cluster take neighbouring row tiles of one column tile
+    const int nparts = (p.n + kCluster * kRowsPerTile - 1) / (kCluster * kRowsPerTile);
+    const int rank = static_cast<int>(cluster_rank());
+    const int first_item = blockIdx.x / kCluster, item_step = gridDim.x / kCluster;
     constexpr int kBlockBytes = FMT == 0 ? 32 : 16;
     int it = 0;                                     // blocks since the start, over all tiles
     int expert, row0, cols;
@@ -212,27 +273,40 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     if (warp < 4) {
         // ---- decode: thread = lane of tensor memory = weight row ----
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16) + kTmemA;
-        for (int item = blockIdx.x; find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
-            const int n0 = (item % ntiles) * kRowsPerTile;
-            const int r = min(GATEUP ? n0 + (tid >> 1) : n0 + tid, p.n - 1);
-            const uint8_t *codes = p.codes[GATEUP ? tid & 1 : 0];
+        int group = 0;
+        for (int item = first_item; find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
+            const int n0 = ((item % nparts) * kCluster + rank) * kRowsPerTile;
+            const int r = min(GATEUP ? n0 + 16 * warp + 8 * (lane >> 4) + (lane & 7) : n0 + tid, p.n - 1);
+            const uint8_t *codes = p.codes[GATEUP ? (lane >> 3) & 1 : 0];
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 codes + (static_cast<int64_t>(expert) * p.n + r) * nb * kBlockBytes);
+            const uint16_t *wsp = p.scales[GATEUP ? (lane >> 3) & 1 : 0] + (static_cast<int64_t>(expert) * p.n + r) * nb;
             constexpr int kVec = kBlockBytes / 16;
-            // four blocks per fetch, one fetch ahead
-            uint4 next[4 * kVec];
+            // two blocks per fetch, one fetch ahead
+            uint4 next[2 * kVec];
 #pragma unroll
-            for (int i = 0; i < 4 * kVec; ++i)
+            for (int i = 0; i < 2 * kVec; ++i)
                 if (i < nb * kVec) next[i] = __ldg(src + i);
-            for (int b0 = 0; b0 < nb; b0 += 4) {
-                uint4 cur[4 * kVec];
+            for (int b0 = 0; b0 < nb; b0 += 2) {
+                uint4 cur[2 * kVec];
 #pragma unroll
-                for (int i = 0; i < 4 * kVec; ++i) {
+                for (int i = 0; i < 2 * kVec; ++i) {
                     cur[i] = next[i];
-                    if ((b0 + 4) * kVec + i < nb * kVec) next[i] = __ldg(src + (b0 + 4) * kVec + i);
+                    if ((b0 + 2) * kVec + i < nb * kVec) next[i] = __ldg(src + (b0 + 2) * kVec + i);
+                }
+                if (b0 % kGroup == 0) {             // this row's weight scales of the group, to the fold's place
+                    const int slot = group % kGroups;
+                    if (!warp_wait<64>(sm, sm.s_empty[slot], ((group / kGroups) & 1) ^ 1, args.err, 1u << 6)) goto done;
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j)
+                        if (b0 + j < nb)
+                            sm.ws[slot][j][32 * warp + 4 * (lane & 7) + (lane >> 3)] = f16_bits_to_f32(ldg_u16(wsp + b0 + j));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[slot]));
+                    ++group;
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 2; ++j) {
                     if (b0 + j >= nb) break;
                     const int buf = it & 1;
                     uint32_t v[32];
@@ -252,16 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
     } else if (warp == 4) {
         // ---- issue ----
-        for (int item = blockIdx.x; find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
+        for (int item = first_item; find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
             const uint32_t n16 = static_cast<uint32_t>(max(cols + 15, 16)) / 16 * 16;
             const uint32_t idesc = idesc_e4m3(128, static_cast<int>(n16));
             bool ok = true;
             if (lane == 0) {
                 for (int b = 0; b < nb && ok; ++b, ++it) {
                     const int st = it % kStages, buf = it & 1;
-                    ok = wait_or_die(sm, sm.d_empty[buf], ((it >> 1) & 1) ^ 1, args.err, 1u << 1) &&
-                         wait_or_die(sm, sm.a_full[buf], (it >> 1) & 1, args.err, 1u << 2) &&
-                         wait_or_die(sm, sm.b_full[st], (it / kStages) & 1, args.err, 1u << 3);
+                    ok = wait_or_die(sm, sm.a_full[buf], (it >> 1) & 1, args.err, 1u << 2) &&
+                         wait_or_die(sm, sm.b_full[st], (it / kStages) & 1, args.err, 1u << 3) &&
+                         wait_or_die(sm, sm.d_empty[buf], ((it >> 1) & 1) ^ 1, args.err, 1u << 1);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + buf * kCols, a = tmem + kTmemA + buf * 32;
@@ -271,8 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         tc_mma_e4m3_ts(d, a + 8 * i, hi + 2 * i, idesc, i > 0);
                         tc_mma_e4m3_ts(d, a + 8 * i, lo + 2 * i, idesc, 1);
                     }
-                    // one commit frees the stage and the A buffer and hands over the accumulator
-                    // (each waits for the block that it needs; none is ever six blocks behind)
+                    // frees the stage in both CTAs; frees the A buffer and hands over the accumulator
+                    // (who waits, waits for the block that it needs; none is ever six blocks behind)
+                    tc_commit_cluster(smem_u32(&sm.b_empty[st]));
                     tc_commit(smem_u32(&sm.done[it % kDone]));
                 }
             }
@@ -285,24 +360,22 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp < 8) {
-        // ---- copy: warp 5 brings activation rows, 32 per copy, lane i rows 32 i
-        // (i < 7) of one part and lane 8 + i of the other; warps 6 and 7 the scales ----
+        // ---- copy: warp 5 brings one part of the activation rows' codes (each CTA of the
+        // cluster another), 32 rows per copy, for both CTAs; warps 6 and 7 the scales ----
         if (warp == 5) {
             bool ok = true;
-            for (int item = blockIdx.x; ok && find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
+            for (int item = first_item; ok && find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
                 const int boxes = (cols + kBoxRows - 1) / kBoxRows;
-                const int part = lane >> 3, box = lane & 7;
                 for (int b = 0; b < nb; ++b, ++it) {
                     const int st = it % kStages;
-                    ok = it < kStages || warp_wait<64>(sm, sm.done[(it - kStages) % kDone], ((it - kStages) / kDone) & 1,
-                                                       args.err, 1u << 5);
+                    ok = warp_wait<64>(sm, sm.b_empty[st], ((it / kStages) & 1) ^ 1, args.err, 1u << 5);
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&sm.b_full[st]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes) * 2 * kBoxRows * 128);
                     __syncwarp();
-                    if (lane < 16 && box < boxes)
-                        copy_box(smem_u32(sm.b[st]) + part * kHalf + box * kBoxRows * 128, &args.map, b * 256 + part * 128,
-                                 row0 + box * kBoxRows, bar);
+                    if (lane < boxes)
+                        copy_box(smem_u32(sm.b[st]) + rank * kHalf + lane * kBoxRows * 128, &args.map, b * 256 + rank * 128,
+                                 row0 + lane * kBoxRows, bar);
                 }
             }
             // none of this CTA's copies may be in flight when it leaves
@@ -311,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         } else {
             const int ct = tid - 192;
             bool ok = true;
-            for (int item = blockIdx.x; ok && find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
+            for (int item = first_item; ok && find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
                 const float *src[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -325,9 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
                     for (int j = 0; j < kGroup; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (b + j < nb && ct + kScaleThreads * i < cols)
-                                cp_async4(smem_u32(&sm.as[slot][j][ct + kScaleThreads * i]), src[i] + b + j);
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = ct + kScaleThreads * i;
+                            if (b + j < nb && c < cols) {
+                                // columns c, c + 4, c + 8, c + 12 of 16 are one lane's: side by side
+                                const uint32_t dst = smem_u32(&sm.as[slot][j][(c & ~15) + 4 * (c & 3) + ((c >> 2) & 3)]);
+                                cp_async4(dst, src[i] + b + j);
+                                cp_async4(dst + 4, src[i] + b + j);
+                            }
+                        }
                     cp_async_commit();
                     if (it >= 1) {
                         cp_async_wait<1>();         // the group before has landed
@@ -340,51 +419,49 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
     } else {
         // ---- fold ----
-        const int quarter = warp & 3, half = (warp - 8) >> 2;
-        const int r_tile = 32 * quarter + lane;
+        // A lane (i = lane / 4, t = lane % 4) holds rows i, i + 8, i + 16, i + 24 of its
+        // quarter and every fourth column from t on (shape 16x128b, register pairs are
+        // rows i and i + 8), so a column's scale serves eight lanes and four rows.  With
+        // a row and all columns per lane (32x32b) every scale is read in all 32 lanes, 530 of
+        // the 1024 cycles that a block's MMAs take, from the shared memory that also feeds
+        // the MMAs (896): the fold of a block then took 1200 cycles.
+        const int quarter = warp & 3, half = (warp - 8) >> 2, i = lane >> 2, t = lane & 3;
         int group = 0;                              // groups of scales since the start
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kFoldCols;
-        for (int item = blockIdx.x; find_tile(p, args.above, item / ntiles, expert, row0, cols); item += gridDim.x) {
-            const int n0 = (item % ntiles) * kRowsPerTile;
-            const int out_r = GATEUP ? n0 + (r_tile >> 1) : n0 + r_tile;
-            const uint16_t *wsp = p.scales[GATEUP ? r_tile & 1 : 0] +
-                                  (static_cast<int64_t>(expert) * p.n + min(out_r, p.n - 1)) * nb;
+        for (int item = first_item; find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
+            const int n0 = ((item % nparts) * kCluster + rank) * kRowsPerTile;
             const int mine = min(max(cols - half * kFoldCols, 0), kFoldCols);   // columns of this warp
-            uint64_t acc[kFoldCols / 2];
+            uint64_t acc[kFoldCols / 4][2];         // [column t + 4 n][h]
 #pragma unroll
-            for (int i = 0; i < kFoldCols / 2; ++i) acc[i] = 0;
-            uint16_t ws_next[2] = {ldg_u16(wsp), ldg_u16(wsp + min(1, nb - 1))};   // two blocks ahead
+            for (int n = 0; n < kFoldCols / 4; ++n) acc[n][0] = acc[n][1] = 0;
             for (int b = 0; b < nb; ++b, ++it) {
                 const int buf = it & 1, slot = group % kGroups, in_group = b % kGroup;
-                const float ws = f16_bits_to_f32(ws_next[0]);
-                ws_next[0] = ws_next[1];
-                if (b + 2 < nb) ws_next[1] = ldg_u16(wsp + b + 2);
-                const uint64_t ws2 = pack2(ws, ws);
                 if (in_group == 0 && !warp_wait(sm, sm.s_full[slot], (group / kGroups) & 1, args.err, 1u << 6)) goto done;
+                // weight scales of lane rows 16 h + i, 16 h + 8 + i
+                const ulonglong2 ws2 = *reinterpret_cast<const ulonglong2 *>(&sm.ws[slot][in_group][32 * quarter + 4 * i]);
                 if (!warp_wait(sm, sm.done[it % kDone], (it / kDone) & 1, args.err, 1u << 7)) goto done;
                 tc_fence_after();
-                const float *as = &sm.as[slot][in_group][half * kFoldCols];
+                const float2 *as = &sm.as[slot][in_group][half * kFoldCols + 4 * t];
                 const uint32_t dcol = lane_base + buf * kCols;
                 // all columns, whether the tile has them or not (what the others hold goes
-                // nowhere), eight at a time: while they are folded the next are on their way
-                uint32_t v[2][8];
-                ulonglong2 s4[2][2];
-                tmem_ld<8>(dcol, v[0]);
-                s4[0][0] = *reinterpret_cast<const ulonglong2 *>(as);
-                s4[0][1] = *reinterpret_cast<const ulonglong2 *>(as + 4);
+                // nowhere), 16 at a time: while they are folded the next are on their way
+                uint32_t v[2][16];
+                ld_chunk(dcol, v[0]);
 #pragma unroll
-                for (int c = 0; c < kFoldCols / 8; ++c) {
-                    const int x = c & 1;
-                    wait_ld8(v[x]);
-                    if (c + 1 < kFoldCols / 8) {
-                        tmem_ld<8>(dcol + 8 * c + 8, v[x ^ 1]);
-                        s4[x ^ 1][0] = *reinterpret_cast<const ulonglong2 *>(as + 8 * c + 8);
-                        s4[x ^ 1][1] = *reinterpret_cast<const ulonglong2 *>(as + 8 * c + 12);
+                for (int c = 0; c < kFoldCols / 16; ++c) {
+                    uint32_t (&x)[16] = v[c & 1];
+                    const ulonglong2 s01 = *reinterpret_cast<const ulonglong2 *>(as + 16 * c),
+                                     s23 = *reinterpret_cast<const ulonglong2 *>(as + 16 * c + 2);
+                    wait_ld16(x);
+                    if (c + 1 < kFoldCols / 16) ld_chunk(dcol + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const uint64_t s = n == 0 ? s01.x : n == 1 ? s01.y : n == 2 ? s23.x : s23.y;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            acc[4 * c + n][h] = fma2(pack2(__uint_as_float(x[8 * h + 2 * n]), __uint_as_float(x[8 * h + 2 * n + 1])),
+                                                     mul2(h == 0 ? ws2.x : ws2.y, s), acc[4 * c + n][h]);
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[4 * c + i] = fma2(pack2(__uint_as_float(v[x][2 * i]), __uint_as_float(v[x][2 * i + 1])),
-                                              mul2(ws2, i & 1 ? s4[x][i >> 1].y : s4[x][i >> 1].x), acc[4 * c + i]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -394,38 +471,40 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 }
                 if (in_group == kGroup - 1 || b + 1 == nb) ++group;
             }
-            const int64_t first = row0 + half * kFoldCols;
-            if (GATEUP) {
-                // even lanes hold gate and take column 2i, odd lanes hold up and take 2i + 1
-                const bool odd = (lane & 1) != 0;
-                uint16_t *out = p.h + (first + (odd ? 1 : 0)) * p.n + out_r;
-                const int have = out_r < p.n ? mine - (odd ? 1 : 0) : 0;
+            // outputs of lane rows 16 h + i, 16 h + 8 + i: gate and up of one, or two
+            int out_r[2][2];
 #pragma unroll
-                for (int i0 = 0; i0 < kFoldCols / 2; i0 += 8) {
-                    if (2 * i0 >= mine) break;
-                    float g[8], u[8], s[8];
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float x, y;
-                        unpack2(acc[i0 + i], x, y);
-                        const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
-                        g[i] = odd ? other : x;
-                        u[i] = odd ? y : other;
+                for (int j = 0; j < 2; ++j)
+                    out_r[h][j] = GATEUP ? n0 + 16 * quarter + 8 * h + i : n0 + 32 * quarter + 16 * h + 8 * j + i;
+            const int64_t first = static_cast<int64_t>(row0 + half * kFoldCols + t) * p.n;
+            const int have = mine - t;              // columns 4 n below this are the lane's own
+#pragma unroll
+            for (int n0c = 0; n0c < kFoldCols / 4; n0c += 4) {
+                if (4 * n0c >= mine) break;
+                if (GATEUP) {
+                    float gate[8], up[8], s[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) unpack2(acc[n0c + (x >> 1)][x & 1], gate[x], up[x]);
+                    moe_silu(gate, s);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int n = n0c + (x >> 1), h = x & 1;
+                        if (4 * n < have && out_r[h][0] < p.n)
+                            p.h[first + static_cast<int64_t>(4 * n) * p.n + out_r[h][0]] = f32_to_bf16_bits(__fmul_rn(s[x], up[x]));
                     }
-                    moe_silu(g, s);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (2 * (i0 + i) < have) out[static_cast<int64_t>(2 * (i0 + i)) * p.n] = f32_to_bf16_bits(__fmul_rn(s[i], u[i]));
-                }
-            } else if (out_r < p.n) {
-                float *out = p.y + first * p.n + out_r;
+                    for (int x = 0; x < 8; ++x) {
+                        const int n = n0c + (x >> 1), h = x & 1;
+                        float y[2];
+                        unpack2(acc[n][h], y[0], y[1]);
 #pragma unroll
-                for (int i = 0; i < kFoldCols / 2; ++i) {
-                    if (2 * i >= mine) break;
-                    float x, y;
-                    unpack2(acc[i], x, y);
-                    out[static_cast<int64_t>(2 * i) * p.n] = x;
-                    if (2 * i + 1 < mine) out[static_cast<int64_t>(2 * i + 1) * p.n] = y;
+                        for (int j = 0; j < 2; ++j)
+                            if (4 * n < have && out_r[h][j] < p.n)
+                                p.y[first + static_cast<int64_t>(4 * n) * p.n + out_r[h][j]] = y[j];
+                    }
                 }
             }
         }
@@ -433,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 done:
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();                                 // the other CTA's copies and commits reach into this one
     tc_fence_after();
     if (warp == 4) tmem_dealloc(tmem, 512);
 }
@@ -493,7 +572,25 @@ cudaError_t launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *e
     e = make_tmap_2d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, operand, static_cast<uint64_t>(2) * p.k,
                      static_cast<uint64_t>(p.slots), static_cast<uint64_t>(2) * p.k, 128, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tile_kernel<FMT, GATEUP>, dim3(sms), dim3(kThreads), smem, stream, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / kCluster * kCluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {kCluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    // every cluster is resident from the start: the tiles are dealt out by cluster index
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, tile_kernel<FMT, GATEUP>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    if (clusters < sms / kCluster) cfg.gridDim = dim3(static_cast<unsigned>(clusters * kCluster));
+    return cudaLaunchKernelEx(&cfg, tile_kernel<FMT, GATEUP>, a);
 }
 
 }  // namespace
