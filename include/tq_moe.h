@@ -122,7 +122,8 @@ tq_status tq_moe_plan(const int32_t *ids, int32_t m, int32_t topk, int32_t exper
  * y: fp32 [slots][n]; rows from offsets[experts] on are left as they are.
  * n: 1 .. TQ_MOE_MAX_WIDTH, k: a multiple of 128 up to TQ_MOE_MAX_WIDTH.
  * workspace: a tq_moe_* workspace of the layer that the product belongs to, or
- * any of at least 256 + 2 * slots * k bytes that follows its conventions. */
+ * any of at least 256 + slots * (2 * k + 16 * ceil(k / 512)) bytes that
+ * follows its conventions. */
 tq_status tq_moe_gemv(const tq_experts *w, const int8_t *q, const float *s, int32_t m,
                       const int32_t *rows, const int32_t *offsets, int32_t slots, float *y,
                       void *workspace, size_t workspace_bytes, tq_stream_t stream);

@@ -63,27 +63,27 @@ __device__ __forceinline__ void split4_whole(uint32_t w, uint32_t &hi, uint32_t 
     lo = ((small & ~pick) | (large & pick)) | sign;
 }
 
-// One row's 128 weights (32 or 16 bytes of codes) -> 32 registers of four e4m3
-// numbers -1, 0, +1 each, in staged order.
+// Half (s = 0, 1) of one row's 128 weights (32 or 16 bytes of codes) -> 16 registers of
+// four e4m3 numbers -1, 0, +1 each, in staged order.
 template <int FMT>
-__device__ __forceinline__ void decode_block(const uint4 *c, uint32_t (&v)[32]) {
+__device__ __forceinline__ void decode_half(const uint4 *c, int s, uint32_t (&v)[16]) {
     if (FMT == 0) {
         constexpr uint32_t kTable = 0x00b83800u;                // codes 0, 1, 2 -> 0, +1, -1
+        const uint32_t w[4] = {c[s].x, c[s].y, c[s].z, c[s].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w = i & 2 ? (i & 1 ? c[i >> 2].w : c[i >> 2].z) : (i & 1 ? c[i >> 2].y : c[i >> 2].x);
-            const uint32_t even = w & 0x33333333u, odd = (w >> 2) & 0x33333333u;
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t even = w[i] & 0x33333333u, odd = (w[i] >> 2) & 0x33333333u;
             v[4 * i + 0] = prmt(kTable, 0u, even);
             v[4 * i + 1] = prmt(kTable, 0u, even >> 16);
             v[4 * i + 2] = prmt(kTable, 0u, odd);
             v[4 * i + 3] = prmt(kTable, 0u, odd >> 16);
         }
     } else {
-        const uint32_t w[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
+        const uint32_t w[2] = {s == 0 ? c[0].x : c[0].z, s == 0 ? c[0].y : c[0].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int s = 0; s < 8; ++s) v[8 * i + s] = ((w[i] << (7 - s)) & 0x80808080u) ^ 0xb8b8b8b8u;
+            for (int b = 0; b < 8; ++b) v[8 * i + b] = ((w[i] << (7 - b)) & 0x80808080u) ^ 0xb8b8b8b8u;
     }
 }
 

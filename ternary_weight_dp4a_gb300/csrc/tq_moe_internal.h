@@ -11,11 +11,15 @@
 namespace tq {
 
 // Workspace: err u32 | operand (the tile kernel's copy of a product's input:
-// 2 bytes per value and slot) | hist (the sort's
+// 2 bytes per value and slot, and the scales) | hist (the sort's
 // counts per block of slots) | offsets | rows | pos | h | hq | hs | y.
 struct MoeWorkspace {
     size_t err, operand, hist, offsets, rows, pos, h, hq, hs, y, total;
 };
+
+// A product's input as the tile kernel reads it: two bytes per value, and the
+// scales with their rows filled up to 16 bytes.
+constexpr int64_t moe_operand_bytes(int64_t slots, int64_t k) { return slots * (2 * k + ws_cdiv(k / 128, 4) * 16); }
 
 // slots sorted by one CTA of the plan kernels
 constexpr int kPlanChunk = 1024;
@@ -23,10 +27,9 @@ constexpr int kPlanChunk = 1024;
 constexpr MoeWorkspace moe_layout(int64_t m, int64_t topk, int64_t experts, int64_t hidden, int64_t inter) {
     MoeWorkspace w{};
     const int64_t slots = m * topk;
-    const int64_t in = slots * (hidden > inter ? hidden : inter);
     size_t off = 0;
     w.err = off; off = ws_round(off + 4);
-    w.operand = off; off = ws_round(off + static_cast<size_t>(2 * in));
+    w.operand = off; off = ws_round(off + static_cast<size_t>(moe_operand_bytes(slots, hidden > inter ? hidden : inter)));
     w.hist = off; off = ws_round(off + static_cast<size_t>(ws_cdiv(slots, kPlanChunk) * experts * 4));
     w.offsets = off; off = ws_round(off + static_cast<size_t>((experts + 1) * 4));
     w.rows = off; off = ws_round(off + static_cast<size_t>(slots * 4));
@@ -40,7 +43,7 @@ constexpr MoeWorkspace moe_layout(int64_t m, int64_t topk, int64_t experts, int6
 }
 
 // What a product alone needs: the error word and its input's operand copy.
-constexpr size_t moe_product_bytes(int64_t slots, int64_t k) { return ws_round(4) + static_cast<size_t>(2 * slots * k); }
+constexpr size_t moe_product_bytes(int64_t slots, int64_t k) { return ws_round(4) + static_cast<size_t>(moe_operand_bytes(slots, k)); }
 
 // One grouped product (up == nullptr: y; else gate and up into h).
 struct MoeProduct {
@@ -59,7 +62,7 @@ struct MoeProduct {
 };
 
 // The experts with at most `limit` rows, and those with more than `above`
-// (operand: 2 * slots * k bytes of workspace for the laid-out input).
+// (operand: moe_operand_bytes of workspace for the laid-out input).
 cudaError_t moe_stream_launch(const MoeProduct &p, int limit, cudaStream_t stream);
 cudaError_t moe_tile_launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *err, cudaStream_t stream);
 

@@ -19,7 +19,7 @@
 // two accumulators (448 of 512 columns) and two blocks of A (64 columns).
 //
 // Warps: 0-3 decode weights, 4 issues MMAs, 5 copies activation rows (TMA),
-// 6-7 their scales, 8-15 fold (a quarter of the lanes and half of the columns
+// 6 packed weights (TMA), 7 activation scales, 8-15 fold (a quarter of the lanes and half of the columns
 // each).  The fold's 112 accumulators per thread need more than an even share of
 // the registers, so the roles resize theirs.
 #include <cuda_runtime.h>
@@ -34,37 +34,42 @@
 namespace tq {
 namespace {
 
-constexpr int kCols = 224;                          // most activation rows per tile
+constexpr int kCols = 192;                          // most activation rows per tile
 constexpr int kCluster = 2;                         // CTAs that share activation rows: each brings one part
 constexpr int kStages = 3;
 constexpr int kBoxRows = 32;                        // rows per TMA copy
 constexpr int kDone = 6;                            // multiple of the 3 stages and the 2 buffers
 constexpr int kGroup = 4;                           // blocks whose scales come together
 constexpr int kGroups = 3;
-constexpr int kThreads = 512;
-constexpr int kScaleThreads = 64;                   // warps 6 and 7
+constexpr int kCodeGroups = 2;                      // groups of packed codes in shared memory
+constexpr int kFoldWarps = 12;
+constexpr int kThreads = 256 + 32 * kFoldWarps;
 constexpr uint32_t kHalf = kCols * 128;             // bytes of one part of a stage
 constexpr uint32_t kStageBytes = 2 * kHalf;
 constexpr uint32_t kTmemA = 2 * kCols;              // first column of the A buffers
-constexpr int kFoldCols = kCols / 2;                // columns per fold warp
+constexpr int kFoldCols = kCols / (kFoldWarps / 4); // columns per fold warp
 
-// register shares (launched with 128 per thread): 128 x (80 + 48 + 2 x 192) = 512 x 128
-constexpr int kRegsDecode = 80, kRegsIssue = 48, kRegsFold = 192;
+// register shares (launched with 96 per thread): 128 x (96 + 48 + 3 x 112) = 640 x 96
+constexpr int kRegsIssue = 48, kRegsFold = 112;
+constexpr int kABufs = 4;                           // blocks of decoded weights: 32 columns each
 
 struct __align__(1024) TileSmem {
     uint8_t b[kStages][kStageBytes];
+    uint8_t codes[kCodeGroups][128 * 128];          // 128 rows x 4 blocks (1-bit: 64 bytes a row), swizzled
     float2 as[kGroups][kGroup][kCols];              // activation scales, each twice, in fold order
     float ws[kGroups][kGroup][128];                 // weight scales, in fold order
     int offsets[TQ_MOE_MAX_EXPERTS + 1];            // clamped to 0 .. slots
     int tiles[TQ_MOE_MAX_EXPERTS + 1];              // column tiles of the experts before
     int warp_sum[kThreads / 32];
-    uint64_t b_full[kStages], b_empty[kStages], a_full[2], d_empty[2], done[kDone], s_full[kGroups], s_empty[kGroups], drain;
+    uint64_t b_full[kStages], b_empty[kStages], a_full[kABufs], d_empty[2], done[kDone], c_full[kCodeGroups], c_empty[kCodeGroups], s_full[kGroups], s_empty[kGroups], drain;
     uint32_t tmem;
     uint32_t dead;                                  // a bounded wait ran out
 };
 
 struct TileArgs {
     MoeProduct p;
+    CUtensorMap codes[2];       // packed weights, [experts * n][row bytes], boxes of 64 rows x 4 blocks
+    const float *scales;        // [slots][k/128 rounded up to 4]: the operand's scales
     CUtensorMap map;            // the operand, [slots][k/128][16 h: 128 | l: 128] bytes, boxes of kBoxRows x 128
     unsigned *err;
     int above;                  // experts with more rows than this are this kernel's
@@ -156,12 +161,13 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// A box of packed weights at (byte x, row y), for this CTA alone.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int R>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
@@ -187,6 +193,13 @@ __device__ __forceinline__ void ld_chunk(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(taddr + (16u << 16))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
 
@@ -234,14 +247,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             mbar_init(smem_u32(&sm.b_full[i]), 1);
             mbar_init(smem_u32(&sm.b_empty[i]), kCluster);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sm.a_full[i]), 4);
-            mbar_init(smem_u32(&sm.d_empty[i]), 8);
+        for (int i = 0; i < kABufs; ++i) mbar_init(smem_u32(&sm.a_full[i]), 4);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sm.d_empty[i]), kFoldWarps);
+        for (int i = 0; i < kCodeGroups; ++i) {
+            mbar_init(smem_u32(&sm.c_full[i]), 1);
+            mbar_init(smem_u32(&sm.c_empty[i]), 4);
         }
         for (int i = 0; i < kDone; ++i) mbar_init(smem_u32(&sm.done[i]), 1);
         for (int i = 0; i < kGroups; ++i) {
-            mbar_init(smem_u32(&sm.s_full[i]), kScaleThreads + 4);
-            mbar_init(smem_u32(&sm.s_empty[i]), 8);
+            mbar_init(smem_u32(&sm.s_full[i]), 1 + 4);
+            mbar_init(smem_u32(&sm.s_empty[i]), kFoldWarps);
         }
         mbar_init(smem_u32(&sm.drain), 1);
         sm.dead = 0;
@@ -266,60 +281,72 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     int it = 0;                                     // blocks since the start, over all tiles
     int expert, row0, cols;
 
-    if (warp < 4) regs_down<kRegsDecode>();
-    else if (warp < 8) regs_down<kRegsIssue>();
-    else regs_up<kRegsFold>();
+    // (the decode warps keep what they have)
+    if (warp >= 8) regs_up<kRegsFold>();
+    else if (warp >= 4) regs_down<kRegsIssue>();
 
     if (warp < 4) {
         // ---- decode: thread = lane of tensor memory = weight row ----
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16) + kTmemA;
         int group = 0;
+        // this lane's row in shared memory: gate/up hold 64 rows each
+        const int tile_row = GATEUP ? 16 * warp + 8 * (lane >> 4) + (lane & 7) : tid;
+        const int smem_row = GATEUP ? 64 * ((lane >> 3) & 1) + tile_row : tid;
+        const bool wide = nb % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales[0]) & 7) == 0 &&
+                          (!GATEUP || (reinterpret_cast<uintptr_t>(p.scales[1]) & 7) == 0);
         for (int item = first_item; find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
             const int n0 = ((item % nparts) * kCluster + rank) * kRowsPerTile;
-            const int r = min(GATEUP ? n0 + 16 * warp + 8 * (lane >> 4) + (lane & 7) : n0 + tid, p.n - 1);
-            const uint8_t *codes = p.codes[GATEUP ? (lane >> 3) & 1 : 0];
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                codes + (static_cast<int64_t>(expert) * p.n + r) * nb * kBlockBytes);
+            const int r = min(n0 + tile_row, p.n - 1);
             const uint16_t *wsp = p.scales[GATEUP ? (lane >> 3) & 1 : 0] + (static_cast<int64_t>(expert) * p.n + r) * nb;
-            constexpr int kVec = kBlockBytes / 16;
-            // two blocks per fetch, one fetch ahead
-            uint4 next[2 * kVec];
+            for (int b0 = 0; b0 < nb; b0 += kGroup, ++group) {
+                // the group's weight scales, to the fold's place
+                float w[kGroup];
+                if (wide) {
+                    const uint2 h = __ldg(reinterpret_cast<const uint2 *>(wsp + b0));
+                    w[0] = f16_bits_to_f32(h.x & 0xffffu); w[1] = f16_bits_to_f32(h.x >> 16);
+                    w[2] = f16_bits_to_f32(h.y & 0xffffu); w[3] = f16_bits_to_f32(h.y >> 16);
+                } else {
 #pragma unroll
-            for (int i = 0; i < 2 * kVec; ++i)
-                if (i < nb * kVec) next[i] = __ldg(src + i);
-            for (int b0 = 0; b0 < nb; b0 += 2) {
-                uint4 cur[2 * kVec];
-#pragma unroll
-                for (int i = 0; i < 2 * kVec; ++i) {
-                    cur[i] = next[i];
-                    if ((b0 + 2) * kVec + i < nb * kVec) next[i] = __ldg(src + (b0 + 2) * kVec + i);
+                    for (int j = 0; j < kGroup; ++j) w[j] = f16_bits_to_f32(ldg_u16(wsp + min(b0 + j, nb - 1)));
                 }
-                if (b0 % kGroup == 0) {             // this row's weight scales of the group, to the fold's place
-                    const int slot = group % kGroups;
-                    if (!warp_wait<64>(sm, sm.s_empty[slot], ((group / kGroups) & 1) ^ 1, args.err, 1u << 6)) goto done;
+                const int slot = group % kGroups, cslot = group % kCodeGroups;
+                if (!warp_wait<64>(sm, sm.s_empty[slot], ((group / kGroups) & 1) ^ 1, args.err, 1u << 6)) goto done;
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j)
-                        if (b0 + j < nb)
-                            sm.ws[slot][j][32 * warp + 4 * (lane & 7) + (lane >> 3)] = f16_bits_to_f32(ldg_u16(wsp + b0 + j));
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[slot]));
-                    ++group;
-                }
+                for (int j = 0; j < kGroup; ++j) sm.ws[slot][j][32 * warp + 4 * (lane & 7) + (lane >> 3)] = w[j];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[slot]));
+                if (!warp_wait<64>(sm, sm.c_full[cslot], (group / kCodeGroups) & 1, args.err, 1u << 9)) goto done;
+                const uint8_t *row = sm.codes[cslot] + smem_row * (kGroup * kBlockBytes);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < kGroup; ++j) {
                     if (b0 + j >= nb) break;
-                    const int buf = it & 1;
-                    uint32_t v[32];
-                    decode_block<FMT>(&cur[j * kVec], v);
-                    if (it >= 2 && !warp_wait<64>(sm, sm.done[(it - 2) % kDone], ((it - 2) / kDone) & 1, args.err, 1u << 0))
+                    const int abuf = it % kABufs;
+                    uint4 c[kBlockBytes / 16];
+#pragma unroll
+                    for (int i = 0; i < kBlockBytes / 16; ++i) {
+                        const int chunk = j * (kBlockBytes / 16) + i;
+                        c[i] = *reinterpret_cast<const uint4 *>(
+                            row + ((FMT == 0 ? chunk ^ (smem_row & 7) : chunk ^ ((smem_row >> 1) & 3)) << 4));
+                    }
+                    if (j == kGroup - 1 || b0 + j + 1 == nb) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sm.c_empty[cslot]));
+                    }
+                    if (it >= kABufs &&
+                        !warp_wait<64>(sm, sm.done[(it - kABufs) % kDone], ((it - kABufs) / kDone) & 1, args.err, 1u << 0))
                         goto done;
                     tc_fence_after();
                     __syncwarp();
-                    tmem_st_x32(lane_base + buf * 32, v);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        uint32_t v[16];
+                        decode_half<FMT>(c, s, v);
+                        tmem_st_x16(lane_base + abuf * 32 + 16 * s, v);
+                    }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.a_full[buf]));
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.a_full[abuf]));
                     ++it;
                 }
             }
@@ -330,15 +357,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             const uint32_t n16 = static_cast<uint32_t>(max(cols + 15, 16)) / 16 * 16;
             const uint32_t idesc = idesc_e4m3(128, static_cast<int>(n16));
             bool ok = true;
-            if (lane == 0) {
-                for (int b = 0; b < nb && ok; ++b, ++it) {
-                    const int st = it % kStages, buf = it & 1;
-                    ok = wait_or_die(sm, sm.a_full[buf], (it >> 1) & 1, args.err, 1u << 2) &&
-                         wait_or_die(sm, sm.b_full[st], (it / kStages) & 1, args.err, 1u << 3) &&
-                         wait_or_die(sm, sm.d_empty[buf], ((it >> 1) & 1) ^ 1, args.err, 1u << 1);
-                    if (!ok) break;
+            for (int b = 0; b < nb; ++b, ++it) {
+                const int st = it % kStages, buf = it & 1, abuf = it % kABufs;
+                // three waits at once, one lane each
+                uint64_t &bar = lane == 0 ? sm.a_full[abuf] : lane == 1 ? sm.b_full[st] : sm.d_empty[buf];
+                const uint32_t parity = lane == 1 ? (it / kStages) & 1 : lane == 0 ? (it / kABufs) & 1 : ((it >> 1) & 1) ^ 1;
+                ok = warp_wait(sm, bar, parity, args.err, 1u << (lane < 2 ? lane + 2 : 1));
+                if (!ok) break;
+                if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t d = tmem + buf * kCols, a = tmem + kTmemA + buf * 32;
+                    const uint32_t d = tmem + buf * kCols, a = tmem + kTmemA + abuf * 32;
                     const uint64_t hi = desc_sw128(smem_u32(sm.b[st])), lo = desc_sw128(smem_u32(sm.b[st]) + kHalf);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -350,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     tc_commit_cluster(smem_u32(&sm.b_empty[st]));
                     tc_commit(smem_u32(&sm.done[it % kDone]));
                 }
+                __syncwarp();
             }
-            it = __shfl_sync(0xffffffffu, it, 0);
-            if (!__shfl_sync(0xffffffffu, static_cast<int>(ok), 0)) break;
+            if (!ok) break;
         }
         if (lane == 0) {
             tc_commit(smem_u32(&sm.drain));
@@ -361,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         __syncwarp();
     } else if (warp < 8) {
         // ---- copy: warp 5 brings one part of the activation rows' codes (each CTA of the
-        // cluster another), 32 rows per copy, for both CTAs; warps 6 and 7 the scales ----
+        // cluster another), 32 rows per copy, for both CTAs; warp 6 the packed weights,
+        // warp 7 the activation scales ----
         if (warp == 5) {
             bool ok = true;
             for (int item = first_item; ok && find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
@@ -381,41 +410,56 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             // none of this CTA's copies may be in flight when it leaves
             for (int j = max(it - kStages, 0); j < it; ++j)
                 if (!mbar_wait(smem_u32(&sm.b_full[j % kStages]), (j / kStages) & 1)) atomicOr(args.err, 1u << 8);
-        } else {
-            const int ct = tid - 192;
+        } else if (warp == 6) {
+            // packed weights: two boxes of 64 rows, gate and up or one matrix's 128
             bool ok = true;
             for (int item = first_item; ok && find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
-                const float *src[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = row0 + min(ct + kScaleThreads * i, cols - 1);
-                    src[i] = p.s + static_cast<int64_t>(min(max(p.rows != nullptr ? p.rows[r] : r, 0), p.m - 1)) * nb;
+                const int y = expert * p.n + ((item % nparts) * kCluster + rank) * kRowsPerTile;
+                for (int b = 0; b < nb; b += kGroup, ++it) {
+                    const int slot = it % kCodeGroups;
+                    ok = warp_wait<64>(sm, sm.c_empty[slot], ((it / kCodeGroups) & 1) ^ 1, args.err, 1u << 10);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const uint32_t bar = smem_u32(&sm.c_full[slot]), dst = smem_u32(sm.codes[slot]);
+                        constexpr uint32_t kBox = 64 * kGroup * kBlockBytes;
+                        mbar_arrive_expect_tx(bar, 2 * kBox);
+                        load_box(dst, &args.codes[0], b * kBlockBytes, y, bar);
+                        load_box(dst + kBox, &args.codes[1], b * kBlockBytes, GATEUP ? y : y + 64, bar);
+                    }
+                    __syncwarp();
                 }
+            }
+            for (int j = max(it - kCodeGroups, 0); j < it; ++j)
+                if (!mbar_wait(smem_u32(&sm.c_full[j % kCodeGroups]), (j / kCodeGroups) & 1)) atomicOr(args.err, 1u << 11);
+        } else {
+            // activation scales of four blocks at a time, each lane six rows
+            constexpr int kRows = kCols / 32;
+            const int ld = (nb + 3) / 4 * 4;
+            bool ok = true;
+            for (int item = first_item; ok && find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
+                const float *src = args.scales + static_cast<int64_t>(row0) * ld;
                 for (int b = 0; b < nb; b += kGroup, ++it) {
                     const int slot = it % kGroups;
+                    float4 v[kRows];
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+                        v[i] = __ldg(reinterpret_cast<const float4 *>(src + min(lane + 32 * i, cols - 1) * ld + b));
                     ok = warp_wait<64>(sm, sm.s_empty[slot], ((it / kGroups) & 1) ^ 1, args.err, 1u << 6);
                     if (!ok) break;
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int c = ct + kScaleThreads * i;
-                            if (b + j < nb && c < cols) {
-                                // columns c, c + 4, c + 8, c + 12 of 16 are one lane's: side by side
-                                const uint32_t dst = smem_u32(&sm.as[slot][j][(c & ~15) + 4 * (c & 3) + ((c >> 2) & 3)]);
-                                cp_async4(dst, src[i] + b + j);
-                                cp_async4(dst + 4, src[i] + b + j);
-                            }
-                        }
-                    cp_async_commit();
-                    if (it >= 1) {
-                        cp_async_wait<1>();         // the group before has landed
-                        mbar_arrive(smem_u32(&sm.s_full[(it - 1) % kGroups]));
+                    for (int i = 0; i < kRows; ++i) {
+                        const int c = lane + 32 * i;
+                        // columns c, c + 4, c + 8, c + 12 of 16 are one fold lane's: side by side
+                        float2 *dst = &sm.as[slot][0][(c & ~15) + 4 * (c & 3) + ((c >> 2) & 3)];
+                        dst[0] = make_float2(v[i].x, v[i].x);
+                        dst[kCols] = make_float2(v[i].y, v[i].y);
+                        dst[2 * kCols] = make_float2(v[i].z, v[i].z);
+                        dst[3 * kCols] = make_float2(v[i].w, v[i].w);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[slot]));
                 }
             }
-            cp_async_wait<0>();
-            if (it >= 1) mbar_arrive(smem_u32(&sm.s_full[(it - 1) % kGroups]));
         }
     } else {
         // ---- fold ----
@@ -425,12 +469,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         // a row and all columns per lane (32x32b) every scale is read in all 32 lanes, 530 of
         // the 1024 cycles that a block's MMAs take, from the shared memory that also feeds
         // the MMAs (896): the fold of a block then took 1200 cycles.
-        const int quarter = warp & 3, half = (warp - 8) >> 2, i = lane >> 2, t = lane & 3;
+        const int quarter = warp & 3, part = (warp - 8) >> 2, i = lane >> 2, t = lane & 3;
         int group = 0;                              // groups of scales since the start
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kFoldCols;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * kFoldCols;
         for (int item = first_item; find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
             const int n0 = ((item % nparts) * kCluster + rank) * kRowsPerTile;
-            const int mine = min(max(cols - half * kFoldCols, 0), kFoldCols);   // columns of this warp
+            const int mine = min(max(cols - part * kFoldCols, 0), kFoldCols);   // columns of this warp
             uint64_t acc[kFoldCols / 4][2];         // [column t + 4 n][h]
 #pragma unroll
             for (int n = 0; n < kFoldCols / 4; ++n) acc[n][0] = acc[n][1] = 0;
@@ -441,19 +485,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 const ulonglong2 ws2 = *reinterpret_cast<const ulonglong2 *>(&sm.ws[slot][in_group][32 * quarter + 4 * i]);
                 if (!warp_wait(sm, sm.done[it % kDone], (it / kDone) & 1, args.err, 1u << 7)) goto done;
                 tc_fence_after();
-                const float2 *as = &sm.as[slot][in_group][half * kFoldCols + 4 * t];
+                const float2 *as = &sm.as[slot][in_group][part * kFoldCols + 4 * t];
                 const uint32_t dcol = lane_base + buf * kCols;
-                // all columns, whether the tile has them or not (what the others hold goes
-                // nowhere), 16 at a time: while they are folded the next are on their way
-                uint32_t v[2][16];
-                ld_chunk(dcol, v[0]);
+                // all columns, whether the tile has them or not (what the others hold goes nowhere)
 #pragma unroll
                 for (int c = 0; c < kFoldCols / 16; ++c) {
-                    uint32_t (&x)[16] = v[c & 1];
+                    uint32_t x[16];
+                    ld_chunk(dcol + 16 * c, x);
                     const ulonglong2 s01 = *reinterpret_cast<const ulonglong2 *>(as + 16 * c),
                                      s23 = *reinterpret_cast<const ulonglong2 *>(as + 16 * c + 2);
                     wait_ld16(x);
-                    if (c + 1 < kFoldCols / 16) ld_chunk(dcol + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         const uint64_t s = n == 0 ? s01.x : n == 1 ? s01.y : n == 2 ? s23.x : s23.y;
@@ -478,26 +519,26 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     out_r[h][j] = GATEUP ? n0 + 16 * quarter + 8 * h + i : n0 + 32 * quarter + 16 * h + 8 * j + i;
-            const int64_t first = static_cast<int64_t>(row0 + half * kFoldCols + t) * p.n;
+            const int64_t first = static_cast<int64_t>(row0 + part * kFoldCols + t) * p.n;
             const int have = mine - t;              // columns 4 n below this are the lane's own
 #pragma unroll
-            for (int n0c = 0; n0c < kFoldCols / 4; n0c += 4) {
-                if (4 * n0c >= mine) break;
+            for (int c = 0; c < kFoldCols / 4; c += 4) {
+                if (4 * c >= mine) break;
                 if (GATEUP) {
                     float gate[8], up[8], s[8];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) unpack2(acc[n0c + (x >> 1)][x & 1], gate[x], up[x]);
+                    for (int x = 0; x < 8; ++x) unpack2(acc[c + (x >> 1)][x & 1], gate[x], up[x]);
                     moe_silu(gate, s);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        const int n = n0c + (x >> 1), h = x & 1;
+                        const int n = c + (x >> 1), h = x & 1;
                         if (4 * n < have && out_r[h][0] < p.n)
                             p.h[first + static_cast<int64_t>(4 * n) * p.n + out_r[h][0]] = f32_to_bf16_bits(__fmul_rn(s[x], up[x]));
                     }
                 } else {
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        const int n = n0c + (x >> 1), h = x & 1;
+                        const int n = c + (x >> 1), h = x & 1;
                         float y[2];
                         unpack2(acc[n][h], y[0], y[1]);
 #pragma unroll
@@ -527,7 +568,8 @@ done:
 template <int FMT>
 __global__ void __launch_bounds__(256) operand_kernel(const int8_t *__restrict__ q, const int *__restrict__ rows,
                                                       const int *__restrict__ offsets, int experts, int m, int slots,
-                                                      int k, uint8_t *__restrict__ out) {
+                                                      int k, uint8_t *__restrict__ out, const float *__restrict__ s,
+                                                      float *__restrict__ s_out) {
     pdl_launch_dependents();
     pdl_wait();
     const int per_row = k / 32;
@@ -543,6 +585,8 @@ __global__ void __launch_bounds__(256) operand_kernel(const int8_t *__restrict__
         stage_order<FMT>(w, o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) split4_whole(o[j], hi[j], lo[j]);
+        if ((c & 3) == 0)
+            s_out[static_cast<int64_t>(r) * ((k / kBlock + 3) / 4 * 4) + (c >> 2)] = __ldg(s + static_cast<int64_t>(a) * (k / kBlock) + (c >> 2));
         uint8_t *dst = out + (i >> 2) * 256 + (i & 3) * 32;
         *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
@@ -557,10 +601,11 @@ cudaError_t launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *e
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    float *scales = reinterpret_cast<float *>(operand + static_cast<int64_t>(2) * p.slots * p.k);
     const int64_t groups = static_cast<int64_t>(p.slots) * p.k / 32;
     const int64_t want = (groups + 255) / 256;
     e = launch_pdl(operand_kernel<FMT>, dim3(static_cast<unsigned>(want < (1 << 20) ? want : (1 << 20))), dim3(256), 0,
-                   stream, p.q, p.rows, p.offsets, p.experts, p.m, p.slots, p.k, operand);
+                   stream, p.q, p.rows, p.offsets, p.experts, p.m, p.slots, p.k, operand, p.s, scales);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = sizeof(TileSmem) + 1024;
     e = cudaFuncSetAttribute(tile_kernel<FMT, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -572,6 +617,15 @@ cudaError_t launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *e
     e = make_tmap_2d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, operand, static_cast<uint64_t>(2) * p.k,
                      static_cast<uint64_t>(p.slots), static_cast<uint64_t>(2) * p.k, 128, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
+    a.scales = scales;
+    constexpr int kBlockBytes = FMT == 0 ? 32 : 16;
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t row_bytes = static_cast<uint64_t>(p.k / kBlock) * kBlockBytes;
+        e = make_tmap_2d(&a.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes[GATEUP ? i : 0], row_bytes,
+                         static_cast<uint64_t>(p.experts) * p.n, row_bytes, kGroup * kBlockBytes, 64,
+                         FMT == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(sms / kCluster * kCluster));
     cfg.blockDim = dim3(kThreads);

@@ -516,7 +516,7 @@ def moe_workspace(m: int, topk: int, experts: int, hidden: int = 0, inter: int =
 def _moe_product_workspace(workspace, q, slots):
     import torch
     if workspace is None:
-        return torch.zeros(256 + 2 * slots * q.shape[1], dtype=torch.uint8, device=q.device)
+        return torch.zeros(256 + slots * (2 * q.shape[1] + 16 * -(-q.shape[1] // 512)), dtype=torch.uint8, device=q.device)
     return _tensor("workspace", workspace, torch.uint8)
 
 

@@ -33,7 +33,7 @@ def _up256(v):
 def test_workspace_bytes(lib):
     m, topk, e, h, i = 3, 2, 4, 256, 512
     slots = m * topk
-    want = 256 + _up256(2 * slots * max(h, i)) + _up256(e * 4) + _up256((e + 1) * 4) + 2 * _up256(slots * 4) \
+    want = 256 + _up256(slots * (2 * max(h, i) + 16)) + _up256(e * 4) + _up256((e + 1) * 4) + 2 * _up256(slots * 4) \
         + _up256(slots * i * 2) + _up256(slots * i) + _up256(slots * (i // 128) * 4) + _up256(slots * h * 4)
     assert lib.tq_moe_workspace_bytes(m, topk, e, h, i) == want
     assert lib.tq_moe_workspace_bytes(m, topk, e, 0, 0) > 0                 # for the plan alone
@@ -76,7 +76,7 @@ def test_route_and_plan_reject(lib):
 
 
 def test_products_reject(lib):
-    need = 256 + 2 * 6 * 256
+    need = 256 + 6 * (2 * 256 + 16)
 
     def gemv(w=_x(), q=0x3000, s=0x4000, m=3, rows=0x5000, off=0x6000, slots=6, y=0x7000, ws=0x10000, wsb=need):
         return lib.tq_moe_gemv(ctypes.byref(w) if w else None, P(q), P(s), m, P(rows), P(off), slots, P(y), P(ws), wsb, ST)
