@@ -115,21 +115,18 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
 
 // SiLU of N (even) gates, g / (1 + exp(-g)), the division correctly rounded.  For
-// 2^-80 <= |g| < 64 or g = 0 without a branch and two at a time: tq_expf's polynomial
+// 2^-80 <= |g| < 64 without a branch and two at a time: tq_expf's polynomial
 // with 2^n put in at once (2^n is a normal number there), a reciprocal refined by one
 // Newton step, and the quotient corrected with its exact remainder (P. Markstein,
 // "IA-64 and Elementary Functions", 2000, chapter 8).  Other arguments take tq_silu.
 // The bits are tq_silu's for every g (compared over all 2^32).
 template <int N>
 __device__ __forceinline__ void moe_silu(const float (&g)[N], float (&s)[N]) {
-    bool other = false;
+    uint32_t far = 0;                               // |g|'s distance above 2^-80, as bits
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float a = fabsf(g[i + j]);
-            other |= !(a < 64.0f) || (a < 8.2718061e-25f && a != 0.0f);
-        }
+        for (int j = 0; j < 2; ++j) far = max(far, (__float_as_uint(g[i + j]) & 0x7fffffffu) - 0x17800000u);
         const uint64_t gg = pack2(g[i], g[i + 1]), z = neg2(gg);
         const uint64_t magic = pack2(0x4b400000u), minus = pack2(0xcb400000u);   // +-12582912
         // (a packed product here would be fused with the addition: the product is rounded by itself)
@@ -160,7 +157,7 @@ __device__ __forceinline__ void moe_silu(const float (&g)[N], float (&s)[N]) {
         const uint64_t q = mul2(gg, y);
         unpack2(fma2(fma2(nd, q, gg), y, q), s[i], s[i + 1]);
     }
-    if (other) {
+    if (far >= 0x42800000u - 0x17800000u) {         // some |g| below 2^-80 (0, too) or at least 64
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] = tq_silu(g[i]);
     }

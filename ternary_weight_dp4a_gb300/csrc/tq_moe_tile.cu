@@ -38,9 +38,9 @@ constexpr int kCols = 192;                          // most activation rows per 
 constexpr int kCluster = 2;                         // CTAs that share activation rows: each brings one part
 constexpr int kStages = 3;
 constexpr int kBoxRows = 32;                        // rows per TMA copy
-constexpr int kDone = 6;                            // multiple of the 3 stages and the 2 buffers
+constexpr int kDone = 4;
 constexpr int kGroup = 4;                           // blocks whose scales come together
-constexpr int kGroups = 3;
+constexpr int kGroups = 4;
 constexpr int kCodeGroups = 2;                      // groups of packed codes in shared memory
 constexpr int kFoldWarps = 12;
 constexpr int kThreads = 256 + 32 * kFoldWarps;
@@ -51,7 +51,7 @@ constexpr int kFoldCols = kCols / (kFoldWarps / 4); // columns per fold warp
 
 // register shares (launched with 96 per thread): 128 x (96 + 48 + 3 x 112) = 640 x 96
 constexpr int kRegsIssue = 48, kRegsFold = 112;
-constexpr int kABufs = 4;                           // blocks of decoded weights: 32 columns each
+constexpr int kABufs = kDone;                           // blocks of decoded weights: 32 columns each
 
 struct __align__(1024) TileSmem {
     uint8_t b[kStages][kStageBytes];
@@ -203,32 +203,39 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
                  : "memory");
 }
 
-// A bounded wait; once one ran out every later wait of the CTA gives up at once.
-template <int SLEEP = 0>
-__device__ __forceinline__ bool wait_or_die(TileSmem &sm, uint64_t &bar, uint32_t parity, unsigned *err, unsigned bit) {
-    const uint32_t addr = smem_u32(&bar);
-    if (mbar_try_wait(addr, parity)) return true;
+// A bounded wait.  One that runs out sets `dead` and the error word; every later
+// wait of the CTA then gives up at once, so that all roles come to their end.
+template <int SLEEP>
+__device__ __forceinline__ void wait_slow(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned *err, unsigned bit) {
     const long long t0 = clock64();
     for (;;) {
-        // polls take issue slots and shared memory from the fold: few, with pauses
 #pragma unroll 1
         for (int i = 0; i < 32; ++i) {
-            if (mbar_try_wait(addr, parity)) return true;
-            if (SLEEP > 0) __nanosleep(SLEEP);
+            if (mbar_try_wait(bar, parity)) return;
+            if (SLEEP > 0) __nanosleep(SLEEP);      // polls take issue slots from the fold
         }
-        if (*reinterpret_cast<volatile uint32_t *>(&sm.dead)) return false;
+        if (*reinterpret_cast<volatile uint32_t *>(&sm.dead)) return;
         if (clock64() - t0 > kWaitBudgetCycles) {
             *reinterpret_cast<volatile uint32_t *>(&sm.dead) = 1;
             atomicOr(err, bit);
-            return false;
+            return;
         }
     }
 }
-
-// The same for a whole warp, with one answer for all of its lanes.
 template <int SLEEP = 0>
-__device__ __forceinline__ bool warp_wait(TileSmem &sm, uint64_t &bar, uint32_t parity, unsigned *err, unsigned bit) {
-    return __all_sync(0xffffffffu, wait_or_die<SLEEP>(sm, bar, parity, err, bit));
+__device__ __forceinline__ void warp_wait(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned *err, unsigned bit) {
+    if (!mbar_try_wait(bar, parity)) wait_slow<SLEEP>(sm, bar, parity, err, bit);
+    __syncwarp();
+}
+// The same, and whether the CTA is still alive (one answer for the whole warp).
+template <int SLEEP = 0>
+__device__ __forceinline__ bool warp_wait_alive(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned *err, unsigned bit) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        wait_slow<SLEEP>(sm, bar, parity, err, bit);
+        ok = *reinterpret_cast<volatile uint32_t *>(&sm.dead) == 0;
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 template <int FMT, bool GATEUP>
@@ -310,12 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     for (int j = 0; j < kGroup; ++j) w[j] = f16_bits_to_f32(ldg_u16(wsp + min(b0 + j, nb - 1)));
                 }
                 const int slot = group % kGroups, cslot = group % kCodeGroups;
-                if (!warp_wait<64>(sm, sm.s_empty[slot], ((group / kGroups) & 1) ^ 1, args.err, 1u << 6)) goto done;
+                warp_wait<64>(sm, smem_u32(&sm.s_empty[slot]), ((group / kGroups) & 1) ^ 1, args.err, 1u << 6);
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j) sm.ws[slot][j][32 * warp + 4 * (lane & 7) + (lane >> 3)] = w[j];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[slot]));
-                if (!warp_wait<64>(sm, sm.c_full[cslot], (group / kCodeGroups) & 1, args.err, 1u << 9)) goto done;
+                warp_wait<64>(sm, smem_u32(&sm.c_full[cslot]), (group / kCodeGroups) & 1, args.err, 1u << 9);
                 const uint8_t *row = sm.codes[cslot] + smem_row * (kGroup * kBlockBytes);
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j) {
@@ -332,11 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&sm.c_empty[cslot]));
                     }
-                    if (it >= kABufs &&
-                        !warp_wait<64>(sm, sm.done[(it - kABufs) % kDone], ((it - kABufs) / kDone) & 1, args.err, 1u << 0))
-                        goto done;
+                    // the buffer's last reader is done (kABufs == kDone: the phase before this block's)
+                    warp_wait<64>(sm, smem_u32(&sm.done[abuf]), ((it / kDone) & 1) ^ 1, args.err, 1u << 0);
                     tc_fence_after();
-                    __syncwarp();
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         uint32_t v[16];
@@ -360,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             for (int b = 0; b < nb; ++b, ++it) {
                 const int st = it % kStages, buf = it & 1, abuf = it % kABufs;
                 // three waits at once, one lane each
-                uint64_t &bar = lane == 0 ? sm.a_full[abuf] : lane == 1 ? sm.b_full[st] : sm.d_empty[buf];
+                const uint32_t bar = smem_u32(lane == 0 ? &sm.a_full[abuf] : lane == 1 ? &sm.b_full[st] : &sm.d_empty[buf]);
                 const uint32_t parity = lane == 1 ? (it / kStages) & 1 : lane == 0 ? (it / kABufs) & 1 : ((it >> 1) & 1) ^ 1;
-                ok = warp_wait(sm, bar, parity, args.err, 1u << (lane < 2 ? lane + 2 : 1));
+                ok = warp_wait_alive(sm, bar, parity, args.err, 1u << (lane < 2 ? lane + 2 : 1));
                 if (!ok) break;
                 if (lane == 0) {
                     tc_fence_after();
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 const int boxes = (cols + kBoxRows - 1) / kBoxRows;
                 for (int b = 0; b < nb; ++b, ++it) {
                     const int st = it % kStages;
-                    ok = warp_wait<64>(sm, sm.b_empty[st], ((it / kStages) & 1) ^ 1, args.err, 1u << 5);
+                    ok = warp_wait_alive<64>(sm, smem_u32(&sm.b_empty[st]), ((it / kStages) & 1) ^ 1, args.err, 1u << 5);
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&sm.b_full[st]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes) * 2 * kBoxRows * 128);
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 const int y = expert * p.n + ((item % nparts) * kCluster + rank) * kRowsPerTile;
                 for (int b = 0; b < nb; b += kGroup, ++it) {
                     const int slot = it % kCodeGroups;
-                    ok = warp_wait<64>(sm, sm.c_empty[slot], ((it / kCodeGroups) & 1) ^ 1, args.err, 1u << 10);
+                    ok = warp_wait_alive<64>(sm, smem_u32(&sm.c_empty[slot]), ((it / kCodeGroups) & 1) ^ 1, args.err, 1u << 10);
                     if (!ok) break;
                     if (lane == 0) {
                         const uint32_t bar = smem_u32(&sm.c_full[slot]), dst = smem_u32(sm.codes[slot]);
@@ -435,8 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             // activation scales of four blocks at a time, each lane six rows
             constexpr int kRows = kCols / 32;
             const int ld = (nb + 3) / 4 * 4;
-            bool ok = true;
-            for (int item = first_item; ok && find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
+            for (int item = first_item; find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
                 const float *src = args.scales + static_cast<int64_t>(row0) * ld;
                 for (int b = 0; b < nb; b += kGroup, ++it) {
                     const int slot = it % kGroups;
@@ -444,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
                     for (int i = 0; i < kRows; ++i)
                         v[i] = __ldg(reinterpret_cast<const float4 *>(src + min(lane + 32 * i, cols - 1) * ld + b));
-                    ok = warp_wait<64>(sm, sm.s_empty[slot], ((it / kGroups) & 1) ^ 1, args.err, 1u << 6);
-                    if (!ok) break;
+                    warp_wait<64>(sm, smem_u32(&sm.s_empty[slot]), ((it / kGroups) & 1) ^ 1, args.err, 1u << 6);
 #pragma unroll
                     for (int i = 0; i < kRows; ++i) {
                         const int c = lane + 32 * i;
@@ -478,39 +481,41 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             uint64_t acc[kFoldCols / 4][2];         // [column t + 4 n][h]
 #pragma unroll
             for (int n = 0; n < kFoldCols / 4; ++n) acc[n][0] = acc[n][1] = 0;
-            for (int b = 0; b < nb; ++b, ++it) {
-                const int buf = it & 1, slot = group % kGroups, in_group = b % kGroup;
-                if (in_group == 0 && !warp_wait(sm, sm.s_full[slot], (group / kGroups) & 1, args.err, 1u << 6)) goto done;
-                // weight scales of lane rows 16 h + i, 16 h + 8 + i
-                const ulonglong2 ws2 = *reinterpret_cast<const ulonglong2 *>(&sm.ws[slot][in_group][32 * quarter + 4 * i]);
-                if (!warp_wait(sm, sm.done[it % kDone], (it / kDone) & 1, args.err, 1u << 7)) goto done;
-                tc_fence_after();
-                const float2 *as = &sm.as[slot][in_group][part * kFoldCols + 4 * t];
-                const uint32_t dcol = lane_base + buf * kCols;
-                // all columns, whether the tile has them or not (what the others hold goes nowhere)
+            for (int b0 = 0; b0 < nb; b0 += kGroup, ++group) {
+                const int slot = group % kGroups;
+                const float2 *as = &sm.as[slot][0][part * kFoldCols + 4 * t];
+                const float *ws = &sm.ws[slot][0][32 * quarter + 4 * i];
+                warp_wait(sm, smem_u32(&sm.s_full[slot]), (group / kGroups) & 1, args.err, 1u << 6);
+                const int end = it + min(nb - b0, kGroup);
+#pragma unroll 1
+                for (; it < end; ++it, as += kCols, ws += 128) {
+                    const ulonglong2 ws2 = *reinterpret_cast<const ulonglong2 *>(ws);  // lane rows 16 h + i, 16 h + 8 + i
+                    const uint32_t dcol = lane_base + (it & 1) * kCols;
+                    warp_wait(sm, smem_u32(&sm.done[it % kDone]), (it / kDone) & 1, args.err, 1u << 7);
+                    tc_fence_after();
+                    // all columns, whether the tile has them or not (what the others hold goes nowhere)
 #pragma unroll
-                for (int c = 0; c < kFoldCols / 16; ++c) {
-                    uint32_t x[16];
-                    ld_chunk(dcol + 16 * c, x);
-                    const ulonglong2 s01 = *reinterpret_cast<const ulonglong2 *>(as + 16 * c),
-                                     s23 = *reinterpret_cast<const ulonglong2 *>(as + 16 * c + 2);
-                    wait_ld16(x);
+                    for (int c = 0; c < kFoldCols / 16; ++c) {
+                        uint32_t x[16];
+                        ld_chunk(dcol + 16 * c, x);
+                        const ulonglong2 s01 = *reinterpret_cast<const ulonglong2 *>(as + 16 * c),
+                                         s23 = *reinterpret_cast<const ulonglong2 *>(as + 16 * c + 2);
+                        wait_ld16(x);
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const uint64_t s = n == 0 ? s01.x : n == 1 ? s01.y : n == 2 ? s23.x : s23.y;
+                        for (int n = 0; n < 4; ++n) {
+                            const uint64_t s = n == 0 ? s01.x : n == 1 ? s01.y : n == 2 ? s23.x : s23.y;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            acc[4 * c + n][h] = fma2(pack2(__uint_as_float(x[8 * h + 2 * n]), __uint_as_float(x[8 * h + 2 * n + 1])),
-                                                     mul2(h == 0 ? ws2.x : ws2.y, s), acc[4 * c + n][h]);
+                            for (int h = 0; h < 2; ++h)
+                                acc[4 * c + n][h] =
+                                    fma2(pack2(__uint_as_float(x[8 * h + 2 * n]), __uint_as_float(x[8 * h + 2 * n + 1])),
+                                         mul2(h == 0 ? ws2.x : ws2.y, s), acc[4 * c + n][h]);
+                        }
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.d_empty[it & 1]));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sm.d_empty[buf]));
-                    if (in_group == kGroup - 1 || b + 1 == nb) mbar_arrive(smem_u32(&sm.s_empty[slot]));
-                }
-                if (in_group == kGroup - 1 || b + 1 == nb) ++group;
+                if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[slot]));
             }
             // outputs of lane rows 16 h + i, 16 h + 8 + i: gate and up of one, or two
             int out_r[2][2];
@@ -550,7 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
         }
     }
-done:
     __syncwarp();
     tc_fence_before();
     cluster_sync();                                 // the other CTA's copies and commits reach into this one
