@@ -6,19 +6,6 @@
 
 namespace tq {
 
-// Four int8 codes -> the e4m3 bytes of L * 2^-9 and of 16 H * 2^-9.
-__device__ __forceinline__ void split4(uint32_t w, uint32_t &hi, uint32_t &lo) {
-    const uint32_t sign = w & 0x80808080u;
-    const uint32_t mask = prmt(w, w, 0xba98u);                              // 0xff where negative
-    const uint32_t a = (w ^ mask) + (mask & 0x01010101u);                   // |q|, no carry between bytes
-    lo = (a & 0x0f0f0f0fu) | sign;
-    uint32_t sel = (a >> 4) & 0x07070707u;                                  // H per byte -> one nibble each
-    sel = (sel | (sel >> 4)) & 0x00ff00ffu;
-    sel = sel | (sel >> 8);
-    // 16 H * 2^-9 = H * 2^-5: e4m3 patterns of 0, 1, 2, 3 | 4, 5, 6, 7 times 2^-5
-    hi = prmt(0x1c181000u, 0x26242220u, sel) | sign;
-}
-
 // 32 consecutive codes (8 words) in the order in which the decoded weights meet
 // them (tq_dp4a.cuh, staged_pos).
 template <int FMT>
