@@ -5,10 +5,16 @@
 // Mathematics.  A block dot d = sum w*q over 128 weights in {-1, 0, +1} and int8
 // q is an exact integer below 2^14; fp16 operands hold both sides exactly and
 // the matrix instruction (m16n8k16, the weights as its 16 rows) adds in fp32.
-//   2-bit: codes 0, 1, 2 become 0, 1, 3 (one operation for 16 codes); the two bits of
-//   0, 1, 3, moved to the top of a half word, are the fp16 numbers 0, +2, -2:
-//   a shift and a mask make two weights.  The activations are q / 2.
-//   1-bit: the bit, moved to the sign, turns -1 into +1: a shift and a mask-and-xor.
+//   A weight's bits stay where they are in the word: masked out and joined with
+//   the exponent of 1.0 they are the mantissa of 1 + v * 2^(p - 10), p the lowest
+//   bit's place in its half word, one operation for two weights.  p is kept in
+//   4 .. 9 (the word itself, and it shifted by 6 right and by 4 left).  The
+//   activation there is q * s, s = 2^(10 - p) (1-bit: 2^(11 - p)), so the product is
+//   q * s + q * v (1-bit: + 2 q v), and the sums over q * s and over v's offset are
+//   known when the activations are laid out and added to the sum with a minus.
+//   2-bit: codes 0, 1, 2 become 0, 1, 3 (two operations for 16 codes); with their
+//   upper bit inverted, in the masking operation, v = w + 2.   1-bit: w = 2 v - 1.
+//   Everything is a whole number below 2^20.
 // Per 128-block and output the kernel then adds one fma(d, scale_w * scale_a,
 // acc), blocks in ascending order, the order that tq_moe.h documents.
 //
@@ -49,32 +55,96 @@ __device__ __forceinline__ Codes<FMT> load_codes(const uint8_t *p) {
     return c;
 }
 
-// Two weights as fp16: pair i (0..15) of a lane's 32.  2-bit: weights 7 - i and 15 - i
-// of the first word for i < 8, of the second for the others (each +-2 or 0, codes
-// already 0, 1, 3).  1-bit: weights 15 - i and 31 - i (+-1).
+// Where pair i (0..15) of a lane's 32 weights sits: the weight of its lower half
+// (the other is 8 or 16 further), and the place p of its lowest bit once shifted.
 template <int FMT>
-__device__ __forceinline__ uint32_t weight_pair(const Codes<FMT> &c, int i) {
-    if (FMT == 0) return (c.w[FMT == 0 ? i >> 3 : 0] << (2 * (i & 7))) & 0xc000c000u;
-    return ((c.w[0] << i) & 0x80008000u) ^ 0xbc00bc00u;
+__host__ __device__ constexpr int pair_weight(int i) {
+    return FMT == 0 ? 16 * (i >> 3) + ((i & 7) < 6 ? (i & 7) + 2 : (i & 7) - 6) : (i < 12 ? i + 4 : i - 12);
+}
+template <int FMT>
+__host__ __device__ constexpr int pair_place(int i) {
+    return FMT == 0 ? 4 + 2 * ((i & 7) % 3) : 4 + i % 6;
 }
 
-// Codes 0, 1, 2 -> 0, 1, 3.
+// A lane's weights of one row and block, ready for masking: each word as it is,
+// shifted right by 6 and left by 4.
+template <int FMT> struct Fields { uint32_t w[FMT == 0 ? 2 : 1][3]; };
+
 template <int FMT>
-__device__ __forceinline__ void signed_codes(Codes<FMT> &c) {
-    if (FMT == 0) {
-        c.w[0] |= (c.w[0] >> 1) & 0x55555555u;
-        c.w[FMT == 0 ? 1 : 0] |= (c.w[FMT == 0 ? 1 : 0] >> 1) & 0x55555555u;
+__device__ __forceinline__ Fields<FMT> fields(const Codes<FMT> &c) {
+    Fields<FMT> f;
+#pragma unroll
+    for (int i = 0; i < (FMT == 0 ? 2 : 1); ++i) {
+        const uint32_t w = FMT == 0 ? c.w[i] | ((c.w[i] >> 1) & 0x55555555u) : c.w[i];       // codes 0, 1, 2 -> 0, 1, 3
+        f.w[i][0] = w;
+        f.w[i][1] = w >> 6;
+        f.w[i][2] = w << 4;
     }
+    return f;
 }
 
-// Two int8 codes (bytes i and j of w ^ 0x80808080, so 0..255) as fp16: q / 2 or q.
+// What joins the masked bits: the exponent of 1.0, and for 2-bit codes the inversion of
+// the upper bit (one word for each place).  Kept in registers: lop3 takes one
+// immediate, and as two immediates the compiler makes two instructions of it.
+template <int FMT> struct Joins { uint32_t w[FMT == 0 ? 3 : 1]; };
+
 template <int FMT>
-__device__ __forceinline__ uint32_t act_pair(uint32_t a, uint32_t b, uint32_t sel) {
-    // 0x64nn is 1024 + n
-    const uint32_t u = prmt(prmt(a, b, sel), 0x64646464u, 0x4140u);
+__device__ __forceinline__ Joins<FMT> joins() {
+    Joins<FMT> j;
+#pragma unroll
+    for (int i = 0; i < (FMT == 0 ? 3 : 1); ++i)
+        asm volatile("mov.b32 %0, %1;" : "=r"(j.w[i]) : "n"(0x3c003c00u));
+    if (FMT == 0) {
+        j.w[0] |= 0x00020002u << 4;
+        j.w[FMT == 0 ? 1 : 0] |= 0x00020002u << 6;
+        j.w[FMT == 0 ? 2 : 0] |= 0x00020002u << 8;
+    }
+    return j;
+}
+
+// Pair i as two fp16 numbers.
+template <int FMT>
+__device__ __forceinline__ uint32_t weight_pair(const Fields<FMT> &f, const Joins<FMT> &join, int i) {
+    const int p = pair_place<FMT>(i);
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;"                         // (field & mask) ^ join
+        : "=r"(r)
+        : "r"(FMT == 0 ? f.w[FMT == 0 ? i >> 3 : 0][(i & 7) / 3] : f.w[0][i / 6]),
+          "r"((FMT == 0 ? 0x00030003u : 0x00010001u) << p), "r"(join.w[FMT == 0 ? (i & 7) % 3 : 0]));
+    return r;
+}
+
+// What the activation of pair i is multiplied with.
+template <int FMT>
+__host__ __device__ constexpr int pair_scale(int i) { return 1 << ((FMT == 0 ? 10 : 11) - pair_place<FMT>(i)); }
+
+// The same / 4 for four consecutive weights e .. e + 3, as bytes for dp4a.
+template <int FMT>
+__host__ __device__ constexpr uint32_t scale_bytes(int e) {
+    uint32_t r = 0;
+    for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 16; ++i) {
+            const int w = pair_weight<FMT>(i);
+            if (w == e + j || w + (FMT == 0 ? 8 : 16) == e + j)
+                r |= static_cast<uint32_t>(pair_scale<FMT>(i) / 4) << (8 * j);
+        }
+    return r;
+}
+
+// The first of a block's matrix instructions: nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Two int8 codes (plus 128, picked from the bytes of a and b) as fp16, times s.
+__device__ __forceinline__ uint32_t act_pair(uint32_t a, uint32_t b, uint32_t sel, int s) {
+    const uint32_t u = prmt(prmt(a, b, sel), 0x64646464u, 0x4140u);                          // 0x64nn is 1024 + n
     __half2 h = *reinterpret_cast<const __half2 *>(&u);
-    h = FMT == 0 ? __hfma2(h, __half2half2(__ushort_as_half(0x3800)), __half2half2(__ushort_as_half(0xe080)))   // * 0.5 - 576
-                 : __hadd2(h, __half2half2(__ushort_as_half(0xe480)));                                          // - 1152
+    h = __hmul2(__hadd2(h, __half2half2(__ushort_as_half(0xe480))), __half2half2(__int2half_rn(s)));   // - 1152
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
@@ -88,7 +158,7 @@ struct StreamArgs {
 //   offsets, chunks (of the experts before) int [experts + 1] each
 //   activations fp16 [chunk][block][quarter][t][8]: the 32 of lane t in the order of its
 //     weight pairs, 8 at a time; 64 bytes between rows
-//   scales [block][8]
+//   (scale, what the sum is short of d) [block][8]
 //   per warp the weight scales of 8 blocks, [2][32 rows][8] fp16
 __host__ __device__ constexpr int list_bytes(int experts) { return (2 * (experts + 1) * 4 + 15) / 16 * 16; }
 __host__ __device__ constexpr int row_pitch(int nb) { return nb * 256 + 64; }
@@ -96,7 +166,7 @@ constexpr int kScaleBytes = 2 * 32 * 8 * 2;
 
 size_t stream_smem(int experts, int chunk, int nb, int warps) {
     return static_cast<size_t>(list_bytes(experts)) + static_cast<size_t>(chunk) * row_pitch(nb) +
-           static_cast<size_t>(nb) * kCols * sizeof(float) + static_cast<size_t>(warps) * kScaleBytes;
+           static_cast<size_t>(nb) * kCols * sizeof(float2) + static_cast<size_t>(warps) * kScaleBytes;
 }
 
 // Fill offsets (clamped) and chunks (all threads); returns the number of chunks.
@@ -127,7 +197,7 @@ __device__ __forceinline__ int list_chunks(const MoeProduct &p, int chunk, int l
 
 // Lay the codes of `rows` activation rows out in shared memory (all threads).
 template <int FMT>
-__device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int rows, uint8_t *act, float *meta) {
+__device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int rows, uint8_t *act, float2 *meta) {
     const int tid = threadIdx.x, nb = p.k / kBlock, pitch = row_pitch(nb), per = nb * 4;
 #pragma unroll 2
     for (int i = tid; i < rows * per; i += blockDim.x) {
@@ -137,6 +207,18 @@ __device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int ro
         const uint4 *qp = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(a) * p.k + c * 32);
         const uint4 q0 = __ldg(qp), q1 = __ldg(qp + 1);
         const float sa = (c & 3) == 0 ? __ldg(p.s + static_cast<int64_t>(a) * nb + (c >> 2)) : 0.0f;
+        // minus the sums over q * s and over the offset of v
+        const uint32_t raw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        int sum = 0, scaled = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sum = __dp4a(static_cast<int>(raw[j]), 0x01010101, sum);
+            scaled = __dp4a(static_cast<int>(raw[j]), static_cast<int>(scale_bytes<FMT>(4 * j)), scaled);
+        }
+        int start = -(4 * scaled + (FMT == 0 ? 2 : 1) * sum);
+        const unsigned quad = 0xfu << (tid & 28);                    // a block's four lanes take this turn together
+        start += __shfl_xor_sync(quad, start, 1);
+        start += __shfl_xor_sync(quad, start, 2);
         const uint32_t flip = 0x80808080u;
         const uint32_t w[8] = {q0.x ^ flip, q0.y ^ flip, q0.z ^ flip, q0.w ^ flip,
                                q1.x ^ flip, q1.y ^ flip, q1.z ^ flip, q1.w ^ flip};
@@ -147,15 +229,15 @@ __device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int ro
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const int i = 4 * x + y;                             // the pair
-                const int e0 = FMT == 0 ? 16 * (i >> 3) + 7 - (i & 7) : 15 - i, e1 = e0 + (FMT == 0 ? 8 : 16);
-                o[y] = act_pair<FMT>(w[e0 >> 2], w[e1 >> 2], (e0 & 3) | ((4 + (e1 & 3)) << 4));
+                const int e0 = pair_weight<FMT>(i), e1 = e0 + (FMT == 0 ? 8 : 16);
+                o[y] = act_pair(w[e0 >> 2], w[e1 >> 2], (e0 & 3) | ((4 + (e1 & 3)) << 4), pair_scale<FMT>(i));
             }
             *reinterpret_cast<uint4 *>(dst + 64 * x) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if ((c & 3) == 0) meta[(c >> 2) * kCols + r] = sa;
+        if ((c & 3) == 0) meta[(c >> 2) * kCols + r] = make_float2(sa, static_cast<float>(start));
     }
     const int none = kCols - rows;
-    for (int i = tid; i < none * nb; i += blockDim.x) meta[(i / none) * kCols + rows + i % none] = 0.0f;
+    for (int i = tid; i < none * nb; i += blockDim.x) meta[(i / none) * kCols + rows + i % none] = make_float2(0.0f, 0.0f);
 }
 
 // The blocks whose codes are on their way while one is computed.
@@ -165,7 +247,7 @@ template <int FMT> constexpr int kAhead = FMT == 0 ? 4 : 8;
 // the staged activation rows, over all of k.
 template <int FMT, bool GATEUP>
 __device__ __forceinline__ void unit(const MoeProduct &p, int expert, int row0, int rows, int n0, bool wide,
-                                     const uint8_t *act, const float *meta, uint16_t *wsc) {
+                                     const uint8_t *act, const float2 *meta, uint16_t *wsc) {
     constexpr int kA = kAhead<FMT>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nb = p.k / kBlock;
@@ -206,12 +288,14 @@ __device__ __forceinline__ void unit(const MoeProduct &p, int expert, int row0, 
         return v;
     };
     uint4 snext = load_scales(0);
+    const Joins<FMT> join = joins<FMT>();
 
     float acc[2][4] = {};
-    const bool have = g < rows;
-    const uint8_t *ap = act + (have ? g : 0) * row_pitch(nb) + t * 16;
+    // a column without a row computes the last row's products again; they go nowhere
+    const uint8_t *ap = act + min(g, rows - 1) * row_pitch(nb) + t * 16;
+    const float2 *mp = meta + 2 * t;
 #pragma unroll 1
-    for (int b0 = 0; b0 < nb; b0 += 8) {
+    for (int b0 = 0; b0 < nb; b0 += 8, ap += 8 * 256, mp += 8 * kCols) {
         uint16_t *sbuf = wsc + ((b0 >> 3) & 1) * 256;
         *reinterpret_cast<uint4 *>(sbuf + (8 * t + g) * 8) = snext;
         if (b0 + 8 < nb) snext = load_scales(b0 + 8);
@@ -222,31 +306,28 @@ __device__ __forceinline__ void unit(const MoeProduct &p, int expert, int row0, 
             if (b >= nb) break;
             uint4 bq[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                bq[i] = have ? *reinterpret_cast<const uint4 *>(ap + b * 256 + 64 * i)
-                             : make_uint4(0, 0, 0, 0);
-            const float2 sa = *reinterpret_cast<const float2 *>(meta + b * kCols + 2 * t);   // of columns 2t, 2t + 1
-            float c[2][4] = {};
+            for (int i = 0; i < 4; ++i) bq[i] = *reinterpret_cast<const uint4 *>(ap + a * 256 + 64 * i);
+            // (scale, what is missing) of columns 2t, 2t + 1
+            const float4 sa = *reinterpret_cast<const float4 *>(mp + a * kCols);
+            float c[2][4];
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-                signed_codes<FMT>(ring[x][mt][0]);
-                signed_codes<FMT>(ring[x][mt][1]);
-            }
+                const Fields<FMT> f0 = fields<FMT>(ring[x][mt][0]), f1 = fields<FMT>(ring[x][mt][1]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 &v = bq[i >> 1];
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-                    mma_f16(c[mt], weight_pair<FMT>(ring[x][mt][0], 2 * i), weight_pair<FMT>(ring[x][mt][1], 2 * i),
-                            weight_pair<FMT>(ring[x][mt][0], 2 * i + 1), weight_pair<FMT>(ring[x][mt][1], 2 * i + 1),
-                            (i & 1) ? v.z : v.x, (i & 1) ? v.w : v.y);
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 &v = bq[i >> 1];
+                    const uint32_t a0 = weight_pair<FMT>(f0, join, 2 * i), a1 = weight_pair<FMT>(f1, join, 2 * i),
+                                   a2 = weight_pair<FMT>(f0, join, 2 * i + 1), a3 = weight_pair<FMT>(f1, join, 2 * i + 1);
+                    if (i == 0) mma_f16_first(c[mt], a0, a1, a2, a3, v.x, v.y);
+                    else mma_f16(c[mt], a0, a1, a2, a3, (i & 1) ? v.z : v.x, (i & 1) ? v.w : v.y);
+                }
             }
             if (b + kA < nb)
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        ring[x][mt][h] = load_codes<FMT>(src[mt][h] + static_cast<int64_t>(b + kA) * kBlockBytes);
+                        ring[x][mt][h] = load_codes<FMT>(src[mt][h] + (a + kA) * kBlockBytes);
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -254,9 +335,13 @@ __device__ __forceinline__ void unit(const MoeProduct &p, int expert, int row0, 
                     const float sw = f16_bits_to_f32(sbuf[(16 * mt + 8 * h + g) * 8 + a]);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        acc[mt][2 * h + j] = __fmaf_rn(c[mt][2 * h + j], __fmul_rn(sw, j == 0 ? sa.x : sa.y), acc[mt][2 * h + j]);
+                        acc[mt][2 * h + j] = __fmaf_rn(__fadd_rn(c[mt][2 * h + j], j == 0 ? sa.y : sa.w), __fmul_rn(sw, j == 0 ? sa.x : sa.z), acc[mt][2 * h + j]);
                 }
         }
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) src[mt][h] += 8 * kBlockBytes;
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -291,7 +376,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) stream_kernel(const __grid_
     const int nb = p.k / kBlock, warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
     int *offsets = reinterpret_cast<int *>(smem), *chunks = offsets + p.experts + 1;
     uint8_t *act = smem + list_bytes(p.experts);
-    float *meta = reinterpret_cast<float *>(act + args.chunk * row_pitch(nb));
+    float2 *meta = reinterpret_cast<float2 *>(act + args.chunk * row_pitch(nb));
     uint16_t *wsc = reinterpret_cast<uint16_t *>(meta + nb * kCols) + warp * (kScaleBytes / 2);
     constexpr int kUnitRows = GATEUP ? 16 : 32;
     const int units = (p.n + kUnitRows - 1) / kUnitRows, per_chunk = (units + warps - 1) / warps;
