@@ -243,6 +243,52 @@ __device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int ro
 // The blocks whose codes are on their way while one is computed.
 template <int FMT> constexpr int kAhead = FMT == 0 ? 4 : 8;
 
+// This lane's four weight rows of the unit from output n0 on: rows g and g + 8 of the
+// row tiles mt = 0, 1 (gate and up, or two of one matrix).
+template <int FMT, bool GATEUP>
+__device__ __forceinline__ void unit_rows(const MoeProduct &p, int expert, int n0, const uint8_t *(&src)[2][2]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr int kBlockBytes = FMT == 0 ? 32 : 16;
+    const int64_t row_bytes = static_cast<int64_t>(p.k / kBlock) * kBlockBytes;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = min(n0 + (GATEUP ? 0 : 16 * mt) + g + 8 * h, p.n - 1);
+            src[mt][h] = p.codes[GATEUP ? mt : 0] + (static_cast<int64_t>(expert) * p.n + r) * row_bytes + t * (kBlockBytes / 4);
+        }
+}
+
+template <int FMT>
+__device__ __forceinline__ void load_block(const uint8_t *const (&src)[2][2], int b, Codes<FMT> (&c)[2][2]) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) c[mt][h] = load_codes<FMT>(src[mt][h] + b * (FMT == 0 ? 32 : 16));
+}
+
+// c[mt][2 h + j]: the block's products of weight row 16 mt + 8 h + g and column 2 t + j,
+// short of d by what stage_rows put beside the scale.  ap: this lane's column and t.
+template <int FMT>
+__device__ __forceinline__ void block_products(const Codes<FMT> (&codes)[2][2], const uint8_t *ap, const Joins<FMT> &join,
+                                               float (&c)[2][4]) {
+    uint4 bq[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bq[i] = *reinterpret_cast<const uint4 *>(ap + 64 * i);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+        const Fields<FMT> f0 = fields<FMT>(codes[mt][0]), f1 = fields<FMT>(codes[mt][1]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 &v = bq[i >> 1];
+            const uint32_t a0 = weight_pair<FMT>(f0, join, 2 * i), a1 = weight_pair<FMT>(f1, join, 2 * i),
+                           a2 = weight_pair<FMT>(f0, join, 2 * i + 1), a3 = weight_pair<FMT>(f1, join, 2 * i + 1);
+            if (i == 0) mma_f16_first(c[mt], a0, a1, a2, a3, v.x, v.y);
+            else mma_f16(c[mt], a0, a1, a2, a3, (i & 1) ? v.z : v.x, (i & 1) ? v.w : v.y);
+        }
+    }
+}
+
 // A warp's unit: 32 weight rows (16 of gate and of up, or 32 of one matrix) against
 // the staged activation rows, over all of k.
 template <int FMT, bool GATEUP>
@@ -252,25 +298,12 @@ __device__ __forceinline__ void unit(const MoeProduct &p, int expert, int row0, 
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nb = p.k / kBlock;
     constexpr int kBlockBytes = FMT == 0 ? 32 : 16;
-    const int64_t row_bytes = static_cast<int64_t>(nb) * kBlockBytes;
-
-    // rows g and g + 8 of the row tiles mt = 0, 1 (gate and up, or two of one matrix)
     const uint8_t *src[2][2];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = min(n0 + (GATEUP ? 0 : 16 * mt) + g + 8 * h, p.n - 1);
-            src[mt][h] = p.codes[GATEUP ? mt : 0] + (static_cast<int64_t>(expert) * p.n + r) * row_bytes + t * (kBlockBytes / 4);
-        }
+    unit_rows<FMT, GATEUP>(p, expert, n0, src);
     Codes<FMT> ring[kA][2][2];
 #pragma unroll
     for (int a = 0; a < kA; ++a)
-        if (a < nb)
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) ring[a][mt][h] = load_codes<FMT>(src[mt][h] + a * kBlockBytes);
+        if (a < nb) load_block<FMT>(src, a, ring[a]);
 
     // weight scales: lane (g, t) brings row g of (mt, h) = (t / 2, t % 2), 8 blocks at a time
     const int sr = min(n0 + (GATEUP ? 0 : 16 * (t >> 1)) + g + 8 * (t & 1), p.n - 1);
@@ -304,30 +337,11 @@ __device__ __forceinline__ void unit(const MoeProduct &p, int expert, int row0, 
         for (int a = 0; a < 8; ++a) {
             const int b = b0 + a, x = a % kA;
             if (b >= nb) break;
-            uint4 bq[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) bq[i] = *reinterpret_cast<const uint4 *>(ap + a * 256 + 64 * i);
             // (scale, what is missing) of columns 2t, 2t + 1
             const float4 sa = *reinterpret_cast<const float4 *>(mp + a * kCols);
             float c[2][4];
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                const Fields<FMT> f0 = fields<FMT>(ring[x][mt][0]), f1 = fields<FMT>(ring[x][mt][1]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 &v = bq[i >> 1];
-                    const uint32_t a0 = weight_pair<FMT>(f0, join, 2 * i), a1 = weight_pair<FMT>(f1, join, 2 * i),
-                                   a2 = weight_pair<FMT>(f0, join, 2 * i + 1), a3 = weight_pair<FMT>(f1, join, 2 * i + 1);
-                    if (i == 0) mma_f16_first(c[mt], a0, a1, a2, a3, v.x, v.y);
-                    else mma_f16(c[mt], a0, a1, a2, a3, (i & 1) ? v.z : v.x, (i & 1) ? v.w : v.y);
-                }
-            }
-            if (b + kA < nb)
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        ring[x][mt][h] = load_codes<FMT>(src[mt][h] + (a + kA) * kBlockBytes);
+            block_products<FMT>(ring[x], ap + a * 256, join, c);
+            if (b + kA < nb) load_block<FMT>(src, a + kA, ring[x]);
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -407,6 +421,139 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) stream_kernel(const __grid_
     }
 }
 
+// ---------------------------------------------------------------------------
+// The same for few units in all (one or a few tokens): the four warps of a unit
+// take a quarter of the blocks each, so that a warp's chain of loads and matrix
+// instructions is a quarter as long; the exact block products meet in shared
+// memory, where one thread per output folds them in order.  The codes of the
+// next round are on their way while a round is folded.
+// ---------------------------------------------------------------------------
+// Up to this many units per SM: 3.4 (one token, top 8 of 64 experts, 2 x 1024 x 2048) take 7.8 us split and
+// 12.2 whole; 27 (33 tokens, 1-bit) 43.8 and 27.7; 34 (8 tokens, 5120 x 1536) 30.2 and 22.6.
+constexpr int kSplitMost = 8;
+constexpr int kSplit = 4, kSplitUnits = kMaxWarps / kSplit;
+constexpr int kDotPitch = 36;                       // 32 rows; columns 2t two apart fall on other banks
+constexpr int kSplitScalePitch = 32 * kSplitUnits + 2;
+
+// Behind the activations and their scales: [2] weight scales fp16 [block][row],
+// [2][unit] products [block][column][row]
+size_t split_smem(int experts, int chunk, int nb) {
+    return static_cast<size_t>(list_bytes(experts)) + static_cast<size_t>(chunk) * row_pitch(nb) +
+           static_cast<size_t>(nb) * kCols * sizeof(float2) + 2 * static_cast<size_t>(nb) * kSplitScalePitch * 2 +
+           2 * static_cast<size_t>(kSplitUnits) * nb * chunk * kDotPitch * 4;
+}
+
+template <int FMT, bool GATEUP>
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) split_kernel(const __grid_constant__ StreamArgs args) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const MoeProduct &p = args.p;
+    constexpr int kA = kAhead<FMT>, kUnitRows = GATEUP ? 16 : 32;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int nb = p.k / kBlock, slot = warp / kSplit;
+    const int per = (nb + kSplit - 1) / kSplit, lo = min((warp % kSplit) * per, nb), hi = min(lo + per, nb);
+    int *offsets = reinterpret_cast<int *>(smem), *chunks = offsets + p.experts + 1;
+    uint8_t *act = smem + list_bytes(p.experts);
+    float2 *meta = reinterpret_cast<float2 *>(act + args.chunk * row_pitch(nb));
+    float *dots = reinterpret_cast<float *>(meta + nb * kCols);
+    const int unit_dots = nb * args.chunk * kDotPitch;
+    uint16_t *wsc = reinterpret_cast<uint16_t *>(dots + 2 * kSplitUnits * unit_dots);
+    const int units = (p.n + kUnitRows - 1) / kUnitRows, per_chunk = (units + kSplitUnits - 1) / kSplitUnits;
+    const int64_t rounds = static_cast<int64_t>(list_chunks(p, args.chunk, args.limit, offsets, chunks)) * per_chunk;
+    const int64_t first = rounds * blockIdx.x / gridDim.x, end = rounds * (blockIdx.x + 1) / gridDim.x;
+    const Joins<FMT> join = joins<FMT>();
+
+    struct Place { int chunk, expert, row0, rows, n0; };            // n0: first output of the round
+    const auto locate = [&](int64_t r) {
+        Place q;
+        q.chunk = static_cast<int>(r / per_chunk);
+        q.n0 = static_cast<int>(r % per_chunk) * kSplitUnits * kUnitRows;
+        int a = 0, b = p.experts;
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (chunks[mid] <= q.chunk) a = mid;
+            else b = mid;
+        }
+        q.expert = a;
+        q.row0 = offsets[a] + (q.chunk - chunks[a]) * args.chunk;
+        q.rows = min(args.chunk, offsets[a + 1] - q.row0);
+        return q;
+    };
+    const uint8_t *src[2][2];
+    Codes<FMT> ring[kA][2][2];
+    const auto fetch = [&](const Place &q) {
+        unit_rows<FMT, GATEUP>(p, q.expert, q.n0 + slot * kUnitRows, src);
+#pragma unroll
+        for (int a = 0; a < kA; ++a)
+            if (lo + a < hi) load_block<FMT>(src, lo + a, ring[a]);
+    };
+
+    if (first >= end) return;
+    int staged = -1;
+    Place at = locate(first);
+    fetch(at);
+    for (int64_t r = first; r < end; ++r) {
+        const int buf = static_cast<int>(r - first) & 1;
+        for (int i = tid; i < 32 * kSplitUnits * nb; i += blockDim.x) {
+            const int lr = i / nb, b = i - lr * nb;
+            const int n = at.n0 + (lr >> 5) * kUnitRows + (GATEUP ? lr & 15 : lr & 31);
+            wsc[(buf * nb + b) * kSplitScalePitch + lr] =
+                ldg_u16(p.scales[GATEUP ? (lr >> 4) & 1 : 0] + (static_cast<int64_t>(at.expert) * p.n + min(n, p.n - 1)) * nb + b);
+        }
+        if (at.chunk != staged) {
+            if (staged >= 0) __syncthreads();                       // the fold before reads what is staged now
+            stage_rows<FMT>(p, at.row0, at.rows, act, meta);
+            __syncthreads();
+            staged = at.chunk;
+        }
+        float *mine = dots + (buf * kSplitUnits + slot) * unit_dots;
+        const uint8_t *ap = act + min(g, at.rows - 1) * row_pitch(nb) + t * 16 + lo * 256;
+#pragma unroll 1
+        for (int b0 = lo; b0 < hi; b0 += kA, ap += kA * 256)
+#pragma unroll
+            for (int a = 0; a < kA; ++a) {
+                const int b = b0 + a;
+                if (b >= hi) break;
+                float c[2][4];
+                block_products<FMT>(ring[a], ap + a * 256, join, c);
+                if (b + kA < hi) load_block<FMT>(src, b + kA, ring[a]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (2 * t + j < at.rows) {
+                        float *d = mine + (b * at.rows + 2 * t + j) * kDotPitch + g;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) d[8 * x] = c[x >> 1][2 * (x & 1) + j];
+                    }
+            }
+        const Place done = at;
+        if (r + 1 < end) {
+            at = locate(r + 1);
+            fetch(at);
+        }
+        __syncthreads();
+        for (int i = tid; i < kSplitUnits * kUnitRows * done.rows; i += blockDim.x) {
+            const int o = i % kUnitRows, rest = i / kUnitRows, col = rest % done.rows, s = rest / done.rows;
+            const int n = done.n0 + s * kUnitRows + o;
+            if (n >= p.n) continue;
+            const float *d = dots + (buf * kSplitUnits + s) * unit_dots + col * kDotPitch + o;
+            const uint16_t *w = wsc + buf * nb * kSplitScalePitch + 32 * s + o;
+            float acc[2] = {0.0f, 0.0f};
+#pragma unroll 4
+            for (int b = 0; b < nb; ++b) {
+                const float2 m = meta[b * kCols + col];
+#pragma unroll
+                for (int x = 0; x < (GATEUP ? 2 : 1); ++x)
+                    acc[x] = __fmaf_rn(__fadd_rn(d[b * done.rows * kDotPitch + 16 * x], m.y),
+                                       __fmul_rn(f16_bits_to_f32(w[b * kSplitScalePitch + 16 * x]), m.x), acc[x]);
+            }
+            const int64_t out = static_cast<int64_t>(done.row0 + col) * p.n + n;
+            if (GATEUP) p.h[out] = f32_to_bf16_bits(__fmul_rn(tq_silu(acc[0]), acc[1]));
+            else p.y[out] = acc[0];
+        }
+    }
+}
+
 template <int FMT, bool GATEUP>
 cudaError_t launch(const MoeProduct &p, int limit, cudaStream_t stream) {
     StreamArgs a{p, 0, limit};
@@ -417,13 +564,30 @@ cudaError_t launch(const MoeProduct &p, int limit, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     constexpr int64_t kUnitRows = GATEUP ? 16 : 32;
     const int64_t units = ws_cdiv(p.n, kUnitRows);
-    // fewer warps to a CTA where one chunk for each expert would not give every SM two CTAs
+    constexpr size_t kSmem = 227 * 1024;
+    // the chunks that an even routing of few slots gives, and with them the units
     const int64_t active = p.experts < p.slots ? p.experts : p.slots;
+    int chunk = p.max_rows < kCols ? p.max_rows : kCols;
+    // an upper bound of the chunks: one per expert and one more for every full one
+    const auto most_chunks = [&](int c) {
+        int64_t most = static_cast<int64_t>(p.experts) + p.slots / c;
+        if (most > p.slots) most = p.slots;
+        const int64_t cap = static_cast<int64_t>(p.experts) * ws_cdiv(limit, c);
+        return most > cap ? cap : most;
+    };
+    if (active * units <= kSplitMost * sms && split_smem(p.experts, chunk, nb) <= kSmem / 2 - 1024) {
+        const size_t smem = split_smem(p.experts, chunk, nb);
+        a.chunk = chunk;
+        e = cudaFuncSetAttribute(split_kernel<FMT, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        int64_t grid = most_chunks(chunk) * ws_cdiv(units, kSplitUnits);
+        if (grid > 2 * sms) grid = 2 * sms;
+        return launch_pdl(split_kernel<FMT, GATEUP>, dim3(static_cast<unsigned>(grid)), dim3(32 * kMaxWarps), smem, stream, a);
+    }
+    // fewer warps to a CTA where one chunk for each expert would not give every SM two CTAs
     int warps = kMaxWarps;
     while (warps > 2 && active * ws_cdiv(units, warps) < 2 * sms) warps /= 2;
     // as many rows at once as fit in shared memory (two CTAs on an SM), at most 8 and no more than an expert has
-    constexpr size_t kSmem = 227 * 1024;
-    int chunk = p.max_rows < kCols ? p.max_rows : kCols;
     while (chunk > 1 && stream_smem(p.experts, chunk, nb, warps) > kSmem) --chunk;
     const size_t smem = stream_smem(p.experts, chunk, nb, warps);
     if (smem > kSmem) return cudaErrorInvalidValue;
@@ -433,12 +597,7 @@ cudaError_t launch(const MoeProduct &p, int limit, cudaStream_t stream) {
     int per_sm = static_cast<int>((kSmem + 1024) / (smem + 1024));
     if (per_sm > 16 / warps) per_sm = 16 / warps;
     if (per_sm < 1) per_sm = 1;
-    // an upper bound of the chunks: one per expert and one more for every full one
-    int64_t most = static_cast<int64_t>(p.experts) + p.slots / chunk;
-    if (most > p.slots) most = p.slots;
-    const int64_t cap = static_cast<int64_t>(p.experts) * ws_cdiv(limit, chunk);
-    if (most > cap) most = cap;
-    int64_t grid = most * ws_cdiv(units, warps);
+    int64_t grid = most_chunks(chunk) * ws_cdiv(units, warps);
     if (grid > static_cast<int64_t>(sms) * per_sm) grid = static_cast<int64_t>(sms) * per_sm;
     return launch_pdl(stream_kernel<FMT, GATEUP>, dim3(static_cast<unsigned>(grid)), dim3(32 * warps), smem, stream, a);
 }

@@ -87,6 +87,8 @@ class _Lifecycle(ctypes.Structure):
 def load():
     """Load libtq.so (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -164,10 +166,18 @@ def _check(fn: str, status: int) -> None:
         raise TQError(fn, status, load().tq_last_cuda_error())
 
 
+_raw_stream = None
+
+
 def _stream(stream):
     import torch
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        global _raw_stream
+        if _raw_stream is None:
+            # the stream object costs 3 us a call, the raw handle 0.1 us
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -381,7 +391,7 @@ def rmsnorm_bf16(y, eps: float = 1e-6, x_out=None, stream=None):
 # mixture-of-experts layer (include/tq_moe.h)
 # ---------------------------------------------------------------------------
 
-@dataclass
+@dataclass(frozen=True)
 class PackedExperts:
     """The packed weights of all experts on the device: codes
     [experts][n][k/4] (2-bit) or [experts][n][k/8] (1-bit) uint8, scales
@@ -396,11 +406,13 @@ class PackedExperts:
     def __post_init__(self):
         import torch
         per = 4 if self.fmt == FMT_TERNARY2 else 8
-        _tensor("codes", self.codes, torch.uint8, (self.experts, self.n, self.k // per))
-        _tensor("scales", self.scales, torch.float16, (self.experts, self.n, self.k // BLOCK))
+        _tensor("codes", self.codes, (torch.uint8,), (self.experts, self.n, self.k // per))
+        _tensor("scales", self.scales, (torch.float16,), (self.experts, self.n, self.k // BLOCK))
+        object.__setattr__(self, "_c", _Experts(self.codes.data_ptr(), self.scales.data_ptr(), self.experts, self.n,
+                                                self.k, self.fmt))
 
     def c_struct(self) -> _Experts:
-        return _Experts(self.codes.data_ptr(), self.scales.data_ptr(), self.experts, self.n, self.k, self.fmt)
+        return self._c
 
     @property
     def nbytes(self) -> int:
@@ -420,33 +432,26 @@ class MoePlan:
         return self.rows.numel()
 
 
-def _tensor(name: str, t, dtype, shape=None):
+def _tensor(name: str, t, dtypes, shape=None):
     """Check a tensor argument of a mixture-of-experts call: the kernels read raw
-    contiguous device memory of one type."""
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    if not t.is_cuda or t.dtype not in dtypes or not t.is_contiguous():
+    contiguous device memory of one type.  Returns its address."""
+    if not (t.is_cuda and t.dtype in dtypes and t.is_contiguous()):
         raise ValueError(f"{name}: a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} is "
                          f"needed, got {t.dtype} on {t.device}, strides {tuple(t.stride())}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
-    return t
-
-
-def _dtype_code(t) -> int:
-    import torch
-    return 1 if t.dtype == torch.bfloat16 else 0
+    return t.data_ptr()
 
 
 def pack_experts(codes, fmt: int, scales, stream=None) -> PackedExperts:
     """codes: uint8 CUDA tensor [experts][n][k] (as pack_weights); scales: float16
     CUDA tensor [experts][n][k/128]."""
     import torch
-    _tensor("codes", codes, torch.uint8)
+    ptr = _tensor("codes", codes, (torch.uint8,))
     experts, n, k = codes.shape
     packed = torch.empty((experts, n, k // (4 if fmt == FMT_TERNARY2 else 8)), dtype=torch.uint8,
                          device=codes.device)
-    _check("tq_pack_weights", load().tq_pack_weights(_ptr(codes), experts * n, k, fmt, _ptr(packed),
-                                                      _stream(stream)))
+    _check("tq_pack_weights", load().tq_pack_weights(ptr, experts * n, k, fmt, packed.data_ptr(), _stream(stream)))
     return PackedExperts(packed, scales.contiguous(), experts, n, k, fmt)
 
 
@@ -457,27 +462,31 @@ def add_rmsnorm_rotq(residual, delta=None, gamma=None, eps: float = 1e-6, residu
     and quantised.  residual_out may be residual itself; a bf16 x_out also
     receives the norm before the rotation."""
     import torch
-    floats = (torch.float32, torch.bfloat16)
-    _tensor("residual", residual, floats)
-    m, n = residual.shape
-    if delta is not None:
-        _tensor("delta", delta, floats, (m, n))
-    if gamma is not None:
-        _tensor("gamma", gamma, torch.bfloat16, (n,))
-    if x_out is not None:
-        _tensor("x_out", x_out, torch.bfloat16, (m, n))
+    f32, bf16 = torch.float32, torch.bfloat16
+    p_res = _tensor("residual", residual, (f32, bf16))
+    shape = residual.shape
+    m, n = shape
+    p_delta = 0 if delta is None else _tensor("delta", delta, (f32, bf16), shape)
+    p_gamma = 0 if gamma is None else _tensor("gamma", gamma, (bf16,), (n,))
+    p_x = 0 if x_out is None else _tensor("x_out", x_out, (bf16,), shape)
     if residual_out is None:
         residual_out = torch.empty_like(residual)
+        p_out = residual_out.data_ptr()
+    else:
+        p_out = _tensor("residual_out", residual_out, (residual.dtype,), shape)
     if q is None:
-        q = torch.empty((m, n), dtype=torch.int8, device=residual.device)
+        q = torch.empty(shape, dtype=torch.int8, device=residual.device)
+        p_q = q.data_ptr()
+    else:
+        p_q = _tensor("q", q, (torch.int8,), shape)
     if s is None:
-        s = torch.empty((m, n // BLOCK), dtype=torch.float32, device=residual.device)
-    _tensor("residual_out", residual_out, residual.dtype, (m, n))
-    _tensor("q", q, torch.int8, (m, n))
-    _tensor("s", s, torch.float32, (m, n // BLOCK))
+        s = torch.empty((m, n // BLOCK), dtype=f32, device=residual.device)
+        p_s = s.data_ptr()
+    else:
+        p_s = _tensor("s", s, (f32,), (m, n // BLOCK))
     _check("tq_add_rmsnorm_rotq", load().tq_add_rmsnorm_rotq(
-        _ptr(residual), _dtype_code(residual), _ptr(delta), 0 if delta is None else _dtype_code(delta),
-        _ptr(gamma), m, n, eps, _ptr(residual_out), _ptr(x_out), _ptr(q), _ptr(s), _stream(stream)))
+        p_res, int(residual.dtype == bf16), p_delta, int(delta is not None and delta.dtype == bf16), p_gamma, m, n,
+        eps, p_out, p_x, p_q, p_s, _stream(stream)))
     return residual_out, q, s
 
 
@@ -485,16 +494,20 @@ def moe_route(logits, topk: int, renormalize: bool = True, ids=None, weights=Non
     """logits float32 or bf16 [m][experts] -> (ids int32 [m][topk], weights
     float32 [m][topk]); -1 and 0 where a token has no expert left."""
     import torch
-    _tensor("logits", logits, (torch.float32, torch.bfloat16))
+    p_logits = _tensor("logits", logits, (torch.float32, torch.bfloat16))
     m, experts = logits.shape
     if ids is None:
         ids = torch.empty((m, topk), dtype=torch.int32, device=logits.device)
+        p_ids = ids.data_ptr()
+    else:
+        p_ids = _tensor("ids", ids, (torch.int32,), (m, topk))
     if weights is None:
         weights = torch.empty((m, topk), dtype=torch.float32, device=logits.device)
-    _tensor("ids", ids, torch.int32, (m, topk))
-    _tensor("weights", weights, torch.float32, (m, topk))
-    _check("tq_moe_route", load().tq_moe_route(_ptr(logits), _dtype_code(logits), m, experts, topk,
-                                               int(renormalize), _ptr(ids), _ptr(weights), _stream(stream)))
+        p_weights = weights.data_ptr()
+    else:
+        p_weights = _tensor("weights", weights, (torch.float32,), (m, topk))
+    _check("tq_moe_route", load().tq_moe_route(p_logits, int(logits.dtype == torch.bfloat16), m, experts, topk,
+                                               int(renormalize), p_ids, p_weights, _stream(stream)))
     return ids, weights
 
 
@@ -513,43 +526,42 @@ def moe_workspace(m: int, topk: int, experts: int, hidden: int = 0, inter: int =
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
-def _moe_product_workspace(workspace, q, slots):
-    import torch
-    if workspace is None:
-        return torch.zeros(256 + slots * (2 * q.shape[1] + 16 * -(-q.shape[1] // 512)), dtype=torch.uint8, device=q.device)
-    return _tensor("workspace", workspace, torch.uint8)
-
-
 def moe_plan(ids, experts: int, plan: MoePlan = None, workspace=None, stream=None) -> MoePlan:
     """ids int32 [m][topk] -> MoePlan; an id outside 0 .. experts-1 leaves its slot out."""
     import torch
-    _tensor("ids", ids, torch.int32)
+    p_ids = _tensor("ids", ids, (torch.int32,))
     m, topk = ids.shape
     if plan is None:
-        plan = MoePlan(*(torch.empty(n, dtype=torch.int32, device=ids.device)
-                         for n in (experts + 1, m * topk, (m, topk))))
-    _tensor("offsets", plan.offsets, torch.int32, (experts + 1,))
-    for name, t in (("rows", plan.rows), ("pos", plan.pos)):
-        if _tensor(name, t, torch.int32).numel() != m * topk:
-            raise ValueError(f"{name}: {m * topk} entries are needed, got {t.numel()}")
+        plan = MoePlan(torch.empty(experts + 1, dtype=torch.int32, device=ids.device),
+                       torch.empty(m * topk, dtype=torch.int32, device=ids.device), torch.empty_like(ids))
+    p_offsets = _tensor("offsets", plan.offsets, (torch.int32,), (experts + 1,))
+    p_rows, p_pos = (_tensor(name, t, (torch.int32,)) for name, t in (("rows", plan.rows), ("pos", plan.pos)))
+    if plan.rows.numel() != m * topk or plan.pos.numel() != m * topk:
+        raise ValueError(f"rows, pos: {m * topk} entries are needed, got {plan.rows.numel()}, {plan.pos.numel()}")
     if workspace is None:
         workspace = moe_workspace(m, topk, experts, device=ids.device)
-    _check("tq_moe_plan", load().tq_moe_plan(_ptr(ids), m, topk, experts, _ptr(plan.offsets), _ptr(plan.rows),
-                                             _ptr(plan.pos), _ptr(workspace), workspace.numel(),
-                                             _stream(stream)))
+    _check("tq_moe_plan", load().tq_moe_plan(p_ids, m, topk, experts, p_offsets, p_rows, p_pos,
+                                             workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return plan
 
 
-def _moe_inputs(w: PackedExperts, q, s, plan: MoePlan):
+def _moe_inputs(w: PackedExperts, q, s, plan: MoePlan, gather: bool, workspace):
+    """The checked inputs of a grouped product: addresses of q, s, rows and offsets, rows of q,
+    slots, and a workspace."""
     import torch
-    _tensor("q", q, torch.int8)
+    p_q = _tensor("q", q, (torch.int8,))
     m, k = q.shape
     if k != w.k:
         raise ValueError(f"q: rows of {w.k} codes are needed, got {k}")
-    _tensor("s", s, torch.float32, (m, k // BLOCK))
-    _tensor("offsets", plan.offsets, torch.int32, (w.experts + 1,))
-    _tensor("rows", plan.rows, torch.int32)
-    return m
+    p_s = _tensor("s", s, (torch.float32,), (m, k // BLOCK))
+    p_offsets = _tensor("offsets", plan.offsets, (torch.int32,), (w.experts + 1,))
+    p_rows = _tensor("rows", plan.rows, (torch.int32,))
+    slots = plan.rows.numel()
+    if workspace is None:
+        workspace = torch.zeros(256 + slots * (2 * k + 16 * -(-k // 512)), dtype=torch.uint8, device=q.device)
+    elif workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace: uint8 is needed, got {workspace.dtype}")
+    return p_q, p_s, p_rows if gather else 0, p_offsets, m, slots, workspace
 
 
 def moe_gemv(w: PackedExperts, q, s, plan: MoePlan, gather: bool = False, y=None, workspace=None,
@@ -557,15 +569,15 @@ def moe_gemv(w: PackedExperts, q, s, plan: MoePlan, gather: bool = False, y=None
     """y float32 [slots][n], one row per sorted slot.  q int8, s float32: one row
     per sorted slot, or with ``gather`` one per token, picked by plan.rows."""
     import torch
-    m = _moe_inputs(w, q, s, plan)
+    p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(w, q, s, plan, gather, workspace)
     if y is None:
-        y = torch.empty((plan.slots, w.n), dtype=torch.float32, device=q.device)
-    _tensor("y", y, torch.float32, (plan.slots, w.n))
-    workspace = _moe_product_workspace(workspace, q, plan.slots)
-    ws = w.c_struct()
+        y = torch.empty((slots, w.n), dtype=torch.float32, device=q.device)
+        p_y = y.data_ptr()
+    else:
+        p_y = _tensor("y", y, (torch.float32,), (slots, w.n))
     _check("tq_moe_gemv", load().tq_moe_gemv(
-        ctypes.byref(ws), _ptr(q), _ptr(s), m, _ptr(plan.rows if gather else None), _ptr(plan.offsets),
-        plan.slots, _ptr(y), _ptr(workspace), workspace.numel(), _stream(stream)))
+        w.c_struct(), p_q, p_s, m, p_rows, p_offsets, slots, p_y, workspace.data_ptr(), workspace.numel(),
+        _stream(stream)))
     return y
 
 
@@ -575,15 +587,15 @@ def moe_gateup(gate: PackedExperts, up: PackedExperts, q, s, plan: MoePlan, gath
     float32: one row per token, picked by plan.rows (``gather``), or one per
     sorted slot."""
     import torch
-    m = _moe_inputs(gate, q, s, plan)
+    p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(gate, q, s, plan, gather, workspace)
     if h is None:
-        h = torch.empty((plan.slots, gate.n), dtype=torch.bfloat16, device=q.device)
-    _tensor("h", h, torch.bfloat16, (plan.slots, gate.n))
-    workspace = _moe_product_workspace(workspace, q, plan.slots)
-    g, u = gate.c_struct(), up.c_struct()
+        h = torch.empty((slots, gate.n), dtype=torch.bfloat16, device=q.device)
+        p_h = h.data_ptr()
+    else:
+        p_h = _tensor("h", h, (torch.bfloat16,), (slots, gate.n))
     _check("tq_moe_gateup", load().tq_moe_gateup(
-        ctypes.byref(g), ctypes.byref(u), _ptr(q), _ptr(s), m, _ptr(plan.rows if gather else None),
-        _ptr(plan.offsets), plan.slots, _ptr(h), _ptr(workspace), workspace.numel(), _stream(stream)))
+        gate.c_struct(), up.c_struct(), p_q, p_s, m, p_rows, p_offsets, slots, p_h, workspace.data_ptr(),
+        workspace.numel(), _stream(stream)))
     return h
 
 
@@ -591,16 +603,17 @@ def moe_combine(y, plan: MoePlan, weights, out=None, dtype=None, stream=None):
     """y float32 [slots][n], weights float32 [m][topk] -> the weighted sum over each
     token's experts [m][n] (float32 unless dtype or out says bf16)."""
     import torch
-    _tensor("y", y, torch.float32)
-    _tensor("weights", weights, torch.float32)
+    p_y = _tensor("y", y, (torch.float32,))
+    p_weights = _tensor("weights", weights, (torch.float32,))
     m, topk = weights.shape
-    if _tensor("pos", plan.pos, torch.int32).numel() != m * topk:
+    p_pos = _tensor("pos", plan.pos, (torch.int32,))
+    if plan.pos.numel() != m * topk:
         raise ValueError(f"pos: {m * topk} entries are needed, got {plan.pos.numel()}")
     if out is None:
         out = torch.empty((m, y.shape[1]), dtype=dtype or torch.float32, device=y.device)
-    _tensor("out", out, (torch.float32, torch.bfloat16), (m, y.shape[1]))
+    p_out = _tensor("out", out, (torch.float32, torch.bfloat16), (m, y.shape[1]))
     _check("tq_moe_combine", load().tq_moe_combine(
-        _ptr(y), _ptr(plan.pos), _ptr(weights), m, topk, y.shape[0], y.shape[1], _ptr(out), _dtype_code(out),
+        p_y, p_pos, p_weights, m, topk, y.shape[0], y.shape[1], p_out, int(out.dtype == torch.bfloat16),
         _stream(stream)))
     return out
 
@@ -611,24 +624,22 @@ def moe_ffn(gate: PackedExperts, up: PackedExperts, down: PackedExperts, q, s, i
     [m][hidden/128], ids int32 and weights float32 [m][topk] -> [m][hidden]
     (float32 unless dtype or out says bf16)."""
     import torch
-    _tensor("q", q, torch.int8)
+    p_q = _tensor("q", q, (torch.int8,))
     m, hidden = q.shape
-    _tensor("s", s, torch.float32, (m, hidden // BLOCK))
-    _tensor("ids", ids, torch.int32)
-    topk = ids.shape[1]
-    _tensor("ids", ids, torch.int32, (m, topk))
-    _tensor("weights", weights, torch.float32, (m, topk))
+    p_s = _tensor("s", s, (torch.float32,), (m, hidden // BLOCK))
+    topk = ids.shape[-1]
+    p_ids = _tensor("ids", ids, (torch.int32,), (m, topk))
+    p_weights = _tensor("weights", weights, (torch.float32,), (m, topk))
     if hidden != gate.k:
         raise ValueError(f"q: rows of {gate.k} codes are needed, got {hidden}")
     if out is None:
         out = torch.empty((m, hidden), dtype=dtype or torch.float32, device=q.device)
-    _tensor("out", out, (torch.float32, torch.bfloat16), (m, hidden))
+    p_out = _tensor("out", out, (torch.float32, torch.bfloat16), (m, hidden))
     if workspace is None:
         workspace = moe_workspace(m, topk, gate.experts, hidden, gate.n, q.device)
-    g, u, d = gate.c_struct(), up.c_struct(), down.c_struct()
     _check("tq_moe_ffn", load().tq_moe_ffn(
-        ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), _ptr(q), _ptr(s), _ptr(ids), _ptr(weights), m, topk,
-        _ptr(out), _dtype_code(out), _ptr(workspace), workspace.numel(), _stream(stream)))
+        gate.c_struct(), up.c_struct(), down.c_struct(), p_q, p_s, p_ids, p_weights, m, topk, p_out,
+        int(out.dtype == torch.bfloat16), workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return out
 
 
