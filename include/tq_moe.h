@@ -61,8 +61,8 @@ typedef struct {
  *   x[i]   = bf16_rn(t[i] * inv), or bf16_rn((t[i] * inv) * gamma[i])
  *   q, s   = tq_rotate_quant(x)
  * and residual_out = t, x_out = x.  The sum of squares is held as an unevaluated
- * pair of fp32 numbers and inv is computed in 64 bits, so inv is the correctly
- * rounded value but for about one row in 10^7 (then its neighbour), whatever the
+ * pair of fp32 numbers and so is the mean, so inv is the correctly rounded
+ * value but for about one row in 10^5 (then its neighbour), whatever the
  * order of the sum: a code that an ulp of inv would move across a rounding
  * border does not depend on how rows are split over threads.  A row's results do
  * not depend on m.  A NaN in x gives its block a NaN scale and zero codes.

@@ -222,7 +222,8 @@ tq_status tq_moe_ffn(const tq_experts *gate, const tq_experts *up, const tq_expe
     a.h = h;
     a.max_rows = m;
     if ((st = run_product(a, workspace, str)) != TQ_OK) return st;
-    if ((st = tq_rotate_quant(h, slots, inter, hq, hs, stream)) != TQ_OK) return st;
+    if ((e = tq::moe_rotq_launch(h, static_cast<int64_t>(slots) * (inter / 128), hq, hs, str)) != cudaSuccess)
+        return cuda_status(e);
     tq::MoeProduct b = product(down, nullptr, hq, hs, slots, nullptr, offsets, slots);
     b.y = y;
     b.max_rows = m;

@@ -69,6 +69,8 @@ cudaError_t moe_tile_launch(const MoeProduct &p, int above, uint8_t *operand, un
 cudaError_t moe_norm_launch(const void *res, bool res_bf16, const void *delta, bool delta_bf16, const uint16_t *gamma,
                             int m, int n, float eps, void *res_out, uint16_t *x_out, int8_t *q, float *s,
                             cudaStream_t stream);
+// tq_rotate_quant of `blocks` 128-blocks behind one another (16-byte aligned).
+cudaError_t moe_rotq_launch(const uint16_t *x, int64_t blocks, int8_t *q, float *s, cudaStream_t stream);
 cudaError_t moe_combine_launch(const float *y, const int *pos, const float *weights, int m, int topk, int slots, int n,
                                void *out, bool out_bf16, cudaStream_t stream);
 cudaError_t moe_route_launch(const void *logits, bool bf16, int m, int experts, int topk, bool renorm, int *ids,
