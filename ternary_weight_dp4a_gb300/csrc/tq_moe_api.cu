@@ -87,9 +87,9 @@ tq_status run_product(const tq::MoeProduct &p, void *workspace, cudaStream_t str
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     cudaError_t e = cudaSuccess;
     const bool tiles = p.max_rows > kTileAbove;
-    if (tiles)
-        e = tq::moe_tile_launch(p, kTileAbove, ws + L.operand, reinterpret_cast<unsigned *>(ws + L.err), stream);
-    if (e == cudaSuccess) e = tq::moe_stream_launch(p, tiles ? kTileAbove : p.slots, stream);
+    unsigned *err = reinterpret_cast<unsigned *>(ws + L.err);
+    if (tiles) e = tq::moe_tile_launch(p, kTileAbove, ws + L.operand, err, stream);
+    if (e == cudaSuccess) e = tq::moe_stream_launch(p, tiles ? kTileAbove : p.slots, err, stream);
     return cuda_status(e);
 }
 

@@ -63,7 +63,7 @@ struct MoeProduct {
 
 // The experts with at most `limit` rows, and those with more than `above`
 // (operand: moe_operand_bytes of workspace for the laid-out input).
-cudaError_t moe_stream_launch(const MoeProduct &p, int limit, cudaStream_t stream);
+cudaError_t moe_stream_launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t stream);
 cudaError_t moe_tile_launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *err, cudaStream_t stream);
 
 cudaError_t moe_norm_launch(const void *res, bool res_bf16, const void *delta, bool delta_bf16, const uint16_t *gamma,

@@ -26,13 +26,15 @@
 #include "tq_device.cuh"
 #include "tq_launch.h"
 #include "tq_moe_internal.h"
+#include "tq_tmap.h"
 
 namespace tq {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kCols = 8;                     // activation rows per chunk
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 16;
+constexpr int kSplitWarps = 8;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -152,21 +154,30 @@ struct StreamArgs {
     MoeProduct p;
     int chunk;      // rows of an expert that share a pass over its weights, at most kCols
     int limit;      // experts with more rows are another kernel's
+    unsigned *err;
+    CUtensorMap codes[2];   // packed weights, [experts * n][row bytes], boxes of 16 rows x 4 blocks
 };
 
-// Shared memory of a CTA, behind one another:
+// Shared memory of a CTA, behind one another (the rings only in the stream kernel):
+//   per warp a ring of stages of four blocks: packed weights [32 rows][4 blocks], swizzled, and
+//     behind all rings the stages' weight scales [32 rows][4] fp16 and barriers
 //   offsets, chunks (of the experts before) int [experts + 1] each
 //   activations fp16 [chunk][block][quarter][t][8]: the 32 of lane t in the order of its
 //     weight pairs, 8 at a time; 64 bytes between rows
 //   (scale, what the sum is short of d) [block][8]
-//   per warp the weight scales of 8 blocks, [2][32 rows][8] fp16
 __host__ __device__ constexpr int list_bytes(int experts) { return (2 * (experts + 1) * 4 + 15) / 16 * 16; }
 __host__ __device__ constexpr int row_pitch(int nb) { return nb * 256 + 64; }
-constexpr int kScaleBytes = 2 * 32 * 8 * 2;
+constexpr int kStageBlocks = 4;
+// stages per warp: 16 warps have 128 KB (1-bit: 96 KB) on their way on an SM
+template <int FMT> constexpr int kDepth = FMT == 0 ? 2 : 3;
+template <int FMT> constexpr int kStageBytes = 32 * kStageBlocks * (FMT == 0 ? 32 : 16);
+template <int FMT> constexpr int kSideBytes = 32 * 8 + 16;           // a stage's scales, and its barrier
 
+template <int FMT>
 size_t stream_smem(int experts, int chunk, int nb, int warps) {
-    return static_cast<size_t>(list_bytes(experts)) + static_cast<size_t>(chunk) * row_pitch(nb) +
-           static_cast<size_t>(nb) * kCols * sizeof(float2) + static_cast<size_t>(warps) * kScaleBytes;
+    return 1024 + static_cast<size_t>(warps) * kDepth<FMT> * (kStageBytes<FMT> + kSideBytes<FMT>) +
+           static_cast<size_t>(list_bytes(experts)) + static_cast<size_t>(chunk) * row_pitch(nb) +
+           static_cast<size_t>(nb) * kCols * sizeof(float2);
 }
 
 // Fill offsets (clamped) and chunks (all threads); returns the number of chunks.
@@ -289,136 +300,194 @@ __device__ __forceinline__ void block_products(const Codes<FMT> (&codes)[2][2], 
     }
 }
 
-// A warp's unit: 32 weight rows (16 of gate and of up, or 32 of one matrix) against
-// the staged activation rows, over all of k.
-template <int FMT, bool GATEUP>
-__device__ __forceinline__ void unit(const MoeProduct &p, int expert, int row0, int rows, int n0, bool wide,
-                                     const uint8_t *act, const float2 *meta, uint16_t *wsc) {
-    constexpr int kA = kAhead<FMT>;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int nb = p.k / kBlock;
-    constexpr int kBlockBytes = FMT == 0 ? 32 : 16;
-    const uint8_t *src[2][2];
-    unit_rows<FMT, GATEUP>(p, expert, n0, src);
-    Codes<FMT> ring[kA][2][2];
-#pragma unroll
-    for (int a = 0; a < kA; ++a)
-        if (a < nb) load_block<FMT>(src, a, ring[a]);
-
-    // weight scales: lane (g, t) brings row g of (mt, h) = (t / 2, t % 2), 8 blocks at a time
-    const int sr = min(n0 + (GATEUP ? 0 : 16 * (t >> 1)) + g + 8 * (t & 1), p.n - 1);
-    const uint16_t *ssrc = p.scales[GATEUP ? t >> 1 : 0] + (static_cast<int64_t>(expert) * p.n + sr) * nb;
-    const auto load_scales = [&](int b) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (wide) {
-            v = __ldg(reinterpret_cast<const uint4 *>(ssrc + b));
-        } else {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = ldg_u16(ssrc + min(b + i, nb - 1));
-            v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-        }
-        return v;
-    };
-    uint4 snext = load_scales(0);
-    const Joins<FMT> join = joins<FMT>();
-
-    float acc[2][4] = {};
-    // a column without a row computes the last row's products again; they go nowhere
-    const uint8_t *ap = act + min(g, rows - 1) * row_pitch(nb) + t * 16;
-    const float2 *mp = meta + 2 * t;
-#pragma unroll 1
-    for (int b0 = 0; b0 < nb; b0 += 8, ap += 8 * 256, mp += 8 * kCols) {
-        uint16_t *sbuf = wsc + ((b0 >> 3) & 1) * 256;
-        *reinterpret_cast<uint4 *>(sbuf + (8 * t + g) * 8) = snext;
-        if (b0 + 8 < nb) snext = load_scales(b0 + 8);
-        __syncwarp();
-#pragma unroll
-        for (int a = 0; a < 8; ++a) {
-            const int b = b0 + a, x = a % kA;
-            if (b >= nb) break;
-            // (scale, what is missing) of columns 2t, 2t + 1
-            const float4 sa = *reinterpret_cast<const float4 *>(mp + a * kCols);
-            float c[2][4];
-            block_products<FMT>(ring[x], ap + a * 256, join, c);
-            if (b + kA < nb) load_block<FMT>(src, a + kA, ring[x]);
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float sw = f16_bits_to_f32(sbuf[(16 * mt + 8 * h + g) * 8 + a]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[mt][2 * h + j] = __fmaf_rn(__fadd_rn(c[mt][2 * h + j], j == 0 ? sa.y : sa.w), __fmul_rn(sw, j == 0 ? sa.x : sa.z), acc[mt][2 * h + j]);
-                }
-        }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) src[mt][h] += 8 * kBlockBytes;
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int col = 2 * t + j;
-        if (col >= rows) continue;
-        const int64_t out = static_cast<int64_t>(row0 + col) * p.n;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (GATEUP) {
-                const int r = n0 + g + 8 * h;
-                if (r < p.n) p.h[out + r] = f32_to_bf16_bits(__fmul_rn(tq_silu(acc[0][2 * h + j]), acc[1][2 * h + j]));
-            } else {
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    const int r = n0 + 16 * mt + g + 8 * h;
-                    if (r < p.n) p.y[out + r] = acc[mt][2 * h + j];
-                }
-            }
-        }
-    }
-    __syncwarp();                                                    // wsc is the next unit's
+__device__ __forceinline__ void cp_async8(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 
-// A CTA takes a contiguous share of the rounds (chunk by chunk, `warps` units
-// each), so that it stages a chunk's activations once for many units.
+// A unit is 32 weight rows (16 of gate and of up, or 32 of one matrix) against one chunk
+// of activation rows.  A CTA takes a contiguous share of all units, chunk by chunk, so
+// that it stages a chunk's activations once for many units; its warps take them in
+// turn.  Each warp brings its own units' codes through a ring in shared memory, four
+// blocks at a time and across the ends of units.  (Copies by TMA: with a cp.async per
+// lane every row costs the load pipe a turn of its own, which then bounds the kernel.)
 template <int FMT, bool GATEUP>
-__global__ void __launch_bounds__(32 * kMaxWarps, 2) stream_kernel(const __grid_constant__ StreamArgs args) {
-    extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_constant__ StreamArgs args) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const MoeProduct &p = args.p;
+    constexpr int kD = kDepth<FMT>, kBlockBytes = FMT == 0 ? 32 : 16, kUnitRows = GATEUP ? 16 : 32;
+    const int nb = p.k / kBlock, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t *ring = smem + warp * kD * kStageBytes<FMT>;
+    uint8_t *side = smem + warps * kD * kStageBytes<FMT> + warp * kD * kSideBytes<FMT>;
+    const auto bar = [&](int slot) { return smem_u32(side + slot * kSideBytes<FMT> + 256); };
+    int *offsets = reinterpret_cast<int *>(smem + warps * kD * (kStageBytes<FMT> + kSideBytes<FMT>));
+    int *chunks = offsets + p.experts + 1;
+    uint8_t *act = reinterpret_cast<uint8_t *>(offsets) + list_bytes(p.experts);
+    float2 *meta = reinterpret_cast<float2 *>(act + args.chunk * row_pitch(nb));
+    if (lane == 0) {
+        for (int i = 0; i < kD; ++i) mbar_init(bar(i), 1);
+        mbar_init_fence();
+    }
     pdl_launch_dependents();
     pdl_wait();
-    const int nb = p.k / kBlock, warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
-    int *offsets = reinterpret_cast<int *>(smem), *chunks = offsets + p.experts + 1;
-    uint8_t *act = smem + list_bytes(p.experts);
-    float2 *meta = reinterpret_cast<float2 *>(act + args.chunk * row_pitch(nb));
-    uint16_t *wsc = reinterpret_cast<uint16_t *>(meta + nb * kCols) + warp * (kScaleBytes / 2);
-    constexpr int kUnitRows = GATEUP ? 16 : 32;
-    const int units = (p.n + kUnitRows - 1) / kUnitRows, per_chunk = (units + warps - 1) / warps;
-    const int64_t rounds = static_cast<int64_t>(list_chunks(p, args.chunk, args.limit, offsets, chunks)) * per_chunk;
-    int64_t r = rounds * blockIdx.x / gridDim.x;
-    const int64_t end = rounds * (blockIdx.x + 1) / gridDim.x;
-    const bool wide = nb % 8 == 0 && (reinterpret_cast<uintptr_t>(p.scales[0]) & 15) == 0 &&
-                      (!GATEUP || (reinterpret_cast<uintptr_t>(p.scales[1]) & 15) == 0);
-    int staged = -1, expert = 0, row0 = 0, rows = 0;
-    for (; r < end; ++r) {
-        const int chunk = static_cast<int>(r / per_chunk), u = static_cast<int>(r % per_chunk) * warps + warp;
-        if (chunk != staged) {
-            int lo = 0, hi = p.experts;                              // chunks[lo] <= chunk < chunks[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (chunks[mid] <= chunk) lo = mid;
-                else hi = mid;
-            }
-            expert = lo;
-            row0 = offsets[lo] + (chunk - chunks[lo]) * args.chunk;
-            rows = min(args.chunk, offsets[lo + 1] - row0);
-            if (staged >= 0) __syncthreads();                        // every warp is done with the chunk before
-            stage_rows<FMT>(p, row0, rows, act, meta);
-            __syncthreads();
-            staged = chunk;
+    const int units = (p.n + kUnitRows - 1) / kUnitRows;
+    const int64_t all = static_cast<int64_t>(list_chunks(p, args.chunk, args.limit, offsets, chunks)) * units;
+    const int64_t first = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x;
+    if (first >= end) return;
+    const bool wide = nb % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales[0]) & 7) == 0 &&
+                      (!GATEUP || (reinterpret_cast<uintptr_t>(p.scales[1]) & 7) == 0);
+    const auto find = [&](int chunk) {                               // its expert
+        int lo = 0, hi = p.experts;                                  // chunks[lo] <= chunk < chunks[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (chunks[mid] <= chunk) lo = mid;
+            else hi = mid;
         }
-        if (u < units) unit<FMT, GATEUP>(p, expert, row0, rows, u * kUnitRows, wide, act, meta, wsc);
+        return lo;
+    };
+    // this warp's units: warp, warp + warps, .. of the `mine` in the CTA's share
+    const int mine = static_cast<int>(end - first);
+    const int first_chunk = static_cast<int>(first / units), first_u = static_cast<int>(first % units);
+
+    // the issuing side; lane l brings the scales of row l of the unit (gate 0-15, up 16-31)
+    int in_unit = warp, in_u = first_u + warp, in_chunk = first_chunk, in_block = 0, in_slot = 0, in_expert = -1, in_y = 0;
+    const uint16_t *scale_src = nullptr;
+    const auto issue = [&]() {
+        if (in_unit < mine) {
+            if (in_block == 0) {                                     // a new unit
+                while (in_u >= units) {
+                    in_u -= units;
+                    ++in_chunk;
+                    in_expert = -1;
+                }
+                if (in_expert < 0) in_expert = find(in_chunk);
+                in_y = in_expert * p.n + in_u * kUnitRows;
+                const int n = min(in_u * kUnitRows + (GATEUP ? lane & 15 : lane), p.n - 1);
+                scale_src = p.scales[GATEUP ? lane >> 4 : 0] + (static_cast<int64_t>(in_expert) * p.n + n) * nb;
+            }
+            if (lane == 0) {
+                const uint32_t dst = smem_u32(ring + in_slot * kStageBytes<FMT>);
+                mbar_arrive_expect_tx(bar(in_slot), kStageBytes<FMT>);
+                load_box(dst, &args.codes[0], in_block * kBlockBytes, in_y, bar(in_slot));
+                load_box(dst + kStageBytes<FMT> / 2, &args.codes[1], in_block * kBlockBytes, GATEUP ? in_y : in_y + 16, bar(in_slot));
+            }
+            uint16_t *sd = reinterpret_cast<uint16_t *>(side + in_slot * kSideBytes<FMT>) + lane * 4;
+            if (wide) {
+                cp_async8(sd, scale_src + in_block);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sd[i] = ldg_u16(scale_src + min(in_block + i, nb - 1));
+            }
+            in_block += kStageBlocks;
+            if (in_block >= nb) {
+                in_block = 0;
+                in_unit += warps;
+                in_u += warps;
+            }
+            in_slot = in_slot == kD - 1 ? 0 : in_slot + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < kD; ++i) issue();
+
+    const Joins<FMT> join = joins<FMT>();
+    int slot = 0, unit = warp, u = first_u + warp;
+    uint32_t phase = 0;
+    for (int chunk = first_chunk, chunk_end = units - first_u;; ++chunk, u -= units, chunk_end += units) {
+        const int expert = find(chunk);
+        const int row0 = offsets[expert] + (chunk - chunks[expert]) * args.chunk;
+        const int rows = min(args.chunk, offsets[expert + 1] - row0);
+        if (chunk > first_chunk) __syncthreads();                    // every warp is done with the chunk before
+        stage_rows<FMT>(p, row0, rows, act, meta);
+        __syncthreads();
+        // a column without a row computes the last row's products again; they go nowhere
+        const uint8_t *act_lane = act + min(g, rows - 1) * row_pitch(nb) + t * 16;
+        for (; unit < min(mine, chunk_end); unit += warps, u += warps) {
+            const uint8_t *ap = act_lane;
+            const float2 *mp = meta + 2 * t;
+            float acc[2][4] = {};
+#pragma unroll 1
+            for (int b0 = 0; b0 < nb; b0 += kStageBlocks) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kD - 1) : "memory");
+                if (!mbar_wait(bar(slot), phase)) atomicOr(args.err, 1u << 12);
+                __syncwarp();
+                const uint8_t *stage = ring + slot * kStageBytes<FMT> + g * kStageBlocks * kBlockBytes;
+                const uint16_t *ws = reinterpret_cast<const uint16_t *>(side + slot * kSideBytes<FMT>) + 4 * g;
+                const int end_b = min(kStageBlocks, nb - b0);
+#pragma unroll 1
+                for (int b = 0; b < end_b; ++b, ap += 256, mp += kCols, ++ws) {
+                    Codes<FMT> c[2][2];
+                    // rows g + 8 x: 16-byte pieces of a row change places by the row's number
+                    const uint8_t *cp = FMT == 0 ? stage + (((2 * b + (t >> 1)) ^ g) << 4) + 8 * (t & 1)
+                                                 : stage + ((b ^ (g >> 1)) << 4) + 4 * t;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint8_t *cx = cp + x * 8 * kStageBlocks * kBlockBytes;
+                        if (FMT == 0) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(cx);
+                            c[x >> 1][x & 1].w[0] = v.x;
+                            c[x >> 1][x & 1].w[FMT == 0 ? 1 : 0] = v.y;
+                        } else {
+                            c[x >> 1][x & 1].w[0] = *reinterpret_cast<const uint32_t *>(cx);
+                        }
+                    }
+                    // (scale, what is missing) of columns 2t, 2t + 1
+                    const float4 sa = *reinterpret_cast<const float4 *>(mp);
+                    float d[2][4];
+                    block_products<FMT>(c, ap, join, d);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float sw = f16_bits_to_f32(ws[32 * x]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float &a = acc[x >> 1][2 * (x & 1) + j];
+                            a = __fmaf_rn(__fadd_rn(d[x >> 1][2 * (x & 1) + j], j == 0 ? sa.y : sa.w),
+                                          __fmul_rn(sw, j == 0 ? sa.x : sa.z), a);
+                        }
+                    }
+                }
+                __syncwarp();                                        // the stage is read
+                issue();
+                if (slot == kD - 1) {
+                    slot = 0;
+                    phase ^= 1;
+                } else {
+                    ++slot;
+                }
+            }
+            const int n0 = u * kUnitRows;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int col = 2 * t + j;
+                if (col >= rows) continue;
+                const int64_t out = static_cast<int64_t>(row0 + col) * p.n;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (GATEUP) {
+                        const int n = n0 + g + 8 * h;
+                        if (n < p.n) p.h[out + n] = f32_to_bf16_bits(__fmul_rn(tq_silu(acc[0][2 * h + j]), acc[1][2 * h + j]));
+                    } else {
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt) {
+                            const int n = n0 + 16 * mt + g + 8 * h;
+                            if (n < p.n) p.y[out + n] = acc[mt][2 * h + j];
+                        }
+                    }
+                }
+            }
+        }
+        if (chunk_end >= mine) break;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -431,7 +500,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) stream_kernel(const __grid_
 // Up to this many units per SM: 3.4 (one token, top 8 of 64 experts, 2 x 1024 x 2048) take 7.8 us split and
 // 12.2 whole; 27 (33 tokens, 1-bit) 43.8 and 27.7; 34 (8 tokens, 5120 x 1536) 30.2 and 22.6.
 constexpr int kSplitMost = 8;
-constexpr int kSplit = 4, kSplitUnits = kMaxWarps / kSplit;
+constexpr int kSplit = 4, kSplitUnits = kSplitWarps / kSplit;
 constexpr int kDotPitch = 36;                       // 32 rows; columns 2t two apart fall on other banks
 constexpr int kSplitScalePitch = 32 * kSplitUnits + 2;
 
@@ -444,7 +513,7 @@ size_t split_smem(int experts, int chunk, int nb) {
 }
 
 template <int FMT, bool GATEUP>
-__global__ void __launch_bounds__(32 * kMaxWarps, 2) split_kernel(const __grid_constant__ StreamArgs args) {
+__global__ void __launch_bounds__(32 * kSplitWarps, 2) split_kernel(const __grid_constant__ StreamArgs args) {
     extern __shared__ __align__(16) uint8_t smem[];
     const MoeProduct &p = args.p;
     constexpr int kA = kAhead<FMT>, kUnitRows = GATEUP ? 16 : 32;
@@ -555,8 +624,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) split_kernel(const __grid_c
 }
 
 template <int FMT, bool GATEUP>
-cudaError_t launch(const MoeProduct &p, int limit, cudaStream_t stream) {
-    StreamArgs a{p, 0, limit};
+cudaError_t launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t stream) {
+    StreamArgs a{};
+    a.p = p;
+    a.limit = limit;
+    a.err = err;
     const int nb = p.k / kBlock;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -582,20 +654,29 @@ cudaError_t launch(const MoeProduct &p, int limit, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         int64_t grid = most_chunks(chunk) * ws_cdiv(units, kSplitUnits);
         if (grid > 2 * sms) grid = 2 * sms;
-        return launch_pdl(split_kernel<FMT, GATEUP>, dim3(static_cast<unsigned>(grid)), dim3(32 * kMaxWarps), smem, stream, a);
+        return launch_pdl(split_kernel<FMT, GATEUP>, dim3(static_cast<unsigned>(grid)), dim3(32 * kSplitWarps), smem, stream, a);
     }
-    // fewer warps to a CTA where one chunk for each expert would not give every SM two CTAs
+    // fewer warps to a CTA where one chunk for each expert would not give every SM a CTA
     int warps = kMaxWarps;
-    while (warps > 2 && active * ws_cdiv(units, warps) < 2 * sms) warps /= 2;
-    // as many rows at once as fit in shared memory (two CTAs on an SM), at most 8 and no more than an expert has
-    while (chunk > 1 && stream_smem(p.experts, chunk, nb, warps) > kSmem) --chunk;
-    const size_t smem = stream_smem(p.experts, chunk, nb, warps);
+    while (warps > 4 && active * ws_cdiv(units, warps) < sms) warps /= 2;
+    // as many rows at once as fit in shared memory, at most 8 and no more than an expert has
+    while (warps > 4 && stream_smem<FMT>(p.experts, chunk, nb, warps) > kSmem) warps /= 2;
+    while (chunk > 1 && stream_smem<FMT>(p.experts, chunk, nb, warps) > kSmem) --chunk;
+    const size_t smem = stream_smem<FMT>(p.experts, chunk, nb, warps);
     if (smem > kSmem) return cudaErrorInvalidValue;
     a.chunk = chunk;
+    constexpr int kBlockBytes = FMT == 0 ? 32 : 16;
+    const uint64_t row_bytes = static_cast<uint64_t>(nb) * kBlockBytes;
+    for (int i = 0; i < 2; ++i) {
+        e = make_tmap_2d(&a.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes[GATEUP ? i : 0], row_bytes,
+                         static_cast<uint64_t>(p.experts) * p.n, row_bytes, kStageBlocks * kBlockBytes, 16,
+                         FMT == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+        if (e != cudaSuccess) return e;
+    }
     e = cudaFuncSetAttribute(stream_kernel<FMT, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     int per_sm = static_cast<int>((kSmem + 1024) / (smem + 1024));
-    if (per_sm > 16 / warps) per_sm = 16 / warps;
+    if (per_sm > kMaxWarps / warps) per_sm = kMaxWarps / warps;
     if (per_sm < 1) per_sm = 1;
     int64_t grid = most_chunks(chunk) * ws_cdiv(units, warps);
     if (grid > static_cast<int64_t>(sms) * per_sm) grid = static_cast<int64_t>(sms) * per_sm;
@@ -604,9 +685,9 @@ cudaError_t launch(const MoeProduct &p, int limit, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t moe_stream_launch(const MoeProduct &p, int limit, cudaStream_t stream) {
-    if (p.h != nullptr) return p.fmt == TQ_FMT_TERNARY2 ? launch<0, true>(p, limit, stream) : launch<1, true>(p, limit, stream);
-    return p.fmt == TQ_FMT_TERNARY2 ? launch<0, false>(p, limit, stream) : launch<1, false>(p, limit, stream);
+cudaError_t moe_stream_launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t stream) {
+    if (p.h != nullptr) return p.fmt == TQ_FMT_TERNARY2 ? launch<0, true>(p, limit, err, stream) : launch<1, true>(p, limit, err, stream);
+    return p.fmt == TQ_FMT_TERNARY2 ? launch<0, false>(p, limit, err, stream) : launch<1, false>(p, limit, err, stream);
 }
 
 }  // namespace tq
