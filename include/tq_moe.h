@@ -118,7 +118,8 @@ tq_status tq_moe_plan(const int32_t *ids, int32_t m, int32_t topk, int32_t exper
  * rows have the bits that they have alone.
  * q: int8 [m][k], 16-byte aligned; s: fp32 [m][k/128]; offsets, rows: a plan
  * over `slots` slots (offsets[experts] <= slots; offsets ascending from 0; rows in
- * 0 .. m-1).  Entries of a bad plan are clamped to these ranges, not followed.
+ * 0 .. m-1).  Entries of a bad plan are clamped to these ranges, not followed, and
+ * offsets that do not ascend have no rows at all.
  * y: fp32 [slots][n]; rows from offsets[experts] on are left as they are.
  * n: 1 .. TQ_MOE_MAX_WIDTH, k: a multiple of 128 up to TQ_MOE_MAX_WIDTH.
  * workspace: a tq_moe_* workspace of the layer that the product belongs to, or

@@ -12,7 +12,7 @@ namespace tq {
 
 // Workspace: err u32 | operand (the tile kernel's copy of a product's input:
 // 2 bytes per value and slot, and the scales) | hist (the sort's
-// counts per block of slots) | offsets | rows | pos | h | hq | hs | y.
+// counts per chunk of slots, and their sums) | offsets | rows | pos | h | hq | hs | y.
 struct MoeWorkspace {
     size_t err, operand, hist, offsets, rows, pos, h, hq, hs, y, total;
 };
@@ -30,7 +30,7 @@ constexpr MoeWorkspace moe_layout(int64_t m, int64_t topk, int64_t experts, int6
     size_t off = 0;
     w.err = off; off = ws_round(off + 4);
     w.operand = off; off = ws_round(off + static_cast<size_t>(moe_operand_bytes(slots, hidden > inter ? hidden : inter)));
-    w.hist = off; off = ws_round(off + static_cast<size_t>(ws_cdiv(slots, kPlanChunk) * experts * 4));
+    w.hist = off; off = ws_round(off + static_cast<size_t>((ws_cdiv(slots, kPlanChunk) + 1) * experts * 4));
     w.offsets = off; off = ws_round(off + static_cast<size_t>((experts + 1) * 4));
     w.rows = off; off = ws_round(off + static_cast<size_t>(slots * 4));
     w.pos = off; off = ws_round(off + static_cast<size_t>(slots * 4));
@@ -60,6 +60,20 @@ struct MoeProduct {
     uint16_t *h;
     int max_rows;           // most rows that an expert can be expected to have
 };
+
+// Put the clamped offsets into shared memory (all threads; synchronises).  False if they do
+// not ascend: the experts' rows could then add up to more than `slots`, and counts of tiles
+// to more than 32 bits, so nothing is computed.
+__device__ __forceinline__ bool load_offsets(const MoeProduct &p, int *offsets) {
+    bool bad = false;
+    for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) {
+        const int at = min(max(p.offsets[e], 0), p.slots);
+        const int before = e > 0 ? min(max(p.offsets[e - 1], 0), p.slots) : 0;
+        bad |= at < before;
+        offsets[e] = at;
+    }
+    return __syncthreads_or(bad) == 0;
+}
 
 // The experts with at most `limit` rows, and those with more than `above`
 // (operand: moe_operand_bytes of workspace for the laid-out input).

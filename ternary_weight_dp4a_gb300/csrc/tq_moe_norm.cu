@@ -206,9 +206,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_rotq_kernel(const void *res,
         lo = __shfl_sync(kFull, lo, 0);
     }
     float inv;
-    if (hi > 1e-25f && hi < 1e37f) {
+    if (hi > 1e-25f && hi < 1e37f && eps < 1e30f) {
         inv = inv_rms(hi, lo, static_cast<float>(n), eps);
-    } else {                                                     // squares beyond binary32's range: in 64 bits
+    } else {                                                     // out of binary32's comfortable range: in 64 bits
         double acc = 0.0;
 #pragma unroll
         for (int j = 0; j < G; ++j)

@@ -92,10 +92,12 @@ __global__ void __launch_bounds__(256) route_kernel(const void *__restrict__ log
 
 // ---------------------------------------------------------------------------
 // The plan.  Slots are dealt to CTAs in chunks of kPlanChunk in order, one slot
-// per thread.  count_kernel writes each chunk's slots per expert; place_kernel
-// adds up the chunks before its own (and every expert before each expert) and
-// ranks its slots: within a warp by match, across the warps by a prefix over
-// per-warp counts in shared memory.  One chunk needs no count_kernel.
+// per thread.  count_kernel writes each chunk's slots per expert; scan_kernel
+// turns them into the slots of the chunks before, and the sums; place_kernel
+// adds every expert before each expert and ranks its slots: within a warp by
+// match, across the warps by a prefix over per-warp counts in shared memory.
+// One chunk needs place_kernel alone.  Every step reads the chunks once: the
+// time is that of three launches until there are thousands of chunks.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int slot_expert(const int *ids, int64_t slot, int64_t slots, int experts) {
     if (slot >= slots) return -1;
@@ -114,6 +116,44 @@ __global__ void __launch_bounds__(kPlanChunk) count_kernel(const int *__restrict
     if (e >= 0) atomicAdd(&count[e], 1);
     __syncthreads();
     for (int i = threadIdx.x; i < experts; i += kPlanChunk) hist[static_cast<int64_t>(blockIdx.x) * experts + i] = count[i];
+}
+
+// hist [chunks][experts] -> exclusive sums over the chunks; the whole sums go behind them.
+// A CTA takes 32 experts, its warps a run of the chunks each.
+__global__ void __launch_bounds__(1024) scan_kernel(int *__restrict__ hist, int chunks, int experts) {
+    __shared__ int sum[32][33];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
+    const int per = (chunks + 31) / 32, first = min(warp * per, chunks), last = min(first + per, chunks);
+    int *column = hist + e;
+    int run = 0;
+    if (e < experts) {
+#pragma unroll 8
+        for (int c = first; c < last; ++c) run += column[static_cast<int64_t>(c) * experts];
+    }
+    sum[warp][lane] = run;
+    __syncthreads();
+    if (e >= experts) return;
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+        if (w == warp) before = all;
+        all += sum[w][lane];
+    }
+    if (warp == 0) column[static_cast<int64_t>(chunks) * experts] = all;
+    constexpr int kAhead = 8;                                    // loads under way before the stores
+    for (int c0 = first; c0 < last; c0 += kAhead) {
+        int v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) v[i] = c0 + i < last ? column[static_cast<int64_t>(c0 + i) * experts] : 0;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (c0 + i < last) column[static_cast<int64_t>(c0 + i) * experts] = before;
+            before += v[i];
+        }
+    }
 }
 
 // shared memory: warp counts [32][experts] (16 bits), base [experts + 1], scan [32]
@@ -148,12 +188,8 @@ __global__ void __launch_bounds__(kPlanChunk) place_kernel(const int *__restrict
         }
         all = run;
         if (hist != nullptr) {
-            all = 0;
-            for (unsigned c = 0; c < gridDim.x; ++c) {
-                const int h = hist[static_cast<int64_t>(c) * experts + tid];
-                if (c < blockIdx.x) before += h;
-                all += h;
-            }
+            before = hist[static_cast<int64_t>(blockIdx.x) * experts + tid];
+            all = hist[static_cast<int64_t>(gridDim.x) * experts + tid];
         }
     }
     // exclusive scan of `all` over the experts (one per thread; experts <= 1024)
@@ -222,10 +258,14 @@ cudaError_t moe_plan_launch(const int *ids, int m, int topk, int experts, int *o
     const int64_t slots = static_cast<int64_t>(m) * topk;
     const unsigned chunks = static_cast<unsigned>(ws_cdiv(slots, kPlanChunk));
     cudaError_t e = cudaSuccess;
-    if (chunks > 1)
+    if (chunks > 1) {
         e = launch_pdl(count_kernel, dim3(chunks), dim3(kPlanChunk), experts * sizeof(int), stream, ids, slots, experts,
                        hist);
-    if (e != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(scan_kernel, dim3((experts + 31) / 32), dim3(1024), 0, stream, hist, static_cast<int>(chunks),
+                       experts);
+        if (e != cudaSuccess) return e;
+    }
     const size_t smem = (experts + 1 + 32) * sizeof(int) + static_cast<size_t>(32) * experts * sizeof(uint16_t);
     if (smem > 48 * 1024)
         e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

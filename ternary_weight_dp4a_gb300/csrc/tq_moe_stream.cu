@@ -183,13 +183,12 @@ size_t stream_smem(int experts, int chunk, int nb, int warps) {
 // Fill offsets (clamped) and chunks (all threads); returns the number of chunks.
 __device__ __forceinline__ int list_chunks(const MoeProduct &p, int chunk, int limit, int *offsets, int *chunks) {
     const int tid = threadIdx.x, lane = tid & 31;
-    for (int e = tid; e <= p.experts; e += blockDim.x) offsets[e] = min(max(p.offsets[e], 0), p.slots);
-    __syncthreads();
+    if (!load_offsets(p, offsets)) return 0;
     if (tid < 32) {
         int base = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int e = e0 + lane;
-            const int n = e < p.experts ? max(offsets[e + 1] - offsets[e], 0) : 0;
+            const int n = e < p.experts ? offsets[e + 1] - offsets[e] : 0;
             const int c = n <= limit ? (n + chunk - 1) / chunk : 0;
             int incl = c;
 #pragma unroll

@@ -81,12 +81,11 @@ __device__ __forceinline__ int expert_tiles(int rows, int above) { return rows >
 // Fill sm.offsets and sm.tiles (all threads).
 __device__ __forceinline__ void list_tiles(TileSmem &sm, const MoeProduct &p, int above) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e <= p.experts; e += kThreads) sm.offsets[e] = min(max(p.offsets[e], 0), p.slots);
-    __syncthreads();
+    const bool ok = load_offsets(p, sm.offsets);
     int base = 0;
     for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
         const int e = e0 + tid;
-        const int c = e < p.experts ? expert_tiles(sm.offsets[e + 1] - sm.offsets[e], above) : 0;
+        const int c = ok && e < p.experts ? expert_tiles(sm.offsets[e + 1] - sm.offsets[e], above) : 0;
         int incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

@@ -348,6 +348,37 @@ def test_a_bad_plan_is_clamped(tq):
     assert (y[8:] == 0).all() and torch.isfinite(y).all()
 
 
+@pytest.mark.parametrize("rows", [8, 512])
+def test_offsets_that_do_not_ascend_have_no_rows(tq, rows):
+    """Overlapping shares would add up to more rows than there are: nothing is written."""
+    import torch
+    w = Experts(tq, 3, 64, 256, 0, seed=1)
+    q, s = act(rows, 256)
+    y = torch.full((rows, 64), -1.0, device="cuda")
+    order = cuda(np.arange(rows, dtype=np.int32).reshape(rows, 1))
+    plan = tq.MoePlan(cuda(np.array([0, rows, 1, rows], np.int32)), order, order)
+    tq.moe_gemv(w.dev, cuda(q), cuda(s), plan, y=y)
+    torch.cuda.synchronize()
+    assert (y == -1.0).all()
+
+
+@pytest.mark.parametrize("m,topk,experts", [(9000, 8, 33), (70000, 2, 1000), (300000, 5, 8)])
+def test_plan_of_many_chunks(tq, m, topk, experts):
+    """The sort's counts are summed over many chunks of slots; every slot has one place."""
+    rng = np.random.default_rng(m)
+    ids = rng.integers(-1, experts, (m, topk)).astype(np.int32)
+    plan = tq.moe_plan(cuda(ids), experts)
+    order = np.argsort(np.where(ids.ravel() < 0, experts, ids.ravel()), kind="stable")
+    total = int((ids >= 0).sum())
+    pos = np.full(m * topk, -1, np.int32)
+    pos[order[:total]] = np.arange(total, dtype=np.int32)
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(ids[ids >= 0], minlength=experts))])
+    assert np.array_equal(plan.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(plan.pos.cpu().numpy().ravel(), pos)
+    assert np.array_equal(plan.rows.cpu().numpy().ravel()[:total], order[:total] // topk)
+    assert (plan.rows.cpu().numpy().ravel()[total:] == -1).all()
+
+
 # ----------------------------------------------------------------------------
 # sum over experts, and the layer
 # ----------------------------------------------------------------------------
