@@ -78,15 +78,25 @@ tq::MoeProduct product(const tq_experts *w, const tq_experts *up, const int8_t *
     return p;
 }
 
-// Experts with more rows than this run on the tile kernel, the others on the
-// stream kernel; the bits are the same.
-constexpr int kTileAbove = 64;
+// Experts with more rows than this run on the tile kernel, the others on the stream
+// kernel; the bits are the same.  A block of 128 weight rows costs the tile kernel about 2000
+// cycles for any number of activation rows, the stream kernel 300 for every eight; the
+// tile kernel's launches are paid for anyway once there is one.  Gate/up with 24, 32, 40 and
+// 48: 400 tokens, top 8 of 64, 125, 120, 114, 126 us; top 8 of 128, 106, 110, 103, 104; 256
+// tokens, top 2 of 8, 67, 79, 98, 105; from 1000 tokens on all are alike.
+constexpr int kTileAbove = 32;
+// The tile kernel's launches cost 10 us and its turns are long (2000 cycles for each of k/128
+// blocks), so it is left out where few experts can have that many rows: gate/up of 96
+// tokens, top 8 of 128, takes 53 us without and 74 with it, of 256 tokens, top 4 of 32, 169
+// and 187; but of 400 tokens 117 and 104, 249 and 224.
+constexpr int kTileSlots = 2560;
 
 tq_status run_product(const tq::MoeProduct &p, void *workspace, cudaStream_t stream) {
     const tq::MoeWorkspace L = tq::moe_layout(1, 1, 1, 0, 0);      // err and operand come first
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     cudaError_t e = cudaSuccess;
-    const bool tiles = p.max_rows > kTileAbove;
+    const bool tiles = p.max_rows > kTileAbove && p.slots >= 8 * p.experts &&
+                       (p.slots >= kTileSlots || p.slots > 48 * p.experts);
     unsigned *err = reinterpret_cast<unsigned *>(ws + L.err);
     if (tiles) e = tq::moe_tile_launch(p, kTileAbove, ws + L.operand, err, stream);
     if (e == cudaSuccess) e = tq::moe_stream_launch(p, tiles ? kTileAbove : p.slots, err, stream);

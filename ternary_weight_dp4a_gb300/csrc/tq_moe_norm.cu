@@ -145,7 +145,8 @@ __device__ __forceinline__ float inv_rms(float hi, float lo, float n, float eps)
 // ---------------------------------------------------------------------------
 // Residual addition, RMS norm, rotation, quantisation: one CTA per row; a warp's
 // sums t stay in registers between the two passes (sum of squares; normalise,
-// rotate, quantise), so the row is read once.
+// rotate, quantise), so the row is read once.  Bound by memory and instructions alike:
+// 8192 x 5120 bf16 with gamma 83 us, 3.5 TB/s (the bytes alone: 43 us); one row 3.5 us, launch to launch.
 // ---------------------------------------------------------------------------
 template <bool RB, bool DB, int G>
 __global__ void __launch_bounds__(1024) add_rmsnorm_rotq_kernel(const void *res, const void *delta,
@@ -206,7 +207,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_rotq_kernel(const void *res,
         lo = __shfl_sync(kFull, lo, 0);
     }
     float inv;
-    if (hi > 1e-25f && hi < 1e37f && eps < 1e30f) {
+    // (with an ordinary eps small sums are fine, too: what they lose is far below eps's last bit)
+    if ((hi > 1e-25f || eps > 1e-12f) && hi < 1e37f && eps < 1e30f) {
         inv = inv_rms(hi, lo, static_cast<float>(n), eps);
     } else {                                                     // out of binary32's comfortable range: in 64 bits
         double acc = 0.0;
@@ -280,7 +282,8 @@ cudaError_t norm_launch(const void *res, const void *delta, const uint16_t *gamm
 }
 
 // ---------------------------------------------------------------------------
-// Weighted sum over a token's experts: four columns per thread, choices in order.
+// Weighted sum over a token's experts: four columns per thread, choices in order.  Bound
+// by memory: 4096 x 5120, top 8: 111 us, 6.4 TB/s.
 // ---------------------------------------------------------------------------
 template <bool OB>
 __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ y, const int *__restrict__ pos,

@@ -8,15 +8,26 @@
 //   A weight's bits stay where they are in the word: masked out and joined with
 //   the exponent of 1.0 they are the mantissa of 1 + v * 2^(p - 10), p the lowest
 //   bit's place in its half word, one operation for two weights.  p is kept in
-//   4 .. 9 (the word itself, and it shifted by 6 right and by 4 left).  The
-//   activation there is q * s, s = 2^(10 - p) (1-bit: 2^(11 - p)), so the product is
-//   q * s + q * v (1-bit: + 2 q v), and the sums over q * s and over v's offset are
-//   known when the activations are laid out and added to the sum with a minus.
+//   2 .. 9, where q * 2^(10 - p) is still an fp16 number (2-bit: the word itself, and
+//   with its bytes changed in pairs; 1-bit: 4 .. 9, the word itself, and it shifted by
+//   6 right and by 4 left).  The activation there is q * s, s = 2^(10 - p) (1-bit:
+//   2^(11 - p)), so the product is q * s + q * v (1-bit: + 2 q v), and the sums over
+//   q * s and over v's offset are known when the activations are laid out: with a
+//   minus they are what the sum starts from.
 //   2-bit: codes 0, 1, 2 become 0, 1, 3 (two operations for 16 codes); with their
 //   upper bit inverted, in the masking operation, v = w + 2.   1-bit: w = 2 v - 1.
-//   Everything is a whole number below 2^20.
+//   Everything is a whole number below 2^23.
 // Per 128-block and output the kernel then adds one fma(d, scale_w * scale_a,
 // acc), blocks in ascending order, the order that tq_moe.h documents.
+//
+// What bounds it.  With some rows for every expert the weights are read once and turned
+// into fp16 once for eight rows; four masking operations and one matrix instruction per
+// 512 weights share a scheduler at 10.5 cycles (8.0 for the matrix instruction by
+// itself), what prepares and folds them comes on top: 267 (1-bit) and 313 (2-bit)
+// cycles per warp for 32 weight rows and a block of 128.  Memory would take a quarter to
+// a half of that: 8 tokens, top 4 of 32 experts, 5120 x 1536 take 23.4 us, 21.1 with all
+// weights in L2, 6.4 for the bytes.  16 rows at a time (two matrix instructions for a
+// masked pair) gain 5% where experts have many rows and lose 22% where they have few.
 //
 // (fp8 operands would need fewer decode operations, but mma.sync on fp8 is
 // emulated here: 11 instructions and 6.1 cycles per SM for m16n8k32, against
@@ -25,6 +36,7 @@
 
 #include "tq_device.cuh"
 #include "tq_launch.h"
+#include "tq_moe_codes.cuh"
 #include "tq_moe_internal.h"
 #include "tq_tmap.h"
 
@@ -58,19 +70,19 @@ __device__ __forceinline__ Codes<FMT> load_codes(const uint8_t *p) {
 }
 
 // Where pair i (0..15) of a lane's 32 weights sits: the weight of its lower half
-// (the other is 8 or 16 further), and the place p of its lowest bit once shifted.
+// (the other is 8 or 16 further), and the place p of its lowest bit in the word that is masked.
 template <int FMT>
 __host__ __device__ constexpr int pair_weight(int i) {
-    return FMT == 0 ? 16 * (i >> 3) + ((i & 7) < 6 ? (i & 7) + 2 : (i & 7) - 6) : (i < 12 ? i + 4 : i - 12);
+    return FMT == 0 ? 16 * (i >> 3) + ((i & 7) + 1) % 8 : (i < 12 ? i + 4 : i - 12);
 }
 template <int FMT>
 __host__ __device__ constexpr int pair_place(int i) {
-    return FMT == 0 ? 4 + 2 * ((i & 7) % 3) : 4 + i % 6;
+    return FMT == 0 ? 2 + 2 * (i & 3) : 4 + i % 6;
 }
 
-// A lane's weights of one row and block, ready for masking: each word as it is,
-// shifted right by 6 and left by 4.
-template <int FMT> struct Fields { uint32_t w[FMT == 0 ? 2 : 1][3]; };
+// A lane's weights of one row and block, ready for masking: each word as it is, and
+// (2-bit) with bytes 0, 1 and 2, 3 changed, (1-bit) shifted right by 6 and left by 4.
+template <int FMT> struct Fields { uint32_t w[FMT == 0 ? 2 : 1][FMT == 0 ? 2 : 3]; };
 
 template <int FMT>
 __device__ __forceinline__ Fields<FMT> fields(const Codes<FMT> &c) {
@@ -79,8 +91,12 @@ __device__ __forceinline__ Fields<FMT> fields(const Codes<FMT> &c) {
     for (int i = 0; i < (FMT == 0 ? 2 : 1); ++i) {
         const uint32_t w = FMT == 0 ? c.w[i] | ((c.w[i] >> 1) & 0x55555555u) : c.w[i];       // codes 0, 1, 2 -> 0, 1, 3
         f.w[i][0] = w;
-        f.w[i][1] = w >> 6;
-        f.w[i][2] = w << 4;
+        if (FMT == 0) {
+            f.w[i][1] = prmt(w, w, 0x2301u);
+        } else {
+            f.w[i][1] = w >> 6;
+            f.w[i][FMT == 0 ? 1 : 2] = w << 4;
+        }
     }
     return f;
 }
@@ -88,19 +104,14 @@ __device__ __forceinline__ Fields<FMT> fields(const Codes<FMT> &c) {
 // What joins the masked bits: the exponent of 1.0, and for 2-bit codes the inversion of
 // the upper bit (one word for each place).  Kept in registers: lop3 takes one
 // immediate, and as two immediates the compiler makes two instructions of it.
-template <int FMT> struct Joins { uint32_t w[FMT == 0 ? 3 : 1]; };
+template <int FMT> struct Joins { uint32_t w[FMT == 0 ? 4 : 1]; };
 
 template <int FMT>
 __device__ __forceinline__ Joins<FMT> joins() {
     Joins<FMT> j;
 #pragma unroll
-    for (int i = 0; i < (FMT == 0 ? 3 : 1); ++i)
-        asm volatile("mov.b32 %0, %1;" : "=r"(j.w[i]) : "n"(0x3c003c00u));
-    if (FMT == 0) {
-        j.w[0] |= 0x00020002u << 4;
-        j.w[FMT == 0 ? 1 : 0] |= 0x00020002u << 6;
-        j.w[FMT == 0 ? 2 : 0] |= 0x00020002u << 8;
-    }
+    for (int i = 0; i < (FMT == 0 ? 4 : 1); ++i)
+        asm volatile("mov.b32 %0, %1;" : "=r"(j.w[i]) : "r"(0x3c003c00u | (FMT == 0 ? 0x00020002u << (2 + 2 * i) : 0u)));
     return j;
 }
 
@@ -111,8 +122,8 @@ __device__ __forceinline__ uint32_t weight_pair(const Fields<FMT> &f, const Join
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0x6a;"                         // (field & mask) ^ join
         : "=r"(r)
-        : "r"(FMT == 0 ? f.w[FMT == 0 ? i >> 3 : 0][(i & 7) / 3] : f.w[0][i / 6]),
-          "r"((FMT == 0 ? 0x00030003u : 0x00010001u) << p), "r"(join.w[FMT == 0 ? (i & 7) % 3 : 0]));
+        : "r"(FMT == 0 ? f.w[FMT == 0 ? i >> 3 : 0][(i & 7) / 4] : f.w[0][FMT == 0 ? 0 : i / 6]),
+          "r"((FMT == 0 ? 0x00030003u : 0x00010001u) << p), "r"(join.w[FMT == 0 ? i & 3 : 0]));
     return r;
 }
 
@@ -133,13 +144,13 @@ __host__ __device__ constexpr uint32_t scale_bytes(int e) {
     return r;
 }
 
-// The first of a block's matrix instructions: nothing to add to.
+// The first of a block's matrix instructions: it starts from the columns' start values.
 __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                              uint32_t b1) {
+                                              uint32_t b1, float2 start) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(start.x), "f"(start.y));
 }
 
 // Two int8 codes (plus 128, picked from the bytes of a and b) as fp16, times s.
@@ -164,7 +175,7 @@ struct StreamArgs {
 //   offsets, chunks (of the experts before) int [experts + 1] each
 //   activations fp16 [chunk][block][quarter][t][8]: the 32 of lane t in the order of its
 //     weight pairs, 8 at a time; 64 bytes between rows
-//   (scale, what the sum is short of d) [block][8]
+//   per two columns their scales and the values that their sums start from [block][4][4]
 __host__ __device__ constexpr int list_bytes(int experts) { return (2 * (experts + 1) * 4 + 15) / 16 * 16; }
 __host__ __device__ constexpr int row_pitch(int nb) { return nb * 256 + 64; }
 constexpr int kStageBlocks = 4;
@@ -177,7 +188,7 @@ template <int FMT>
 size_t stream_smem(int experts, int chunk, int nb, int warps) {
     return 1024 + static_cast<size_t>(warps) * kDepth<FMT> * (kStageBytes<FMT> + kSideBytes<FMT>) +
            static_cast<size_t>(list_bytes(experts)) + static_cast<size_t>(chunk) * row_pitch(nb) +
-           static_cast<size_t>(nb) * kCols * sizeof(float2);
+           static_cast<size_t>(nb) * kCols * 8;
 }
 
 // Fill offsets (clamped) and chunks (all threads); returns the number of chunks.
@@ -205,9 +216,12 @@ __device__ __forceinline__ int list_chunks(const MoeProduct &p, int chunk, int l
     return chunks[p.experts];
 }
 
+// A column's scale in its block's row of `meta`; the start value is two further.
+__device__ __forceinline__ int meta_column(int c) { return 4 * (c >> 1) + (c & 1); }
+
 // Lay the codes of `rows` activation rows out in shared memory (all threads).
 template <int FMT>
-__device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int rows, uint8_t *act, float2 *meta) {
+__device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int rows, uint8_t *act, float *meta) {
     const int tid = threadIdx.x, nb = p.k / kBlock, pitch = row_pitch(nb), per = nb * 4;
 #pragma unroll 2
     for (int i = tid; i < rows * per; i += blockDim.x) {
@@ -244,10 +258,17 @@ __device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int ro
             }
             *reinterpret_cast<uint4 *>(dst + 64 * x) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if ((c & 3) == 0) meta[(c >> 2) * kCols + r] = make_float2(sa, static_cast<float>(start));
+        if ((c & 3) == 0) {
+            float *m = meta + (c >> 2) * 2 * kCols + meta_column(r);
+            m[0] = sa;
+            m[2] = static_cast<float>(start);
+        }
     }
     const int none = kCols - rows;
-    for (int i = tid; i < none * nb; i += blockDim.x) meta[(i / none) * kCols + rows + i % none] = make_float2(0.0f, 0.0f);
+    for (int i = tid; i < none * nb; i += blockDim.x) {
+        float *m = meta + (i / none) * 2 * kCols + meta_column(rows + i % none);
+        m[0] = m[2] = 0.0f;
+    }
 }
 
 // The blocks whose codes are on their way while one is computed.
@@ -277,23 +298,28 @@ __device__ __forceinline__ void load_block(const uint8_t *const (&src)[2][2], in
         for (int h = 0; h < 2; ++h) c[mt][h] = load_codes<FMT>(src[mt][h] + b * (FMT == 0 ? 32 : 16));
 }
 
-// c[mt][2 h + j]: the block's products of weight row 16 mt + 8 h + g and column 2 t + j,
-// short of d by what stage_rows put beside the scale.  ap: this lane's column and t.
+// c[mt][2 h + j]: the block's products of weight row 16 mt + 8 h + g and column 2 t + j.
+// ap: this lane's column and t; start: the start values of columns 2 t, 2 t + 1.
 template <int FMT>
-__device__ __forceinline__ void block_products(const Codes<FMT> (&codes)[2][2], const uint8_t *ap, const Joins<FMT> &join,
-                                               float (&c)[2][4]) {
+__device__ __forceinline__ void block_products(const Codes<FMT> (&codes)[2][2], const uint8_t *ap, float2 start,
+                                               const Joins<FMT> &join, float (&c)[2][4]) {
     uint4 bq[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) bq[i] = *reinterpret_cast<const uint4 *>(ap + 64 * i);
+    Fields<FMT> f[2][2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-        const Fields<FMT> f0 = fields<FMT>(codes[mt][0]), f1 = fields<FMT>(codes[mt][1]);
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint4 &v = bq[i >> 1];
+        for (int h = 0; h < 2; ++h) f[mt][h] = fields<FMT>(codes[mt][h]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 &v = bq[i >> 1];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {                             // two sums in turn: neither waits for itself
+            const Fields<FMT> &f0 = f[mt][0], &f1 = f[mt][1];
             const uint32_t a0 = weight_pair<FMT>(f0, join, 2 * i), a1 = weight_pair<FMT>(f1, join, 2 * i),
                            a2 = weight_pair<FMT>(f0, join, 2 * i + 1), a3 = weight_pair<FMT>(f1, join, 2 * i + 1);
-            if (i == 0) mma_f16_first(c[mt], a0, a1, a2, a3, v.x, v.y);
+            if (i == 0) mma_f16_first(c[mt], a0, a1, a2, a3, v.x, v.y, start);
             else mma_f16(c[mt], a0, a1, a2, a3, (i & 1) ? v.z : v.x, (i & 1) ? v.w : v.y);
         }
     }
@@ -329,7 +355,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
     int *offsets = reinterpret_cast<int *>(smem + warps * kD * (kStageBytes<FMT> + kSideBytes<FMT>));
     int *chunks = offsets + p.experts + 1;
     uint8_t *act = reinterpret_cast<uint8_t *>(offsets) + list_bytes(p.experts);
-    float2 *meta = reinterpret_cast<float2 *>(act + args.chunk * row_pitch(nb));
+    float *meta = reinterpret_cast<float *>(act + args.chunk * row_pitch(nb));
     if (lane == 0) {
         for (int i = 0; i < kD; ++i) mbar_init(bar(i), 1);
         mbar_init_fence();
@@ -409,25 +435,27 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
         stage_rows<FMT>(p, row0, rows, act, meta);
         __syncthreads();
         // a column without a row computes the last row's products again; they go nowhere
+        const uint32_t piece = g * kStageBlocks * kBlockBytes +
+                               (FMT == 0 ? (((t >> 1) ^ g) << 4) + 8 * (t & 1) : ((g >> 1) << 4) + 4 * t);
         const uint8_t *act_lane = act + min(g, rows - 1) * row_pitch(nb) + t * 16;
         for (; unit < min(mine, chunk_end); unit += warps, u += warps) {
             const uint8_t *ap = act_lane;
-            const float2 *mp = meta + 2 * t;
-            float acc[2][4] = {};
+            const float *mp = meta + 4 * t;
+            uint64_t acc[2][2] = {};                                 // [mt][h]: columns 2 t, 2 t + 1
 #pragma unroll 1
             for (int b0 = 0; b0 < nb; b0 += kStageBlocks) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kD - 1) : "memory");
                 if (!mbar_wait(bar(slot), phase)) atomicOr(args.err, 1u << 12);
                 __syncwarp();
-                const uint8_t *stage = ring + slot * kStageBytes<FMT> + g * kStageBlocks * kBlockBytes;
+                const uint8_t *stage = ring + slot * kStageBytes<FMT>;
                 const uint16_t *ws = reinterpret_cast<const uint16_t *>(side + slot * kSideBytes<FMT>) + 4 * g;
-                const int end_b = min(kStageBlocks, nb - b0);
-#pragma unroll 1
-                for (int b = 0; b < end_b; ++b, ap += 256, mp += kCols, ++ws) {
+                const int end_b = nb - b0;
+#pragma unroll
+                for (int b = 0; b < kStageBlocks; ++b, ap += 256, mp += 2 * kCols, ++ws) {
+                    if (b >= end_b) break;
                     Codes<FMT> c[2][2];
                     // rows g + 8 x: 16-byte pieces of a row change places by the row's number
-                    const uint8_t *cp = FMT == 0 ? stage + (((2 * b + (t >> 1)) ^ g) << 4) + 8 * (t & 1)
-                                                 : stage + ((b ^ (g >> 1)) << 4) + 4 * t;
+                    const uint8_t *cp = stage + (piece ^ (b * (FMT == 0 ? 32 : 16)));
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const uint8_t *cx = cp + x * 8 * kStageBlocks * kBlockBytes;
@@ -439,19 +467,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
                             c[x >> 1][x & 1].w[0] = *reinterpret_cast<const uint32_t *>(cx);
                         }
                     }
-                    // (scale, what is missing) of columns 2t, 2t + 1
+                    // scales and start values of columns 2 t, 2 t + 1
                     const float4 sa = *reinterpret_cast<const float4 *>(mp);
                     float d[2][4];
-                    block_products<FMT>(c, ap, join, d);
+                    block_products<FMT>(c, ap, make_float2(sa.z, sa.w), join, d);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const float sw = f16_bits_to_f32(ws[32 * x]);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float &a = acc[x >> 1][2 * (x & 1) + j];
-                            a = __fmaf_rn(__fadd_rn(d[x >> 1][2 * (x & 1) + j], j == 0 ? sa.y : sa.w),
-                                          __fmul_rn(sw, j == 0 ? sa.x : sa.z), a);
-                        }
+                        uint64_t &a = acc[x >> 1][x & 1];
+                        a = fma2(pack2(d[x >> 1][2 * (x & 1)], d[x >> 1][2 * (x & 1) + 1]),
+                                 mul2(pack2(sw, sw), pack2(sa.x, sa.y)), a);
                     }
                 }
                 __syncwarp();                                        // the stage is read
@@ -464,6 +489,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
                 }
             }
             const int n0 = u * kUnitRows;
+            float y[2][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) unpack2(acc[x >> 1][x & 1], y[x >> 1][2 * (x & 1)], y[x >> 1][2 * (x & 1) + 1]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int col = 2 * t + j;
@@ -473,12 +501,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
                 for (int h = 0; h < 2; ++h) {
                     if (GATEUP) {
                         const int n = n0 + g + 8 * h;
-                        if (n < p.n) p.h[out + n] = f32_to_bf16_bits(__fmul_rn(tq_silu(acc[0][2 * h + j]), acc[1][2 * h + j]));
+                        if (n < p.n) p.h[out + n] = f32_to_bf16_bits(__fmul_rn(tq_silu(y[0][2 * h + j]), y[1][2 * h + j]));
                     } else {
 #pragma unroll
                         for (int mt = 0; mt < 2; ++mt) {
                             const int n = n0 + 16 * mt + g + 8 * h;
-                            if (n < p.n) p.y[out + n] = acc[mt][2 * h + j];
+                            if (n < p.n) p.y[out + n] = y[mt][2 * h + j];
                         }
                     }
                 }
@@ -496,8 +524,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
 // memory, where one thread per output folds them in order.  The codes of the
 // next round are on their way while a round is folded.
 // ---------------------------------------------------------------------------
-// Up to this many units per SM: 3.4 (one token, top 8 of 64 experts, 2 x 1024 x 2048) take 7.8 us split and
-// 12.2 whole; 27 (33 tokens, 1-bit) 43.8 and 27.7; 34 (8 tokens, 5120 x 1536) 30.2 and 22.6.
+// Up to this many units per SM: 3.4 (one token, top 8 of 64 experts, 2 x 1024 x 2048) take 8.0 us split and
+// 12.7 whole; 27 (33 tokens, 1-bit) 44 and 29; 34 (8 tokens, 5120 x 1536) 31 and 23.
 constexpr int kSplitMost = 8;
 constexpr int kSplit = 4, kSplitUnits = kSplitWarps / kSplit;
 constexpr int kDotPitch = 36;                       // 32 rows; columns 2t two apart fall on other banks
@@ -507,7 +535,7 @@ constexpr int kSplitScalePitch = 32 * kSplitUnits + 2;
 // [2][unit] products [block][column][row]
 size_t split_smem(int experts, int chunk, int nb) {
     return static_cast<size_t>(list_bytes(experts)) + static_cast<size_t>(chunk) * row_pitch(nb) +
-           static_cast<size_t>(nb) * kCols * sizeof(float2) + 2 * static_cast<size_t>(nb) * kSplitScalePitch * 2 +
+           static_cast<size_t>(nb) * kCols * 8 + 2 * static_cast<size_t>(nb) * kSplitScalePitch * 2 +
            2 * static_cast<size_t>(kSplitUnits) * nb * chunk * kDotPitch * 4;
 }
 
@@ -523,8 +551,8 @@ __global__ void __launch_bounds__(32 * kSplitWarps, 2) split_kernel(const __grid
     const int per = (nb + kSplit - 1) / kSplit, lo = min((warp % kSplit) * per, nb), hi = min(lo + per, nb);
     int *offsets = reinterpret_cast<int *>(smem), *chunks = offsets + p.experts + 1;
     uint8_t *act = smem + list_bytes(p.experts);
-    float2 *meta = reinterpret_cast<float2 *>(act + args.chunk * row_pitch(nb));
-    float *dots = reinterpret_cast<float *>(meta + nb * kCols);
+    float *meta = reinterpret_cast<float *>(act + args.chunk * row_pitch(nb));
+    float *dots = meta + nb * 2 * kCols;
     const int unit_dots = nb * args.chunk * kDotPitch;
     uint16_t *wsc = reinterpret_cast<uint16_t *>(dots + 2 * kSplitUnits * unit_dots);
     const int units = (p.n + kUnitRows - 1) / kUnitRows, per_chunk = (units + kSplitUnits - 1) / kSplitUnits;
@@ -584,7 +612,8 @@ __global__ void __launch_bounds__(32 * kSplitWarps, 2) split_kernel(const __grid
                 const int b = b0 + a;
                 if (b >= hi) break;
                 float c[2][4];
-                block_products<FMT>(ring[a], ap + a * 256, join, c);
+                block_products<FMT>(ring[a], ap + a * 256,
+                                    *reinterpret_cast<const float2 *>(meta + b * 2 * kCols + 4 * t + 2), join, c);
                 if (b + kA < hi) load_block<FMT>(src, b + kA, ring[a]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -609,11 +638,11 @@ __global__ void __launch_bounds__(32 * kSplitWarps, 2) split_kernel(const __grid
             float acc[2] = {0.0f, 0.0f};
 #pragma unroll 4
             for (int b = 0; b < nb; ++b) {
-                const float2 m = meta[b * kCols + col];
+                const float sa = meta[b * 2 * kCols + meta_column(col)];
 #pragma unroll
                 for (int x = 0; x < (GATEUP ? 2 : 1); ++x)
-                    acc[x] = __fmaf_rn(__fadd_rn(d[b * done.rows * kDotPitch + 16 * x], m.y),
-                                       __fmul_rn(f16_bits_to_f32(w[b * kSplitScalePitch + 16 * x]), m.x), acc[x]);
+                    acc[x] = __fmaf_rn(d[b * done.rows * kDotPitch + 16 * x],
+                                       __fmul_rn(f16_bits_to_f32(w[b * kSplitScalePitch + 16 * x]), sa), acc[x]);
             }
             const int64_t out = static_cast<int64_t>(done.row0 + col) * p.n + n;
             if (GATEUP) p.h[out] = f32_to_bf16_bits(__fmul_rn(tq_silu(acc[0]), acc[1]));

@@ -1,7 +1,7 @@
 // tq_moe_tile.cu -- products grouped by expert for many rows per expert, on the
 // 5th-generation tensor core.
 //
-// A tile is 128 weight rows x up to 224 activation rows of one expert (gate/up:
+// A tile is 128 weight rows x up to 192 activation rows of one expert (gate/up:
 // 64 rows of each, eight by eight, so that one lane folds both values of an
 // output).  The weights are the A operand, decoded from their codes to e4m3
 // -1, 0, +1 straight into tensor memory; the activations are the B operand in
@@ -12,16 +12,24 @@
 //   acc = fma(d, scale_w * scale_a, acc),
 // in registers, blocks in ascending order: the stream kernel's bits.
 //
-// What bounds it.  With A in tensor memory an MMA of M = 128, K = 32 takes 128
-// cycles for every N <= 224 (measured; 140 at N = 256, and 173 with A in shared
-// memory), so N = 224 gives 7159 MACs per cycle and SM, half of them for each part
-// of the code: 3580 int8 x ternary MACs.  224 columns also leave room for
-// two accumulators (448 of 512 columns) and two blocks of A (64 columns).
+// What bounds it.  With A in tensor memory an MMA of M = 128, K = 32 takes 128 cycles
+// for every N <= 224 (measured; 140 at N = 256, and 173 with A in shared memory): 1024
+// cycles for a block.  Every block's accumulator has to leave tensor memory and be folded
+// meanwhile, and the hand-over (commit, wait, read, release) has its latency on each side:
+// a block takes about 2000 cycles, and that is the bound, not the tensor core, nor memory.
+// Two accumulators of 192 columns leave room for four blocks of A, and a third of them for
+// each of three warps to a quarter of the lanes (two of 224: two blocks of A, two warps;
+// with the shorter waits that came with it 465 us, now 408, for the gate/up below).
+// 4096 tokens, top 8 of 64 experts, 2 x 1024 x 2048: 408 us, 337 T code products/s (twice
+// as many e4m3 ones); 2 x 1536 x 5120 with its down product: 1234 + 714 us, 397 T/s.
 //
-// Warps: 0-3 decode weights, 4 issues MMAs, 5 copies activation rows (TMA),
-// 6 packed weights (TMA), 7 activation scales, 8-15 fold (a quarter of the lanes and half of the columns
-// each).  The fold's 112 accumulators per thread need more than an even share of
-// the registers, so the roles resize theirs.
+// Pairs of CTAs take neighbouring row tiles of the same columns: each copies one part (h or
+// l) of the activations to both, half of what L2 would have to deliver.
+//
+// Warps: 0-3 decode weights, 4 issues MMAs, 5 copies activation rows (TMA), 6 packed
+// weights (TMA), 7 activation scales, 8-19 fold (a quarter of the lanes and a third of the
+// columns each).  The fold needs more than an even share of the registers, so the roles
+// resize theirs.
 #include <cuda_runtime.h>
 
 #include "tq_device.cuh"
@@ -36,11 +44,11 @@ namespace {
 
 constexpr int kCols = 192;                          // most activation rows per tile
 constexpr int kCluster = 2;                         // CTAs that share activation rows: each brings one part
-constexpr int kStages = 3;
+constexpr int kStages = 3;                          // blocks of activations in shared memory
 constexpr int kBoxRows = 32;                        // rows per TMA copy
-constexpr int kDone = 4;
+constexpr int kDone = 4;                            // blocks between a barrier's uses
 constexpr int kGroup = 4;                           // blocks whose scales come together
-constexpr int kGroups = 4;
+constexpr int kGroups = 4;                          // groups of scales in shared memory
 constexpr int kCodeGroups = 2;                      // groups of packed codes in shared memory
 constexpr int kFoldWarps = 12;
 constexpr int kThreads = 256 + 32 * kFoldWarps;
@@ -61,7 +69,8 @@ struct __align__(1024) TileSmem {
     int offsets[TQ_MOE_MAX_EXPERTS + 1];            // clamped to 0 .. slots
     int tiles[TQ_MOE_MAX_EXPERTS + 1];              // column tiles of the experts before
     int warp_sum[kThreads / 32];
-    uint64_t b_full[kStages], b_empty[kStages], a_full[kABufs], d_empty[2], done[kDone], c_full[kCodeGroups], c_empty[kCodeGroups], s_full[kGroups], s_empty[kGroups], drain;
+    uint64_t b_full[kStages], b_empty[kStages], a_full[kABufs], d_empty[2], done[kDone];
+    uint64_t c_full[kCodeGroups], c_empty[kCodeGroups], s_full[kGroups], s_empty[kGroups], drain;
     uint32_t tmem;
     uint32_t dead;                                  // a bounded wait ran out
 };

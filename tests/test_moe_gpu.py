@@ -238,7 +238,8 @@ def test_plan_with_no_expert_at_all(tq):
 
 # rows per expert: none, one, around the 8-row and 16-row chunks, and on both sides of
 # the tile kernel's first row and of its one, two and three tiles
-COUNTS = [[1], [0, 0, 3], [8, 0, 1, 9], [7, 17, 0, 2, 33], [0, 130, 5], [64, 225, 65, 0, 449, 224]]
+COUNTS = [[1], [0, 0, 3], [8, 0, 1, 9], [7, 17, 0, 2, 33], [0, 130, 5], [64, 225, 65, 0, 449, 224],
+          [48, 193, 49, 385], [32, 33, 192, 31], [0, 290, 5, 0]]
 SHAPES = [(1, 128), (96, 256), (130, 384), (256, 1152), (100, 5120)]
 
 
