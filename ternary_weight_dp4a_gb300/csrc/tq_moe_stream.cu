@@ -25,8 +25,8 @@
 // 512 weights share a scheduler at 10.5 cycles (8.0 for the matrix instruction by
 // itself), what prepares and folds them comes on top: 267 (1-bit) and 313 (2-bit)
 // cycles per warp for 32 weight rows and a block of 128.  Memory would take a quarter to
-// a half of that: 8 tokens, top 4 of 32 experts, 5120 x 1536 take 23.4 us, 21.1 with all
-// weights in L2, 6.4 for the bytes.  16 rows at a time (two matrix instructions for a
+// a half of that: 8 tokens, top 4 of 32 experts, 5120 x 1536 take 22.4 us, two less with
+// all weights in L2, 6.4 for the bytes.  16 rows at a time (two matrix instructions for a
 // masked pair) gain 5% where experts have many rows and lose 22% where they have few.
 //
 // (fp8 operands would need fewer decode operations, but mma.sync on fp8 is
@@ -216,21 +216,56 @@ __device__ __forceinline__ int list_chunks(const MoeProduct &p, int chunk, int l
     return chunks[p.experts];
 }
 
+// a / b for 0 <= a; in 32 bits where they hold it (64 take some 400 cycles).
+__device__ __forceinline__ int64_t quotient(int64_t a, unsigned b) {
+    return a <= 0xffffffffll ? static_cast<int64_t>(static_cast<uint32_t>(a) / b) : a / b;
+}
+
+// This CTA's share of `all` items: first .. end - 1.
+__device__ __forceinline__ void share(int64_t all, int64_t &first, int64_t &end) {
+    const int64_t each = quotient(all, gridDim.x), more = all - each * gridDim.x;
+    first = each * blockIdx.x + min(static_cast<int64_t>(blockIdx.x), more);
+    end = first + each + (blockIdx.x < more ? 1 : 0);
+}
+
+// The expert of a chunk: chunks[expert] <= chunk < chunks[expert + 1] (a whole warp, every
+// lane with the same chunk): its 32 lanes look at every 32nd entry, then at the 32 behind it.
+__device__ __forceinline__ int find_expert(const int *chunks, int experts, int chunk) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    if (experts > 32) lo = 32 * (__popc(__ballot_sync(kFull, 32 * lane < experts && chunks[min(32 * lane, experts)] <= chunk)) - 1);
+    return lo + __popc(__ballot_sync(kFull, lo + lane < experts && chunks[min(lo + lane, experts)] <= chunk)) - 1;
+}
+
 // A column's scale in its block's row of `meta`; the start value is two further.
 __device__ __forceinline__ int meta_column(int c) { return 4 * (c >> 1) + (c & 1); }
 
-// Lay the codes of `rows` activation rows out in shared memory (all threads).
+// 32 codes of activation row `a`, its c-th group; a block's first has its scale, too.
+struct RowPart { uint4 q0, q1; float s; };
+
+__device__ __forceinline__ int activation_row(const MoeProduct &p, int slot) {
+    return min(max(p.rows != nullptr ? p.rows[slot] : slot, 0), p.m - 1);
+}
+__device__ __forceinline__ RowPart load_part(const MoeProduct &p, int a, int c) {
+    RowPart v;
+    const uint4 *qp = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(a) * p.k + c * 32);
+    v.q0 = __ldg(qp);
+    v.q1 = __ldg(qp + 1);
+    v.s = (c & 3) == 0 ? __ldg(p.s + static_cast<int64_t>(a) * (p.k / kBlock) + (c >> 2)) : 0.0f;
+    return v;
+}
+
+// Lay the codes of `rows` activation rows out in shared memory (all threads).  part: what
+// thread tid < 4 rows nb loads first, group tid % (4 nb) of row tid / (4 nb).
 template <int FMT>
-__device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int rows, uint8_t *act, float *meta) {
+__device__ __forceinline__ void stage_rows(const MoeProduct &p, int row0, int rows, RowPart part, uint8_t *act, float *meta) {
     const int tid = threadIdx.x, nb = p.k / kBlock, pitch = row_pitch(nb), per = nb * 4;
 #pragma unroll 2
     for (int i = tid; i < rows * per; i += blockDim.x) {
         const int r = i / per, c = i - r * per;                      // c: group of 32 codes
-        int a = p.rows != nullptr ? p.rows[row0 + r] : row0 + r;
-        a = min(max(a, 0), p.m - 1);
-        const uint4 *qp = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(a) * p.k + c * 32);
-        const uint4 q0 = __ldg(qp), q1 = __ldg(qp + 1);
-        const float sa = (c & 3) == 0 ? __ldg(p.s + static_cast<int64_t>(a) * nb + (c >> 2)) : 0.0f;
+        if (i != tid) part = load_part(p, activation_row(p, row0 + r), c);
+        const uint4 q0 = part.q0, q1 = part.q1;
+        const float sa = part.s;
         // minus the sums over q * s and over the offset of v
         const uint32_t raw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
         int sum = 0, scaled = 0;
@@ -364,25 +399,25 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
     pdl_wait();
     const int units = (p.n + kUnitRows - 1) / kUnitRows;
     const int64_t all = static_cast<int64_t>(list_chunks(p, args.chunk, args.limit, offsets, chunks)) * units;
-    const int64_t first = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x;
+    int64_t first, end;
+    share(all, first, end);
     if (first >= end) return;
     const bool wide = nb % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales[0]) & 7) == 0 &&
                       (!GATEUP || (reinterpret_cast<uintptr_t>(p.scales[1]) & 7) == 0);
-    const auto find = [&](int chunk) {                               // its expert
-        int lo = 0, hi = p.experts;                                  // chunks[lo] <= chunk < chunks[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (chunks[mid] <= chunk) lo = mid;
-            else hi = mid;
-        }
-        return lo;
-    };
     // this warp's units: warp, warp + warps, .. of the `mine` in the CTA's share
     const int mine = static_cast<int>(end - first);
-    const int first_chunk = static_cast<int>(first / units), first_u = static_cast<int>(first % units);
+    const int first_chunk = static_cast<int>(quotient(first, units));
+    const int first_u = static_cast<int>(first - static_cast<int64_t>(first_chunk) * units);
+    int expert = find_expert(chunks, p.experts, first_chunk);
+    int row0 = offsets[expert] + (first_chunk - chunks[expert]) * args.chunk;
+    int rows = min(args.chunk, offsets[expert + 1] - row0);
+    // what is staged first is on its way while the first weights are asked for
+    const int part_r = threadIdx.x / (4 * nb), part_c = threadIdx.x - part_r * 4 * nb;
+    const bool has_part = part_r < rows;
+    const int part_a = has_part ? activation_row(p, row0 + part_r) : 0;
 
     // the issuing side; lane l brings the scales of row l of the unit (gate 0-15, up 16-31)
-    int in_unit = warp, in_u = first_u + warp, in_chunk = first_chunk, in_block = 0, in_slot = 0, in_expert = -1, in_y = 0;
+    int in_unit = warp, in_u = first_u + warp, in_chunk = first_chunk, in_block = 0, in_slot = 0, in_expert = expert, in_y = 0;
     const uint16_t *scale_src = nullptr;
     const auto issue = [&]() {
         if (in_unit < mine) {
@@ -392,7 +427,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
                     ++in_chunk;
                     in_expert = -1;
                 }
-                if (in_expert < 0) in_expert = find(in_chunk);
+                if (in_expert < 0) in_expert = find_expert(chunks, p.experts, in_chunk);
                 in_y = in_expert * p.n + in_u * kUnitRows;
                 const int n = min(in_u * kUnitRows + (GATEUP ? lane & 15 : lane), p.n - 1);
                 scale_src = p.scales[GATEUP ? lane >> 4 : 0] + (static_cast<int64_t>(in_expert) * p.n + n) * nb;
@@ -421,18 +456,24 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     __syncwarp();
+    issue();
+    RowPart part{};
+    if (has_part) part = load_part(p, part_a, part_c);
 #pragma unroll 1
-    for (int i = 0; i < kD; ++i) issue();
+    for (int i = 1; i < kD; ++i) issue();
 
     const Joins<FMT> join = joins<FMT>();
     int slot = 0, unit = warp, u = first_u + warp;
     uint32_t phase = 0;
     for (int chunk = first_chunk, chunk_end = units - first_u;; ++chunk, u -= units, chunk_end += units) {
-        const int expert = find(chunk);
-        const int row0 = offsets[expert] + (chunk - chunks[expert]) * args.chunk;
-        const int rows = min(args.chunk, offsets[expert + 1] - row0);
-        if (chunk > first_chunk) __syncthreads();                    // every warp is done with the chunk before
-        stage_rows<FMT>(p, row0, rows, act, meta);
+        if (chunk > first_chunk) {
+            expert = find_expert(chunks, p.experts, chunk);
+            row0 = offsets[expert] + (chunk - chunks[expert]) * args.chunk;
+            rows = min(args.chunk, offsets[expert + 1] - row0);
+            if (part_r < rows) part = load_part(p, activation_row(p, row0 + part_r), part_c);
+            __syncthreads();                                         // every warp is done with the chunk before
+        }
+        stage_rows<FMT>(p, row0, rows, part, act, meta);
         __syncthreads();
         // a column without a row computes the last row's products again; they go nowhere
         const uint32_t piece = g * kStageBlocks * kBlockBytes +
@@ -524,7 +565,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
 // memory, where one thread per output folds them in order.  The codes of the
 // next round are on their way while a round is folded.
 // ---------------------------------------------------------------------------
-// Up to this many units per SM: 3.4 (one token, top 8 of 64 experts, 2 x 1024 x 2048) take 8.0 us split and
+// Up to this many units per SM: 3.4 (one token, top 8 of 64 experts, 2 x 1024 x 2048) take 7.6 us split and
 // 12.7 whole; 27 (33 tokens, 1-bit) 44 and 29; 34 (8 tokens, 5120 x 1536) 31 and 23.
 constexpr int kSplitMost = 8;
 constexpr int kSplit = 4, kSplitUnits = kSplitWarps / kSplit;
@@ -557,23 +598,18 @@ __global__ void __launch_bounds__(32 * kSplitWarps, 2) split_kernel(const __grid
     uint16_t *wsc = reinterpret_cast<uint16_t *>(dots + 2 * kSplitUnits * unit_dots);
     const int units = (p.n + kUnitRows - 1) / kUnitRows, per_chunk = (units + kSplitUnits - 1) / kSplitUnits;
     const int64_t rounds = static_cast<int64_t>(list_chunks(p, args.chunk, args.limit, offsets, chunks)) * per_chunk;
-    const int64_t first = rounds * blockIdx.x / gridDim.x, end = rounds * (blockIdx.x + 1) / gridDim.x;
+    int64_t first, end;
+    share(rounds, first, end);
     const Joins<FMT> join = joins<FMT>();
 
     struct Place { int chunk, expert, row0, rows, n0; };            // n0: first output of the round
     const auto locate = [&](int64_t r) {
         Place q;
-        q.chunk = static_cast<int>(r / per_chunk);
-        q.n0 = static_cast<int>(r % per_chunk) * kSplitUnits * kUnitRows;
-        int a = 0, b = p.experts;
-        while (b - a > 1) {
-            const int mid = (a + b) >> 1;
-            if (chunks[mid] <= q.chunk) a = mid;
-            else b = mid;
-        }
-        q.expert = a;
-        q.row0 = offsets[a] + (q.chunk - chunks[a]) * args.chunk;
-        q.rows = min(args.chunk, offsets[a + 1] - q.row0);
+        q.chunk = static_cast<int>(quotient(r, per_chunk));
+        q.n0 = static_cast<int>(r - static_cast<int64_t>(q.chunk) * per_chunk) * kSplitUnits * kUnitRows;
+        q.expert = find_expert(chunks, p.experts, q.chunk);
+        q.row0 = offsets[q.expert] + (q.chunk - chunks[q.expert]) * args.chunk;
+        q.rows = min(args.chunk, offsets[q.expert + 1] - q.row0);
         return q;
     };
     const uint8_t *src[2][2];
@@ -599,7 +635,10 @@ __global__ void __launch_bounds__(32 * kSplitWarps, 2) split_kernel(const __grid
         }
         if (at.chunk != staged) {
             if (staged >= 0) __syncthreads();                       // the fold before reads what is staged now
-            stage_rows<FMT>(p, at.row0, at.rows, act, meta);
+            const int part_r = tid / (4 * nb);
+            RowPart part{};
+            if (part_r < at.rows) part = load_part(p, activation_row(p, at.row0 + part_r), tid - part_r * 4 * nb);
+            stage_rows<FMT>(p, at.row0, at.rows, part, act, meta);
             __syncthreads();
             staged = at.chunk;
         }
