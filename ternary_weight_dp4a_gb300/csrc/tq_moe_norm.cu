@@ -5,6 +5,7 @@
 
 #include "tq_device.cuh"
 #include "tq_launch.h"
+#include "tq_moe_codes.cuh"
 #include "tq_moe_internal.h"
 
 namespace tq {
@@ -71,26 +72,61 @@ __device__ __forceinline__ void round_store_bf16(float (&v)[16], uint16_t *out) 
     }
 }
 
+// Sum of the squares of a lane's 16 values as a pair, in four operations each: with
+// t = fma(x, x, hi), t - hi is exact as long as hi >= x^2, and fma(x, x, -(t - hi)) is what the
+// rounding of t lost (the product's own low half with it).  So the sum starts from the largest
+// square, which is taken off again.
+__device__ __forceinline__ void pair_squares(const float (&v)[16], float &hi, float &lo) {
+    float top = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, fabsf(v[i]));
+    const float base = __fmul_rn(top, top), base_lo = __fmaf_rn(top, top, -base);
+    hi = base;
+    lo = base_lo;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float t = __fmaf_rn(v[i], v[i], hi);
+        lo = __fadd_rn(lo, __fmaf_rn(v[i], v[i], __fsub_rn(hi, t)));
+        hi = t;
+    }
+    pair_add(hi, lo, -base, -base_lo);
+}
+
 // tq_rotate_quant's transform of the warp's four blocks, stage by stage in its order.
+// Elements i and i + 8 are the halves of one packed operation.
 __device__ __forceinline__ void wht128_x16(float (&v)[16], int lane) {
+    uint64_t w[8];
+    const uint64_t minus = pack2(-1.0f, -1.0f);                  // a - b is fma(b, -1, a)
 #pragma unroll
-    for (int h = 1; h < 16; h <<= 1)
+    for (int i = 0; i < 8; ++i) w[i] = pack2(v[i], v[i + 8]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
             if (!(i & h)) {
-                const float a = v[i], b = v[i + h];
-                v[i] = __fadd_rn(a, b);
-                v[i + h] = __fsub_rn(a, b);
+                const uint64_t a = w[i], b = w[i + h];
+                w[i] = add2(a, b);
+                w[i + h] = fma2(b, minus, a);
             }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float a, b;
+        unpack2(w[i], a, b);
+        v[i] = __fadd_rn(a, b);
+        v[i + 8] = __fsub_rn(a, b);
+    }
 #pragma unroll
     for (int h = 1; h < 8; h <<= 1) {
         const float sign = (lane & h) ? -1.0f : 1.0f;            // upper: other - mine; lower: other + mine
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __fmaf_rn(v[i], sign, __shfl_xor_sync(kFull, v[i], h));
+        for (int i = 0; i < 8; ++i)
+            unpack2(fma2(pack2(v[i], v[i + 8]), pack2(sign, sign),
+                         pack2(__shfl_xor_sync(kFull, v[i], h), __shfl_xor_sync(kFull, v[i + 8], h))),
+                    v[i], v[i + 8]);
     }
     const float c128 = __uint_as_float(0x3db504f3u);             // (float)(1/sqrt(128))
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], c128);
+    for (int i = 0; i < 8; ++i) unpack2(mul2(pack2(v[i], v[i + 8]), pack2(c128, c128)), v[i], v[i + 8]);
 }
 
 // Quantise as tq_rotate_quant: s = max|v| / 127 and round-half-even(v / s), both IEEE
@@ -145,11 +181,13 @@ __device__ __forceinline__ float inv_rms(float hi, float lo, float n, float eps)
 // ---------------------------------------------------------------------------
 // Residual addition, RMS norm, rotation, quantisation: one CTA per row; a warp's
 // sums t stay in registers between the two passes (sum of squares; normalise,
-// rotate, quantise), so the row is read once.  Bound by memory and instructions alike:
-// 8192 x 5120 bf16 with gamma 83 us, 3.5 TB/s (the bytes alone: 43 us); one row 3.5 us, launch to launch.
+// rotate, quantise), so the row is read once.  Bound by latency (the barrier between
+// the passes) and instructions before memory: 8192 x 5120 bf16 with gamma 71 us, 4.1 TB/s (the
+// bytes alone: 43 us); one row 3.5 us, launch to launch.  48 registers let four CTAs of this width
+// share an SM: 79 us with the 49 that the compiler takes by itself, 72 with 32.
 // ---------------------------------------------------------------------------
 template <bool RB, bool DB, int G>
-__global__ void __launch_bounds__(1024) add_rmsnorm_rotq_kernel(const void *res, const void *delta,
+__global__ void __maxnreg__(G == 1 ? 48 : 64) add_rmsnorm_rotq_kernel(const void *res, const void *delta,
                                                                 const uint16_t *__restrict__ gamma, int n, float eps,
                                                                 void *res_out, uint16_t *__restrict__ x_out,
                                                                 int8_t *__restrict__ q, float *__restrict__ s) {
@@ -183,10 +221,13 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_rotq_kernel(const void *res,
                 for (int i = 0; i < 4; ++i)
                     out[i] = make_float4(t[j][4 * i], t[j][4 * i + 1], t[j][4 * i + 2], t[j][4 * i + 3]);
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float p = __fmul_rn(t[j][i], t[j][i]);
-                pair_add(hi, lo, p, RB ? 0.0f : __fmaf_rn(t[j][i], t[j][i], -p));   // a bf16's square is exact
+            float sum, sum_lo;
+            pair_squares(t[j], sum, sum_lo);
+            if (j == 0) {
+                hi = sum;
+                lo = sum_lo;
+            } else {
+                pair_add(hi, lo, sum, sum_lo);
             }
         }
     }
@@ -200,8 +241,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_rotq_kernel(const void *res,
         const float2 w = lane < warps ? warp_sum[lane] : make_float2(0.0f, 0.0f);
         hi = w.x;
         lo = w.y;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = warps > 16 ? 16 : warps > 8 ? 8 : 4; o > 0; o >>= 1)
             pair_add(hi, lo, __shfl_xor_sync(kFull, hi, o), __shfl_xor_sync(kFull, lo, o));
         hi = __shfl_sync(kFull, hi, 0);                          // lanes may differ in lo's last bit
         lo = __shfl_sync(kFull, lo, 0);
