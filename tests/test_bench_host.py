@@ -65,6 +65,21 @@ def test_source_hash_leaves_out_host_only_sources(monkeypatch, tmp_path):
     assert bench.source_hash() != h0                 # kernel file: new hash
 
 
+def test_source_hash_leaves_out_the_experts_sources(monkeypatch, tmp_path):
+    """The expert layer's files are no part of the step kernel, and none of its files includes one."""
+    real = os.path.join(bench.ROOT, "ternary_weight_dp4a_gb300", "csrc")
+    for name in os.listdir(real):
+        if name.endswith((".cu", ".cuh", ".h")) and not name.startswith(bench.OTHER_KERNELS_PREFIX):
+            assert f'#include "{bench.OTHER_KERNELS_PREFIX}' not in open(os.path.join(real, name)).read(), name
+    csrc = tmp_path / "ternary_weight_dp4a_gb300" / "csrc"
+    csrc.mkdir(parents=True)
+    (csrc / "k.cu").write_text("kernel")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    h0 = bench.source_hash()
+    (csrc / "tq_moe_other.cu").write_text("another layer's kernel")
+    assert bench.source_hash() == h0
+
+
 def test_reference_arm_runs_the_requested_steps(monkeypatch):
     """The reference arm times exactly --warmup untimed and --steps timed
     oracle steps: whole layer steps when they fit the budget, else the same
