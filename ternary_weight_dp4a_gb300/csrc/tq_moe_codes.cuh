@@ -32,7 +32,8 @@ __device__ __forceinline__ void stage_order(const uint32_t (&w)[8], uint32_t (&o
     }
 }
 
-// Four int8 codes -> the e4m3 numbers 16 H and L themselves, |q| = 16 H + L.
+// Four int8 codes -> the e4m3 numbers 16 H and L themselves, |q| = 16 H + L, H in 0 .. 8, L in
+// 0 .. 15, both with q's sign.
 __device__ __forceinline__ void split4_whole(uint32_t w, uint32_t &hi, uint32_t &lo) {
     const uint32_t sign = w & 0x80808080u;
     const uint32_t mask = prmt(w, w, 0xba98u);
@@ -40,7 +41,8 @@ __device__ __forceinline__ void split4_whole(uint32_t w, uint32_t &hi, uint32_t 
     uint32_t sel = (a >> 4) & 0x07070707u;
     sel = (sel | (sel >> 4)) & 0x00ff00ffu;
     sel = sel | (sel >> 8);
-    hi = prmt(0x64605800u, 0x6e6c6a68u, sel) | sign;            // 0, 16, 32, 48 | 64, 80, 96, 112
+    const uint32_t full = a & 0x80808080u;                      // -128: 0x70 is 128 (0x80 - 0x10)
+    hi = prmt(0x64605800u, 0x6e6c6a68u, sel) | (full - (full >> 3)) | sign;  // 0, 16, 32, 48 | 64, 80, 96, 112
     uint32_t low = a & 0x07070707u;
     low = (low | (low >> 4)) & 0x00ff00ffu;
     low = low | (low >> 8);
