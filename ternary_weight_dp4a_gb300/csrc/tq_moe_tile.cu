@@ -20,11 +20,8 @@
 // Two accumulators of 192 columns leave room for four blocks of A, and a third of them for
 // each of three warps to a quarter of the lanes (two of 224: two blocks of A, two warps;
 // with the shorter waits that came with it 465 us, now 408, for the gate/up below).
-// 4096 tokens, top 8 of 64 experts, 2 x 1024 x 2048: 408 us, 337 T code products/s (twice
-// as many e4m3 ones); 2 x 1536 x 5120 with its down product: 1234 + 714 us, 397 T/s.
-//
-// Pairs of CTAs take neighbouring row tiles of the same columns: each copies one part (h or
-// l) of the activations to both, half of what L2 would have to deliver.
+// 4096 tokens, top 8 of 64 experts, 2 x 1024 x 2048: 413 us, 333 T code products/s (twice
+// as many e4m3 ones).
 //
 // Warps: 0-3 decode weights, 4 issues MMAs, 5 copies activation rows (TMA), 6 packed
 // weights (TMA), 7 activation scales, 8-19 fold (a quarter of the lanes and a third of the
@@ -43,7 +40,6 @@ namespace tq {
 namespace {
 
 constexpr int kCols = 192;                          // most activation rows per tile
-constexpr int kCluster = 2;                         // CTAs that share activation rows: each brings one part
 constexpr int kStages = 3;                          // blocks of activations in shared memory
 constexpr int kBoxRows = 32;                        // rows per TMA copy
 constexpr int kDone = 4;                            // blocks between a barrier's uses
@@ -145,31 +141,7 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
     return d;
 }
 
-// kBoxRows rows of 128 bytes at (byte x, row y) of the operand, to the same place in both
-// CTAs of the cluster; counted on each one's `bar`.
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-        "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>((1u << kCluster) - 1))
-        : "memory");
-}
-// tc_commit to the barrier at this address in every CTA of the cluster.
-__device__ __forceinline__ void tc_commit_cluster(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"(static_cast<uint16_t>((1u << kCluster) - 1))
-                 : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// A box of packed weights at (byte x, row y), for this CTA alone.
+// The box of `map` at (byte x, row y); counted on `bar`.
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -260,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sm.b_full[i]), 1);
-            mbar_init(smem_u32(&sm.b_empty[i]), kCluster);
+            mbar_init(smem_u32(&sm.b_empty[i]), 1);
         }
         for (int i = 0; i < kABufs; ++i) mbar_init(smem_u32(&sm.a_full[i]), 4);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sm.d_empty[i]), kFoldWarps);
@@ -279,7 +251,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();                                 // the other CTA's barriers are ready, too
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     pdl_launch_dependents();
@@ -288,10 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 
     const int nb = p.k / kBlock;
     constexpr int kRowsPerTile = GATEUP ? 64 : 128;
-    // the CTAs of a cluster take neighbouring row tiles of one column tile
-    const int nparts = (p.n + kCluster * kRowsPerTile - 1) / (kCluster * kRowsPerTile);
-    const int rank = static_cast<int>(cluster_rank());
-    const int first_item = blockIdx.x / kCluster, item_step = gridDim.x / kCluster;
+    // neighbouring CTAs take neighbouring row tiles of one column tile: its activation rows meet in L2
+    const int nparts = (p.n + kRowsPerTile - 1) / kRowsPerTile;
+    const int first_item = blockIdx.x, item_step = gridDim.x;
     constexpr int kBlockBytes = FMT == 0 ? 32 : 16;
     int it = 0;                                     // blocks since the start, over all tiles
     int expert, row0, cols;
@@ -310,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         const bool wide = nb % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales[0]) & 7) == 0 &&
                           (!GATEUP || (reinterpret_cast<uintptr_t>(p.scales[1]) & 7) == 0);
         for (int item = first_item; find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
-            const int n0 = ((item % nparts) * kCluster + rank) * kRowsPerTile;
+            const int n0 = item % nparts * kRowsPerTile;
             const int r = min(n0 + tile_row, p.n - 1);
             const uint16_t *wsp = p.scales[GATEUP ? (lane >> 3) & 1 : 0] + (static_cast<int64_t>(expert) * p.n + r) * nb;
             for (int b0 = 0; b0 < nb; b0 += kGroup, ++group) {
@@ -386,9 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         tc_mma_e4m3_ts(d, a + 8 * i, hi + 2 * i, idesc, i > 0);
                         tc_mma_e4m3_ts(d, a + 8 * i, lo + 2 * i, idesc, 1);
                     }
-                    // frees the stage in both CTAs; frees the A buffer and hands over the accumulator
-                    // (who waits, waits for the block that it needs; none is ever six blocks behind)
-                    tc_commit_cluster(smem_u32(&sm.b_empty[st]));
+                    // frees the stage; frees the A buffer and hands over the accumulator (who waits,
+                    // waits for the block that it needs: the fold for one of the last two, the decode
+                    // for the one before kDone more, so a barrier is never a whole turn ahead of a waiter)
+                    tc_commit(smem_u32(&sm.b_empty[st]));
                     tc_commit(smem_u32(&sm.done[it % kDone]));
                 }
                 __syncwarp();
@@ -401,9 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp < 8) {
-        // ---- copy: warp 5 brings one part of the activation rows' codes (each CTA of the
-        // cluster another), 32 rows per copy, for both CTAs; warp 6 the packed weights,
-        // warp 7 the activation scales ----
+        // ---- copy: warp 5 brings both parts of the activation rows' codes, 32 rows per copy;
+        // warp 6 the packed weights, warp 7 the activation scales ----
         if (warp == 5) {
             bool ok = true;
             for (int item = first_item; ok && find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
@@ -415,9 +385,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     const uint32_t bar = smem_u32(&sm.b_full[st]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes) * 2 * kBoxRows * 128);
                     __syncwarp();
-                    if (lane < boxes)
-                        copy_box(smem_u32(sm.b[st]) + rank * kHalf + lane * kBoxRows * 128, &args.map, b * 256 + rank * 128,
-                                 row0 + lane * kBoxRows, bar);
+                    if (lane < 2 * boxes) {
+                        const int part = lane & 1, box = lane >> 1;
+                        load_box(smem_u32(sm.b[st]) + part * kHalf + box * kBoxRows * 128, &args.map, b * 256 + part * 128,
+                                 row0 + box * kBoxRows, bar);
+                    }
                 }
             }
             // none of this CTA's copies may be in flight when it leaves
@@ -427,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             // packed weights: two boxes of 64 rows, gate and up or one matrix's 128
             bool ok = true;
             for (int item = first_item; ok && find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
-                const int y = expert * p.n + ((item % nparts) * kCluster + rank) * kRowsPerTile;
+                const int y = expert * p.n + item % nparts * kRowsPerTile;
                 for (int b = 0; b < nb; b += kGroup, ++it) {
                     const int slot = it % kCodeGroups;
                     ok = warp_wait_alive<64>(sm, smem_u32(&sm.c_empty[slot]), ((it / kCodeGroups) & 1) ^ 1, args.err, 1u << 10);
@@ -484,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         int group = 0;                              // groups of scales since the start
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * kFoldCols;
         for (int item = first_item; find_tile(sm, p.experts, item / nparts, expert, row0, cols); item += item_step) {
-            const int n0 = ((item % nparts) * kCluster + rank) * kRowsPerTile;
+            const int n0 = item % nparts * kRowsPerTile;
             const int mine = min(max(cols - part * kFoldCols, 0), kFoldCols);   // columns of this warp
             uint64_t acc[kFoldCols / 4][2];         // [column t + 4 n][h]
 #pragma unroll
@@ -565,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();                                 // the other CTA's copies and commits reach into this one
+    __syncthreads();
     tc_fence_after();
     if (warp == 4) tmem_dealloc(tmem, 512);
 }
@@ -638,25 +610,7 @@ cudaError_t launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *e
                          FMT == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms / kCluster * kCluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {kCluster, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    // every cluster is resident from the start: the tiles are dealt out by cluster index
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, tile_kernel<FMT, GATEUP>, &cfg);
-    if (e != cudaSuccess) return e;
-    if (clusters < 1) return cudaErrorInvalidConfiguration;
-    if (clusters < sms / kCluster) cfg.gridDim = dim3(static_cast<unsigned>(clusters * kCluster));
-    return cudaLaunchKernelEx(&cfg, tile_kernel<FMT, GATEUP>, a);
+    return launch_pdl(tile_kernel<FMT, GATEUP>, dim3(static_cast<unsigned>(sms)), dim3(kThreads), smem, stream, a);
 }
 
 }  // namespace
