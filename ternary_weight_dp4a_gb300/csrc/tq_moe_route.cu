@@ -159,6 +159,10 @@ __global__ void __launch_bounds__(1024) scan_kernel(int *__restrict__ hist, int 
 }
 
 // shared memory: warp counts [32][experts] (16 bits), base [experts + 1], scan [32]
+constexpr size_t place_smem(int experts) {
+    return (experts + 1 + 32) * sizeof(int) + static_cast<size_t>(32) * experts * sizeof(uint16_t);
+}
+
 __global__ void __launch_bounds__(kPlanChunk) place_kernel(const int *__restrict__ ids, int64_t slots, int experts,
                                                            int topk, const int *__restrict__ hist,
                                                            int *__restrict__ offsets, int *__restrict__ rows,
@@ -268,11 +272,9 @@ cudaError_t moe_plan_launch(const int *ids, int m, int topk, int experts, int *o
                        experts);
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = (experts + 1 + 32) * sizeof(int) + static_cast<size_t>(32) * experts * sizeof(uint16_t);
-    if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(place_kernel, dim3(chunks), dim3(kPlanChunk), smem, stream, ids, slots, experts, topk,
+    static SmemLimit limit;
+    if ((e = limit.raise(place_kernel, place_smem(TQ_MOE_MAX_EXPERTS))) != cudaSuccess) return e;
+    return launch_pdl(place_kernel, dim3(chunks), dim3(kPlanChunk), place_smem(experts), stream, ids, slots, experts, topk,
                       chunks > 1 ? static_cast<const int *>(hist) : nullptr, offsets, rows, pos);
 }
 

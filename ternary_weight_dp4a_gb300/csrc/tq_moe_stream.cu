@@ -703,7 +703,8 @@ cudaError_t launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t s
     if (e != cudaSuccess) return e;
     constexpr int64_t kUnitRows = GATEUP ? 16 : 32;
     const int64_t units = ws_cdiv(p.n, kUnitRows);
-    constexpr size_t kSmem = 227 * 1024;
+    constexpr size_t kSmem = 227 * 1024, kSplitSmem = kSmem / 2 - 1024;
+    static SmemLimit limits[2];
     // the chunks that an even routing of few slots gives, and with them the units
     const int64_t active = p.experts < p.slots ? p.experts : p.slots;
     int chunk = p.max_rows < kCols ? p.max_rows : kCols;
@@ -714,10 +715,10 @@ cudaError_t launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t s
         const int64_t cap = static_cast<int64_t>(p.experts) * ws_cdiv(limit, c);
         return most > cap ? cap : most;
     };
-    if (active * units <= kSplitMost * sms && split_smem(p.experts, chunk, nb) <= kSmem / 2 - 1024) {
+    if (active * units <= kSplitMost * sms && split_smem(p.experts, chunk, nb) <= kSplitSmem) {
         const size_t smem = split_smem(p.experts, chunk, nb);
         a.chunk = chunk;
-        e = cudaFuncSetAttribute(split_kernel<FMT, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        e = limits[0].raise(split_kernel<FMT, GATEUP>, kSplitSmem);
         if (e != cudaSuccess) return e;
         int64_t grid = most_chunks(chunk) * ws_cdiv(units, kSplitUnits);
         if (grid > 2 * sms) grid = 2 * sms;
@@ -740,7 +741,7 @@ cudaError_t launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t s
                          FMT == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
         if (e != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(stream_kernel<FMT, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = limits[1].raise(stream_kernel<FMT, GATEUP>, kSmem);
     if (e != cudaSuccess) return e;
     int per_sm = static_cast<int>((kSmem + 1024) / (smem + 1024));
     if (per_sm > kMaxWarps / warps) per_sm = kMaxWarps / warps;

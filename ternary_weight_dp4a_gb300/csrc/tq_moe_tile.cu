@@ -592,7 +592,8 @@ cudaError_t launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *e
                    stream, p.q, p.rows, p.offsets, p.experts, p.m, p.slots, p.k, operand, p.s, scales);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = sizeof(TileSmem) + 1024;
-    e = cudaFuncSetAttribute(tile_kernel<FMT, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static SmemLimit limit;
+    e = limit.raise(tile_kernel<FMT, GATEUP>, smem);
     if (e != cudaSuccess) return e;
     TileArgs a{};
     a.p = p;
