@@ -1,6 +1,7 @@
 """The mixture-of-experts products called from several host threads, each with its own stream,
 workspace and sizes."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -28,6 +29,54 @@ class Job:
         self.y = torch.empty((slots, n), device="cuda")
         self.want = tq.moe_gemv(self.w, self.q, self.s, self.plan, workspace=self.ws)
         torch.cuda.synchronize()
+
+    def call(self):
+        self.tq.moe_gemv(self.w, self.q, self.s, self.plan, y=self.y, workspace=self.ws, stream=self.stream)
+
+
+def _run(targets):
+    errors = []
+
+    def guarded(target):
+        try:
+            target()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=guarded, args=(t,)) for t in targets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+# (experts, n, k, rows per expert): the split, the stream and the tile kernel
+SPLIT, STREAM, TILE = (2, 64, 256, 1), (64, 1000, 256, 1), (2, 64, 256, 100)
+
+
+@pytest.mark.parametrize("size", [SPLIT, STREAM, TILE], ids=["split", "stream", "tile"])
+def test_the_first_cuda_call_of_a_thread(tq, size):  # noqa: F811
+    """A thread that has made no CUDA call before has no context yet."""
+    import torch
+    job = Job(tq, *size, seed=1)
+    _run([job.call])
+    torch.cuda.synchronize()
+    assert torch.equal(job.y, job.want)
+
+
+def test_the_first_cuda_call_of_a_thread_is_a_dense_product(tq):  # noqa: F811
+    import torch
+    from ternary_weight_dp4a_gb300 import synth
+    codes, scales = synth.weight(256, 256, 0, 1, device="cuda")
+    w = tq.pack_weights(codes, 0, scales)
+    q, s = tq.rotate_quant(torch.randn((2, 256), device="cuda").bfloat16())
+    ws, y, stream = tq.gemv_workspace(2, 256, 256), torch.empty((2, 256), device="cuda"), torch.cuda.Stream()
+    want = tq.gemv(w, q, s, workspace=ws)
+    torch.cuda.synchronize()
+    _run([lambda: tq.gemv(w, q, s, y=y, workspace=ws, stream=stream)])
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
 
 
 class _Product(ctypes.Structure):
