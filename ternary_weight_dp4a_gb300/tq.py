@@ -3,7 +3,8 @@
 Every function takes torch CUDA tensors (PyTorch provides device memory and
 streams), passes raw device pointers to the C ABI and raises ``TQError`` on a
 non-OK status.  Work is enqueued on the current torch CUDA stream unless a
-``stream`` is given.  There is no CPU path: if ``libtq.so`` has not been built
+``stream`` is given; outputs and workspaces that a call allocates belong to the
+stream that it runs on.  There is no CPU path: if ``libtq.so`` has not been built
 (``python -m ternary_weight_dp4a_gb300.build``), the first call raises.
 """
 from __future__ import annotations
@@ -183,6 +184,19 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(stream, make, *args, **kwargs):
+    """make(*args, **kwargs): a tensor that a call allocates for itself, on the stream that the call
+    runs on.  (Filled on the current stream it could be filled after the call's kernels have
+    written to it; allocated there, and released, it could be another tensor's while they run.)"""
+    import torch
+    if stream is None:
+        return make(*args, **kwargs)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return make(*args, **kwargs)
+
+
 def _ptr(t):
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
 
@@ -210,10 +224,10 @@ def pack_weights(codes, fmt: int, scales, stream=None) -> PackedWeight:
     import torch
     n, k = codes.shape
     per = 4 if fmt == FMT_TERNARY2 else 8
-    packed = torch.empty((n, k // per), dtype=torch.uint8, device=codes.device)
+    packed = _new(stream, torch.empty, (n, k // per), dtype=torch.uint8, device=codes.device)
     _check("tq_pack_weights", load().tq_pack_weights(_ptr(codes), n, k, fmt, _ptr(packed),
                                                       _stream(stream)))
-    return PackedWeight(packed, scales.contiguous(), n, k, fmt)
+    return PackedWeight(packed, _new(stream, scales.contiguous), n, k, fmt)
 
 
 def rotate_quant(x, q=None, s=None, stream=None):
@@ -221,9 +235,9 @@ def rotate_quant(x, q=None, s=None, stream=None):
     import torch
     m, k = x.shape
     if q is None:
-        q = torch.empty((m, k), dtype=torch.int8, device=x.device)
+        q = _new(stream, torch.empty, (m, k), dtype=torch.int8, device=x.device)
     if s is None:
-        s = torch.empty((m, k // BLOCK), dtype=torch.float32, device=x.device)
+        s = _new(stream, torch.empty, (m, k // BLOCK), dtype=torch.float32, device=x.device)
     _check("tq_rotate_quant", load().tq_rotate_quant(_ptr(x), m, k, _ptr(q), _ptr(s),
                                                       _stream(stream)))
     return q, s
@@ -263,11 +277,11 @@ def gemv(w: PackedWeight, q, s, y=None, blockdots: bool = False, workspace=None,
     import torch
     m = q.shape[0]
     if y is None:
-        y = torch.empty((m, w.n), dtype=torch.float32, device=q.device)
-    d = torch.empty((m, w.n, w.k // BLOCK), dtype=torch.int32, device=q.device) \
+        y = _new(stream, torch.empty, (m, w.n), dtype=torch.float32, device=q.device)
+    d = _new(stream, torch.empty, (m, w.n, w.k // BLOCK), dtype=torch.int32, device=q.device) \
         if blockdots else None
     if workspace is None:
-        workspace = gemv_workspace(m, w.n, w.k, q.device)
+        workspace = _new(stream, gemv_workspace, m, w.n, w.k, q.device)
     ws = w.c_struct()
     _check("tq_gemv", load().tq_gemv(ctypes.byref(ws), _ptr(q), _ptr(s), m, _ptr(y), _ptr(d),
                                      _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -279,9 +293,9 @@ def ffn_gateup(gate: PackedWeight, up: PackedWeight, qx, sx, h=None, workspace=N
     import torch
     m = qx.shape[0]
     if h is None:
-        h = torch.empty((m, gate.n), dtype=torch.bfloat16, device=qx.device)
+        h = _new(stream, torch.empty, (m, gate.n), dtype=torch.bfloat16, device=qx.device)
     if workspace is None:
-        workspace = ffn_workspace(m, gate.k, gate.n, qx.device)
+        workspace = _new(stream, ffn_workspace, m, gate.k, gate.n, qx.device)
     g, u = gate.c_struct(), up.c_struct()
     _check("tq_ffn_gateup", load().tq_ffn_gateup(ctypes.byref(g), ctypes.byref(u), _ptr(qx),
                                                  _ptr(sx), m, _ptr(h), _ptr(workspace),
@@ -336,9 +350,9 @@ def ffn_stack(layers, x, eps: float = 1e-6, y=None, workspace=None, stream=None)
     m, hidden = x.shape
     inter = layers[0][0].n
     if y is None:
-        y = torch.empty((m, hidden), dtype=torch.float32, device=x.device)
+        y = _new(stream, torch.empty, (m, hidden), dtype=torch.float32, device=x.device)
     if workspace is None:
-        workspace = ffn_workspace(m, hidden, inter, x.device)
+        workspace = _new(stream, ffn_workspace, m, hidden, inter, x.device)
     arr = (_Weight * (3 * len(layers)))(*[w.c_struct() for layer in layers for w in layer])
     _check("tq_ffn_stack", load().tq_ffn_stack(arr, len(layers), _ptr(x), m, eps, _ptr(y),
                                                _ptr(workspace), workspace.numel(),
@@ -352,9 +366,9 @@ def ffn_step(gate: PackedWeight, up: PackedWeight, down: PackedWeight, x, y=None
     import torch
     m, hidden = x.shape
     if y is None:
-        y = torch.empty((m, hidden), dtype=torch.float32, device=x.device)
+        y = _new(stream, torch.empty, (m, hidden), dtype=torch.float32, device=x.device)
     if workspace is None:
-        workspace = ffn_workspace(m, hidden, gate.n, x.device)
+        workspace = _new(stream, ffn_workspace, m, hidden, gate.n, x.device)
     g, u, d = gate.c_struct(), up.c_struct(), down.c_struct()
     _check("tq_ffn_step", load().tq_ffn_step(ctypes.byref(g), ctypes.byref(u), ctypes.byref(d),
                                              _ptr(x), m, _ptr(y), _ptr(workspace),
@@ -369,7 +383,7 @@ def ffn_step_static(gate: PackedWeight, up: PackedWeight, down: PackedWeight, x,
     import torch
     m, hidden = x.shape
     if y is None:
-        y = torch.empty((m, hidden), dtype=torch.float32, device=x.device)
+        y = _new(stream, torch.empty, (m, hidden), dtype=torch.float32, device=x.device)
     g, u, d = gate.c_struct(), up.c_struct(), down.c_struct()
     _check("tq_ffn_step_static", load().tq_ffn_step_static(
         ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), _ptr(x), m, _ptr(y), _stream(stream)))
@@ -381,7 +395,7 @@ def rmsnorm_bf16(y, eps: float = 1e-6, x_out=None, stream=None):
     import torch
     m, n = y.shape
     if x_out is None:
-        x_out = torch.empty((m, n), dtype=torch.bfloat16, device=y.device)
+        x_out = _new(stream, torch.empty, (m, n), dtype=torch.bfloat16, device=y.device)
     _check("tq_rmsnorm_bf16", load().tq_rmsnorm_bf16(_ptr(y), m, n, eps, _ptr(x_out),
                                                      _stream(stream)))
     return x_out
@@ -449,10 +463,10 @@ def pack_experts(codes, fmt: int, scales, stream=None) -> PackedExperts:
     import torch
     ptr = _tensor("codes", codes, (torch.uint8,))
     experts, n, k = codes.shape
-    packed = torch.empty((experts, n, k // (4 if fmt == FMT_TERNARY2 else 8)), dtype=torch.uint8,
+    packed = _new(stream, torch.empty, (experts, n, k // (4 if fmt == FMT_TERNARY2 else 8)), dtype=torch.uint8,
                          device=codes.device)
     _check("tq_pack_weights", load().tq_pack_weights(ptr, experts * n, k, fmt, packed.data_ptr(), _stream(stream)))
-    return PackedExperts(packed, scales.contiguous(), experts, n, k, fmt)
+    return PackedExperts(packed, _new(stream, scales.contiguous), experts, n, k, fmt)
 
 
 def add_rmsnorm_rotq(residual, delta=None, gamma=None, eps: float = 1e-6, residual_out=None,
@@ -470,17 +484,17 @@ def add_rmsnorm_rotq(residual, delta=None, gamma=None, eps: float = 1e-6, residu
     p_gamma = 0 if gamma is None else _tensor("gamma", gamma, (bf16,), (n,))
     p_x = 0 if x_out is None else _tensor("x_out", x_out, (bf16,), shape)
     if residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _new(stream, torch.empty_like, residual)
         p_out = residual_out.data_ptr()
     else:
         p_out = _tensor("residual_out", residual_out, (residual.dtype,), shape)
     if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=residual.device)
+        q = _new(stream, torch.empty, shape, dtype=torch.int8, device=residual.device)
         p_q = q.data_ptr()
     else:
         p_q = _tensor("q", q, (torch.int8,), shape)
     if s is None:
-        s = torch.empty((m, n // BLOCK), dtype=f32, device=residual.device)
+        s = _new(stream, torch.empty, (m, n // BLOCK), dtype=f32, device=residual.device)
         p_s = s.data_ptr()
     else:
         p_s = _tensor("s", s, (f32,), (m, n // BLOCK))
@@ -497,12 +511,12 @@ def moe_route(logits, topk: int, renormalize: bool = True, ids=None, weights=Non
     p_logits = _tensor("logits", logits, (torch.float32, torch.bfloat16))
     m, experts = logits.shape
     if ids is None:
-        ids = torch.empty((m, topk), dtype=torch.int32, device=logits.device)
+        ids = _new(stream, torch.empty, (m, topk), dtype=torch.int32, device=logits.device)
         p_ids = ids.data_ptr()
     else:
         p_ids = _tensor("ids", ids, (torch.int32,), (m, topk))
     if weights is None:
-        weights = torch.empty((m, topk), dtype=torch.float32, device=logits.device)
+        weights = _new(stream, torch.empty, (m, topk), dtype=torch.float32, device=logits.device)
         p_weights = weights.data_ptr()
     else:
         p_weights = _tensor("weights", weights, (torch.float32,), (m, topk))
@@ -532,20 +546,21 @@ def moe_plan(ids, experts: int, plan: MoePlan = None, workspace=None, stream=Non
     p_ids = _tensor("ids", ids, (torch.int32,))
     m, topk = ids.shape
     if plan is None:
-        plan = MoePlan(torch.empty(experts + 1, dtype=torch.int32, device=ids.device),
-                       torch.empty(m * topk, dtype=torch.int32, device=ids.device), torch.empty_like(ids))
+        plan = MoePlan(_new(stream, torch.empty, experts + 1, dtype=torch.int32, device=ids.device),
+                       _new(stream, torch.empty, m * topk, dtype=torch.int32, device=ids.device),
+                       _new(stream, torch.empty_like, ids))
     p_offsets = _tensor("offsets", plan.offsets, (torch.int32,), (experts + 1,))
     p_rows, p_pos = (_tensor(name, t, (torch.int32,)) for name, t in (("rows", plan.rows), ("pos", plan.pos)))
     if plan.rows.numel() != m * topk or plan.pos.numel() != m * topk:
         raise ValueError(f"rows, pos: {m * topk} entries are needed, got {plan.rows.numel()}, {plan.pos.numel()}")
     if workspace is None:
-        workspace = moe_workspace(m, topk, experts, device=ids.device)
+        workspace = _new(stream, moe_workspace, m, topk, experts, device=ids.device)
     _check("tq_moe_plan", load().tq_moe_plan(p_ids, m, topk, experts, p_offsets, p_rows, p_pos,
                                              workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return plan
 
 
-def _moe_inputs(w: PackedExperts, q, s, plan: MoePlan, gather: bool, workspace):
+def _moe_inputs(w: PackedExperts, q, s, plan: MoePlan, gather: bool, workspace, stream):
     """The checked inputs of a grouped product: addresses of q, s, rows and offsets, rows of q,
     slots, and a workspace."""
     import torch
@@ -558,7 +573,8 @@ def _moe_inputs(w: PackedExperts, q, s, plan: MoePlan, gather: bool, workspace):
     p_rows = _tensor("rows", plan.rows, (torch.int32,))
     slots = plan.rows.numel()
     if workspace is None:
-        workspace = torch.zeros(256 + slots * (2 * k + 16 * -(-k // 512)), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.zeros, 256 + slots * (2 * k + 16 * -(-k // 512)), dtype=torch.uint8,
+                         device=q.device)
     elif workspace.dtype != torch.uint8:
         raise ValueError(f"workspace: uint8 is needed, got {workspace.dtype}")
     return p_q, p_s, p_rows if gather else 0, p_offsets, m, slots, workspace
@@ -569,9 +585,9 @@ def moe_gemv(w: PackedExperts, q, s, plan: MoePlan, gather: bool = False, y=None
     """y float32 [slots][n], one row per sorted slot.  q int8, s float32: one row
     per sorted slot, or with ``gather`` one per token, picked by plan.rows."""
     import torch
-    p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(w, q, s, plan, gather, workspace)
+    p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(w, q, s, plan, gather, workspace, stream)
     if y is None:
-        y = torch.empty((slots, w.n), dtype=torch.float32, device=q.device)
+        y = _new(stream, torch.empty, (slots, w.n), dtype=torch.float32, device=q.device)
         p_y = y.data_ptr()
     else:
         p_y = _tensor("y", y, (torch.float32,), (slots, w.n))
@@ -587,9 +603,9 @@ def moe_gateup(gate: PackedExperts, up: PackedExperts, q, s, plan: MoePlan, gath
     float32: one row per token, picked by plan.rows (``gather``), or one per
     sorted slot."""
     import torch
-    p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(gate, q, s, plan, gather, workspace)
+    p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(gate, q, s, plan, gather, workspace, stream)
     if h is None:
-        h = torch.empty((slots, gate.n), dtype=torch.bfloat16, device=q.device)
+        h = _new(stream, torch.empty, (slots, gate.n), dtype=torch.bfloat16, device=q.device)
         p_h = h.data_ptr()
     else:
         p_h = _tensor("h", h, (torch.bfloat16,), (slots, gate.n))
@@ -610,7 +626,7 @@ def moe_combine(y, plan: MoePlan, weights, out=None, dtype=None, stream=None):
     if plan.pos.numel() != m * topk:
         raise ValueError(f"pos: {m * topk} entries are needed, got {plan.pos.numel()}")
     if out is None:
-        out = torch.empty((m, y.shape[1]), dtype=dtype or torch.float32, device=y.device)
+        out = _new(stream, torch.empty, (m, y.shape[1]), dtype=dtype or torch.float32, device=y.device)
     p_out = _tensor("out", out, (torch.float32, torch.bfloat16), (m, y.shape[1]))
     _check("tq_moe_combine", load().tq_moe_combine(
         p_y, p_pos, p_weights, m, topk, y.shape[0], y.shape[1], p_out, int(out.dtype == torch.bfloat16),
@@ -633,10 +649,10 @@ def moe_ffn(gate: PackedExperts, up: PackedExperts, down: PackedExperts, q, s, i
     if hidden != gate.k:
         raise ValueError(f"q: rows of {gate.k} codes are needed, got {hidden}")
     if out is None:
-        out = torch.empty((m, hidden), dtype=dtype or torch.float32, device=q.device)
+        out = _new(stream, torch.empty, (m, hidden), dtype=dtype or torch.float32, device=q.device)
     p_out = _tensor("out", out, (torch.float32, torch.bfloat16), (m, hidden))
     if workspace is None:
-        workspace = moe_workspace(m, topk, gate.experts, hidden, gate.n, q.device)
+        workspace = _new(stream, moe_workspace, m, topk, gate.experts, hidden, gate.n, q.device)
     _check("tq_moe_ffn", load().tq_moe_ffn(
         gate.c_struct(), up.c_struct(), down.c_struct(), p_q, p_s, p_ids, p_weights, m, topk, p_out,
         int(out.dtype == torch.bfloat16), workspace.data_ptr(), workspace.numel(), _stream(stream)))
