@@ -168,17 +168,30 @@ def _check(fn: str, status: int) -> None:
 
 
 _raw_stream = None
+_raw_device = None
+
+
+def _device() -> int:
+    """Where a call launches: the current device (no tensor's, if CUDA is not in use)."""
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        if not torch.cuda.is_initialized():
+            return -2
+        # (torch.cuda.current_device looks again whether CUDA is in use)
+        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _raw_device()
 
 
 def _stream(stream):
-    import torch
     if stream is None:
+        import torch
         global _raw_stream
         if _raw_stream is None:
             # the stream object costs 3 us a call, the raw handle 0.1 us
             _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
                 lambda device: torch.cuda.current_stream(device).cuda_stream)
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device() if _raw_device is None else _raw_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -188,9 +201,9 @@ def _new(stream, make, *args, **kwargs):
     """make(*args, **kwargs): a tensor that a call allocates for itself, on the stream that the call
     runs on.  (Filled on the current stream it could be filled after the call's kernels have
     written to it; allocated there, and released, it could be another tensor's while they run.)"""
-    import torch
     if stream is None:
         return make(*args, **kwargs)
+    import torch
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
@@ -420,8 +433,8 @@ class PackedExperts:
     def __post_init__(self):
         import torch
         per = 4 if self.fmt == FMT_TERNARY2 else 8
-        _tensor("codes", self.codes, (torch.uint8,), (self.experts, self.n, self.k // per))
-        _tensor("scales", self.scales, (torch.float16,), (self.experts, self.n, self.k // BLOCK))
+        _tensor(None, "codes", self.codes, (torch.uint8,), (self.experts, self.n, self.k // per))
+        _tensor(None, "scales", self.scales, (torch.float16,), (self.experts, self.n, self.k // BLOCK))
         object.__setattr__(self, "_c", _Experts(self.codes.data_ptr(), self.scales.data_ptr(), self.experts, self.n,
                                                 self.k, self.fmt))
 
@@ -446,25 +459,36 @@ class MoePlan:
         return self.rows.numel()
 
 
-def _tensor(name: str, t, dtypes, shape=None):
+def _tensor(device, name: str, t, dtypes, shape=None):
     """Check a tensor argument of a mixture-of-experts call: the kernels read raw
-    contiguous device memory of one type.  Returns its address."""
-    if not (t.is_cuda and t.dtype in dtypes and t.is_contiguous()):
-        raise ValueError(f"{name}: a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} is "
+    contiguous device memory of one type, on the device where they run (None: on any).
+    Returns its address."""
+    at = t.get_device()                                              # -1: not a CUDA tensor
+    if not ((at >= 0 if device is None else at == device) and t.dtype in dtypes and t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} on the current device is "
                          f"needed, got {t.dtype} on {t.device}, strides {tuple(t.stride())}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
+def _weights(device, **weights):
+    """Check that the matrices of a call are on the device where it runs."""
+    for name, w in weights.items():
+        if w.codes.get_device() != device or w.scales.get_device() != device:
+            raise ValueError(f"{name}: weights on the current device are needed, got codes on {w.codes.device}, "
+                             f"scales on {w.scales.device}")
+
+
 def pack_experts(codes, fmt: int, scales, stream=None) -> PackedExperts:
     """codes: uint8 CUDA tensor [experts][n][k] (as pack_weights); scales: float16
     CUDA tensor [experts][n][k/128]."""
     import torch
-    ptr = _tensor("codes", codes, (torch.uint8,))
+    dev = _device()
+    ptr = _tensor(dev, "codes", codes, (torch.uint8,))
     experts, n, k = codes.shape
     packed = _new(stream, torch.empty, (experts, n, k // (4 if fmt == FMT_TERNARY2 else 8)), dtype=torch.uint8,
-                         device=codes.device)
+                  device=codes.device)
     _check("tq_pack_weights", load().tq_pack_weights(ptr, experts * n, k, fmt, packed.data_ptr(), _stream(stream)))
     return PackedExperts(packed, _new(stream, scales.contiguous), experts, n, k, fmt)
 
@@ -477,27 +501,28 @@ def add_rmsnorm_rotq(residual, delta=None, gamma=None, eps: float = 1e-6, residu
     receives the norm before the rotation."""
     import torch
     f32, bf16 = torch.float32, torch.bfloat16
-    p_res = _tensor("residual", residual, (f32, bf16))
+    dev = _device()
+    p_res = _tensor(dev, "residual", residual, (f32, bf16))
     shape = residual.shape
     m, n = shape
-    p_delta = 0 if delta is None else _tensor("delta", delta, (f32, bf16), shape)
-    p_gamma = 0 if gamma is None else _tensor("gamma", gamma, (bf16,), (n,))
-    p_x = 0 if x_out is None else _tensor("x_out", x_out, (bf16,), shape)
+    p_delta = 0 if delta is None else _tensor(dev, "delta", delta, (f32, bf16), shape)
+    p_gamma = 0 if gamma is None else _tensor(dev, "gamma", gamma, (bf16,), (n,))
+    p_x = 0 if x_out is None else _tensor(dev, "x_out", x_out, (bf16,), shape)
     if residual_out is None:
         residual_out = _new(stream, torch.empty_like, residual)
         p_out = residual_out.data_ptr()
     else:
-        p_out = _tensor("residual_out", residual_out, (residual.dtype,), shape)
+        p_out = _tensor(dev, "residual_out", residual_out, (residual.dtype,), shape)
     if q is None:
         q = _new(stream, torch.empty, shape, dtype=torch.int8, device=residual.device)
         p_q = q.data_ptr()
     else:
-        p_q = _tensor("q", q, (torch.int8,), shape)
+        p_q = _tensor(dev, "q", q, (torch.int8,), shape)
     if s is None:
         s = _new(stream, torch.empty, (m, n // BLOCK), dtype=f32, device=residual.device)
         p_s = s.data_ptr()
     else:
-        p_s = _tensor("s", s, (f32,), (m, n // BLOCK))
+        p_s = _tensor(dev, "s", s, (f32,), (m, n // BLOCK))
     _check("tq_add_rmsnorm_rotq", load().tq_add_rmsnorm_rotq(
         p_res, int(residual.dtype == bf16), p_delta, int(delta is not None and delta.dtype == bf16), p_gamma, m, n,
         eps, p_out, p_x, p_q, p_s, _stream(stream)))
@@ -508,18 +533,19 @@ def moe_route(logits, topk: int, renormalize: bool = True, ids=None, weights=Non
     """logits float32 or bf16 [m][experts] -> (ids int32 [m][topk], weights
     float32 [m][topk]); -1 and 0 where a token has no expert left."""
     import torch
-    p_logits = _tensor("logits", logits, (torch.float32, torch.bfloat16))
+    dev = _device()
+    p_logits = _tensor(dev, "logits", logits, (torch.float32, torch.bfloat16))
     m, experts = logits.shape
     if ids is None:
         ids = _new(stream, torch.empty, (m, topk), dtype=torch.int32, device=logits.device)
         p_ids = ids.data_ptr()
     else:
-        p_ids = _tensor("ids", ids, (torch.int32,), (m, topk))
+        p_ids = _tensor(dev, "ids", ids, (torch.int32,), (m, topk))
     if weights is None:
         weights = _new(stream, torch.empty, (m, topk), dtype=torch.float32, device=logits.device)
         p_weights = weights.data_ptr()
     else:
-        p_weights = _tensor("weights", weights, (torch.float32,), (m, topk))
+        p_weights = _tensor(dev, "weights", weights, (torch.float32,), (m, topk))
     _check("tq_moe_route", load().tq_moe_route(p_logits, int(logits.dtype == torch.bfloat16), m, experts, topk,
                                                int(renormalize), p_ids, p_weights, _stream(stream)))
     return ids, weights
@@ -543,41 +569,43 @@ def moe_workspace(m: int, topk: int, experts: int, hidden: int = 0, inter: int =
 def moe_plan(ids, experts: int, plan: MoePlan = None, workspace=None, stream=None) -> MoePlan:
     """ids int32 [m][topk] -> MoePlan; an id outside 0 .. experts-1 leaves its slot out."""
     import torch
-    p_ids = _tensor("ids", ids, (torch.int32,))
+    dev = _device()
+    p_ids = _tensor(dev, "ids", ids, (torch.int32,))
     m, topk = ids.shape
     if plan is None:
         plan = MoePlan(_new(stream, torch.empty, experts + 1, dtype=torch.int32, device=ids.device),
                        _new(stream, torch.empty, m * topk, dtype=torch.int32, device=ids.device),
                        _new(stream, torch.empty_like, ids))
-    p_offsets = _tensor("offsets", plan.offsets, (torch.int32,), (experts + 1,))
-    p_rows, p_pos = (_tensor(name, t, (torch.int32,)) for name, t in (("rows", plan.rows), ("pos", plan.pos)))
+    p_offsets = _tensor(dev, "offsets", plan.offsets, (torch.int32,), (experts + 1,))
+    p_rows, p_pos = (_tensor(dev, name, t, (torch.int32,)) for name, t in (("rows", plan.rows), ("pos", plan.pos)))
     if plan.rows.numel() != m * topk or plan.pos.numel() != m * topk:
         raise ValueError(f"rows, pos: {m * topk} entries are needed, got {plan.rows.numel()}, {plan.pos.numel()}")
     if workspace is None:
         workspace = _new(stream, moe_workspace, m, topk, experts, device=ids.device)
-    _check("tq_moe_plan", load().tq_moe_plan(p_ids, m, topk, experts, p_offsets, p_rows, p_pos,
-                                             workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    p_ws = _tensor(dev, "workspace", workspace, (torch.uint8,))
+    _check("tq_moe_plan", load().tq_moe_plan(p_ids, m, topk, experts, p_offsets, p_rows, p_pos, p_ws,
+                                             workspace.numel(), _stream(stream)))
     return plan
 
 
 def _moe_inputs(w: PackedExperts, q, s, plan: MoePlan, gather: bool, workspace, stream):
-    """The checked inputs of a grouped product: addresses of q, s, rows and offsets, rows of q,
-    slots, and a workspace."""
+    """The checked inputs of a grouped product: the device, addresses of q, s, rows and offsets, rows
+    of q, slots, and a workspace."""
     import torch
-    p_q = _tensor("q", q, (torch.int8,))
+    dev = _device()
+    p_q = _tensor(dev, "q", q, (torch.int8,))
     m, k = q.shape
     if k != w.k:
         raise ValueError(f"q: rows of {w.k} codes are needed, got {k}")
-    p_s = _tensor("s", s, (torch.float32,), (m, k // BLOCK))
-    p_offsets = _tensor("offsets", plan.offsets, (torch.int32,), (w.experts + 1,))
-    p_rows = _tensor("rows", plan.rows, (torch.int32,))
+    p_s = _tensor(dev, "s", s, (torch.float32,), (m, k // BLOCK))
+    p_offsets = _tensor(dev, "offsets", plan.offsets, (torch.int32,), (w.experts + 1,))
+    p_rows = _tensor(dev, "rows", plan.rows, (torch.int32,))
     slots = plan.rows.numel()
     if workspace is None:
         workspace = _new(stream, torch.zeros, 256 + slots * (2 * k + 16 * -(-k // 512)), dtype=torch.uint8,
                          device=q.device)
-    elif workspace.dtype != torch.uint8:
-        raise ValueError(f"workspace: uint8 is needed, got {workspace.dtype}")
-    return p_q, p_s, p_rows if gather else 0, p_offsets, m, slots, workspace
+    _tensor(dev, "workspace", workspace, (torch.uint8,))
+    return dev, p_q, p_s, p_rows if gather else 0, p_offsets, m, slots, workspace
 
 
 def moe_gemv(w: PackedExperts, q, s, plan: MoePlan, gather: bool = False, y=None, workspace=None,
@@ -585,12 +613,13 @@ def moe_gemv(w: PackedExperts, q, s, plan: MoePlan, gather: bool = False, y=None
     """y float32 [slots][n], one row per sorted slot.  q int8, s float32: one row
     per sorted slot, or with ``gather`` one per token, picked by plan.rows."""
     import torch
-    p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(w, q, s, plan, gather, workspace, stream)
+    dev, p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(w, q, s, plan, gather, workspace, stream)
+    _weights(dev, w=w)
     if y is None:
         y = _new(stream, torch.empty, (slots, w.n), dtype=torch.float32, device=q.device)
         p_y = y.data_ptr()
     else:
-        p_y = _tensor("y", y, (torch.float32,), (slots, w.n))
+        p_y = _tensor(dev, "y", y, (torch.float32,), (slots, w.n))
     _check("tq_moe_gemv", load().tq_moe_gemv(
         w.c_struct(), p_q, p_s, m, p_rows, p_offsets, slots, p_y, workspace.data_ptr(), workspace.numel(),
         _stream(stream)))
@@ -603,12 +632,13 @@ def moe_gateup(gate: PackedExperts, up: PackedExperts, q, s, plan: MoePlan, gath
     float32: one row per token, picked by plan.rows (``gather``), or one per
     sorted slot."""
     import torch
-    p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(gate, q, s, plan, gather, workspace, stream)
+    dev, p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(gate, q, s, plan, gather, workspace, stream)
+    _weights(dev, gate=gate, up=up)
     if h is None:
         h = _new(stream, torch.empty, (slots, gate.n), dtype=torch.bfloat16, device=q.device)
         p_h = h.data_ptr()
     else:
-        p_h = _tensor("h", h, (torch.bfloat16,), (slots, gate.n))
+        p_h = _tensor(dev, "h", h, (torch.bfloat16,), (slots, gate.n))
     _check("tq_moe_gateup", load().tq_moe_gateup(
         gate.c_struct(), up.c_struct(), p_q, p_s, m, p_rows, p_offsets, slots, p_h, workspace.data_ptr(),
         workspace.numel(), _stream(stream)))
@@ -619,15 +649,16 @@ def moe_combine(y, plan: MoePlan, weights, out=None, dtype=None, stream=None):
     """y float32 [slots][n], weights float32 [m][topk] -> the weighted sum over each
     token's experts [m][n] (float32 unless dtype or out says bf16)."""
     import torch
-    p_y = _tensor("y", y, (torch.float32,))
-    p_weights = _tensor("weights", weights, (torch.float32,))
+    dev = _device()
+    p_y = _tensor(dev, "y", y, (torch.float32,))
+    p_weights = _tensor(dev, "weights", weights, (torch.float32,))
     m, topk = weights.shape
-    p_pos = _tensor("pos", plan.pos, (torch.int32,))
+    p_pos = _tensor(dev, "pos", plan.pos, (torch.int32,))
     if plan.pos.numel() != m * topk:
         raise ValueError(f"pos: {m * topk} entries are needed, got {plan.pos.numel()}")
     if out is None:
         out = _new(stream, torch.empty, (m, y.shape[1]), dtype=dtype or torch.float32, device=y.device)
-    p_out = _tensor("out", out, (torch.float32, torch.bfloat16), (m, y.shape[1]))
+    p_out = _tensor(dev, "out", out, (torch.float32, torch.bfloat16), (m, y.shape[1]))
     _check("tq_moe_combine", load().tq_moe_combine(
         p_y, p_pos, p_weights, m, topk, y.shape[0], y.shape[1], p_out, int(out.dtype == torch.bfloat16),
         _stream(stream)))
@@ -640,22 +671,25 @@ def moe_ffn(gate: PackedExperts, up: PackedExperts, down: PackedExperts, q, s, i
     [m][hidden/128], ids int32 and weights float32 [m][topk] -> [m][hidden]
     (float32 unless dtype or out says bf16)."""
     import torch
-    p_q = _tensor("q", q, (torch.int8,))
+    dev = _device()
+    p_q = _tensor(dev, "q", q, (torch.int8,))
     m, hidden = q.shape
-    p_s = _tensor("s", s, (torch.float32,), (m, hidden // BLOCK))
+    p_s = _tensor(dev, "s", s, (torch.float32,), (m, hidden // BLOCK))
     topk = ids.shape[-1]
-    p_ids = _tensor("ids", ids, (torch.int32,), (m, topk))
-    p_weights = _tensor("weights", weights, (torch.float32,), (m, topk))
+    p_ids = _tensor(dev, "ids", ids, (torch.int32,), (m, topk))
+    p_weights = _tensor(dev, "weights", weights, (torch.float32,), (m, topk))
     if hidden != gate.k:
         raise ValueError(f"q: rows of {gate.k} codes are needed, got {hidden}")
     if out is None:
         out = _new(stream, torch.empty, (m, hidden), dtype=dtype or torch.float32, device=q.device)
-    p_out = _tensor("out", out, (torch.float32, torch.bfloat16), (m, hidden))
+    p_out = _tensor(dev, "out", out, (torch.float32, torch.bfloat16), (m, hidden))
     if workspace is None:
         workspace = _new(stream, moe_workspace, m, topk, gate.experts, hidden, gate.n, q.device)
+    p_ws = _tensor(dev, "workspace", workspace, (torch.uint8,))
+    _weights(dev, gate=gate, up=up, down=down)
     _check("tq_moe_ffn", load().tq_moe_ffn(
         gate.c_struct(), up.c_struct(), down.c_struct(), p_q, p_s, p_ids, p_weights, m, topk, p_out,
-        int(out.dtype == torch.bfloat16), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        int(out.dtype == torch.bfloat16), p_ws, workspace.numel(), _stream(stream)))
     return out
 
 

@@ -30,6 +30,7 @@ def allocations(monkeypatch):
 
     monkeypatch.setattr(tq, "load", lambda: Library())
     monkeypatch.setattr(tq, "_tensor", lambda *a, **k: 0x1000)
+    monkeypatch.setattr(tq, "_device", lambda: -1)                   # where CPU tensors are
     monkeypatch.setattr(torch.cuda, "stream", under)
     for name in ("empty", "empty_like", "zeros"):
         real = getattr(torch, name)
