@@ -435,11 +435,9 @@ class PackedExperts:
         per = 4 if self.fmt == FMT_TERNARY2 else 8
         _tensor(None, "codes", self.codes, (torch.uint8,), (self.experts, self.n, self.k // per))
         _tensor(None, "scales", self.scales, (torch.float16,), (self.experts, self.n, self.k // BLOCK))
-        object.__setattr__(self, "_c", _Experts(self.codes.data_ptr(), self.scales.data_ptr(), self.experts, self.n,
-                                                self.k, self.fmt))
 
     def c_struct(self) -> _Experts:
-        return self._c
+        return _Experts(self.codes.data_ptr(), self.scales.data_ptr(), self.experts, self.n, self.k, self.fmt)
 
     @property
     def nbytes(self) -> int:

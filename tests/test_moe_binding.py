@@ -1,7 +1,9 @@
 """The mixture-of-experts calls of the binding refuse a tensor that is not on the device where
 they launch, of another type or not contiguous, before anything is launched.  The tensors here
 only say where they are; the library only notes that it was called.  No GPU needed."""
+import copy
 import math
+import pickle
 
 import pytest
 
@@ -117,3 +119,13 @@ def test_every_tensor_is_checked(launched, op):
                 _call(op, t)
                 pytest.fail(f"{name}: {wrong.device}, {wrong.dtype}, contiguous {wrong.contiguous_}")
     assert len(launched) == 1
+
+
+def test_weights_can_be_copied_and_pickled(launched):
+    """As PackedWeight's; and a call takes the addresses that its tensors have then."""
+    import torch
+    w = tq.PackedExperts(Tensor(torch.uint8, E, I, H // 4), Tensor(torch.float16, E, I, H // 128), E, I, H, 0)
+    for other in (copy.deepcopy(w), copy.copy(w), pickle.loads(pickle.dumps(w))):
+        assert (other.experts, other.n, other.k, other.fmt) == (E, I, H, 0) and other.codes.shape == w.codes.shape
+    w.codes.data_ptr = lambda: 0x2000
+    assert w.c_struct().codes == 0x2000 and w.c_struct().scales == 0x1000
