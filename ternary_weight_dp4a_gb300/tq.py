@@ -564,6 +564,16 @@ def moe_workspace(m: int, topk: int, experts: int, hidden: int = 0, inter: int =
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
+def _moe_scratch(nbytes: int, device):
+    """A workspace for one call.  Of all of it only the error word has to be zero."""
+    import torch
+    if nbytes == 0:
+        raise ValueError("sizes out of range for a workspace")
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    workspace[:256].zero_()
+    return workspace
+
+
 def moe_plan(ids, experts: int, plan: MoePlan = None, workspace=None, stream=None) -> MoePlan:
     """ids int32 [m][topk] -> MoePlan; an id outside 0 .. experts-1 leaves its slot out."""
     import torch
@@ -579,7 +589,7 @@ def moe_plan(ids, experts: int, plan: MoePlan = None, workspace=None, stream=Non
     if plan.rows.numel() != m * topk or plan.pos.numel() != m * topk:
         raise ValueError(f"rows, pos: {m * topk} entries are needed, got {plan.rows.numel()}, {plan.pos.numel()}")
     if workspace is None:
-        workspace = _new(stream, moe_workspace, m, topk, experts, device=ids.device)
+        workspace = _new(stream, _moe_scratch, moe_workspace_bytes(m, topk, experts), ids.device)
     p_ws = _tensor(dev, "workspace", workspace, (torch.uint8,))
     _check("tq_moe_plan", load().tq_moe_plan(p_ids, m, topk, experts, p_offsets, p_rows, p_pos, p_ws,
                                              workspace.numel(), _stream(stream)))
@@ -600,8 +610,7 @@ def _moe_inputs(w: PackedExperts, q, s, plan: MoePlan, gather: bool, workspace, 
     p_rows = _tensor(dev, "rows", plan.rows, (torch.int32,))
     slots = plan.rows.numel()
     if workspace is None:
-        workspace = _new(stream, torch.zeros, 256 + slots * (2 * k + 16 * -(-k // 512)), dtype=torch.uint8,
-                         device=q.device)
+        workspace = _new(stream, _moe_scratch, 256 + slots * (2 * k + 16 * -(-k // 512)), q.device)
     _tensor(dev, "workspace", workspace, (torch.uint8,))
     return dev, p_q, p_s, p_rows if gather else 0, p_offsets, m, slots, workspace
 
@@ -682,7 +691,7 @@ def moe_ffn(gate: PackedExperts, up: PackedExperts, down: PackedExperts, q, s, i
         out = _new(stream, torch.empty, (m, hidden), dtype=dtype or torch.float32, device=q.device)
     p_out = _tensor(dev, "out", out, (torch.float32, torch.bfloat16), (m, hidden))
     if workspace is None:
-        workspace = _new(stream, moe_workspace, m, topk, gate.experts, hidden, gate.n, q.device)
+        workspace = _new(stream, _moe_scratch, moe_workspace_bytes(m, topk, gate.experts, hidden, gate.n), q.device)
     p_ws = _tensor(dev, "workspace", workspace, (torch.uint8,))
     _weights(dev, gate=gate, up=up, down=down)
     _check("tq_moe_ffn", load().tq_moe_ffn(

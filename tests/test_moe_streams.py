@@ -48,16 +48,13 @@ def _experts(torch, experts, n, k):
                             experts, n, k, 0)
 
 
-@pytest.mark.parametrize("call", ["norm", "route", "plan", "gemv", "gateup", "combine", "ffn", "pack", "rotq", "dense"])
-def test_a_call_allocates_on_its_stream(allocations, call):
-    import torch
+def _calls(torch):
     m, topk, e, h, i = 3, 2, 4, 256, 128
     q, s = torch.ones((m, h), dtype=torch.int8), torch.ones((m, h // 128))
     ids, w = torch.ones((m, topk), dtype=torch.int32), torch.ones((m, topk))
     plan = tq.MoePlan(torch.ones(e + 1, dtype=torch.int32), torch.ones(m * topk, dtype=torch.int32), ids)
     gate, up, down = _experts(torch, e, i, h), _experts(torch, e, i, h), _experts(torch, e, h, i)
-    allocations.clear()
-    calls = {
+    return {
         "norm": lambda st: tq.add_rmsnorm_rotq(torch.ones((m, h)), stream=st),
         "route": lambda st: tq.moe_route(torch.ones((m, e)), topk, stream=st),
         "plan": lambda st: tq.moe_plan(ids, e, stream=st),
@@ -70,8 +67,35 @@ def test_a_call_allocates_on_its_stream(allocations, call):
         "rotq": lambda st: tq.rotate_quant(torch.ones((m, h)).bfloat16(), stream=st),
         "dense": lambda st: tq.gemv(tq.PackedWeight(gate.codes[0], gate.scales[0], i, h, 0), q, s, stream=st),
     }
+
+
+@pytest.mark.parametrize("call", ["norm", "route", "plan", "gemv", "gateup", "combine", "ffn", "pack", "rotq", "dense"])
+def test_a_call_allocates_on_its_stream(allocations, call):
+    import torch
+    calls = _calls(torch)
+    allocations.clear()
     calls[call](Stream())
     assert allocations and all(allocations)
+
+
+@pytest.mark.parametrize("call", ["plan", "gemv", "gateup", "ffn"])
+def test_a_call_fills_no_more_than_the_error_word(allocations, monkeypatch, call):
+    """Without a workspace a call takes one for itself; a fill of all of it would cost more than the call."""
+    import torch
+    filled = []
+    for owner, name in ((torch, "zeros"), (torch, "full"), (torch.Tensor, "zero_"), (torch.Tensor, "fill_")):
+        real = getattr(owner, name)
+
+        def fill(*a, real=real, **k):
+            out = real(*a, **k)
+            filled.append(out.numel() * out.element_size())
+            return out
+
+        monkeypatch.setattr(owner, name, fill)
+    calls = _calls(torch)
+    filled.clear()
+    calls[call](Stream())
+    assert sum(filled) <= 256
 
 
 @pytest.mark.gpu
