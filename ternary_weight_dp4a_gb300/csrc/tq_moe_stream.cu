@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
     // the issuing side; lane l brings the scales of row l of the unit (gate 0-15, up 16-31)
     int in_unit = warp, in_u = first_u + warp, in_chunk = first_chunk, in_block = 0, in_slot = 0, in_expert = expert, in_y = 0;
     const uint16_t *scale_src = nullptr;
+    bool ok = true;                                                  // false: a wait ran out, nothing is copied or written any more
     const auto issue = [&]() {
         if (in_unit < mine) {
             if (in_block == 0) {                                     // a new unit
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
                 const int n = min(in_u * kUnitRows + (GATEUP ? lane & 15 : lane), p.n - 1);
                 scale_src = p.scales[GATEUP ? lane >> 4 : 0] + (static_cast<int64_t>(in_expert) * p.n + n) * nb;
             }
-            if (lane == 0) {
+            if (lane == 0 && ok) {
                 const uint32_t dst = smem_u32(ring + in_slot * kStageBytes<FMT>);
                 mbar_arrive_expect_tx(bar(in_slot), kStageBytes<FMT>);
                 load_box(dst, &args.codes[0], in_block * kBlockBytes, in_y, bar(in_slot));
@@ -486,7 +487,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
 #pragma unroll 1
             for (int b0 = 0; b0 < nb; b0 += kStageBlocks) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kD - 1) : "memory");
-                if (!mbar_wait(bar(slot), phase)) atomicOr(args.err, 1u << 12);
+                if (ok && !mbar_wait(bar(slot), phase)) {
+                    atomicOr(args.err, 1u << 12);
+                    ok = false;
+                    // the stages behind it are on their way, too: they land before the warp goes on, and out
+                    uint32_t turn = phase;
+#pragma unroll 1
+                    for (int i = slot + 1; i < slot + kD; ++i) {
+                        if (i == kD) turn ^= 1;
+                        mbar_wait(bar(i % kD), turn);
+                    }
+                }
                 __syncwarp();
                 const uint8_t *stage = ring + slot * kStageBytes<FMT>;
                 const uint16_t *ws = reinterpret_cast<const uint16_t *>(side + slot * kSideBytes<FMT>) + 4 * g;
@@ -536,7 +547,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int col = 2 * t + j;
-                if (col >= rows) continue;
+                if (col >= rows || !ok) continue;
                 const int64_t out = static_cast<int64_t>(row0 + col) * p.n;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
