@@ -93,9 +93,28 @@ tq_status tq_moe_route(const void *logits, int32_t logits_type, int32_t m, int32
  * zero-filled once by tq_workspace_init, reusable after every call, 256-byte
  * aligned, not shared by calls that may overlap.  hidden and inter may both be
  * 0 for a workspace that only serves tq_moe_plan.  0 for sizes out of range.
- * Its first 4 bytes are the error word of the bounded waits (tq_read_error_word). */
+ * Its first 4 bytes are the error word of the bounded waits (tq_read_error_word); only
+ * they have to be zero.  Each wait takes about half a second before it sets its bit;
+ * the call's outputs are then not valid.
+ *   bit 0  (tile kernel) the decoders waited for a free buffer of weights
+ *   bit 1  the matrix instructions waited for a free accumulator
+ *   bit 2  for decoded weights        bit 3  for activation rows
+ *   bit 4  (tile kernel) its last matrix instructions, at exit
+ *   bit 5  the activation copies waited for a free stage
+ *   bit 6  the scales' writers or readers waited for each other
+ *   bit 7  the fold waited for an accumulator
+ *   bit 8  the activation copies, bit 11 the weight copies in flight at exit
+ *   bit 9  the decoders waited for packed weights
+ *   bit 10 the weight copies waited for a free stage
+ *   bit 12 (stream kernel) a warp waited for packed weights */
 size_t tq_moe_workspace_bytes(int32_t m, int32_t topk, int32_t experts, int32_t hidden,
                               int32_t inter);
+
+/* The same bits of every tq_moe_* call of this process on the current device since the library
+ * was loaded, whatever workspace it had: for callers that keep none.  (The one thing that the
+ * library itself keeps between calls.)  Synchronises the stream.  TQ_OK, or TQ_ERR_TIMEOUT if
+ * a bit is set. */
+tq_status tq_moe_read_error_word(uint32_t *value, tq_stream_t stream);
 
 /* Sort the m * topk slots by expert (stable).  ids: int32 [m][topk]; an id
  * outside 0 .. experts-1 leaves its slot out.  Outputs:

@@ -140,6 +140,18 @@ size_t tq_moe_workspace_bytes(int32_t m, int32_t topk, int32_t experts, int32_t 
     return tq::moe_layout(m, topk, experts, hidden, inter).total;
 }
 
+tq_status tq_moe_read_error_word(uint32_t *value, tq_stream_t stream) {
+    if (value == nullptr) return TQ_ERR_INVALID_ARG;
+    cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
+    unsigned bits[2] = {};
+    cudaError_t e = tq::moe_stream_waits(&bits[0], str);
+    if (e == cudaSuccess) e = tq::moe_tile_waits(&bits[1], str);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(str);
+    if (e != cudaSuccess) return cuda_status(e);
+    *value = bits[0] | bits[1];
+    return tq_error_status(*value);
+}
+
 tq_status tq_moe_plan(const int32_t *ids, int32_t m, int32_t topk, int32_t experts, int32_t *offsets,
                       int32_t *rows, int32_t *pos, void *workspace, size_t workspace_bytes,
                       tq_stream_t stream) {

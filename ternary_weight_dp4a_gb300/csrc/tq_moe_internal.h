@@ -98,6 +98,17 @@ struct SmemLimit {
     }
 };
 
+// A bounded wait ran out: its bit goes into the error word of the call's workspace, and into the
+// library's own, which outlives a workspace that the caller has not kept.
+__device__ __forceinline__ void record_wait(unsigned *err, unsigned *own, unsigned bit) {
+    atomicOr(err, bit);
+    atomicOr(own, bit);
+}
+
+// The bits in the library's own words, one for each kernel's file,  of the current device (copied in `stream`).
+cudaError_t moe_stream_waits(unsigned *bits, cudaStream_t stream);
+cudaError_t moe_tile_waits(unsigned *bits, cudaStream_t stream);
+
 // The experts with at most `limit` rows, and those with more than `above`
 // (operand: moe_operand_bytes of workspace for the laid-out input).
 cudaError_t moe_stream_launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t stream);

@@ -48,6 +48,8 @@ constexpr int kCols = 8;                     // activation rows per chunk
 constexpr int kMaxWarps = 16;
 constexpr int kSplitWarps = 8;
 
+__device__ unsigned lost_waits;              // bits of all waits that have run out on this device
+
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) stream_kernel(const __grid_
             for (int b0 = 0; b0 < nb; b0 += kStageBlocks) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kD - 1) : "memory");
                 if (ok && !mbar_wait(bar(slot), phase)) {
-                    atomicOr(args.err, 1u << 12);
+                    record_wait(args.err, &lost_waits, 1u << 12);
                     ok = false;
                     // the stages behind it are on their way, too: they land before the warp goes on, and out
                     uint32_t turn = phase;
@@ -763,6 +765,10 @@ cudaError_t launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t s
 }
 
 }  // namespace
+
+cudaError_t moe_stream_waits(unsigned *bits, cudaStream_t stream) {
+    return cudaMemcpyFromSymbolAsync(bits, lost_waits, sizeof(*bits), 0, cudaMemcpyDeviceToHost, stream);
+}
 
 cudaError_t moe_stream_launch(const MoeProduct &p, int limit, unsigned *err, cudaStream_t stream) {
     if (p.h != nullptr) return p.fmt == TQ_FMT_TERNARY2 ? launch<0, true>(p, limit, err, stream) : launch<1, true>(p, limit, err, stream);

@@ -57,6 +57,8 @@ constexpr int kFoldCols = kCols / (kFoldWarps / 4); // columns per fold warp
 constexpr int kRegsIssue = 48, kRegsFold = 112;
 constexpr int kABufs = kDone;                           // blocks of decoded weights: 32 columns each
 
+__device__ unsigned lost_waits;                     // bits of all waits that have run out on this device
+
 struct __align__(1024) TileSmem {
     uint8_t b[kStages][kStageBytes];
     uint8_t codes[kCodeGroups][128 * 128];          // 128 rows x 4 blocks (1-bit: 64 bytes a row), swizzled
@@ -197,7 +199,7 @@ __device__ __forceinline__ void wait_slow(TileSmem &sm, uint32_t bar, uint32_t p
         if (*reinterpret_cast<volatile uint32_t *>(&sm.dead)) return;
         if (clock64() - t0 > kWaitBudgetCycles) {
             *reinterpret_cast<volatile uint32_t *>(&sm.dead) = 1;
-            atomicOr(err, bit);
+            record_wait(err, &lost_waits, bit);
             return;
         }
     }
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
         if (lane == 0) {
             tc_commit(smem_u32(&sm.drain));
-            if (!mbar_wait(smem_u32(&sm.drain), 0)) atomicOr(args.err, 1u << 4);
+            if (!mbar_wait(smem_u32(&sm.drain), 0)) record_wait(args.err, &lost_waits, 1u << 4);
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
             // none of this CTA's copies may be in flight when it leaves
             for (int j = max(it - kStages, 0); j < it; ++j)
-                if (!mbar_wait(smem_u32(&sm.b_full[j % kStages]), (j / kStages) & 1)) atomicOr(args.err, 1u << 8);
+                if (!mbar_wait(smem_u32(&sm.b_full[j % kStages]), (j / kStages) & 1)) record_wait(args.err, &lost_waits, 1u << 8);
         } else if (warp == 6) {
             // packed weights: two boxes of 64 rows, gate and up or one matrix's 128
             bool ok = true;
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 }
             }
             for (int j = max(it - kCodeGroups, 0); j < it; ++j)
-                if (!mbar_wait(smem_u32(&sm.c_full[j % kCodeGroups]), (j / kCodeGroups) & 1)) atomicOr(args.err, 1u << 11);
+                if (!mbar_wait(smem_u32(&sm.c_full[j % kCodeGroups]), (j / kCodeGroups) & 1)) record_wait(args.err, &lost_waits, 1u << 11);
         } else {
             // activation scales of four blocks at a time, each lane six rows
             constexpr int kRows = kCols / 32;
@@ -615,6 +617,10 @@ cudaError_t launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *e
 }
 
 }  // namespace
+
+cudaError_t moe_tile_waits(unsigned *bits, cudaStream_t stream) {
+    return cudaMemcpyFromSymbolAsync(bits, lost_waits, sizeof(*bits), 0, cudaMemcpyDeviceToHost, stream);
+}
 
 cudaError_t moe_tile_launch(const MoeProduct &p, int above, uint8_t *operand, unsigned *err, cudaStream_t stream) {
     if (p.h != nullptr)

@@ -32,7 +32,7 @@ EXPORTS = ("tq_status_string", "tq_last_cuda_error", "tq_set_engine", "tq_get_en
            "tq_ffn_step", "tq_ffn_stage_input", "tq_ffn_stage_gateup", "tq_ffn_stage_down",
            "tq_ffn_stack", "tq_ffn_static_workspace_bytes", "tq_ffn_step_static",
            "tq_rmsnorm_bf16",
-           "tq_add_rmsnorm_rotq", "tq_moe_route", "tq_moe_workspace_bytes", "tq_moe_plan",
+           "tq_add_rmsnorm_rotq", "tq_moe_route", "tq_moe_workspace_bytes", "tq_moe_read_error_word", "tq_moe_plan",
            "tq_moe_gemv", "tq_moe_gateup", "tq_moe_combine", "tq_moe_ffn",
            "tq_lifecycle_init", "tq_lifecycle_load", "tq_lifecycle_copy", "tq_lifecycle_alloc",
            "tq_lifecycle_free", "tq_lifecycle_poll", "tq_lifecycle_release", "tq_lifecycle_destroy")
@@ -133,6 +133,7 @@ def load():
             L.tq_moe_route.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp]
             L.tq_moe_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
             L.tq_moe_workspace_bytes.restype = sz
+            L.tq_moe_read_error_word.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
             L.tq_moe_plan.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
             L.tq_moe_gemv.argtypes = [X, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp]
             L.tq_moe_gateup.argtypes = [X, X, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp]
@@ -564,8 +565,18 @@ def moe_workspace(m: int, topk: int, experts: int, hidden: int = 0, inter: int =
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
+def moe_read_error_word(stream=None) -> int:
+    """The bounded waits that have run out in any moe_* call so far, those without a workspace of
+    the caller's among them: synchronises the stream; raises TQError with status TQ_ERR_TIMEOUT
+    when there is one, else returns 0."""
+    v = ctypes.c_uint32(0)
+    _check("tq_moe_read_error_word", load().tq_moe_read_error_word(ctypes.byref(v), _stream(stream)))
+    return int(v.value)
+
+
 def _moe_scratch(nbytes: int, device):
-    """A workspace for one call.  Of all of it only the error word has to be zero."""
+    """A workspace for one call.  Of all of it only the error word has to be zero; what a wait sets
+    there goes with it, but not what moe_read_error_word reads."""
     import torch
     if nbytes == 0:
         raise ValueError("sizes out of range for a workspace")

@@ -4,6 +4,11 @@
 #define mbar_arrive_expect_tx(bar, bytes) (mbar_arrive_expect_tx)(bar, (bytes) + 16)
 #include "tq_moe_stream.cu"
 
+extern "C" int lost_waits(unsigned *bits) {
+    const cudaError_t e = tq::moe_stream_waits(bits, nullptr);
+    return e != cudaSuccess ? e : cudaStreamSynchronize(nullptr);
+}
+
 extern "C" int stalled_product(const uint8_t *codes, const uint16_t *scales, int experts, int n, int k, int fmt,
                                const int8_t *q, const float *s, const int *offsets, int slots, float *y, unsigned *err) {
     tq::MoeProduct p{};

@@ -129,3 +129,26 @@ def test_weights_can_be_copied_and_pickled(launched):
         assert (other.experts, other.n, other.k, other.fmt) == (E, I, H, 0) and other.codes.shape == w.codes.shape
     w.codes.data_ptr = lambda: 0x2000
     assert w.c_struct().codes == 0x2000 and w.c_struct().scales == 0x1000
+
+
+def test_the_library_keeps_the_bits_of_lost_waits(monkeypatch):
+    """A call without a workspace drops the one that it took; its waits are still to be seen."""
+    from ternary_weight_dp4a_gb300 import build
+    build.build()
+    assert tq.load().tq_moe_read_error_word(None, 0) == 1                   # nowhere to put them
+
+    class Library:
+        def tq_moe_read_error_word(self, value, stream):
+            value._obj.value = 1 << 12
+            return tq.TQ_ERR_TIMEOUT
+
+        def tq_status_string(self, status):
+            return b"timeout"
+
+        def tq_last_cuda_error(self):
+            return 0
+
+    monkeypatch.setattr(tq, "load", lambda: Library())
+    with pytest.raises(tq.TQError) as e:
+        tq.moe_read_error_word(Stream())
+    assert e.value.status == tq.TQ_ERR_TIMEOUT

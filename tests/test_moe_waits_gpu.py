@@ -32,6 +32,8 @@ def test_the_stream_kernel_ends_when_its_copies_do_not(tq, stalled, fmt):  # noq
     offsets = cuda(np.arange(experts + 1, dtype=np.int32) * rows)
     y = torch.full((experts * rows, n), -1.0, device="cuda")
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bits = ctypes.c_uint32(0)
+    assert stalled.lost_waits(ctypes.byref(bits)) == 0 and bits.value in (0, 1 << 12)
     torch.cuda.synchronize()
     t0 = time.perf_counter()
     assert stalled.stalled_product(codes.data_ptr(), scales.data_ptr(), experts, n, k, fmt, q.data_ptr(), s.data_ptr(),
@@ -40,8 +42,11 @@ def test_the_stream_kernel_ends_when_its_copies_do_not(tq, stalled, fmt):  # noq
     took = time.perf_counter() - t0
     assert int(err) == 1 << 12 and (y == -1.0).all()
     assert 0.2 < took < 5.0, took
+    del err                                                          # the bit outlives the caller's word
+    assert stalled.lost_waits(ctypes.byref(bits)) == 0 and bits.value == 1 << 12
     # the device is as usable as before
     w = tq.PackedExperts(codes, scales, experts, n, k, fmt)
     order = cuda(np.arange(experts * rows, dtype=np.int32))
     got = tq.moe_gemv(w, q, s, tq.MoePlan(offsets, order, order))
     assert torch.isfinite(got).all() and (got != -1.0).all()
+    assert tq.moe_read_error_word() == 0                             # (the word of the library, not of this test's copy)
