@@ -247,8 +247,9 @@ __global__ void __maxnreg__(G == 1 ? 48 : 64) add_rmsnorm_rotq_kernel(const void
         lo = __shfl_sync(kFull, lo, 0);
     }
     float inv;
-    // (with an ordinary eps small sums are fine, too: what they lose is far below eps's last bit)
-    if ((hi > 1e-25f || eps > 1e-12f) && hi < 1e37f && eps < 1e30f) {
+    // (with an ordinary eps small sums are fine, too: what they lose is far below eps's last bit;
+    // beyond 1e33 the low half of 1 / mean is subnormal and loses bits that the root needs)
+    if ((hi > 1e-25f || eps > 1e-12f) && hi < 1e33f && eps < 1e30f) {
         inv = inv_rms(hi, lo, static_cast<float>(n), eps);
     } else {                                                     // out of binary32's comfortable range: in 64 bits
         double acc = 0.0;
