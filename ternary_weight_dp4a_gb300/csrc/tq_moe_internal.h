@@ -12,6 +12,11 @@
 
 namespace tq {
 
+// Reading what earlier work of the stream has written.  These kernels start while it may still
+// run, so it is not read-only for as long as they do: its pointers are not const __restrict__
+// and its loads not __ldg, either of which would let a load stand before pdl_wait() or be
+// served from a line that was cached before.  (Weights, and what a kernel only writes, may be.)
+
 // Workspace: err u32 | operand (the tile kernel's copy of a product's input:
 // 2 bytes per value and slot, and the scales) | hist (the sort's
 // counts per chunk of slots, and their sums) | offsets | rows | pos | h | hq | hs | y.

@@ -291,7 +291,7 @@ __global__ void __maxnreg__(G == 1 ? 48 : 64) add_rmsnorm_rotq_kernel(const void
 }
 
 // tq_rotate_quant of `blocks` 128-blocks that lie behind one another: four per warp.
-__global__ void __launch_bounds__(256) rotq_kernel(const uint16_t *__restrict__ x, int64_t blocks, int8_t *__restrict__ q,
+__global__ void __launch_bounds__(256) rotq_kernel(const uint16_t *x, int64_t blocks, int8_t *__restrict__ q,
                                                    float *__restrict__ s) {
     pdl_launch_dependents();
     pdl_wait();
@@ -327,9 +327,9 @@ cudaError_t norm_launch(const void *res, const void *delta, const uint16_t *gamm
 // by memory: 4096 x 5120, top 8: 111 us, 6.4 TB/s.
 // ---------------------------------------------------------------------------
 template <bool OB>
-__global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ y, const int *__restrict__ pos,
-                                                      const float *__restrict__ weights, int64_t quads, int topk,
-                                                      int slots, int n, void *out) {
+__global__ void __launch_bounds__(256) combine_kernel(const float *y, const int *pos, const float *weights,
+                                                      int64_t quads, int topk, int slots, int n,
+                                                      void *__restrict__ out) {
     pdl_launch_dependents();
     pdl_wait();
     const int per_row = n / 4;
@@ -339,10 +339,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
         const int c = static_cast<int>(i - t * per_row) * 4;
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int j = 0; j < topk; ++j) {
-            const int p = __ldg(pos + t * topk + j);
+            const int p = pos[t * topk + j];
             if (p < 0 || p >= slots) continue;
-            const float w = __ldg(weights + t * topk + j);
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(y + static_cast<int64_t>(p) * n + c));
+            const float w = weights[t * topk + j];
+            const float4 v = *reinterpret_cast<const float4 *>(y + static_cast<int64_t>(p) * n + c);
             acc[0] = __fmaf_rn(w, v.x, acc[0]);
             acc[1] = __fmaf_rn(w, v.y, acc[1]);
             acc[2] = __fmaf_rn(w, v.z, acc[2]);

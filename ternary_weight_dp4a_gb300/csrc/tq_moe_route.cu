@@ -31,7 +31,7 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // warp-wide maximum over the keys and one minimum over the indices that have it, so the
 // choices' chain of reductions is the bound: 16384 tokens, top 8 of 256: 16.7 us, 8 tokens 2.1.
 template <bool BF16, int PER>
-__global__ void __launch_bounds__(256) route_kernel(const void *__restrict__ logits, int m, int experts, int topk,
+__global__ void __launch_bounds__(256) route_kernel(const void *logits, int m, int experts, int topk,
                                                     int renorm, int *__restrict__ ids, float *__restrict__ weights) {
     pdl_launch_dependents();
     pdl_wait();
@@ -107,7 +107,7 @@ __device__ __forceinline__ int slot_expert(const int *ids, int64_t slot, int64_t
     return e >= 0 && e < experts ? e : -1;
 }
 
-__global__ void __launch_bounds__(kPlanChunk) count_kernel(const int *__restrict__ ids, int64_t slots, int experts,
+__global__ void __launch_bounds__(kPlanChunk) count_kernel(const int *ids, int64_t slots, int experts,
                                                            int *__restrict__ hist) {
     extern __shared__ int count[];
     pdl_launch_dependents();
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kPlanChunk) count_kernel(const int *__restrict
 
 // hist [chunks][experts] -> exclusive sums over the chunks; the whole sums go behind them.
 // A CTA takes 32 experts, its warps a run of the chunks each.
-__global__ void __launch_bounds__(1024) scan_kernel(int *__restrict__ hist, int chunks, int experts) {
+__global__ void __launch_bounds__(1024) scan_kernel(int *hist, int chunks, int experts) {
     __shared__ int sum[32][33];
     pdl_launch_dependents();
     pdl_wait();
@@ -163,8 +163,8 @@ constexpr size_t place_smem(int experts) {
     return (experts + 1 + 32) * sizeof(int) + static_cast<size_t>(32) * experts * sizeof(uint16_t);
 }
 
-__global__ void __launch_bounds__(kPlanChunk) place_kernel(const int *__restrict__ ids, int64_t slots, int experts,
-                                                           int topk, const int *__restrict__ hist,
+__global__ void __launch_bounds__(kPlanChunk) place_kernel(const int *ids, int64_t slots, int experts,
+                                                           int topk, const int *hist,
                                                            int *__restrict__ offsets, int *__restrict__ rows,
                                                            int *__restrict__ pos) {
     extern __shared__ int smem[];

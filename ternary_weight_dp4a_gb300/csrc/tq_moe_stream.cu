@@ -251,9 +251,9 @@ __device__ __forceinline__ int activation_row(const MoeProduct &p, int slot) {
 __device__ __forceinline__ RowPart load_part(const MoeProduct &p, int a, int c) {
     RowPart v;
     const uint4 *qp = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(a) * p.k + c * 32);
-    v.q0 = __ldg(qp);
-    v.q1 = __ldg(qp + 1);
-    v.s = (c & 3) == 0 ? __ldg(p.s + static_cast<int64_t>(a) * (p.k / kBlock) + (c >> 2)) : 0.0f;
+    v.q0 = qp[0];
+    v.q1 = qp[1];
+    v.s = (c & 3) == 0 ? p.s[static_cast<int64_t>(a) * (p.k / kBlock) + (c >> 2)] : 0.0f;
     return v;
 }
 

@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     float4 v[kRows];
 #pragma unroll
                     for (int i = 0; i < kRows; ++i)
-                        v[i] = __ldg(reinterpret_cast<const float4 *>(src + min(lane + 32 * i, cols - 1) * ld + b));
+                        v[i] = *reinterpret_cast<const float4 *>(src + min(lane + 32 * i, cols - 1) * ld + b);
                     warp_wait<64>(sm, smem_u32(&sm.s_empty[slot]), ((it / kGroups) & 1) ^ 1, args.err, 1u << 6);
 #pragma unroll
                     for (int i = 0; i < kRows; ++i) {
@@ -552,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 // (measured), four times slower than the MMAs use them up.
 // ---------------------------------------------------------------------------
 template <int FMT>
-__global__ void __launch_bounds__(256) operand_kernel(const int8_t *__restrict__ q, const int *__restrict__ rows,
-                                                      const int *__restrict__ offsets, int experts, int m, int slots,
-                                                      int k, uint8_t *__restrict__ out, const float *__restrict__ s,
+__global__ void __launch_bounds__(256) operand_kernel(const int8_t *q, const int *rows, const int *offsets,
+                                                      int experts, int m, int slots, int k,
+                                                      uint8_t *__restrict__ out, const float *s,
                                                       float *__restrict__ s_out) {
     pdl_launch_dependents();
     pdl_wait();
@@ -565,14 +565,14 @@ __global__ void __launch_bounds__(256) operand_kernel(const int8_t *__restrict__
         const int r = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<int64_t>(r) * per_row);
         const int a = min(max(rows != nullptr ? rows[r] : r, 0), m - 1);
         const uint4 *src = reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(a) * k + c * 32);
-        const uint4 q0 = __ldg(src), q1 = __ldg(src + 1);
+        const uint4 q0 = src[0], q1 = src[1];
         const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
         uint32_t o[8], hi[8], lo[8];
         stage_order<FMT>(w, o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) split4_whole(o[j], hi[j], lo[j]);
         if ((c & 3) == 0)
-            s_out[static_cast<int64_t>(r) * ((k / kBlock + 3) / 4 * 4) + (c >> 2)] = __ldg(s + static_cast<int64_t>(a) * (k / kBlock) + (c >> 2));
+            s_out[static_cast<int64_t>(r) * ((k / kBlock + 3) / 4 * 4) + (c >> 2)] = s[static_cast<int64_t>(a) * (k / kBlock) + (c >> 2)];
         uint8_t *dst = out + (i >> 2) * 256 + (i & 3) * 32;
         *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
