@@ -471,12 +471,13 @@ def _tensor(device, name: str, t, dtypes, shape=None):
     return t.data_ptr()
 
 
-def _weights(device, **weights):
-    """Check that the matrices of a call are on the device where it runs."""
-    for name, w in weights.items():
-        if w.codes.get_device() != device or w.scales.get_device() != device:
-            raise ValueError(f"{name}: weights on the current device are needed, got codes on {w.codes.device}, "
-                             f"scales on {w.scales.device}")
+def _matrix(device, name: str, w: PackedExperts) -> _Experts:
+    """The weights of a call, checked to be on the device where it runs."""
+    codes, scales = w.codes, w.scales
+    if codes.get_device() != device or scales.get_device() != device:
+        raise ValueError(f"{name}: weights on the current device are needed, got codes on {codes.device}, "
+                         f"scales on {scales.device}")
+    return _Experts(codes.data_ptr(), scales.data_ptr(), w.experts, w.n, w.k, w.fmt)
 
 
 def pack_experts(codes, fmt: int, scales, stream=None) -> PackedExperts:
@@ -632,14 +633,13 @@ def moe_gemv(w: PackedExperts, q, s, plan: MoePlan, gather: bool = False, y=None
     per sorted slot, or with ``gather`` one per token, picked by plan.rows."""
     import torch
     dev, p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(w, q, s, plan, gather, workspace, stream)
-    _weights(dev, w=w)
     if y is None:
         y = _new(stream, torch.empty, (slots, w.n), dtype=torch.float32, device=q.device)
         p_y = y.data_ptr()
     else:
         p_y = _tensor(dev, "y", y, (torch.float32,), (slots, w.n))
     _check("tq_moe_gemv", load().tq_moe_gemv(
-        w.c_struct(), p_q, p_s, m, p_rows, p_offsets, slots, p_y, workspace.data_ptr(), workspace.numel(),
+        _matrix(dev, "w", w), p_q, p_s, m, p_rows, p_offsets, slots, p_y, workspace.data_ptr(), workspace.numel(),
         _stream(stream)))
     return y
 
@@ -651,15 +651,14 @@ def moe_gateup(gate: PackedExperts, up: PackedExperts, q, s, plan: MoePlan, gath
     sorted slot."""
     import torch
     dev, p_q, p_s, p_rows, p_offsets, m, slots, workspace = _moe_inputs(gate, q, s, plan, gather, workspace, stream)
-    _weights(dev, gate=gate, up=up)
     if h is None:
         h = _new(stream, torch.empty, (slots, gate.n), dtype=torch.bfloat16, device=q.device)
         p_h = h.data_ptr()
     else:
         p_h = _tensor(dev, "h", h, (torch.bfloat16,), (slots, gate.n))
     _check("tq_moe_gateup", load().tq_moe_gateup(
-        gate.c_struct(), up.c_struct(), p_q, p_s, m, p_rows, p_offsets, slots, p_h, workspace.data_ptr(),
-        workspace.numel(), _stream(stream)))
+        _matrix(dev, "gate", gate), _matrix(dev, "up", up), p_q, p_s, m, p_rows, p_offsets, slots, p_h,
+        workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return h
 
 
@@ -704,10 +703,9 @@ def moe_ffn(gate: PackedExperts, up: PackedExperts, down: PackedExperts, q, s, i
     if workspace is None:
         workspace = _new(stream, _moe_scratch, moe_workspace_bytes(m, topk, gate.experts, hidden, gate.n), q.device)
     p_ws = _tensor(dev, "workspace", workspace, (torch.uint8,))
-    _weights(dev, gate=gate, up=up, down=down)
     _check("tq_moe_ffn", load().tq_moe_ffn(
-        gate.c_struct(), up.c_struct(), down.c_struct(), p_q, p_s, p_ids, p_weights, m, topk, p_out,
-        int(out.dtype == torch.bfloat16), p_ws, workspace.numel(), _stream(stream)))
+        _matrix(dev, "gate", gate), _matrix(dev, "up", up), _matrix(dev, "down", down), p_q, p_s, p_ids, p_weights,
+        m, topk, p_out, int(out.dtype == torch.bfloat16), p_ws, workspace.numel(), _stream(stream)))
     return out
 
 
