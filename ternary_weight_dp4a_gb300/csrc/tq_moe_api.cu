@@ -81,14 +81,19 @@ tq::MoeProduct product(const tq_experts *w, const tq_experts *up, const int8_t *
 // Experts with more rows than this run on the tile kernel, the others on the stream
 // kernel; the bits are the same.  A block of 128 weight rows costs the tile kernel about 2000
 // cycles for any number of activation rows, the stream kernel 300 for every eight; the
-// tile kernel's launches are paid for anyway once there is one.  Gate/up with 24, 32, 40 and
-// 48: 400 tokens, top 8 of 64, 125, 120, 114, 126 us; top 8 of 128, 106, 110, 103, 104; 256
-// tokens, top 2 of 8, 67, 79, 98, 105; from 1000 tokens on all are alike.
+// tile kernel's launches are paid for anyway once there is one.  Both grow alike with n and k.
+// With 24, 32 and 48 (us; gate/up 2048 -> 2 x 1024, 5120 -> 2 x 1536, down 1024 -> 2048,
+// 1536 -> 5120; even routing): 400 tokens, top 8 of 64, 127 127 148, 396 397 435, 75 75 83, 221
+// 222 236; top 8 of 128, where most experts are near the border, 194 174 160, 585 524 514, 112
+// 95 88, 334 273 262; from 1000 tokens on all are alike.
 constexpr int kTileAbove = 32;
 // The tile kernel's launches cost 10 us and its turns are long (2000 cycles for each of k/128
-// blocks), so it is left out where few experts can have that many rows: gate/up of 96
-// tokens, top 8 of 128, takes 53 us without and 74 with it, of 256 tokens, top 4 of 32, 169
-// and 187; but of 400 tokens 117 and 104, 249 and 224.
+// blocks), so it is left out where few experts can have that many rows.  Without and with it, in
+// the same four: 96 tokens, top 8 of 128, 57 65, 178 187, 30 38, 91 99; 256 tokens, top 4 of 32,
+// 56 74, 170 213, 29 44, 85 104; top 2 of 8, 46 29, 165 80, 30 20, 48 47; 1000 tokens, top 8 of
+// 64, 324 138, 1111 423, 169 81, 559 232.  Slots say nothing of a strong skew: all tokens on
+// one of 64 experts, 200 of them, 20 27, 45 47, 11 20, 23 23, and 1000, which are left out, too, 50
+// 30, 152 49, 27 21, 77 37.  At top 8 of 128 the 400 tokens lose, 151 174, 500 524, 79 95, 253 273.
 constexpr int kTileSlots = 2560;
 
 tq_status run_product(const tq::MoeProduct &p, void *workspace, cudaStream_t stream) {

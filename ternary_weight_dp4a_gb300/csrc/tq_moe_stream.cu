@@ -25,7 +25,7 @@
 // 512 weights share a scheduler at 10.5 cycles (8.0 for the matrix instruction by
 // itself), what prepares and folds them comes on top: 267 (1-bit) and 313 (2-bit)
 // cycles per warp for 32 weight rows and a block of 128.  Memory would take a quarter to
-// a half of that: 8 tokens, top 4 of 32 experts, 5120 x 1536 take 22.4 us, two less with
+// a half of that: 8 tokens, top 4 of 32 experts, 5120 x 1536 take 22.8 us, two less with
 // all weights in L2, 6.4 for the bytes.  16 rows at a time (two matrix instructions for a
 // masked pair) gain 5% where experts have many rows and lose 22% where they have few.
 //

@@ -19,9 +19,12 @@
 // a block takes about 2000 cycles, and that is the bound, not the tensor core, nor memory.
 // Two accumulators of 192 columns leave room for four blocks of A, and a third of them for
 // each of three warps to a quarter of the lanes (two of 224: two blocks of A, two warps;
-// with the shorter waits that came with it 465 us, now 408, for the gate/up below).
-// 4096 tokens, top 8 of 64 experts, 2 x 1024 x 2048: 413 us, 333 T code products/s (twice
-// as many e4m3 ones).
+// with the shorter waits that came with it 465 us, 408 then, for the gate/up below).
+// 4096 tokens, top 8 of 64 experts, 2 x 1024 x 2048: 417 us, 330 T code products/s (twice
+// as many e4m3 ones); 2 x 1536 x 5120 with its down product: 1252 + 734 us, 389 T/s.  The fold
+// keeps 32 pairs of sums in 112 registers: a 64-byte stack, 108 to 116 bytes of spill stores and 200 to
+// 216 of loads.  Activation rows come to every CTA by its own copies; shared by the two CTAs of
+// a cluster, which halved what L2 delivers, they took 1% less time.
 //
 // Warps: 0-3 decode weights, 4 issues MMAs, 5 copies activation rows (TMA), 6 packed
 // weights (TMA), 7 activation scales, 8-19 fold (a quarter of the lanes and a third of the
