@@ -1,0 +1,32 @@
+// tq_q4_internal.h -- what the translation units of the 4-bit products share.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "tq.h"
+#include "tq_q4.h"
+
+namespace tq {
+
+constexpr int kQ4Strip = 16;            // weight rows per strip
+constexpr int kQ4ChunkBytes = 1024;     // a strip's codes of 128 values of k
+
+constexpr int64_t q4_strips(int64_t n) { return (n + kQ4Strip - 1) / kQ4Strip; }
+
+// One product (mats == 1: y), or gate and up into h (mats == 2).
+struct Q4Product {
+    const uint8_t *codes[2];
+    const uint16_t *scales[2];
+    const uint16_t *mins[2];
+    int mats, n, k, group;
+    const uint16_t *x;
+    int m;
+    void *y;                // [m][n]: fp32, or bf16 where y_bf16 (h: bf16)
+    bool y_bf16;
+};
+
+cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const uint16_t *mins, int n, int k, int group,
+                           uint8_t *out_codes, uint16_t *out_scales, uint16_t *out_mins, cudaStream_t stream);
+cudaError_t q4_stream_launch(const Q4Product &p, cudaStream_t stream);
+
+}  // namespace tq

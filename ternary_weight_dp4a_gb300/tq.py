@@ -1,4 +1,4 @@
-"""ctypes binding of libtq (include/tq.h, include/tq_moe.h).  Argument marshalling only.
+"""ctypes binding of libtq (include/tq.h, tq_moe.h, tq_q4.h, tq_sample.h).  Argument marshalling only.
 
 Every function takes torch CUDA tensors (PyTorch provides device memory and
 streams), passes raw device pointers to the C ABI and raises ``TQError`` on a
@@ -24,7 +24,7 @@ TQ_ERR_TIMEOUT = 6
 BLOCK = 128
 MAX_ROWS = 64
 
-# every entry point include/tq.h, include/tq_moe.h and include/tq_lifecycle.h declare
+# every entry point that the headers in include/ declare
 EXPORTS = ("tq_status_string", "tq_last_cuda_error", "tq_set_engine", "tq_get_engine",
            "tq_error_status", "tq_read_error_word", "tq_workspace_init", "tq_pack_weights",
            "tq_rotate_quant", "tq_gemv_workspace_bytes", "tq_gemv", "tq_ffn_gateup",
@@ -34,6 +34,7 @@ EXPORTS = ("tq_status_string", "tq_last_cuda_error", "tq_set_engine", "tq_get_en
            "tq_rmsnorm_bf16",
            "tq_add_rmsnorm_rotq", "tq_moe_route", "tq_moe_workspace_bytes", "tq_moe_read_error_word", "tq_moe_plan",
            "tq_moe_gemv", "tq_moe_gateup", "tq_moe_combine", "tq_moe_ffn",
+           "tq_q4_codes_bytes", "tq_q4_scales_bytes", "tq_q4_pack", "tq_q4_gemv", "tq_q4_gateup", "tq_sample",
            "tq_lifecycle_init", "tq_lifecycle_load", "tq_lifecycle_copy", "tq_lifecycle_alloc",
            "tq_lifecycle_free", "tq_lifecycle_poll", "tq_lifecycle_release", "tq_lifecycle_destroy")
 
@@ -58,6 +59,11 @@ class _Weight(ctypes.Structure):
 class _Experts(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("experts", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("fmt", ctypes.c_int32)]
+
+
+class _Q4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("mins", ctypes.c_void_p),
+                ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32)]
 
 
 # tq_lifecycle.h
@@ -139,6 +145,15 @@ def load():
             L.tq_moe_gateup.argtypes = [X, X, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp]
             L.tq_moe_combine.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i32, vp]
             L.tq_moe_ffn.argtypes = [X, X, X, vp, vp, vp, vp, i32, i32, vp, i32, vp, sz, vp]
+            Q = ctypes.POINTER(_Q4)
+            L.tq_q4_codes_bytes.argtypes = [i32, i32]
+            L.tq_q4_codes_bytes.restype = sz
+            L.tq_q4_scales_bytes.argtypes = [i32, i32, i32]
+            L.tq_q4_scales_bytes.restype = sz
+            L.tq_q4_pack.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+            L.tq_q4_gemv.argtypes = [Q, vp, i32, vp, i32, vp]
+            L.tq_q4_gateup.argtypes = [Q, Q, vp, i32, vp, vp]
+            L.tq_sample.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
             LC = ctypes.POINTER(_Lifecycle)
             L.tq_lifecycle_init.argtypes = [LC, ctypes.POINTER(_LcConfig), ctypes.POINTER(_LcHooks)]
             L.tq_lifecycle_load.argtypes = [LC]
@@ -155,7 +170,7 @@ def load():
             L.tq_lifecycle_destroy.restype = None
             for name in EXPORTS:
                 if name not in ("tq_status_string", "tq_last_cuda_error", "tq_ffn_workspace_bytes",
-                                "tq_gemv_workspace_bytes", "tq_moe_workspace_bytes",
+                                "tq_gemv_workspace_bytes", "tq_moe_workspace_bytes", "tq_q4_codes_bytes", "tq_q4_scales_bytes",
                                 "tq_ffn_workspace_error_offset", "tq_ffn_static_workspace_bytes", "tq_lifecycle_copy", "tq_lifecycle_alloc",
                                 "tq_lifecycle_free", "tq_lifecycle_release", "tq_lifecycle_destroy"):
                     getattr(L, name).restype = ctypes.c_int
@@ -707,6 +722,139 @@ def moe_ffn(gate: PackedExperts, up: PackedExperts, down: PackedExperts, q, s, i
         _matrix(dev, "gate", gate), _matrix(dev, "up", up), _matrix(dev, "down", down), p_q, p_s, p_ids, p_weights,
         m, topk, p_out, int(out.dtype == torch.bfloat16), p_ws, workspace.numel(), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights (include/tq_q4.h)
+# ---------------------------------------------------------------------------
+
+@dataclass(frozen=True)
+class PackedQ4:
+    """A packed matrix of 4-bit weights on the device, laid out as include/tq_q4.h says, rows padded to
+    a multiple of 16: codes uint8 [rows * k/2], scales and mins (or None) float16 [rows * k/group]."""
+    codes: "object"
+    scales: "object"
+    mins: "object"
+    n: int
+    k: int
+    group: int
+
+    def __post_init__(self):
+        import torch
+        if self.n < 1 or self.k < BLOCK or self.k % BLOCK or self.group not in (32, 64, 128):
+            raise ValueError(f"n {self.n}, k {self.k}, group {self.group}: k in whole blocks of {BLOCK}, groups of 32, 64 or 128")
+        rows = -(-self.n // 16) * 16
+        _tensor(None, "codes", self.codes, (torch.uint8,), (rows * self.k // 2,))
+        _tensor(None, "scales", self.scales, (torch.float16,), (rows * (self.k // self.group),))
+        if self.mins is not None:
+            _tensor(None, "mins", self.mins, (torch.float16,), (rows * (self.k // self.group),))
+
+    def c_struct(self) -> _Q4:
+        return _Q4(self.codes.data_ptr(), self.scales.data_ptr(), 0 if self.mins is None else self.mins.data_ptr(),
+                   self.n, self.k, self.group)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 2 * self.scales.numel() * (1 if self.mins is None else 2)
+
+
+def _q4(device, name: str, w: PackedQ4) -> _Q4:
+    """The weights of a call, checked to be on the device where it runs."""
+    for part in (w.codes, w.scales, w.mins):
+        if part is not None and part.get_device() != device:
+            raise ValueError(f"{name}: weights on the current device are needed, got {part.device}")
+    return w.c_struct()
+
+
+def pack_q4(codes, scales, mins=None, stream=None) -> PackedQ4:
+    """codes: uint8 CUDA tensor [n][k] with entries 0 .. 15; scales: float16 [n][k/group] for groups of
+    32, 64 or 128; a weight is scale * (code - 8), or with mins (as scales) scale * code - min."""
+    import torch
+    dev = _device()
+    p_codes = _tensor(dev, "codes", codes, (torch.uint8,))
+    n, k = codes.shape
+    p_scales = _tensor(dev, "scales", scales, (torch.float16,))
+    if scales.dim() != 2 or scales.shape[0] != n or scales.shape[1] < 1 or k % scales.shape[1]:
+        raise ValueError(f"scales: [{n}][k/group] are needed, got {tuple(scales.shape)}")
+    group = k // scales.shape[1]
+    p_mins = 0 if mins is None else _tensor(dev, "mins", mins, (torch.float16,), scales.shape)
+    L = load()
+    nbytes = L.tq_q4_codes_bytes(n, k)
+    entries = L.tq_q4_scales_bytes(n, k, group) // 2
+    if nbytes == 0 or entries == 0:
+        raise ValueError(f"sizes out of range (n {n}, k {k}, group {group})")
+    out = _new(stream, torch.empty, nbytes, dtype=torch.uint8, device=codes.device)
+    out_scales = _new(stream, torch.empty, entries, dtype=torch.float16, device=codes.device)
+    out_mins = None if mins is None else _new(stream, torch.empty, entries, dtype=torch.float16, device=codes.device)
+    _check("tq_q4_pack", L.tq_q4_pack(p_codes, p_scales, p_mins, n, k, group, out.data_ptr(), out_scales.data_ptr(),
+                                      0 if mins is None else out_mins.data_ptr(), _stream(stream)))
+    return PackedQ4(out, out_scales, out_mins, n, k, group)
+
+
+def q4_gemv(w: PackedQ4, x, y=None, dtype=None, stream=None):
+    """x bf16 [m][k] -> x W^T [m][n] (float32 unless dtype or y says bf16)."""
+    import torch
+    dev = _device()
+    p_x = _tensor(dev, "x", x, (torch.bfloat16,))
+    m, k = x.shape
+    if k != w.k:
+        raise ValueError(f"x: rows of {w.k} values are needed, got {k}")
+    if y is None:
+        y = _new(stream, torch.empty, (m, w.n), dtype=dtype or torch.float32, device=x.device)
+    p_y = _tensor(dev, "y", y, (torch.float32, torch.bfloat16), (m, w.n))
+    _check("tq_q4_gemv", load().tq_q4_gemv(_q4(dev, "w", w), p_x, m, p_y, int(y.dtype == torch.bfloat16), _stream(stream)))
+    return y
+
+
+def q4_gateup(gate: PackedQ4, up: PackedQ4, x, h=None, stream=None):
+    """x bf16 [m][k] -> SiLU(gate) * up as bf16 [m][n]."""
+    import torch
+    dev = _device()
+    p_x = _tensor(dev, "x", x, (torch.bfloat16,))
+    m, k = x.shape
+    if k != gate.k:
+        raise ValueError(f"x: rows of {gate.k} values are needed, got {k}")
+    if h is None:
+        h = _new(stream, torch.empty, (m, gate.n), dtype=torch.bfloat16, device=x.device)
+        p_h = h.data_ptr()
+    else:
+        p_h = _tensor(dev, "h", h, (torch.bfloat16,), (m, gate.n))
+    _check("tq_q4_gateup", load().tq_q4_gateup(_q4(dev, "gate", gate), _q4(dev, "up", up), p_x, m, p_h, _stream(stream)))
+    return h
+
+
+# ---------------------------------------------------------------------------
+# sampling (include/tq_sample.h)
+# ---------------------------------------------------------------------------
+
+def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, ids=None, probs=None, stream=None):
+    """logits float32 or bf16 [m][vocab], uniform float32 [m] in [0, 1) -> (ids int32 [m], probs float32 [m]):
+    a token for each row and its probability among what the row's settings leave (-1 and 0 for a row
+    without candidates).  temperature, top_p, min_p float32 [m], top_k int32 [m], or None."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    dev = _device()
+    p_logits = _tensor(dev, "logits", logits, (f32, torch.bfloat16))
+    m, vocab = logits.shape
+    row = (m,)
+    p_uniform = _tensor(dev, "uniform", uniform, (f32,), row)
+    p_t = 0 if temperature is None else _tensor(dev, "temperature", temperature, (f32,), row)
+    p_k = 0 if top_k is None else _tensor(dev, "top_k", top_k, (i32,), row)
+    p_p = 0 if top_p is None else _tensor(dev, "top_p", top_p, (f32,), row)
+    p_min = 0 if min_p is None else _tensor(dev, "min_p", min_p, (f32,), row)
+    if ids is None:
+        ids = _new(stream, torch.empty, row, dtype=i32, device=logits.device)
+        p_ids = ids.data_ptr()
+    else:
+        p_ids = _tensor(dev, "ids", ids, (i32,), row)
+    if probs is None:
+        probs = _new(stream, torch.empty, row, dtype=f32, device=logits.device)
+        p_probs = probs.data_ptr()
+    else:
+        p_probs = _tensor(dev, "probs", probs, (f32,), row)
+    _check("tq_sample", load().tq_sample(p_logits, int(logits.dtype == torch.bfloat16), m, vocab, p_t, p_k, p_p, p_min,
+                                         p_uniform, p_ids, p_probs, _stream(stream)))
+    return ids, probs
 
 
 # ---------------------------------------------------------------------------
