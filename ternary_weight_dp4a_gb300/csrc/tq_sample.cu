@@ -13,13 +13,23 @@
 // fp32 numbers (difference by Knuth's TwoSum; product by fused multiply-add), so that the error is
 // 2^-30 of a weight.  fp32 alone would move one border in some thousand draws; binary64 runs at
 // 1/60 of the rate here.
+//
+// A cluster of CTAs has a row, a part of it in each CTA's shared memory; the first CTA finishes.
+//   top_k <= 512: the top_k-th largest of a CTA's threads' maxima bounds the cut from below, so a few
+//     times top_k entries at most are candidates; the first CTA sorts them and does the rest on them.
+//   top_p: a histogram of the weights over 1024 bins, even in the logit, brackets the cut to about 0.1%
+//     of the sum; one pass then adds up the exact weights above the bracket and lists its entries,
+//     and the first CTA sorts those.
+//   the draw: every warp's segment has its sum, the first CTA finds the segment and reads it again.
+// Where candidates do not fit their list (thousands of equal logits, or a top_k beyond), the
+// cut is found by a radix search over the key's bytes, which takes any input.
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "tq.h"
 #include "tq_device.cuh"
-#include "tq_launch.h"
+#include "tq_moe_internal.h"
 #include "tq_sample.h"
 
 namespace tq {
@@ -30,10 +40,19 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 256;
+constexpr int kBins = 1024;                     // of the histogram
+constexpr int kRadix = 256;                     // of the radix search
+constexpr int kLocal = 1024;                    // candidates of one CTA
+constexpr int kList = 4096;                     // candidates of a row, sorted by its first CTA
+constexpr int kSmallK = kThreads;               // top_k up to this: by the threads' maxima
+constexpr float kNats = 24.0f;                  // the histogram's range of ln(weight)
+constexpr float kSlack = 5e-4f;                 // of the estimated sums
 constexpr int kOneBits = 42;                    // the largest weight is 2^42: a sum of 2^20 stays below 2^63
-constexpr uint32_t kKeyNone = 0x007fffffu;      // key of -infinity: no candidate
+constexpr int kPart = 16384;                    // entries per CTA from which a cluster grows
+constexpr int kMostPart = 51200;                // entries that fit into shared memory
 constexpr float kColdest = 1.5777218104420236e-30f;     // 2^-99: below, as 0
+
+typedef unsigned long long u64;
 
 __constant__ uint32_t kExp2[32] = {             // 2^(31 + i/32)
     0x80000000u, 0x82cd8699u, 0x85aac368u, 0x88980e81u, 0x8b95c1e4u, 0x8ea4398bu, 0x91c3d374u, 0x94f4efa9u,
@@ -43,7 +62,7 @@ __constant__ uint32_t kExp2[32] = {             // 2^(31 + i/32)
 
 struct SampleArgs {
     const void *logits;
-    int m, vocab, cluster;
+    int m, vocab, cluster, resident;            // resident: a CTA's part is kept in shared memory
     const float *temperature;
     const int *top_k;
     const float *top_p, *min_p, *uniform;
@@ -52,14 +71,21 @@ struct SampleArgs {
 };
 
 struct Shared {
-    unsigned long long hist[kBins];
-    unsigned long long warp_sum[kWarps];
-    unsigned long long cta_sum;
-    uint32_t cta_max;
+    union {
+        uint32_t hist[kBins];
+        u64 radix[kRadix];
+    };
+    u64 local[kLocal];                          // candidates: key << 32 | ~index
+    u64 warp_sum[kWarps];                       // of the draw's segments
+    u64 best;                                   // key << 32 | ~index of the largest
+    u64 sum_all, sum_above, sum_listed;
+    u64 scan[kWarps];
+    u64 buckets[kMaxCluster * kWarps];
+    u64 rest;
+    uint32_t bound, listed, bin, lo, hi;
+    float least;
     int found;
     uint32_t exp2[32];
-    uint32_t bin;
-    unsigned long long above;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -79,54 +105,66 @@ __device__ __forceinline__ uint32_t peer(const void *p, int rank) {
     return a;
 }
 
-__device__ __forceinline__ unsigned long long ld_peer_u64(const unsigned long long *p, int rank, int cluster) {
+// *p of the cluster's CTA `rank`.
+__device__ __forceinline__ u64 at_peer(const u64 *p, int rank, int cluster) {
     if (cluster == 1) return *p;
-    unsigned long long v;
+    u64 v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)) : "memory");
     return v;
 }
 
-__device__ __forceinline__ uint32_t ld_peer_u32(const uint32_t *p, int rank, int cluster) {
+__device__ __forceinline__ uint32_t at_peer(const uint32_t *p, int rank, int cluster) {
     if (cluster == 1) return *p;
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer(p, rank)) : "memory");
     return v;
 }
 
-__device__ __forceinline__ void st_peer_s32(int *p, int rank, int cluster, int v) {
+__device__ __forceinline__ float at_peer(const float *p, int rank, int cluster) {
+    return __uint_as_float(at_peer(reinterpret_cast<const uint32_t *>(p), rank, cluster));
+}
+
+__device__ __forceinline__ void put_peer(int *p, int rank, int cluster, int v) {
     if (cluster == 1) *p = v;
     else asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer(p, rank)), "r"(v) : "memory");
 }
 
-// Ascending in the logit; -0 is +0, NaN is -infinity, +infinity the largest finite number of the type.
+// A logit as it counts: NaN is -infinity, +infinity the largest finite number of the type, -0 is +0.
 template <bool BF16>
+__device__ __forceinline__ float clean(float l) {
+    return l != l ? -INFINITY : fminf(l, BF16 ? 3.3895313892515355e38f : 3.4028234663852886e38f) + 0.0f;
+}
+
+// Ascending in the (clean) logit.
 __device__ __forceinline__ uint32_t key_of(float l) {
-    if (l != l) return kKeyNone;
-    l = fminf(l, BF16 ? 3.3895313892515355e38f : 3.4028234663852886e38f) + 0.0f;
     const uint32_t b = __float_as_uint(l);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+constexpr uint32_t kKeyNone = 0x007fffffu;      // of -infinity: no candidate
 
 __device__ __forceinline__ float logit_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
+
+__device__ __forceinline__ u64 entry_of(uint32_t key, int i) { return static_cast<u64>(key) << 32 | ~static_cast<uint32_t>(i); }
+__device__ __forceinline__ int index_of(u64 entry) { return static_cast<int>(~static_cast<uint32_t>(entry)); }
 
 // One row's weights.  Logits are halved so that no difference overflows.
 struct Weights {
     float half_max, ch, cl;
     bool equal;                                 // infinite temperature
 
-    __device__ __forceinline__ void set(uint32_t max_key, float t) {
-        half_max = 0.5f * logit_of(max_key);
+    __device__ __forceinline__ void set(float largest, float t) {
+        half_max = 0.5f * largest;
         equal = t > 3.4028234663852886e38f;
         const double c = 2.0 * 1.4426950408889634074 / static_cast<double>(t);
         ch = static_cast<float>(c);
         cl = static_cast<float>(c - static_cast<double>(ch));
     }
 
-    __device__ __forceinline__ unsigned long long of(uint32_t key, const uint32_t *exp2) const {
+    __device__ __forceinline__ u64 of(float logit, const uint32_t *exp2) const {
         if (equal) return 1ull << kOneBits;
-        const float l = 0.5f * logit_of(key), b = -half_max;
+        const float l = 0.5f * logit, b = -half_max;
         const float d = __fadd_rn(l, b);
         const float bp = __fsub_rn(d, l);
         const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(d, bp)), __fsub_rn(b, bp));
@@ -145,72 +183,102 @@ struct Weights {
         const uint32_t w = m + static_cast<uint32_t>(__mulhi(static_cast<int>(m >> 1), __float2int_rn(q * 137438953472.0f)) >> 4);
         // w * 2^(floor(at / 32) - 31), scaled by 2^42 and rounded
         const int down = -(at >> 5);
-        return ((static_cast<unsigned long long>(w) << (kOneBits - 31 + 1) >> min(down, 63)) + 1) >> 1;
+        return ((static_cast<u64>(w) << (kOneBits - 31 + 1) >> min(down, 63)) + 1) >> 1;
     }
 };
 
 // The place in the order up to which a row's entries stay.
 struct Cut {
-    uint32_t key;
+    float logit;
     int index;
-    __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
+    __device__ __forceinline__ bool keeps(float l, int i) const { return l > logit || (l == logit && i <= index); }
 };
 
-__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+__device__ __forceinline__ u64 warp_total(u64 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
+__device__ __forceinline__ u64 warp_inclusive(u64 v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Sum over the threads before this one (scratch: kWarps entries; synchronises, and again before its next use).
+__device__ __forceinline__ u64 block_exclusive(u64 v, u64 *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const u64 in = warp_inclusive(v);
+    __syncthreads();
+    if (lane == 31) scratch[warp] = in;
+    __syncthreads();
+    u64 before = in - v;
+    for (int w = 0; w < warp; ++w) before += scratch[w];
+    return before;
+}
+
+// A part of a row that a warp has.
+struct Segment {
+    int from, to;
+};
+
+// CTA r's part of a row, and warp w's segment of it.
+__device__ __forceinline__ Segment segment(int vocab, int cluster, int r, int w) {
+    const int part = (vocab + cluster - 1) / cluster;
+    const int from = min(r * part, vocab), to = min(from + part, vocab);
+    const int len = ((to - from + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int at = min(from + w * len, to);
+    return {at, min(at + len, to)};
+}
+
 template <bool BF16>
 struct Row {
     const void *logits;
-    int from, to;                               // this CTA's part
-    int seg_from, seg_to;                       // this warp's
+    const float *held;                          // this CTA's part in shared memory, or nullptr
+    int first;                                  // of this CTA's part
+    Segment seg;                                // this warp's
     int rank, cluster;
     Shared &sm;
 
-    __device__ __forceinline__ uint32_t key(int i) const {
-        if constexpr (BF16) return key_of<true>(bf16_bits_to_f32(static_cast<const uint16_t *>(logits)[i]));
-        else return key_of<false>(static_cast<const float *>(logits)[i]);
+    __device__ __forceinline__ float read(int i) const {
+        if constexpr (BF16) return clean<true>(bf16_bits_to_f32(static_cast<const uint16_t *>(logits)[i]));
+        else return clean<false>(static_cast<const float *>(logits)[i]);
     }
+    __device__ __forceinline__ float at(int i) const { return held != nullptr ? held[i - first] : read(i); }
 
     // Sum over the cluster of each thread's v.  base: the sum of the CTAs before; warp sums stay in sm.warp_sum.
-    __device__ unsigned long long total(unsigned long long v, unsigned long long *base) const {
+    __device__ u64 total(u64 v, u64 *base) const {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        v = warp_sum(v);
+        v = warp_total(v);
         if (lane == 0) sm.warp_sum[warp] = v;
         __syncthreads();
         if (threadIdx.x == 0) {
-            unsigned long long s = 0;
+            u64 s = 0;
             for (int w = 0; w < kWarps; ++w) s += sm.warp_sum[w];
-            sm.cta_sum = s;
+            sm.sum_all = s;
         }
         sync_all(cluster);
-        unsigned long long all = 0, before = 0;
+        u64 all = 0, before = 0;
         for (int r = 0; r < cluster; ++r) {
             if (r == rank) before = all;
-            all += ld_peer_u64(&sm.cta_sum, r, cluster);
+            all += at_peer(&sm.sum_all, r, cluster);
         }
         sync_all(cluster);
         *base = before;
         return all;
     }
 
-    // The lowest index at which the sum of value(i) over the indices up to it exceeds target (below the total),
-    // for the warp sums and base that total() has left.  Runs on the warp that has it; -1 on the others.
+    // The lowest index of a segment at which base and the sum of value(i) up to it exceed target; -1 if none does.  One warp.
     template <typename Value>
-    __device__ int ordered(unsigned long long target, unsigned long long base, Value value) const {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        for (int w = 0; w < warp; ++w) base += sm.warp_sum[w];
-        if (target < base || target >= base + sm.warp_sum[warp]) return -1;
-        for (int i = seg_from; i < seg_to; i += 32) {
-            unsigned long long v = i + lane < seg_to ? value(i + lane) : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
+    __device__ int ordered(Segment s, u64 target, u64 base, Value value) const {
+        const int lane = threadIdx.x & 31;
+        for (int i = s.from; i < s.to; i += 32) {
+            const u64 v = warp_inclusive(i + lane < s.to ? value(i + lane) : 0);
             const unsigned hit = __ballot_sync(0xffffffffu, base + v > target);
             if (hit) return i + __ffs(hit) - 1;
             base += __shfl_sync(0xffffffffu, v, 31);
@@ -218,66 +286,117 @@ struct Row {
         return -1;
     }
 
-    // Narrow the cut to the shortest run of the order whose sum of value(key) reaches target (1 .. the sum of all that stay).
+    // Narrow the cut to the shortest run of the order whose sum of value(logit) reaches target (1 .. the sum
+    // of all that stay), by the bytes of the key.
     template <typename Value>
-    __device__ void narrow(Cut &cut, unsigned long long target, Value value) const {
-        const int tid = threadIdx.x, lane = tid & 31;
+    __device__ void narrow(Cut &cut, u64 target, Value value) const {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         uint32_t prefix = 0;
         for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int b = tid; b < kBins; b += kThreads) sm.hist[b] = 0;
+            for (int b = tid; b < kRadix; b += kThreads) sm.radix[b] = 0;
             __syncthreads();
-            for (int i = seg_from + lane; i < seg_to; i += 32) {
-                const uint32_t k = key(i);
-                if (!cut.keeps(k, i) || (shift < 24 && k >> (shift + 8) != prefix)) continue;
-                atomicAdd(&sm.hist[(k >> shift) & 255], value(k));
+            for (int i = seg.from + lane; i < seg.to; i += 32) {
+                const float l = at(i);
+                const uint32_t k = key_of(l);
+                if (cut.keeps(l, i) && (shift == 24 || k >> (shift + 8) == prefix)) atomicAdd(&sm.radix[(k >> shift) & 255], value(l));
             }
             sync_all(cluster);
-            unsigned long long mine = 0;
-            if (tid < kBins)
-                for (int r = 0; r < cluster; ++r) mine += ld_peer_u64(&sm.hist[kBins - 1 - tid], r, cluster);
-            sync_all(cluster);
-            if (tid < kBins) sm.hist[tid] = mine;               // descending bins now
-            __syncthreads();
-            if (tid == 0) {
-                unsigned long long above = 0;
-                int b = 0;
-                while (b < kBins - 1 && above + sm.hist[b] < target) above += sm.hist[b++];
-                sm.bin = kBins - 1 - b;
-                sm.above = above;
+            u64 mine = 0;                                           // descending bins
+            if (tid < kRadix)
+                for (int r = 0; r < cluster; ++r) mine += at_peer(&sm.radix[kRadix - 1 - tid], r, cluster);
+            const u64 before = block_exclusive(mine, sm.scan);
+            if (tid < kRadix && before < target && before + mine >= target) {
+                sm.bin = kRadix - 1 - tid;
+                sm.rest = target - before;
             }
-            __syncthreads();
+            sync_all(cluster);
             prefix = prefix << 8 | sm.bin;
-            target -= sm.above;
+            target = sm.rest;
             __syncthreads();
         }
         // equal keys have equal values: the first `need` of them in the order of the indices
-        const unsigned long long each = value(prefix);
-        const unsigned long long need = (target + each - 1) / each;
-        auto tie = [&](int i) -> unsigned long long {
-            const uint32_t k = key(i);
-            return k == prefix && cut.keeps(k, i);
+        const float logit = logit_of(prefix);
+        const u64 each = value(logit), need = (target + each - 1) / each;
+        auto tie = [&](int i) -> u64 {
+            const float l = at(i);
+            return l == logit && cut.keeps(l, i);
         };
-        unsigned long long n = 0, base;
-        for (int i = seg_from + lane; i < seg_to; i += 32) n += tie(i);
+        u64 n = 0, base;
+        for (int i = seg.from + lane; i < seg.to; i += 32) n += tie(i);
         total(n, &base);
-        const int at = ordered(need - 1, base, tie);
-        if (at >= 0 && lane == 0)
-            for (int r = 0; r < cluster; ++r) st_peer_s32(&sm.found, r, cluster, at);
+        for (int w = 0; w < warp; ++w) base += sm.warp_sum[w];
+        if (need - 1 >= base && need - 1 < base + sm.warp_sum[warp]) {
+            const int found = ordered(seg, need - 1, base, tie);
+            if (lane == 0)
+                for (int r = 0; r < cluster; ++r) put_peer(&sm.found, r, cluster, found);
+        }
         sync_all(cluster);
-        cut.key = prefix;
+        cut.logit = logit;
         cut.index = sm.found;
         sync_all(cluster);
     }
+
+    // List this warp's entry if `take` (all lanes call).  The count goes on past the list's end.
+    __device__ __forceinline__ void list(bool take, float l, int i) const {
+        const unsigned who = __ballot_sync(0xffffffffu, take);
+        if (who == 0) return;
+        const int lane = threadIdx.x & 31;
+        uint32_t n = 0;
+        if (lane == 0) n = atomicAdd(&sm.listed, __popc(who));
+        n = __shfl_sync(0xffffffffu, n, 0) + __popc(who & ((1u << lane) - 1));
+        if (take && n < kLocal) sm.local[n] = entry_of(key_of(l), i);
+    }
+
+    // Entries listed in all CTAs; more than kList if they do not fit (all CTAs agree).
+    __device__ int listed() const {
+        int n = 0;
+        for (int r = 0; r < cluster; ++r) {
+            const uint32_t c = at_peer(&sm.listed, r, cluster);
+            n += c > kLocal ? kList + 1 : static_cast<int>(c);
+        }
+        return n;
+    }
+
+    // First CTA: all lists one behind the other, filled up with zeros to a power of two (returned).
+    __device__ int collect(u64 *list, int n) const {
+        int at = 0, size = 64;
+        for (int r = 0; r < cluster; ++r) {
+            const int c = static_cast<int>(at_peer(&sm.listed, r, cluster));
+            for (int i = threadIdx.x; i < c; i += kThreads) list[at + i] = at_peer(&sm.local[i], r, cluster);
+            at += c;
+        }
+        while (size < n) size *= 2;
+        for (int i = n + threadIdx.x; i < size; i += kThreads) list[i] = 0;
+        return size;
+    }
 };
 
+// Sort `size` (a power of two) entries descending.
+__device__ void sort(u64 *list, int size) {
+    for (int k = 2; k <= size; k <<= 1) {
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            __syncthreads();
+            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+                const int a = 2 * t - (t & (j - 1)), b = a + j;
+                const u64 x = list[a], y = list[b];
+                if ((x < y) == ((a & k) == 0)) {
+                    list[a] = y;
+                    list[b] = x;
+                }
+            }
+        }
+    }
+    __syncthreads();
+}
+
 // floor(f * s) for a finite f in 0 .. 1.
-__device__ __forceinline__ unsigned long long scaled(float f, unsigned long long s, bool up) {
+__device__ __forceinline__ u64 scaled(float f, u64 s, bool up) {
     const uint32_t b = __float_as_uint(f);
     const int e = b >> 23;
-    const unsigned long long mant = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
+    const u64 mant = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
     const int shift = 150 - (e ? e : 1);                                   // f = mant * 2^-shift, 23 <= shift <= 149
-    const unsigned long long lo = mant * s, hi = __umul64hi(mant, s);
-    unsigned long long v;
+    const u64 lo = mant * s, hi = __umul64hi(mant, s);
+    u64 v;
     bool rest;
     if (shift < 64) {
         v = hi << (64 - shift) | lo >> shift;
@@ -290,109 +409,351 @@ __device__ __forceinline__ unsigned long long scaled(float f, unsigned long long
     return v + (up && rest);
 }
 
+
+// The target of the draw: the first index whose sum exceeds it is drawn.
+__device__ __forceinline__ u64 draw_target(float u, u64 sum) {
+    u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;
+    return min(scaled(u, sum, false), sum - 1);
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+    extern __shared__ __align__(16) uint8_t dynamic[];
     __shared__ Shared sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = a.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int row = blockIdx.x / a.cluster;
     if (tid < 32) sm.exp2[tid] = kExp2[tid];
+    if (tid == 0) {
+        sm.best = 0;
+        sm.least = INFINITY;
+        sm.listed = 0;
+        sm.lo = kBins;
+        sm.hi = kBins;
+    }
+    for (int b = tid; b < kBins; b += kThreads) sm.hist[b] = 0;
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
 
-    const int part = (a.vocab + a.cluster - 1) / a.cluster;
-    Row<BF16> v{static_cast<const uint8_t *>(a.logits) + static_cast<int64_t>(row) * a.vocab * (BF16 ? 2 : 4), 0, 0, 0, 0, rank, a.cluster, sm};
-    v.from = min(rank * part, a.vocab);
-    v.to = min(v.from + part, a.vocab);
-    const int seg = ((v.to - v.from + kWarps - 1) / kWarps + 31) / 32 * 32;
-    v.seg_from = min(v.from + warp * seg, v.to);
-    v.seg_to = min(v.seg_from + seg, v.to);
-
-    // the largest
-    uint32_t top = kKeyNone;
-    for (int i = v.seg_from + lane; i < v.seg_to; i += 32) top = max(top, v.key(i));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (tid == 0) sm.cta_max = kKeyNone;
-    __syncthreads();
-    if (lane == 0) atomicMax(&sm.cta_max, top);
-    sync_all(a.cluster);
-    for (int r = 0; r < a.cluster; ++r) top = max(top, ld_peer_u32(&sm.cta_max, r, a.cluster));
-    sync_all(a.cluster);
-    if (top == kKeyNone) {
-        if (rank == 0 && tid == 0) {
-            a.ids[row] = -1;
-            if (a.probs != nullptr) a.probs[row] = 0.0f;
-        }
-        return;
-    }
-
+    Row<BF16> v{static_cast<const uint8_t *>(a.logits) + static_cast<int64_t>(row) * a.vocab * (BF16 ? 2 : 4), nullptr,
+                segment(a.vocab, a.cluster, rank, 0).from, segment(a.vocab, a.cluster, rank, warp), rank, a.cluster, sm};
     const float t = a.temperature != nullptr ? a.temperature[row] : 1.0f;
-    unsigned long long base;
-    if (!(t >= kColdest)) {                     // the first of the order
-        auto tie = [&](int i) -> unsigned long long { return v.key(i) == top; };
-        unsigned long long n = 0;
-        for (int i = v.seg_from + lane; i < v.seg_to; i += 32) n += tie(i);
-        v.total(n, &base);
-        const int at = v.ordered(0, base, tie);
-        if (at >= 0 && lane == 0) {
-            a.ids[row] = at;
-            if (a.probs != nullptr) a.probs[row] = 1.0f;
+    const int k = a.top_k != nullptr ? a.top_k[row] : 0;
+    const float p = a.top_p != nullptr ? a.top_p[row] : 1.0f, floor = a.min_p != nullptr ? a.min_p[row] : 0.0f;
+    const float u = a.uniform[row];
+
+    // the row's part, its largest and smallest
+    float *held = reinterpret_cast<float *>(dynamic);
+    float top = -INFINITY, least = INFINITY;
+    int where = 0;
+#pragma unroll 8
+    for (int i = v.seg.from + lane; i < v.seg.to; i += 32) {
+        const float l = v.read(i);
+        if (a.resident) held[i - v.first] = l;
+        if (l > top) {
+            top = l;
+            where = i;
         }
+        if (l > -INFINITY) least = fminf(least, l);
+    }
+    if (a.resident) v.held = held;
+    u64 best = top > -INFINITY ? entry_of(key_of(top), where) : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    }
+    if (lane == 0) {
+        atomicMax(&sm.best, best);
+        sm.scan[warp] = __float_as_uint(least);
+    }
+    __syncthreads();
+    if (tid < kWarps) {
+        least = __uint_as_float(static_cast<uint32_t>(sm.scan[tid]));
+        for (int o = kWarps / 2; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffu, least, o));
+        if (tid == 0) sm.least = least;
+    }
+    const bool small_k = k > 0 && k <= kSmallK;
+    if (small_k) {
+        // a key that at least k of the threads' maxima reach
+        uint32_t lo = 0, hi = static_cast<uint32_t>(sm.best >> 32);
+        const uint32_t mine = top > -INFINITY ? key_of(top) : 0;
+        for (int i = 0; i < 24 && lo < hi; ++i) {
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            if (__syncthreads_count(mine >= mid) >= k) lo = mid;
+            else hi = mid - 1;
+        }
+        if (tid == 0) sm.bound = lo;
+    }
+    sync_all(a.cluster);
+    best = 0;
+    uint32_t bound = 0;
+    least = INFINITY;
+    for (int r = 0; r < a.cluster; ++r) {
+        best = max(best, at_peer(&sm.best, r, a.cluster));
+        least = fminf(least, at_peer(&sm.least, r, a.cluster));
+        if (small_k) bound = max(bound, at_peer(&sm.bound, r, a.cluster));
+    }
+    if (best == 0 || !(t >= kColdest)) {        // no candidate, or the first of the order
+        if (rank == 0 && tid == 0) {
+            a.ids[row] = best == 0 ? -1 : index_of(best);
+            if (a.probs != nullptr) a.probs[row] = best == 0 ? 0.0f : 1.0f;
+        }
+        sync_all(a.cluster);
         return;
     }
+    const float largest = logit_of(static_cast<uint32_t>(best >> 32));
     Weights w;
-    w.set(top, t);
-    Cut cut{kKeyNone, -1};
-
-    const int k = a.top_k != nullptr ? a.top_k[row] : 0;
-    if (k > 0 && k < a.vocab) {
-        unsigned long long n = 0;
-        for (int i = v.seg_from + lane; i < v.seg_to; i += 32) n += v.key(i) > kKeyNone;
-        n = v.total(n, &base);
-        if (static_cast<unsigned long long>(k) < n) v.narrow(cut, k, [](uint32_t) { return 1ull; });
-    }
-    const float floor = a.min_p != nullptr ? a.min_p[row] : 0.0f;
+    w.set(largest, t);
+    auto weight = [&](float l) { return w.of(l, sm.exp2); };
+    Cut cut{-INFINITY, -1};
+    float lowest = -INFINITY;                   // min-p: entries below go
     if (floor > 0.0f && !w.equal) {
         // w >= min_p  <=>  l >= l_max + T ln(min_p)
-        const double least = static_cast<double>(logit_of(top)) + static_cast<double>(t) * log(static_cast<double>(fminf(floor, 1.0f)));
-        const uint32_t key = min(key_of<false>(__double2float_ru(least)), top) - 1;
-        if (key >= cut.key) cut = Cut{key, -1};
+        const double at = static_cast<double>(largest) + static_cast<double>(t) * log(static_cast<double>(fminf(floor, 1.0f)));
+        lowest = fminf(__double2float_ru(at), largest);
     }
-    auto weight = [&](uint32_t key) { return w.of(key, sm.exp2); };
-    const float p = a.top_p != nullptr ? a.top_p[row] : 1.0f;
-    if (p < 1.0f) {
-        unsigned long long s = 0;
-        for (int i = v.seg_from + lane; i < v.seg_to; i += 32) {
-            const uint32_t key = v.key(i);
-            if (cut.keeps(key, i)) s += weight(key);
+    u64 *list = reinterpret_cast<u64 *>(dynamic);           // in the first CTA, when its part is done with
+
+    if (small_k) {
+        const float from = fmaxf(bound > kKeyNone ? logit_of(bound) : -INFINITY, lowest);
+        for (int i = v.seg.from; i < v.seg.to; i += 32) {
+            const float l = i + lane < v.seg.to ? v.at(i + lane) : -INFINITY;
+            v.list(l >= from && l > -INFINITY, l, i + lane);
         }
-        s = v.total(s, &base);
-        const unsigned long long target = p > 0.0f ? scaled(p, s, true) : 1;
-        v.narrow(cut, target > 0 ? target : 1, weight);
+        sync_all(a.cluster);
+        const int n = v.listed();
+        if (n <= kList) {
+            int size = 0;
+            if (rank == 0) size = v.collect(list, n);
+            sync_all(a.cluster);
+            if (rank != 0) return;
+            sort(list, size);
+            const int stay = min(k, n);
+            // weights, in place of the candidates behind the first k (at most kSmallK)
+            u64 *ws = list + kSmallK;
+            __syncthreads();
+            const u64 mine = tid < stay ? weight(logit_of(static_cast<uint32_t>(list[tid] >> 32))) : 0;
+            const u64 before = block_exclusive(mine, sm.scan);
+            if (tid == stay - 1) sm.sum_all = before + mine;
+            __syncthreads();
+            u64 target = sm.sum_all;
+            if (p < 1.0f) target = p > 0.0f ? max(scaled(p, target, true), static_cast<u64>(1)) : 1;
+            const bool kept = tid < stay && before < target;
+            ws[tid] = kept ? mine : 0;
+            const int count = __syncthreads_count(kept);
+            if (tid == count - 1) sm.sum_all = before + mine;
+            __syncthreads();
+            const u64 sum = sm.sum_all, drawn = draw_target(u, sum);
+            if (kept) {
+                // the sum over the indices up to this one, and without it
+                const int me = index_of(list[tid]);
+                u64 upto = 0;
+                for (int j = 0; j < count; ++j) upto += index_of(list[j]) <= me ? ws[j] : 0;
+                if (upto > drawn && upto - mine <= drawn) {
+                    a.ids[row] = me;
+                    if (a.probs != nullptr) a.probs[row] = static_cast<float>(static_cast<double>(mine) / static_cast<double>(sum));
+                }
+            }
+            return;
+        }
+        sync_all(a.cluster);                    // all have read the counts
+        if (tid == 0) sm.listed = 0;
+        __syncthreads();
     }
-    auto kept = [&](int i) -> unsigned long long {
-        const uint32_t key = v.key(i);
-        return cut.keeps(key, i) ? weight(key) : 0;
+    if (k > 0 && k < a.vocab) {
+        u64 n = 0, base;
+        for (int i = v.seg.from + lane; i < v.seg.to; i += 32) n += v.at(i) > -INFINITY;
+        n = v.total(n, &base);
+        if (static_cast<u64>(k) < n) v.narrow(cut, k, [](float) { return static_cast<u64>(1); });
+        for (int b = tid; b < kBins; b += kThreads) sm.hist[b] = 0;
+        __syncthreads();
+    }
+    if (lowest > cut.logit) cut = Cut{lowest, 0x7fffffff};
+
+    u64 mine = 0, above = 0;                    // weights of all that stay, of those that surely do
+    bool done = false;
+    if (p < 1.0f) {
+        const float range = fminf(kNats * t, largest - least), scale = range > 0.0f ? (kBins - 1) / range : 0.0f;
+        const float step = range / t / (kBins - 1);         // of ln(weight), per bin
+        for (int i = v.seg.from + lane; i < v.seg.to; i += 32) {
+            const float l = v.at(i);
+            if (!cut.keeps(l, i)) continue;
+            const float x = fminf((largest - l) * scale, kBins - 1.0f);
+            const int b = static_cast<int>(x);
+            // 1 - (x - b) step is the weight as a share of its bin's upper end, to the second order
+            atomicAdd(&sm.hist[b], 16384u - static_cast<uint32_t>((x - b) * step * 16384.0f));
+        }
+        sync_all(a.cluster);
+        float mass[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int b = 2 * tid + e;
+            u64 n = 0;
+            for (int r = 0; r < a.cluster; ++r) n += at_peer(&sm.hist[b], r, a.cluster);
+            mass[e] = static_cast<float>(n) * __expf(-b * step);
+        }
+        // sums over the bins from the largest on, in fp32: estimates
+        float in = mass[0] + mass[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float other = __shfl_up_sync(0xffffffffu, in, o);
+            if (lane >= o) in += other;
+        }
+        if (lane == 31) sm.scan[warp] = __float_as_uint(in);
+        __syncthreads();
+        float all = 0.0f, before = in - mass[0] - mass[1];
+        for (int o = 0; o < kWarps; ++o) {
+            const float s = __uint_as_float(static_cast<uint32_t>(sm.scan[o]));
+            all += s;
+            if (o < warp) before += s;
+        }
+        const float aim = fmaxf(p, 0.0f) * all, low = aim - kSlack * all, high = aim + kSlack * all;
+        float upto[3] = {before, before + mass[0], before + mass[0] + mass[1]};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // the first bins to reach the one and the other (sums of neighbours may differ by a rounding: the lowest such bin)
+            if (upto[e + 1] >= low) atomicMin(&sm.lo, 2 * tid + e);
+            if (upto[e + 1] >= high) atomicMin(&sm.hi, 2 * tid + e);
+        }
+        __syncthreads();
+        const int lo = sm.lo, hi = sm.hi;
+        u64 bracket = 0;
+        for (int i = v.seg.from; i < v.seg.to; i += 32) {
+            const float l = i + lane < v.seg.to ? v.at(i + lane) : -INFINITY;
+            const bool stays = cut.keeps(l, i + lane) && l > -INFINITY;
+            const int b = stays ? static_cast<int>(fminf((largest - l) * scale, kBins - 1.0f)) : kBins;
+            const u64 value = stays ? weight(l) : 0;
+            mine += value;
+            if (b < lo) above += value;
+            else if (b <= hi) bracket += value;
+            v.list(stays && b >= lo && b <= hi, l, i + lane);
+        }
+        const u64 sums[3] = {warp_total(mine), warp_total(above), warp_total(bracket)};
+        if (tid == 0) sm.sum_all = sm.sum_above = sm.sum_listed = 0;
+        __syncthreads();
+        if (lane == 0) {
+            sm.warp_sum[warp] = sums[1];
+            atomicAdd(&sm.sum_all, sums[0]);
+            atomicAdd(&sm.sum_above, sums[1]);
+            atomicAdd(&sm.sum_listed, sums[2]);
+        }
+        sync_all(a.cluster);
+        u64 total = 0, sure = 0, listed = 0;
+        for (int r = 0; r < a.cluster; ++r) {
+            total += at_peer(&sm.sum_all, r, a.cluster);
+            sure += at_peer(&sm.sum_above, r, a.cluster);
+            listed += at_peer(&sm.sum_listed, r, a.cluster);
+        }
+        const u64 target = p > 0.0f ? max(scaled(p, total, true), static_cast<u64>(1)) : 1;
+        const int n = v.listed();
+        done = n <= kList && sure < target && target <= sure + listed;
+        if (done) {
+            int size = 0;
+            if (rank == 0) {
+                size = v.collect(list, n);
+                if (tid < a.cluster * kWarps) sm.buckets[tid] = at_peer(&sm.warp_sum[tid % kWarps], tid / kWarps, a.cluster);
+            }
+            sync_all(a.cluster);
+            if (rank != 0) return;
+            sort(list, size);
+            // the cut: the entry at which the sum reaches the target
+            constexpr int kEach = kList / kThreads;
+            u64 own[kEach], s = 0;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int i = tid * kEach + e;
+                own[e] = i < n ? weight(logit_of(static_cast<uint32_t>(list[i] >> 32))) : 0;
+                s += own[e];
+            }
+            u64 run = sure + block_exclusive(s, sm.scan);
+            const int part = (a.vocab + a.cluster - 1) / a.cluster;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int i = tid * kEach + e;
+                if (i < n && run < target) {
+                    const int index = index_of(list[i]), r = index / part;
+                    const Segment whole = segment(a.vocab, a.cluster, r, 0);
+                    const int len = max(whole.to - whole.from, 1);      // of every segment but the last ones
+                    atomicAdd(&sm.buckets[r * kWarps + (index - r * part) / len], own[e]);
+                    if (run + own[e] >= target) {
+                        sm.sum_all = run + own[e];
+                        sm.found = index;
+                        sm.bound = static_cast<uint32_t>(list[i] >> 32);
+                    }
+                }
+                run += own[e];
+            }
+            __syncthreads();
+            cut = Cut{logit_of(sm.bound), sm.found};
+        } else {
+            v.narrow(cut, target, weight);
+        }
+    }
+    if (!done) {
+        mine = 0;
+        for (int i = v.seg.from + lane; i < v.seg.to; i += 32) {
+            const float l = v.at(i);
+            if (cut.keeps(l, i)) mine += weight(l);
+        }
+        mine = warp_total(mine);
+        if (lane == 0) sm.warp_sum[warp] = mine;
+        sync_all(a.cluster);
+        if (rank == 0 && tid < a.cluster * kWarps) sm.buckets[tid] = at_peer(&sm.warp_sum[tid % kWarps], tid / kWarps, a.cluster);
+        sync_all(a.cluster);
+        if (rank != 0) return;
+    }
+
+    // first CTA: the segment that has the draw, then the index in it
+    const int buckets = a.cluster * kWarps;
+    const u64 in = tid < buckets ? sm.buckets[tid] : 0;
+    const u64 before = block_exclusive(in, sm.scan);
+    if (tid == buckets - 1) sm.sum_above = before + in;
+    __syncthreads();
+    const u64 sum = sm.sum_above, target = draw_target(u, sum);
+    if (target >= before && target < before + in) {
+        sm.bin = tid;
+        sm.rest = target - before;
+    }
+    __syncthreads();
+    const Segment s = segment(a.vocab, a.cluster, sm.bin / kWarps, sm.bin % kWarps);
+    const u64 rest = sm.rest;
+    auto kept = [&](int i) -> u64 {
+        const float l = v.read(i);
+        return cut.keeps(l, i) ? weight(l) : 0;
     };
-    unsigned long long s = 0;
-    for (int i = v.seg_from + lane; i < v.seg_to; i += 32) s += kept(i);
-    s = v.total(s, &base);
-    float u = a.uniform[row];
-    u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;
-    const unsigned long long target = min(scaled(u, s, false), s - 1);
-    const int at = v.ordered(target, base, kept);
-    if (at >= 0 && lane == 0) {
+    const int len = ((s.to - s.from + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const Segment sub{min(s.from + warp * len, s.to), min(s.from + (warp + 1) * len, s.to)};
+    u64 own = 0;
+    for (int i = sub.from + lane; i < sub.to; i += 32) own += kept(i);
+    own = warp_total(own);
+    __syncthreads();
+    if (lane == 0) sm.scan[warp] = own;
+    __syncthreads();
+    u64 base = 0;
+    for (int o = 0; o < warp; ++o) base += sm.scan[o];
+    if (rest < base || rest >= base + own) return;
+    const int at = v.ordered(sub, rest, base, kept);
+    if (lane == 0) {
         a.ids[row] = at;
-        if (a.probs != nullptr) a.probs[row] = static_cast<float>(static_cast<double>(kept(at)) / static_cast<double>(s));
+        if (a.probs != nullptr) a.probs[row] = static_cast<float>(static_cast<double>(kept(at)) / static_cast<double>(sum));
     }
 }
 
-cudaError_t sample_launch(SampleArgs a, bool bf16, cudaStream_t stream) {
+template <bool BF16>
+cudaError_t sample_launch(SampleArgs a, int sms, cudaStream_t stream) {
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(sample_kernel<BF16>, kMostPart * 4);
+    if (e != cudaSuccess) return e;
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && a.vocab > a.cluster * 8192) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && (a.vocab > a.cluster * kPart || (a.vocab > a.cluster * 1024 && a.m * a.cluster < sms))) a.cluster *= 2;
+    const int part = (a.vocab + a.cluster - 1) / a.cluster;
+    a.resident = part <= kMostPart;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.m) * a.cluster);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = max(a.resident ? static_cast<size_t>(part) * 4 : 0, kList * sizeof(u64));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -402,7 +763,15 @@ cudaError_t sample_launch(SampleArgs a, bool bf16, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, sample_kernel<true>, a) : cudaLaunchKernelEx(&cfg, sample_kernel<false>, a);
+    return cudaLaunchKernelEx(&cfg, sample_kernel<BF16>, a);
+}
+
+cudaError_t sample_launch(const SampleArgs &a, bool bf16, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    return bf16 ? sample_launch<true>(a, sms, stream) : sample_launch<false>(a, sms, stream);
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
