@@ -84,6 +84,18 @@ tq_status tq_q4_gemv(const tq_q4_weight *w, const uint16_t *x, int32_t m, void *
 tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const uint16_t *x,
                        int32_t m, uint16_t *h, tq_stream_t stream);
 
+/* The bits of the bounded waits that have run out in any tq_q4_* call of this
+ * process on the current device since the library was loaded (calls of more than
+ * 16 rows have such waits; each takes about half a second before it sets its bit,
+ * and the call's outputs are then not valid).  Synchronises the stream.  TQ_OK, or
+ * TQ_ERR_TIMEOUT if a bit is set:
+ *   bit 0  the decoders waited for a free stage    bit 5  the copies of x
+ *   bit 1  the matrix instructions waited for x    bit 2  for decoded weights
+ *   bit 3  for a free accumulator                  bit 4  at exit
+ *   bit 6  the copies of x in flight at exit
+ *   bit 7  the fold waited for scales              bit 8  for an accumulator */
+tq_status tq_q4_read_error_word(uint32_t *value, tq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

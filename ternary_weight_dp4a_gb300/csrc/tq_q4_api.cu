@@ -53,6 +53,14 @@ tq::Q4Product product(const tq_q4_weight *w, const tq_q4_weight *up, const uint1
     return p;
 }
 
+// Calls of more rows than this run on the tile kernel.
+constexpr int kStreamRows = 16;
+
+tq_status run(const tq::Q4Product &p, tq_stream_t stream) {
+    cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(p.m > kStreamRows ? tq::q4_tile_launch(p, str) : tq::q4_stream_launch(p, str));
+}
+
 }  // namespace
 
 extern "C" {
@@ -87,7 +95,7 @@ tq_status tq_q4_gemv(const tq_q4_weight *w, const uint16_t *x, int32_t m, void *
     tq::Q4Product p = product(w, nullptr, x, m);
     p.y = y;
     p.y_bf16 = y_type == TQ_BF16;
-    return cuda_status(tq::q4_stream_launch(p, reinterpret_cast<cudaStream_t>(stream)));
+    return run(p, stream);
 }
 
 tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const uint16_t *x,
@@ -101,7 +109,18 @@ tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const u
     tq::Q4Product p = product(gate, up, x, m);
     p.y = h;
     p.y_bf16 = true;
-    return cuda_status(tq::q4_stream_launch(p, reinterpret_cast<cudaStream_t>(stream)));
+    return run(p, stream);
+}
+
+tq_status tq_q4_read_error_word(uint32_t *value, tq_stream_t stream) {
+    if (value == nullptr) return TQ_ERR_INVALID_ARG;
+    cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
+    unsigned bits = 0;
+    cudaError_t e = tq::q4_tile_waits(&bits, str);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(str);
+    if (e != cudaSuccess) return cuda_status(e);
+    *value = bits;
+    return tq_error_status(bits);
 }
 
 }  // extern "C"

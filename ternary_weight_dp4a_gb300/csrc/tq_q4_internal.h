@@ -27,6 +27,10 @@ struct Q4Product {
 
 cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const uint16_t *mins, int n, int k, int group,
                            uint8_t *out_codes, uint16_t *out_scales, uint16_t *out_mins, cudaStream_t stream);
+// Any number of rows, 16 per pass over the weights; and 128 per pass.
 cudaError_t q4_stream_launch(const Q4Product &p, cudaStream_t stream);
+cudaError_t q4_tile_launch(const Q4Product &p, cudaStream_t stream);
+// The bits of the bounded waits that have run out on the current device (copied in `stream`).
+cudaError_t q4_tile_waits(unsigned *bits, cudaStream_t stream);
 
 }  // namespace tq

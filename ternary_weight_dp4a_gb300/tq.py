@@ -34,7 +34,8 @@ EXPORTS = ("tq_status_string", "tq_last_cuda_error", "tq_set_engine", "tq_get_en
            "tq_rmsnorm_bf16",
            "tq_add_rmsnorm_rotq", "tq_moe_route", "tq_moe_workspace_bytes", "tq_moe_read_error_word", "tq_moe_plan",
            "tq_moe_gemv", "tq_moe_gateup", "tq_moe_combine", "tq_moe_ffn",
-           "tq_q4_codes_bytes", "tq_q4_scales_bytes", "tq_q4_pack", "tq_q4_gemv", "tq_q4_gateup", "tq_sample",
+           "tq_q4_codes_bytes", "tq_q4_scales_bytes", "tq_q4_pack", "tq_q4_gemv", "tq_q4_gateup",
+           "tq_q4_read_error_word", "tq_sample",
            "tq_lifecycle_init", "tq_lifecycle_load", "tq_lifecycle_copy", "tq_lifecycle_alloc",
            "tq_lifecycle_free", "tq_lifecycle_poll", "tq_lifecycle_release", "tq_lifecycle_destroy")
 
@@ -153,6 +154,7 @@ def load():
             L.tq_q4_pack.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
             L.tq_q4_gemv.argtypes = [Q, vp, i32, vp, i32, vp]
             L.tq_q4_gateup.argtypes = [Q, Q, vp, i32, vp, vp]
+            L.tq_q4_read_error_word.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
             L.tq_sample.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
             LC = ctypes.POINTER(_Lifecycle)
             L.tq_lifecycle_init.argtypes = [LC, ctypes.POINTER(_LcConfig), ctypes.POINTER(_LcHooks)]
@@ -821,6 +823,14 @@ def q4_gateup(gate: PackedQ4, up: PackedQ4, x, h=None, stream=None):
         p_h = _tensor(dev, "h", h, (torch.bfloat16,), (m, gate.n))
     _check("tq_q4_gateup", load().tq_q4_gateup(_q4(dev, "gate", gate), _q4(dev, "up", up), p_x, m, p_h, _stream(stream)))
     return h
+
+
+def q4_read_error_word(stream=None) -> int:
+    """The bounded waits that have run out in any q4_* call so far: synchronises the stream; raises
+    TQError with status TQ_ERR_TIMEOUT when there is one, else returns 0."""
+    v = ctypes.c_uint32(0)
+    _check("tq_q4_read_error_word", load().tq_q4_read_error_word(ctypes.byref(v), _stream(stream)))
+    return int(v.value)
 
 
 # ---------------------------------------------------------------------------

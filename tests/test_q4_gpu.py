@@ -46,6 +46,12 @@ class Matrix:
         return y, steps * size
 
 
+@pytest.fixture(autouse=True)
+def no_wait_has_run_out(tq):
+    yield
+    assert tq.q4_read_error_word() == 0
+
+
 def _x(m, k, seed):
     import torch
     g = torch.Generator(device="cuda")
