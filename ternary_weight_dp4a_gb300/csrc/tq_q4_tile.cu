@@ -19,6 +19,8 @@
 // Warps: 0-3 decode, 4 issues MMAs, 5 copies x, 8-15 fold (a quarter of the lanes and half of the columns each).
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "tq_device.cuh"
 #include "tq_moe_internal.h"
 #include "tq_q4_internal.h"
@@ -32,7 +34,10 @@ constexpr int kRows = 128;                      // of x, per tile
 constexpr int kCols = 256;                      // rows of B
 constexpr int kStageK = 64;
 constexpr int kStages = 4;
-constexpr int kScaleSlots = 2 * kStages;        // the fold is at most that many stages behind the decode
+// Groups whose scales are kept.  The decode of stage s + 4 knows that the MMAs of stage s are done, hence the
+// fold of all groups but the last two of them: 4, 6 and 10 groups can be between the two.
+template <int GROUP>
+constexpr int scale_groups() { return GROUP == 128 ? 4 : GROUP == 64 ? 6 : 10; }
 constexpr int kFoldWarps = 8;
 constexpr int kThreads = 256 + 32 * kFoldWarps;
 constexpr uint32_t kABytes = kRows * kStageK * 2;
@@ -41,6 +46,7 @@ constexpr uint32_t kABytes = kRows * kStageK * 2;
 // a row's words of one chunk store to different banks.
 constexpr uint32_t kLbo = kCols / 8 * 128 + 32;
 constexpr uint32_t kBBytes = kStageK / 8 * kLbo;
+constexpr int kAhead = 8;                       // chunks of codes in L2 ahead of the decode
 constexpr int kPartLd = kCols + 4;              // floats per row of a part in shared memory
 
 // register shares (launched with 128 per thread): 128 x (120 + 40 + 2 x 176) = 512 x 128
@@ -56,9 +62,10 @@ struct __align__(1024) TileSmem {
         };
         float part[kRows][kPartLd];             // this CTA's sums, when a tile is split along k
     };
-    float s[kScaleSlots][2][kCols];             // scales of a stage's groups, in fold order
-    float m[kScaleSlots][2][kCols];             // 8 s - b
-    uint64_t a_full[kStages], b_full[kStages], empty[kStages], s_full[kScaleSlots], d_full[2], d_empty[2], drain;
+    // per group: the scales, each twice (the operand of a packed multiply-add), and 8 s - b; in fold
+    // order, columns c, c + 4, c + 8, c + 12 of 16 side by side
+    uint8_t scales[scale_groups<32>() * kCols * 12];
+    uint64_t a_full[kStages], b_full[kStages], empty[kStages], s_full[scale_groups<32>()], d_full[2], d_empty[2], drain;
     uint32_t tmem;
     uint32_t dead;                              // a bounded wait ran out
 };
@@ -112,10 +119,9 @@ __device__ __forceinline__ void ld_half(uint32_t taddr, uint32_t (&r)[8]) {
 }
 
 // tcgen05.wait::ld; the registers pass through it, so nothing reads them before.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[8], uint32_t (&q)[8]) {
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[8]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(q[0]), "+r"(q[1]), "+r"(q[2]), "+r"(q[3]), "+r"(q[4]), "+r"(q[5]), "+r"(q[6]), "+r"(q[7])
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
                  :
                  : "memory");
 }
@@ -176,11 +182,27 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
     return v;
 }
 
-__device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;       // 128 + c
-    uint32_t d;
+// Pair i of a word's codes as bf16 c - 8: (w >> 4 i) & mask | 128, minus 136.
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i, uint32_t mask, uint32_t base) {
+    uint32_t v, d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w >> (4 * i)), "r"(mask), "r"(base));
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x43084308u));
     return d;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t at, float a, float b) {
+    asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t at, float a) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(a) : "memory"); }
+__device__ __forceinline__ void lds128(uint32_t at, uint64_t &a, uint64_t &b) {
+    asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];" : "=l"(a), "=l"(b) : "r"(at) : "memory");
 }
 
 template <int GROUP, bool MINS, bool GATEUP>
@@ -189,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     TileSmem &sm = *reinterpret_cast<TileSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Q4Product &p = args.p;
     constexpr int kPer = 128 / GROUP;                               // groups per chunk
+    constexpr int kKept = scale_groups<GROUP>();
     // strips of 16 weight rows per tile and matrix; the ones behind them where there are minima
     constexpr int kStrips = GATEUP ? (MINS ? 7 : 8) : (MINS ? 15 : 16);
     constexpr int kUsed = GATEUP ? 2 * kStrips : kStrips;
@@ -205,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             mbar_init(smem_u32(&sm.b_full[i]), 4);
             mbar_init(smem_u32(&sm.empty[i]), 1);
         }
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&sm.s_full[i]), 4);
+        for (int i = 0; i < scale_groups<32>(); ++i) mbar_init(smem_u32(&sm.s_full[i]), 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.d_full[i]), 1);
             mbar_init(smem_u32(&sm.d_empty[i]), kFoldWarps);
@@ -217,17 +240,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     if (MINS)
         for (int i = tid; i < kStages * (kStageK / 8) * 16; i += kThreads) {
             const int row = i & 15, oct = (i >> 4) % (kStageK / 8), st = (i >> 4) / (kStageK / 8);
-            *reinterpret_cast<uint4 *>(sm.b[st] + oct * kLbo + (kUsed * 2 + row / 8) * 128 + row % 8 * 16) =
-                make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+            sts128(smem_u32(sm.b[st]) + oct * kLbo + (kUsed * 2 + row / 8) * 128 + row % 8 * 16, 0x3f803f80u, 0x3f803f80u,
+                   0x3f803f80u, 0x3f803f80u);
         }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    pdl_launch_dependents();
-    pdl_wait();
-
     const int chunks = p.k >> 7;
     const int rank = blockIdx.x % args.split, tile = blockIdx.x / args.split;
     const int row0 = tile % args.row_tiles * args.rows, ntile = tile / args.row_tiles;
@@ -235,6 +255,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     const int quarter_rows = ((rows + 3) / 4 + 7) / 8 * 8;          // rows of x in a quarter of the lanes
     const int chunk0 = rank * chunks / args.split, chunk1 = (rank + 1) * chunks / args.split;
     const int stages = 2 * (chunk1 - chunk0), groups = (chunk1 - chunk0) * kPer;
+
+    // Packed codes come to L2 well ahead of the decode's loads, which have one chunk in flight: lanes 0-3 of a
+    // decode warp ask for its four strips'.
+    const int my_slot = warp * 4 + lane, my_mat = GATEUP && my_slot >= kStrips;
+    const int64_t my_strip = static_cast<int64_t>(ntile) * kStrips + my_slot - my_mat * kStrips;
+    const bool asks = warp < 4 && lane < 4 && my_slot < kUsed && my_strip < q4_strips(p.n);
+    auto ask = [&](int from, int to) {
+        to = min(to, chunk1 - chunk0);
+        if (asks && from < to)
+            prefetch_l2(p.codes[my_mat] + (my_strip * chunks + chunk0 + from) * kQ4ChunkBytes, (to - from) * kQ4ChunkBytes);
+    };
+    ask(0, kAhead);
+    pdl_launch_dependents();
+    pdl_wait();
 
     if (warp < 4) {
         // ---- decode: a warp has four strips, a lane one row's 16 bytes of each half strip ----
@@ -281,6 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             }
         };
         const int total = chunk1 - chunk0;
+        const uint32_t codes_at = smem_u32(sm.b[0]) + warp * 8 * 128 + (lane >> 2) * 16 + (lane & 3) * kLbo;
+        const uint32_t scales_at = smem_u32(sm.scales), bars = smem_u32(sm.b_full);
+        uint32_t mask = 0x000f000fu, base = 0x43004300u;
+        asm volatile("" : "+r"(mask), "+r"(base));                  // in registers: two constants do not fit one instruction
         load(0, 0);
         bool ok = true;
         for (int c0 = 0; c0 < total && ok; c0 += 2) {
@@ -289,40 +327,43 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 const int c = c0 + buf;
                 if (c >= total || !ok) break;
                 if (c + 1 < total) load(buf ^ 1, c + 1);
+                if (c % 4 == 0) ask(c + kAhead, c + kAhead + 4);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int st = 2 * c + half, ring = st % kStages, slot = st % kScaleSlots;
+                    const int st = 2 * c + half, ring = st % kStages;
                     ok = warp_wait<32>(sm, smem_u32(&sm.empty[ring]), ((st / kStages) & 1) ^ 1, 1u << 0);
                     if (!ok) break;
-                    // (the fold is past what stood here: it has freed the accumulator of the groups of four stages ago)
                     if (GROUP < 128 || half == 0) {
                         constexpr int kHere = GROUP == 32 ? 2 : 1;
 #pragma unroll
                         for (int g = 0; g < kHere; ++g) {
                             const int e = GROUP == 128 ? 0 : half * kHere + g;
+                            const int slot = (c * kPer + e) % kKept;
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 const float s = f16_bits_to_f32(sc[buf][r * kPer + e]);
-                                sm.s[slot][g][place + 2 * r] = s;
-                                if (MINS) sm.m[slot][g][place + 2 * r] = __fmaf_rn(8.0f, s, -f16_bits_to_f32(mn[buf][r * kPer + e]));
+                                sts64(scales_at + (slot * kCols + place + 2 * r) * 8, s, s);
+                                if (MINS)
+                                    sts32(scales_at + kKept * kCols * 8 + (slot * kCols + place + 2 * r) * 4,
+                                          __fmaf_rn(8.0f, s, -f16_bits_to_f32(mn[buf][r * kPer + e])));
                             }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[slot]));
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[slot]));
                     }
+                    const uint32_t dst = codes_at + ring * kBBytes;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if (warp * 4 + (i >> 1) >= kUsed) continue;
+                        if (kUsed < 16 && warp * 4 + (i >> 1) >= kUsed) continue;
                         const uint32_t w[2] = {half ? code[buf][i].z : code[buf][i].x, half ? code[buf][i].w : code[buf][i].y};
-                        uint8_t *dst = sm.b[ring] + ((warp * 4 + (i >> 1)) * 2 + (i & 1)) * 128 + (lane >> 2) * 16 + (lane & 3) * kLbo;
 #pragma unroll
                         for (int g = 0; g < 2; ++g)
-                            *reinterpret_cast<uint4 *>(dst + 4 * g * kLbo) =
-                                make_uint4(decode_pair(w[g], 0), decode_pair(w[g], 1), decode_pair(w[g], 2), decode_pair(w[g], 3));
+                            sts128(dst + i * 128 + 4 * g * kLbo, decode_pair(w[g], 0, mask, base), decode_pair(w[g], 1, mask, base),
+                                   decode_pair(w[g], 2, mask, base), decode_pair(w[g], 3, mask, base));
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.b_full[ring]));
+                    if (lane == 0) mbar_arrive(bars + ring * 8);
                 }
             }
         }
@@ -385,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         // ---- fold: a lane has rows i, i + 8, i + 16, i + 24 of its quarter and every fourth column from t on ----
         regs_up<kRegsFold>();
         const int quarter = warp & 3, part = (warp - 8) >> 2, i = lane >> 2, t = lane & 3;
-        const bool wide = quarter_rows > 16;
         // chunk e (16 columns) of this warp: 8 of 16; gate/up: four of each matrix
         auto column = [&](int e) { return GATEUP ? (e >> 2) * kStrips + 4 * part + (e & 3) : 8 * part + e; };
         auto active = [&](int e) { return GATEUP ? 4 * part + (e & 3) < kStrips : 8 * part + e < kStrips; };
@@ -395,54 +435,70 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         for (int e = 0; e < 8; ++e)
 #pragma unroll
             for (int n = 0; n < 4; ++n) acc[e][n][0] = acc[e][n][1] = 0;
+        const uint32_t s_at = smem_u32(sm.scales) + (column(0) * 16 + 4 * t) * 8;
+        const uint32_t m_at = smem_u32(sm.scales) + kKept * kCols * 8 + (column(0) * 16 + 4 * t) * 4;
+        // WIDE: a quarter has more than 16 rows
+        auto fold = [&](auto wide) {
+            constexpr int kHalves = decltype(wide)::value ? 2 : 1;
+            int slot = 0;
+            uint32_t turn = 0;
 #pragma unroll 1
-        for (int group = 0; group < groups; ++group) {
-            const int st = GROUP == 128 ? 2 * group : GROUP == 64 ? group : group >> 1, sub = GROUP == 32 ? group & 1 : 0;
-            const int slot = st % kScaleSlots;
-            if (!(warp_wait(sm, smem_u32(&sm.s_full[slot]), (st / kScaleSlots) & 1, 1u << 7) &&
-                  warp_wait(sm, smem_u32(&sm.d_full[group & 1]), (group >> 1) & 1, 1u << 8)))
-                break;
-            tc_fence_after();
-            const uint32_t d = lane_base + (group & 1) * kCols;
-            uint64_t sums[2] = {0, 0};
-            if (MINS) {
-                uint32_t x[8], y[8] = {};
-                ld_half(d + kUsed * 16, x);
-                if (wide) ld_half(d + kUsed * 16 + (16u << 16), y);
-                wait_ld(x, y);
-                sums[0] = pack2(x[0], x[1]);
-                sums[1] = pack2(y[0], y[1]);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (!active(e)) continue;
-                uint32_t x[8], y[8];
-                ld_half(d + column(e) * 16, x);
-                if (wide) ld_half(d + column(e) * 16 + (16u << 16), y);
-                const float4 s = *reinterpret_cast<const float4 *>(&sm.s[slot][sub][column(e) * 16 + 4 * t]);
-                wait_ld(x, y);
-                const float sv[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const uint64_t s2 = pack2(sv[n], sv[n]);
-                    acc[e][n][0] = fma2(pack2(x[2 * n], x[2 * n + 1]), s2, acc[e][n][0]);
-                    if (wide) acc[e][n][1] = fma2(pack2(y[2 * n], y[2 * n + 1]), s2, acc[e][n][1]);
-                }
+            for (int group = 0; group < groups; ++group) {
+                if (!(warp_wait(sm, smem_u32(&sm.s_full[slot]), turn, 1u << 7) &&
+                      warp_wait(sm, smem_u32(&sm.d_full[group & 1]), (group >> 1) & 1, 1u << 8)))
+                    break;
+                tc_fence_after();
+                const uint32_t d = lane_base + (group & 1) * kCols;
+                uint64_t sums[kHalves];
                 if (MINS) {
-                    const float4 m = *reinterpret_cast<const float4 *>(&sm.m[slot][sub][column(e) * 16 + 4 * t]);
-                    const float mv[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const uint64_t m2 = pack2(mv[n], mv[n]);
-                        acc[e][n][0] = fma2(sums[0], m2, acc[e][n][0]);
-                        if (wide) acc[e][n][1] = fma2(sums[1], m2, acc[e][n][1]);
+                    for (int h = 0; h < kHalves; ++h) {
+                        uint32_t x[8];
+                        ld_half(d + kUsed * 16 + ((16u * h) << 16), x);
+                        wait_ld(x);
+                        sums[h] = pack2(x[0], x[1]);
                     }
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (kStrips % 8 != 0 && !active(e)) continue;
+                    uint32_t x[kHalves][8];
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) ld_half(d + column(e) * 16 + ((16u * h) << 16), x[h]);
+                    const uint32_t off = slot * kCols + (column(e) - column(0)) * 16;
+                    uint64_t s2[4];
+                    lds128(s_at + off * 8, s2[0], s2[1]);
+                    lds128(s_at + off * 8 + 16, s2[2], s2[3]);
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) wait_ld(x[h]);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h)
+                            acc[e][n][h] = fma2(pack2(x[h][2 * n], x[h][2 * n + 1]), s2[n], acc[e][n][h]);
+                    if (MINS) {
+                        uint64_t m01, m23;
+                        lds128(m_at + off * 4, m01, m23);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const float m = half2of(n < 2 ? m01 : m23, n & 1);
+                            const uint64_t m2 = pack2(m, m);
+#pragma unroll
+                            for (int h = 0; h < kHalves; ++h) acc[e][n][h] = fma2(sums[h], m2, acc[e][n][h]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.d_empty[group & 1]));
+                if (++slot == kKept) {
+                    slot = 0;
+                    turn ^= 1;
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.d_empty[group & 1]));
-        }
+        };
+        if (quarter_rows > 16) fold(std::true_type{});
+        else fold(std::false_type{});
         if (args.split > 1) {
             // (every copy and MMA of this CTA has ended: its stages hold the parts now)
 #pragma unroll
