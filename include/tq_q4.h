@@ -66,6 +66,12 @@ tq_status tq_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint16_
                      int32_t k, int32_t group, uint8_t *packed_codes, uint16_t *packed_scales,
                      uint16_t *packed_mins, tq_stream_t stream);
 
+/* Bytes of the workspace that a product of m rows with a matrix that has minima
+ * takes (the sums of x over the groups); 0 where none is needed, up to 16 rows,
+ * and for sizes out of range.  256-byte aligned, any contents, reusable after every
+ * call, not shared by calls that may overlap.  Matrices without minima need none. */
+size_t tq_q4_workspace_bytes(int32_t m, int32_t k, int32_t group);
+
 /* y[r][i] = sum over j of W[i][j] * x[r][j], for m rows x (bf16 bits [m][k],
  * 16-byte aligned), rounded to y_type (tq_dtype) once.  Per group, the sum of
  * (c - 8) * x over exact products is taken in fp32 by matrix instructions, and
@@ -73,16 +79,17 @@ tq_status tq_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint16_
  * In calls of up to 8 rows (a packed decode step) each row has the bits that it
  * has alone; with more rows the order of the sums may differ.
  * y: [m][n], aligned to its type; n 1 .. TQ_Q4_MAX_N, k up to TQ_Q4_MAX_K, m 1 ..
- * TQ_Q4_MAX_ROWS. */
+ * TQ_Q4_MAX_ROWS.  workspace: as above, may be NULL where none is needed. */
 tq_status tq_q4_gemv(const tq_q4_weight *w, const uint16_t *x, int32_t m, void *y, int32_t y_type,
-                     tq_stream_t stream);
+                     void *workspace, size_t workspace_bytes, tq_stream_t stream);
 
 /* Gate and up of a gated FFN in one pass, each as tq_q4_gemv (g and u in fp32):
  *   h[r][i] = bf16_rn(g / (1 + exp(-g)) * u)                 (as tq_ffn_step)
  * gate, up: same n, k, group, and minima in both or in neither.  h: bf16 bits
- * [m][n]. */
+ * [m][n].  workspace: as above. */
 tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const uint16_t *x,
-                       int32_t m, uint16_t *h, tq_stream_t stream);
+                       int32_t m, uint16_t *h, void *workspace, size_t workspace_bytes,
+                       tq_stream_t stream);
 
 /* The bits of the bounded waits that have run out in any tq_q4_* call of this
  * process on the current device since the library was loaded (calls of more than
@@ -93,7 +100,8 @@ tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const u
  *   bit 1  the matrix instructions waited for x    bit 2  for decoded weights
  *   bit 3  for a free accumulator                  bit 4  at exit
  *   bit 6  the copies of x in flight at exit
- *   bit 7  the fold waited for scales              bit 8  for an accumulator */
+ *   bit 7  the fold waited for the sums of x        bit 8  for an accumulator
+ *   bit 9  the copies of the sums waited for a free place */
 tq_status tq_q4_read_error_word(uint32_t *value, tq_stream_t stream);
 
 #ifdef __cplusplus

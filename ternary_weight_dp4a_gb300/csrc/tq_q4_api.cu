@@ -53,12 +53,15 @@ tq::Q4Product product(const tq_q4_weight *w, const tq_q4_weight *up, const uint1
     return p;
 }
 
-// Calls of more rows than this run on the tile kernel.
-constexpr int kStreamRows = 16;
-
-tq_status run(const tq::Q4Product &p, tq_stream_t stream) {
+tq_status run(const tq::Q4Product &p, void *workspace, size_t workspace_bytes, tq_stream_t stream) {
     cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
-    return cuda_status(p.m > kStreamRows ? tq::q4_tile_launch(p, str) : tq::q4_stream_launch(p, str));
+    if (p.m <= tq::kQ4StreamRows) return cuda_status(tq::q4_stream_launch(p, str));
+    if (p.mins[0] != nullptr) {
+        if (workspace == nullptr) return TQ_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return TQ_ERR_ALIGNMENT;
+        if (workspace_bytes < tq::q4_sums_bytes(p.m, p.k, p.group)) return TQ_ERR_WORKSPACE;
+    }
+    return cuda_status(tq::q4_tile_launch(p, static_cast<float *>(workspace), str));
 }
 
 }  // namespace
@@ -71,6 +74,11 @@ size_t tq_q4_codes_bytes(int32_t n, int32_t k) {
 
 size_t tq_q4_scales_bytes(int32_t n, int32_t k, int32_t group) {
     return sizes_ok(n, k) && group_ok(group) ? static_cast<size_t>(tq::q4_strips(n)) * tq::kQ4Strip * (k / group) * 2 : 0;
+}
+
+size_t tq_q4_workspace_bytes(int32_t m, int32_t k, int32_t group) {
+    if (m < 1 || m > TQ_Q4_MAX_ROWS || !sizes_ok(1, k) || !group_ok(group) || m <= tq::kQ4StreamRows) return 0;
+    return tq::q4_sums_bytes(m, k, group);
 }
 
 tq_status tq_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint16_t *mins, int32_t n,
@@ -87,7 +95,7 @@ tq_status tq_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint16_
 }
 
 tq_status tq_q4_gemv(const tq_q4_weight *w, const uint16_t *x, int32_t m, void *y, int32_t y_type,
-                     tq_stream_t stream) {
+                     void *workspace, size_t workspace_bytes, tq_stream_t stream) {
     tq_status st = check_weight(w);
     if (st != TQ_OK) return st;
     if (y_type != TQ_F32 && y_type != TQ_BF16) return TQ_ERR_INVALID_ARG;
@@ -95,11 +103,12 @@ tq_status tq_q4_gemv(const tq_q4_weight *w, const uint16_t *x, int32_t m, void *
     tq::Q4Product p = product(w, nullptr, x, m);
     p.y = y;
     p.y_bf16 = y_type == TQ_BF16;
-    return run(p, stream);
+    return run(p, workspace, workspace_bytes, stream);
 }
 
 tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const uint16_t *x,
-                       int32_t m, uint16_t *h, tq_stream_t stream) {
+                       int32_t m, uint16_t *h, void *workspace, size_t workspace_bytes,
+                       tq_stream_t stream) {
     tq_status st = check_weight(gate);
     if (st != TQ_OK) return st;
     if ((st = check_weight(up)) != TQ_OK) return st;
@@ -109,7 +118,7 @@ tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const u
     tq::Q4Product p = product(gate, up, x, m);
     p.y = h;
     p.y_bf16 = true;
-    return run(p, stream);
+    return run(p, workspace, workspace_bytes, stream);
 }
 
 tq_status tq_q4_read_error_word(uint32_t *value, tq_stream_t stream) {

@@ -27,9 +27,16 @@ struct Q4Product {
 
 cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const uint16_t *mins, int n, int k, int group,
                            uint8_t *out_codes, uint16_t *out_scales, uint16_t *out_mins, cudaStream_t stream);
-// Any number of rows, 16 per pass over the weights; and 128 per pass.
+// Calls of more rows than this run on the tile kernel.
+constexpr int kQ4StreamRows = 16;
+
+// Workspace of the tile kernel, where there are minima: sums of x over the groups, [k / group][q4_sums_ld(m)].
+constexpr int64_t q4_sums_ld(int64_t m) { return (m + 15) / 16 * 16; }
+constexpr size_t q4_sums_bytes(int64_t m, int64_t k, int64_t group) { return static_cast<size_t>(q4_sums_ld(m) * (k / group) * 4); }
+
+// Any number of rows, 16 per pass over the weights; and 192 per pass.
 cudaError_t q4_stream_launch(const Q4Product &p, cudaStream_t stream);
-cudaError_t q4_tile_launch(const Q4Product &p, cudaStream_t stream);
+cudaError_t q4_tile_launch(const Q4Product &p, float *sums, cudaStream_t stream);
 // The bits of the bounded waits that have run out on the current device (copied in `stream`).
 cudaError_t q4_tile_waits(unsigned *bits, cudaStream_t stream);
 

@@ -23,6 +23,7 @@ ENGINE_AUTO, ENGINE_DP4A, ENGINE_TCGEN05 = 0, 1, 2
 TQ_ERR_TIMEOUT = 6
 BLOCK = 128
 MAX_ROWS = 64
+Q4_STREAM_ROWS = 16
 
 # every entry point that the headers in include/ declare
 EXPORTS = ("tq_status_string", "tq_last_cuda_error", "tq_set_engine", "tq_get_engine",
@@ -34,7 +35,7 @@ EXPORTS = ("tq_status_string", "tq_last_cuda_error", "tq_set_engine", "tq_get_en
            "tq_rmsnorm_bf16",
            "tq_add_rmsnorm_rotq", "tq_moe_route", "tq_moe_workspace_bytes", "tq_moe_read_error_word", "tq_moe_plan",
            "tq_moe_gemv", "tq_moe_gateup", "tq_moe_combine", "tq_moe_ffn",
-           "tq_q4_codes_bytes", "tq_q4_scales_bytes", "tq_q4_pack", "tq_q4_gemv", "tq_q4_gateup",
+           "tq_q4_codes_bytes", "tq_q4_scales_bytes", "tq_q4_workspace_bytes", "tq_q4_pack", "tq_q4_gemv", "tq_q4_gateup",
            "tq_q4_read_error_word", "tq_sample",
            "tq_lifecycle_init", "tq_lifecycle_load", "tq_lifecycle_copy", "tq_lifecycle_alloc",
            "tq_lifecycle_free", "tq_lifecycle_poll", "tq_lifecycle_release", "tq_lifecycle_destroy")
@@ -152,8 +153,10 @@ def load():
             L.tq_q4_scales_bytes.argtypes = [i32, i32, i32]
             L.tq_q4_scales_bytes.restype = sz
             L.tq_q4_pack.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
-            L.tq_q4_gemv.argtypes = [Q, vp, i32, vp, i32, vp]
-            L.tq_q4_gateup.argtypes = [Q, Q, vp, i32, vp, vp]
+            L.tq_q4_workspace_bytes.argtypes = [i32, i32, i32]
+            L.tq_q4_workspace_bytes.restype = sz
+            L.tq_q4_gemv.argtypes = [Q, vp, i32, vp, i32, vp, sz, vp]
+            L.tq_q4_gateup.argtypes = [Q, Q, vp, i32, vp, vp, sz, vp]
             L.tq_q4_read_error_word.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
             L.tq_sample.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
             LC = ctypes.POINTER(_Lifecycle)
@@ -173,7 +176,7 @@ def load():
             for name in EXPORTS:
                 if name not in ("tq_status_string", "tq_last_cuda_error", "tq_ffn_workspace_bytes",
                                 "tq_gemv_workspace_bytes", "tq_moe_workspace_bytes", "tq_q4_codes_bytes", "tq_q4_scales_bytes",
-                                "tq_ffn_workspace_error_offset", "tq_ffn_static_workspace_bytes", "tq_lifecycle_copy", "tq_lifecycle_alloc",
+                                "tq_q4_workspace_bytes", "tq_ffn_workspace_error_offset", "tq_ffn_static_workspace_bytes", "tq_lifecycle_copy", "tq_lifecycle_alloc",
                                 "tq_lifecycle_free", "tq_lifecycle_release", "tq_lifecycle_destroy"):
                     getattr(L, name).restype = ctypes.c_int
             _lib = L
@@ -793,8 +796,24 @@ def pack_q4(codes, scales, mins=None, stream=None) -> PackedQ4:
     return PackedQ4(out, out_scales, out_mins, n, k, group)
 
 
-def q4_gemv(w: PackedQ4, x, y=None, dtype=None, stream=None):
-    """x bf16 [m][k] -> x W^T [m][n] (float32 unless dtype or y says bf16)."""
+def q4_workspace_bytes(m: int, k: int, group: int) -> int:
+    return int(load().tq_q4_workspace_bytes(m, k, group))
+
+
+def _q4_scratch(w: PackedQ4, m: int, device, workspace, stream):
+    """(address, size) of the workspace that a product takes: the caller's, or one for this call where it needs one."""
+    import torch
+    if workspace is None:
+        if w.mins is None or m <= Q4_STREAM_ROWS:
+            return None, 0, 0
+        workspace = _new(stream, torch.empty, q4_workspace_bytes(m, w.k, w.group), dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), workspace.numel()
+    return workspace, _tensor(_device(), "workspace", workspace, (torch.uint8,)), workspace.numel()
+
+
+def q4_gemv(w: PackedQ4, x, y=None, dtype=None, workspace=None, stream=None):
+    """x bf16 [m][k] -> x W^T [m][n] (float32 unless dtype or y says bf16).  workspace: uint8, of
+    q4_workspace_bytes, to keep between calls (only matrices with minima and more than 16 rows need one)."""
     import torch
     dev = _device()
     p_x = _tensor(dev, "x", x, (torch.bfloat16,))
@@ -804,12 +823,14 @@ def q4_gemv(w: PackedQ4, x, y=None, dtype=None, stream=None):
     if y is None:
         y = _new(stream, torch.empty, (m, w.n), dtype=dtype or torch.float32, device=x.device)
     p_y = _tensor(dev, "y", y, (torch.float32, torch.bfloat16), (m, w.n))
-    _check("tq_q4_gemv", load().tq_q4_gemv(_q4(dev, "w", w), p_x, m, p_y, int(y.dtype == torch.bfloat16), _stream(stream)))
+    held, p_ws, size = _q4_scratch(w, m, x.device, workspace, stream)
+    _check("tq_q4_gemv", load().tq_q4_gemv(_q4(dev, "w", w), p_x, m, p_y, int(y.dtype == torch.bfloat16), p_ws, size,
+                                           _stream(stream)))
     return y
 
 
-def q4_gateup(gate: PackedQ4, up: PackedQ4, x, h=None, stream=None):
-    """x bf16 [m][k] -> SiLU(gate) * up as bf16 [m][n]."""
+def q4_gateup(gate: PackedQ4, up: PackedQ4, x, h=None, workspace=None, stream=None):
+    """x bf16 [m][k] -> SiLU(gate) * up as bf16 [m][n].  workspace: as q4_gemv."""
     import torch
     dev = _device()
     p_x = _tensor(dev, "x", x, (torch.bfloat16,))
@@ -821,7 +842,9 @@ def q4_gateup(gate: PackedQ4, up: PackedQ4, x, h=None, stream=None):
         p_h = h.data_ptr()
     else:
         p_h = _tensor(dev, "h", h, (torch.bfloat16,), (m, gate.n))
-    _check("tq_q4_gateup", load().tq_q4_gateup(_q4(dev, "gate", gate), _q4(dev, "up", up), p_x, m, p_h, _stream(stream)))
+    held, p_ws, size = _q4_scratch(gate, m, x.device, workspace, stream)
+    _check("tq_q4_gateup", load().tq_q4_gateup(_q4(dev, "gate", gate), _q4(dev, "up", up), p_x, m, p_h, p_ws, size,
+                                               _stream(stream)))
     return h
 
 

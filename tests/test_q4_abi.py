@@ -50,11 +50,11 @@ def test_pack_rejects(lib):
 
 
 def test_products_reject(lib):
-    def gemv(w=_w(), x=0x7000, m=3, y=0x8000, t=0):
-        return lib.tq_q4_gemv(ctypes.byref(w) if w else None, P(x), m, P(y), t, ST)
+    def gemv(w=_w(), x=0x7000, m=3, y=0x8000, t=0, ws=0, size=0):
+        return lib.tq_q4_gemv(ctypes.byref(w) if w else None, P(x), m, P(y), t, P(ws), size, ST)
 
-    def gateup(g=_w(), u=_w(), x=0x7000, m=3, h=0x8000):
-        return lib.tq_q4_gateup(ctypes.byref(g) if g else None, ctypes.byref(u) if u else None, P(x), m, P(h), ST)
+    def gateup(g=_w(), u=_w(), x=0x7000, m=3, h=0x8000, ws=0, size=0):
+        return lib.tq_q4_gateup(ctypes.byref(g) if g else None, ctypes.byref(u) if u else None, P(x), m, P(h), P(ws), size, ST)
     assert gemv(w=None) == ARG and gateup(g=None) == ARG and gateup(u=None) == ARG
     for bad in BAD:
         assert gemv(w=_w(**bad)) == ARG and gateup(g=_w(**bad)) == ARG and gateup(u=_w(**bad)) == ARG, bad
@@ -65,6 +65,13 @@ def test_products_reject(lib):
         assert call(x=0x7008) == ALIGN
     assert gemv(y=0) == ARG and gemv(t=2) == ARG and gemv(t=-1) == ARG and gemv(y=0x8002) == ALIGN and gemv(y=0x8001, t=1) == ALIGN
     assert gateup(h=0) == ARG and gateup(h=0x8001) == ALIGN
+    m = 17                                                                  # minima: sums of x are needed
+    mins, need = _w(mins=0x3000), lib.tq_q4_workspace_bytes(m, 256, 64)
+    assert need == 32 * 4 * 4 and lib.tq_q4_workspace_bytes(16, 256, 64) == 0
+    for bad in ((0, 256, 64), (17, 200, 64), (17, 256, 16), (1 << 21, 256, 64)):
+        assert lib.tq_q4_workspace_bytes(*bad) == 0
+    for call in (lambda **a: gemv(w=mins, m=m, **a), lambda **a: gateup(g=mins, u=mins, m=m, **a)):
+        assert call() == ARG and call(ws=0x9010, size=need) == ALIGN and call(ws=0x9000, size=need - 1) == 4
     for other in (dict(n=41), dict(k=128), dict(group=32), dict(mins=0x3000)):
         assert gateup(u=_w(**other)) == ARG, other
 
@@ -86,8 +93,8 @@ def _tensors(torch):
     up = {name + "2": kind for name, kind in w.items()}
     return {
         "pack": dict(codes=(u8, 40, 256), scales=(f16, 40, 4), mins=(f16, 40, 4)),
-        "gemv": dict(w, x=(bf16, 3, 256), y=(f32, 3, 40)),
-        "gateup": dict(w, **up, x=(bf16, 3, 256), h=(bf16, 3, 40)),
+        "gemv": dict(w, x=(bf16, 3, 256), y=(f32, 3, 40), workspace=(u8, 4096)),
+        "gateup": dict(w, **up, x=(bf16, 3, 256), h=(bf16, 3, 40), workspace=(u8, 4096)),
         "sample": dict(logits=(bf16, 3, 50), uniform=(f32, 3), temperature=(f32, 3), top_k=(i32, 3), top_p=(f32, 3),
                        min_p=(f32, 3), ids=(i32, 3), probs=(f32, 3)),
     }
@@ -98,9 +105,9 @@ def _call(op, t):
     if op == "pack":
         return tq.pack_q4(t["codes"], t["scales"], t["mins"], stream=0)
     if op == "gemv":
-        return tq.q4_gemv(w(), t["x"], y=t["y"], stream=Stream())
+        return tq.q4_gemv(w(), t["x"], y=t["y"], workspace=t["workspace"], stream=Stream())
     if op == "gateup":
-        return tq.q4_gateup(w(), w("2"), t["x"], h=t["h"], stream=Stream())
+        return tq.q4_gateup(w(), w("2"), t["x"], h=t["h"], workspace=t["workspace"], stream=Stream())
     return tq.sample(t["logits"], t["uniform"], t["temperature"], t["top_k"], t["top_p"], t["min_p"], ids=t["ids"],
                      probs=t["probs"], stream=Stream())
 
@@ -115,8 +122,8 @@ def test_every_tensor_is_checked(launched, op):  # noqa: F811
     for name, kind in kinds.items():
         for wrong in (Tensor(*kind, at=HOST), Tensor(*kind, at=ELSEWHERE), Tensor(*kind, contiguous=False),
                       Tensor(torch.float64, *kind[1:]), Tensor(*kind[:-1], kind[-1] + 1)):
-            if op == "sample" and name == "logits" and wrong.shape != kind[1:]:
-                continue                                                    # any vocabulary
+            if name in ("logits", "workspace") and wrong.shape != kind[1:]:
+                continue                                                    # any vocabulary; the library looks at the size
             t = {n: Tensor(*k) for n, k in kinds.items()}
             t[name] = wrong
             for other in t.values():
