@@ -30,15 +30,14 @@ namespace tq {
 namespace {
 
 constexpr int kCols = 192;                      // most rows of x per tile
-constexpr int kStageK = 64;
-constexpr int kStages = 6;                      // of x in shared memory
-constexpr int kABufs = 4;                       // of decoded weights: 64 values, 32 columns of tensor memory each
+constexpr int kABufs = 4;                       // of decoded weights: 64 values of k, 32 columns of tensor memory each
+constexpr int kStages = 2;                      // of x in shared memory: 128 values each, in two halves
+constexpr int kMaxBufs = 8;                     // accumulators
 constexpr int kSums = 8;                        // groups' sums of x in shared memory
-constexpr int kBoxRows = 32;
 constexpr int kFoldWarps = 12;
 constexpr int kFoldCols = kCols / (kFoldWarps / 4);
 constexpr int kThreads = 256 + 32 * kFoldWarps;
-constexpr uint32_t kStageBytes = kCols * kStageK * 2;
+constexpr uint32_t kHalfBytes = kCols * 128;     // of a stage: 64 values
 constexpr uint32_t kTmemA = 2 * kCols;
 constexpr int kAhead = 16;                      // chunks of codes in L2 ahead of the decode
 constexpr int kPartLd = 128 + 4;                // floats per row of x of a part
@@ -50,11 +49,11 @@ __device__ unsigned lost_waits;                 // bits of all waits that have r
 
 struct __align__(1024) TileSmem {
     union {
-        uint8_t x[kStages][kStageBytes];
+        uint8_t x[kStages][2][kHalfBytes];
         float part[kCols][kPartLd];             // this CTA's sums, when a tile is split along k
     };
     float sums[kSums][kCols];
-    uint64_t x_full[kStages], x_empty[kStages], a_full[kABufs], a_empty[kABufs], d_full[2], d_empty[2];
+    uint64_t x_full[kStages], a_full[kABufs], empty[kABufs], d_full[kMaxBufs], d_empty[kMaxBufs];
     uint64_t s_full[kSums], s_empty[kSums], drain;
     uint32_t tmem;
     uint32_t dead;                              // a bounded wait ran out
@@ -62,7 +61,7 @@ struct __align__(1024) TileSmem {
 
 struct TileArgs {
     Q4Product p;
-    CUtensorMap x;                              // [m][k] bf16, boxes of 32 rows x 64 values
+    CUtensorMap x;                              // [m][k] bf16, boxes of a tile's rows x 64 values
     const float *sums;                          // [k / group][sums_ld]: sums of x over the groups, where there are minima
     int64_t sums_ld;
     int row_tiles, rows;                        // rows of x per tile
@@ -73,11 +72,27 @@ constexpr uint32_t idesc_bf16(int m, int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The whole warp runs this, one thread issues: a branch around it would take the operands out of the uniform registers.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(issue)
         : "memory");
+}
+
+__device__ __forceinline__ void commit_if(uint32_t issue, uint32_t bar) {
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+        "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+    return e;
 }
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
@@ -153,27 +168,32 @@ __device__ __forceinline__ void wait_slow(TileSmem &sm, uint32_t bar, uint32_t p
         }
     }
 }
-// Waits, and says whether the CTA is still alive (one answer for the whole warp).
+// Waits, and says whether the CTA is still alive.
+template <int SLEEP = 0>
+__device__ __forceinline__ bool wait_alive(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned bit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    wait_slow<SLEEP>(sm, bar, parity, bit);
+    return *reinterpret_cast<volatile uint32_t *>(&sm.dead) == 0;
+}
+// The same for a whole warp: one answer.
 template <int SLEEP = 0>
 __device__ __forceinline__ bool warp_wait(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned bit) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        wait_slow<SLEEP>(sm, bar, parity, bit);
-        ok = *reinterpret_cast<volatile uint32_t *>(&sm.dead) == 0;
-    }
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, wait_alive<SLEEP>(sm, bar, parity, bit));
 }
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+// A float of CTA `rank`'s shared memory.
+__device__ __forceinline__ float ld_part(uint32_t addr, uint32_t rank, int cluster) {
     float v;
-    asm volatile("{ .reg .u32 a; mapa.shared::cluster.u32 a, %1, %2; ld.shared::cluster.f32 %0, [a]; }"
-                 : "=f"(v)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
+    if (cluster == 1) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    else
+        asm volatile("{ .reg .u32 a; mapa.shared::cluster.u32 a, %1, %2; ld.shared::cluster.f32 %0, [a]; }"
+                     : "=f"(v)
+                     : "r"(addr), "r"(rank)
+                     : "memory");
     return v;
 }
 
@@ -220,26 +240,34 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     constexpr int kOut = GATEUP ? 64 : 128;                         // outputs per tile
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int chunks = p.k >> 7;
+    const int rank = blockIdx.x % args.split, tile = blockIdx.x / args.split;
+    const int row0 = tile % args.row_tiles * args.rows, ntile = tile / args.row_tiles;
+    const int rows = min(args.rows, p.m - row0), cols = (rows + 15) / 16 * 16;      // (args.rows: a multiple of 16)
+    const int chunk0 = rank * chunks / args.split, chunk1 = (rank + 1) * chunks / args.split;
+    const int total = chunk1 - chunk0, groups = total * kPer;       // chunks and groups of this CTA
+    // Accumulators of 32, 96 or 192 columns.  Up to 64 rows of x, each third of the fold's warps takes all columns
+    // of every third group: a hand-over costs some 300 cycles, and short groups follow each other faster.
+    const int dshift = cols <= 32 ? 3 : cols <= 96 ? 2 : 1, dcols = cols <= 32 ? 32 : 2 * kCols >> dshift;
+    const int teams = cols <= kFoldCols ? 3 : 1;
+
     if (warp == 4) {
         tmem_alloc(smem_u32(&sm.tmem), 512);
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sm.x_full[i]), 1);
-            mbar_init(smem_u32(&sm.x_empty[i]), 1);
-        }
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sm.x_full[i]), 1);
         for (int i = 0; i < kABufs; ++i) {
             mbar_init(smem_u32(&sm.a_full[i]), 4);
-            mbar_init(smem_u32(&sm.a_empty[i]), 1);
+            mbar_init(smem_u32(&sm.empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kMaxBufs; ++i) {
             mbar_init(smem_u32(&sm.d_full[i]), 1);
-            mbar_init(smem_u32(&sm.d_empty[i]), kFoldWarps);
+            mbar_init(smem_u32(&sm.d_empty[i]), teams > 1 ? 4 : kFoldWarps);
         }
         for (int i = 0; i < kSums; ++i) {
             mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.s_empty[i]), kFoldWarps);
+            mbar_init(smem_u32(&sm.s_empty[i]), teams > 1 ? 4 : kFoldWarps);
         }
         mbar_init(smem_u32(&sm.drain), 1);
         sm.dead = 0;
@@ -249,13 +277,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int chunks = p.k >> 7;
-    const int rank = blockIdx.x % args.split, tile = blockIdx.x / args.split;
-    const int row0 = tile % args.row_tiles * args.rows, ntile = tile / args.row_tiles;
-    const int rows = min(args.rows, p.m - row0), cols = (rows + 15) / 16 * 16;
-    const int chunk0 = rank * chunks / args.split, chunk1 = (rank + 1) * chunks / args.split;
-    const int stages = 2 * (chunk1 - chunk0), groups = (chunk1 - chunk0) * kPer;
-
     // The weight row of this thread's lane of tensor memory (decode and fold): a quarter of the lanes is two
     // strips, gate and up of one or two neighbours.  Behind the last strip: the last one, whose results go nowhere.
     const int quarter = warp & 3, mat = GATEUP ? lane >> 4 : 0;
@@ -264,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     const int64_t block0 = strip * chunks + chunk0;
     // Packed codes come to L2 well ahead of the decode's loads, which have one chunk in flight.
     auto ask = [&](int from, int to) {
-        to = min(to, chunk1 - chunk0);
+        to = min(to, total);
         if (warp < 4 && (lane & 15) == 0 && from < to)
             prefetch_l2(p.codes[mat] + (block0 + from) * kQ4ChunkBytes, (to - from) * kQ4ChunkBytes);
     };
@@ -286,12 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                              : "l"(at));
             }
         };
-        const int total = chunk1 - chunk0;
         uint32_t mask = 0x000f000fu, base = 0x43004300u;
         asm volatile("" : "+r"(mask), "+r"(base));                  // in registers: two constants do not fit one instruction
         load(0, 0);
         bool ok = true;
-        for (int c0 = 0; c0 < total && ok; c0 += 2) {
+        uint32_t turn = 1;
+        const uint32_t empty = smem_u32(sm.empty), a_full = smem_u32(sm.a_full);
+        for (int c0 = 0; c0 < total && ok; c0 += 2, turn ^= 1) {
 #pragma unroll
             for (int buf = 0; buf < 2; ++buf) {
                 const int c = c0 + buf;
@@ -300,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 if (c % 4 == 0) ask(c + kAhead, c + kAhead + 4);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int st = 2 * c + half, abuf = st % kABufs;
-                    ok = warp_wait<32>(sm, smem_u32(&sm.a_empty[abuf]), ((st / kABufs) & 1) ^ 1, 1u << 0);
+                    const int abuf = 2 * buf + half;                // (four buffers are two chunks)
+                    ok = warp_wait<32>(sm, empty + 8 * abuf, turn, 1u << 0);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -320,69 +342,73 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.a_full[abuf]));
+                    if (lane == 0) mbar_arrive(a_full + 8 * abuf);
                 }
             }
         }
     } else if (warp < 8) {
         regs_down<kRegsIssue>();
         if (warp == 4) {
-            // ---- issue ----
-            const uint32_t idesc = idesc_bf16(128, cols);
-            int group = 0;
-            for (int st = 0; st < stages; ++st) {
-                const int ring = st % kStages, abuf = st % kABufs;
-                constexpr int kSubs = GROUP == 32 ? 2 : 1;
-                bool ok = true;
+            // ---- issue: one thread issues, the warp stays together ----
+            const uint32_t issue = elect_one();
+            const uint32_t idesc = idesc_bf16(128, cols), bufs = 1u << dshift;
+            const uint32_t x_full = smem_u32(sm.x_full), a_full = smem_u32(sm.a_full), empty = smem_u32(sm.empty);
+            const uint32_t d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
+            const uint64_t x_desc = desc_sw128(smem_u32(sm.x));
+            // (tensor memory is this CTA's as a whole, so its columns count from 0)
+            uint32_t turn = 0, buf = 0, d_turn = 1, d = 0;
+            bool ok = true;
+            for (int c0 = 0; c0 < total && ok; c0 += 2, turn ^= 1) {
 #pragma unroll
-                for (int sub = 0; sub < kSubs && ok; ++sub) {
-                    const bool start = GROUP < 128 || (st & 1) == 0, end = GROUP < 128 || (st & 1) == 1;
-                    // up to three waits at once, one lane each (one that need not wait takes 130 cycles, too)
-                    const int which = sub > 0 ? 2 : min(lane, start ? 2 : 1);
-                    const uint32_t bar = smem_u32(which == 0 ? &sm.x_full[ring] : which == 1 ? &sm.a_full[abuf] : &sm.d_empty[group & 1]);
-                    const uint32_t parity = which == 0 ? (st / kStages) & 1 : which == 1 ? (st / kABufs) & 1 : ((group >> 1) & 1) ^ 1;
-                    ok = warp_wait(sm, bar, parity, 1u << (1 + which));
-                    if (!ok) break;
-                    if (lane == 0) {
+                for (int ring = 0; ring < kABufs; ++ring) {
+                    if (c0 + ring / 2 >= total || !ok) break;
+                    constexpr int kSubs = GROUP == 32 ? 2 : 1, kEach = 4 / kSubs;
+                    const bool start = GROUP < 128 || ring % 2 == 0, end = GROUP < 128 || ring % 2 == 1;
+                    if (ring % 2 == 0) ok = wait_alive(sm, x_full + 4 * ring, turn, 1u << 1);
+                    ok = ok && wait_alive(sm, a_full + 8 * ring, turn, 1u << 2);
+#pragma unroll
+                    for (int sub = 0; sub < kSubs; ++sub) {
+                        if (start) ok = ok && wait_alive(sm, d_empty + 8 * buf, d_turn, 1u << 3);
+                        if (!ok) break;
                         tc_fence_after();
-                        const uint32_t d = tmem + (group & 1) * kCols, a = tmem + kTmemA + abuf * 32;
-                        const uint64_t b = desc_sw128(smem_u32(sm.x[ring]));
 #pragma unroll
-                        for (int i = sub * (4 / kSubs); i < (sub + 1) * (4 / kSubs); ++i)
-                            mma_bf16_ts(d, a + 8 * i, b + 2 * i, idesc, !(start && i == sub * (4 / kSubs)));
-                        if (end) tc_commit(smem_u32(&sm.d_full[group & 1]));
+                        for (int i = sub * kEach; i < (sub + 1) * kEach; ++i)
+                            mma_bf16_ts(issue, d, kTmemA + 32 * ring + 8 * i, x_desc + (ring * (kHalfBytes >> 4) + 2 * i), idesc,
+                                        !(start && i == sub * kEach));
+                        if (end) {
+                            commit_if(issue, d_full + 8 * buf);
+                            d += dcols;
+                            if (++buf == bufs) {
+                                buf = 0;
+                                d = 0;
+                                d_turn ^= 1;
+                            }
+                        }
                     }
-                    __syncwarp();
-                    if (end) ++group;
+                    if (ok) commit_if(issue, empty + 8 * ring);
                 }
-                if (!ok) break;
-                if (lane == 0) {
-                    tc_commit(smem_u32(&sm.x_empty[ring]));
-                    tc_commit(smem_u32(&sm.a_empty[abuf]));
-                }
-                __syncwarp();
             }
-            if (lane == 0) {
-                tc_commit(smem_u32(&sm.drain));
-                if (!mbar_wait(smem_u32(&sm.drain), 0)) atomicOr(&lost_waits, 1u << 4);
-            }
+            __syncwarp();
+            commit_if(issue, smem_u32(&sm.drain));
+            if (!mbar_wait(smem_u32(&sm.drain), 0) && issue) atomicOr(&lost_waits, 1u << 4);
+            __syncwarp();
         } else if (warp == 5) {
-            // ---- copies of x ----
-            const int boxes = (rows + kBoxRows - 1) / kBoxRows;
-            int st = 0;
-            for (; st < stages; ++st) {
-                const int ring = st % kStages;
-                if (!warp_wait<32>(sm, smem_u32(&sm.x_empty[ring]), ((st / kStages) & 1) ^ 1, 1u << 5)) break;
-                const uint32_t bar = smem_u32(&sm.x_full[ring]);
-                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes) * kBoxRows * kStageK * 2);
-                __syncwarp();
-                if (lane < boxes)
-                    load_box(smem_u32(sm.x[ring]) + lane * kBoxRows * kStageK * 2, &args.x, chunk0 * 128 + st * kStageK,
-                             row0 + lane * kBoxRows, bar);
+            // ---- copies of x: one thread ----
+            if (lane == 0) {
+                int c = 0;
+                for (; c < total; ++c) {
+                    const int ring = c % kStages;                   // free with the second of its buffers of weights
+                    if (!wait_alive<32>(sm, smem_u32(&sm.empty[2 * ring + 1]), ((c / kStages) & 1) ^ 1, 1u << 5)) break;
+                    const uint32_t bar = smem_u32(&sm.x_full[ring]);
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(args.rows) * 256);
+                    load_box(smem_u32(sm.x[ring][0]), &args.x, (chunk0 + c) * 128, row0, bar);
+                    load_box(smem_u32(sm.x[ring][1]), &args.x, (chunk0 + c) * 128 + 64, row0, bar);
+                }
+                // none of this CTA's copies may be in flight when it leaves
+                for (int j = max(c - kStages, 0); j < c; ++j)
+                    if (!mbar_wait(smem_u32(&sm.x_full[j % kStages]), (j / kStages) & 1)) atomicOr(&lost_waits, 1u << 6);
             }
-            // none of this CTA's copies may be in flight when it leaves
-            for (int j = max(st - kStages, 0); j < st; ++j)
-                if (!mbar_wait(smem_u32(&sm.x_full[j % kStages]), (j / kStages) & 1)) atomicOr(&lost_waits, 1u << 6);
+            __syncwarp();
         } else if (warp == 6 && MINS) {
             // ---- copies of the sums ----
             const float *src = args.sums + static_cast<int64_t>(chunk0) * kPer * args.sums_ld + row0;
@@ -404,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     } else {
         // ---- fold: a lane is a weight row, a warp has a third of the rows of x ----
         regs_up<kRegsFold>();
-        const int col0 = (warp - 8) / 4 * kFoldCols, mine = min(max(cols - col0, 0), kFoldCols);
+        const int third = (warp - 8) / 4, team = teams > 1 ? third : 0;
+        const int col0 = teams > 1 ? 0 : third * kFoldCols, mine = min(max(cols - col0, 0), kFoldCols);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
         const int64_t sat = (block0 * 8 + (lane & 7)) * (2 * kPer) + ((lane >> 3) & 1) * kPer;
         const uint16_t *ssrc = p.scales[mat] + sat, *msrc = MINS ? p.mins[mat] + sat : nullptr;
@@ -415,32 +442,49 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         load_scales<kPer>(next, ssrc);
         if (MINS) load_scales<kPer>(mnext, msrc);
         bool ok = true;
-        int group = 0;
+        int group = 0, turn = 0;
+        uint32_t buf = 0, d_turn = 0, d_at = lane_base;
+        const uint32_t bufs = 1u << dshift, d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
+        auto step = [&] {
+            d_at += dcols;
+            if (++buf == bufs) {
+                buf = 0;
+                d_at = lane_base;
+                d_turn ^= 1;
+            }
+        };
 #pragma unroll 1
-        for (int c = 0; c < chunk1 - chunk0 && ok; ++c) {
+        for (int c = 0; c < total && ok; ++c) {
 #pragma unroll
             for (int i = 0; i < (kPer + 1) / 2; ++i) {
                 sc[i] = next[i];
                 if (MINS) mn[i] = mnext[i];
             }
-            if (c + 1 < chunk1 - chunk0) {
+            if (c + 1 < total) {
                 load_scales<kPer>(next, ssrc + static_cast<int64_t>(c + 1) * (16 * kPer));
                 if (MINS) load_scales<kPer>(mnext, msrc + static_cast<int64_t>(c + 1) * (16 * kPer));
             }
 #pragma unroll
             for (int e = 0; e < kPer; ++e, ++group) {
+                if (teams > 1) {
+                    const bool others = turn != team;
+                    turn = turn == 2 ? 0 : turn + 1;
+                    if (others) {
+                        step();
+                        continue;
+                    }
+                }
                 const float s = scale_at(sc, e);
                 const uint64_t s2 = pack2(s, s);
                 float m = 0.0f;
                 if (MINS) m = __fmaf_rn(8.0f, s, -scale_at(mn, e));
                 const uint64_t m2 = pack2(m, m);
                 const int slot = group % kSums;
-                const bool sums = MINS && (lane & 1);               // both waits at once
-                ok = warp_wait<20>(sm, smem_u32(sums ? &sm.s_full[slot] : &sm.d_full[group & 1]),
-                                   sums ? (group / kSums) & 1 : (group >> 1) & 1, sums ? 1u << 7 : 1u << 8);
+                ok = warp_wait(sm, d_full + 8 * buf, d_turn, 1u << 8) &&
+                     (!MINS || warp_wait(sm, smem_u32(&sm.s_full[slot]), (group / kSums) & 1, 1u << 7));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t d = lane_base + (group & 1) * kCols;
+                const uint32_t d = d_at;
 #pragma unroll
                 for (int q = 0; q < kFoldCols / 16; ++q) {
                     if (16 * q >= mine) break;
@@ -462,18 +506,21 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_u32(&sm.d_empty[group & 1]));
+                    mbar_arrive(d_empty + 8 * buf);
                     if (MINS) mbar_arrive(smem_u32(&sm.s_empty[slot]));
                 }
+                step();
             }
         }
         const int local = 32 * quarter + lane;                      // row of the tile
-        if (args.split > 1) {
-            // (every MMA and copy of this CTA has ended: its stages hold the part now)
+        if (args.split > 1 || teams > 1) {
+            // the stages hold this CTA's parts now: no copy or MMA uses them once all teams are here
+            named_barrier(1, 32 * kFoldWarps);
 #pragma unroll
             for (int i = 0; i < kFoldCols; ++i)
-                if (i < mine) sm.part[col0 + i][local] = half2of(acc[i >> 1], i & 1);
-            cluster_sync();
+                if (i < mine) sm.part[(teams > 1 ? team * kFoldCols : col0) + i][local] = half2of(acc[i >> 1], i & 1);
+            if (args.split > 1) cluster_sync();
+            else named_barrier(1, 32 * kFoldWarps);
             const int o0 = rank * kOut / args.split, width = (rank + 1) * kOut / args.split - o0;
             const uint32_t base = smem_u32(sm.part);
             for (int o = tid - 256; o < rows * width; o += 32 * kFoldWarps) {
@@ -483,16 +530,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 // gate/up: output e of the tile is lane 32 (e / 16) + e % 16, its up 16 lanes on
                 const uint32_t at = base + static_cast<uint32_t>(r * kPartLd + (GATEUP ? (e >> 4) * 32 + (e & 15) : e)) * 4;
                 float v = 0.0f, u = 0.0f;
-                for (int s = 0; s < args.split; ++s) {
-                    v += ld_cluster_f32(at, s);
-                    if (GATEUP) u += ld_cluster_f32(at + 64, s);
-                }
+                for (int s = 0; s < args.split; ++s)
+                    for (int j = 0; j < teams; ++j) {
+                        const uint32_t of = at + j * (kFoldCols * kPartLd * 4);
+                        v += ld_part(of, s, args.split);
+                        if (GATEUP) u += ld_part(of + 64, s, args.split);
+                    }
                 const int64_t to = static_cast<int64_t>(row0 + r) * p.n + out;
                 if (GATEUP) v = __fmul_rn(tq_silu(v), u);
                 if (GATEUP || p.y_bf16) static_cast<uint16_t *>(p.y)[to] = f32_to_bf16_bits(v);
                 else static_cast<float *>(p.y)[to] = v;
             }
-            cluster_sync();
+            if (args.split > 1) cluster_sync();
         } else {
             const int64_t out = static_cast<int64_t>(ntile) * kOut + (GATEUP ? 16 * quarter + (lane & 15) : local);
 #pragma unroll
@@ -610,7 +659,7 @@ cudaError_t q4_tile_launch(const Q4Product &p, float *sums, cudaStream_t stream)
         if (e != cudaSuccess) return e;
     }
     e = make_tmap_2d(&a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, static_cast<uint64_t>(p.k), static_cast<uint64_t>(p.m),
-                     static_cast<uint64_t>(p.k) * 2, kStageK, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B);
+                     static_cast<uint64_t>(p.k) * 2, 64, static_cast<uint32_t>(a.rows), CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     return p.group == 128 ? pick<128>(a, sms, stream) : p.group == 64 ? pick<64>(a, sms, stream) : pick<32>(a, sms, stream);
 }
