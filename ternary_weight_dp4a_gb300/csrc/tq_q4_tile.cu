@@ -16,7 +16,8 @@
 //
 // Few tiles are split along k over the CTAs of a cluster, which add up their parts through shared memory.
 //
-// Warps: 0-3 decode, 4 issues MMAs, 5 copies x, 8-19 fold (a quarter of the lanes and a third of the columns each).
+// Warps: 0-7 decode (four for every other chunk of 128 values), 8 issues MMAs, 9 copies x, 10 its sums,
+// 12-23 fold (a quarter of the lanes and a third of the columns each).
 #include <cuda_runtime.h>
 
 #include "tq_device.cuh"
@@ -32,18 +33,19 @@ namespace {
 constexpr int kCols = 192;                      // most rows of x per tile
 constexpr int kABufs = 4;                       // of decoded weights: 64 values of k, 32 columns of tensor memory each
 constexpr int kStages = 2;                      // of x in shared memory: 128 values each, in two halves
-constexpr int kMaxBufs = 8;                     // accumulators
-constexpr int kSums = 8;                        // groups' sums of x in shared memory
+constexpr int kSums = 3;                        // chunks' sums of x in shared memory
 constexpr int kFoldWarps = 12;
 constexpr int kFoldCols = kCols / (kFoldWarps / 4);
-constexpr int kThreads = 256 + 32 * kFoldWarps;
+constexpr int kDecodeWarps = 8;
+constexpr int kFirstFold = kDecodeWarps + 4;
+constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
 constexpr uint32_t kHalfBytes = kCols * 128;     // of a stage: 64 values
 constexpr uint32_t kTmemA = 2 * kCols;
 constexpr int kAhead = 16;                      // chunks of codes in L2 ahead of the decode
 constexpr int kPartLd = 128 + 4;                // floats per row of x of a part
 
-// register shares (launched with 96 per thread): 128 x (96 + 48 + 3 x 112) = 640 x 96; the decode keeps what it has
-constexpr int kRegsIssue = 48, kRegsFold = 112;
+// register shares (launched with 80 per thread): 128 x (2 x 56 + 32 + 3 x 112) = 768 x 80
+constexpr int kRegsDecode = 56, kRegsIssue = 32, kRegsFold = 112;
 
 __device__ unsigned lost_waits;                 // bits of all waits that have run out on this device
 
@@ -52,8 +54,8 @@ struct __align__(1024) TileSmem {
         uint8_t x[kStages][2][kHalfBytes];
         float part[kCols][kPartLd];             // this CTA's sums, when a tile is split along k
     };
-    float sums[kSums][kCols];
-    uint64_t x_full[kStages], a_full[kABufs], empty[kABufs], d_full[kMaxBufs], d_empty[kMaxBufs];
+    float sums[kSums][4][kCols];                // of a chunk's groups
+    uint64_t x_full[kStages], a_full[kABufs], empty[kABufs], d_full[2], d_empty[2];
     uint64_t s_full[kSums], s_empty[kSums], drain;
     uint32_t tmem;
     uint32_t dead;                              // a bounded wait ran out
@@ -245,13 +247,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     const int row0 = tile % args.row_tiles * args.rows, ntile = tile / args.row_tiles;
     const int rows = min(args.rows, p.m - row0), cols = (rows + 15) / 16 * 16;      // (args.rows: a multiple of 16)
     const int chunk0 = rank * chunks / args.split, chunk1 = (rank + 1) * chunks / args.split;
-    const int total = chunk1 - chunk0, groups = total * kPer;       // chunks and groups of this CTA
-    // Accumulators of 32, 96 or 192 columns.  Up to 64 rows of x, each third of the fold's warps takes all columns
-    // of every third group: a hand-over costs some 300 cycles, and short groups follow each other faster.
-    const int dshift = cols <= 32 ? 3 : cols <= 96 ? 2 : 1, dcols = cols <= 32 ? 32 : 2 * kCols >> dshift;
+    const int total = chunk1 - chunk0;                              // chunks of this CTA
+    // Accumulators change hands as sets, one set being added to while the fold has the other: all groups
+    // of a chunk where they fit into half of the 384 columns, else half of them, or one.  A hand-over costs some 300
+    // cycles on either side.  Up to 64 rows of x, each third of the fold's warps takes all columns of every third group.
+    const int dcols = (cols + 31) / 32 * 32;
+    const int per_set = kPer * dcols <= kCols ? kPer : kPer == 4 && 2 * dcols <= kCols ? 2 : 1;
     const int teams = cols <= kFoldCols ? 3 : 1;
 
-    if (warp == 4) {
+    if (warp == kDecodeWarps) {
         tmem_alloc(smem_u32(&sm.tmem), 512);
         tmem_relinquish();
     }
@@ -261,13 +265,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             mbar_init(smem_u32(&sm.a_full[i]), 4);
             mbar_init(smem_u32(&sm.empty[i]), 1);
         }
-        for (int i = 0; i < kMaxBufs; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.d_full[i]), 1);
-            mbar_init(smem_u32(&sm.d_empty[i]), teams > 1 ? 4 : kFoldWarps);
+            mbar_init(smem_u32(&sm.d_empty[i]), kFoldWarps);
         }
         for (int i = 0; i < kSums; ++i) {
             mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.s_empty[i]), teams > 1 ? 4 : kFoldWarps);
+            mbar_init(smem_u32(&sm.s_empty[i]), kFoldWarps);
         }
         mbar_init(smem_u32(&sm.drain), 1);
         sm.dead = 0;
@@ -283,80 +287,73 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     const int64_t strips = q4_strips(p.n), first_strip = static_cast<int64_t>(ntile) * (GATEUP ? 4 : 8);
     const int64_t strip = min(first_strip + (GATEUP ? quarter : 2 * quarter + (lane >> 4)), strips - 1);
     const int64_t block0 = strip * chunks + chunk0;
-    // Packed codes come to L2 well ahead of the decode's loads, which have one chunk in flight.
+    // Packed codes come to L2 well ahead of the decode's loads, which have a chunk or two in flight.
     auto ask = [&](int from, int to) {
         to = min(to, total);
-        if (warp < 4 && (lane & 15) == 0 && from < to)
+        if (warp < kDecodeWarps && (lane & 15) == 0 && from < to)
             prefetch_l2(p.codes[mat] + (block0 + from) * kQ4ChunkBytes, (to - from) * kQ4ChunkBytes);
     };
-    ask(0, kAhead);
+    if (warp < 4) ask(0, kAhead);
     pdl_launch_dependents();
     pdl_wait();
 
-    if (warp < 4) {
+    if (warp < kDecodeWarps) {
         // ---- decode: a lane's 128 codes of a chunk are 64 bytes, two halves of them one buffer each ----
+        regs_down<kRegsDecode>();
+        const int odd = warp >> 2;                                  // which chunks
         const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64;
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16) + kTmemA;
-        uint4 code[2][4];
-        auto load = [&](int buf, int c) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint8_t *at = src + static_cast<int64_t>(c) * kQ4ChunkBytes + q * 16;
-                asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(code[buf][q].x), "=r"(code[buf][q].y), "=r"(code[buf][q].z), "=r"(code[buf][q].w)
-                             : "l"(at));
-            }
-        };
+        const uint32_t a_at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemA + odd * 64;
+        const uint32_t empty = smem_u32(sm.empty) + odd * 16, a_full = smem_u32(sm.a_full) + odd * 16;
         uint32_t mask = 0x000f000fu, base = 0x43004300u;
         asm volatile("" : "+r"(mask), "+r"(base));                  // in registers: two constants do not fit one instruction
-        load(0, 0);
+        uint4 code[4];
+        auto load = [&](int c) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(code[q].x), "=r"(code[q].y), "=r"(code[q].z), "=r"(code[q].w)
+                             : "l"(src + static_cast<int64_t>(c) * kQ4ChunkBytes + q * 16));
+        };
+        if (odd < total) load(odd);
         bool ok = true;
         uint32_t turn = 1;
-        const uint32_t empty = smem_u32(sm.empty), a_full = smem_u32(sm.a_full);
-        for (int c0 = 0; c0 < total && ok; c0 += 2, turn ^= 1) {
+        for (int c = odd; c < total && ok; c += 2, turn ^= 1) {
+            if (c % 4 == 0) ask(c + kAhead, c + kAhead + 4);
 #pragma unroll
-            for (int buf = 0; buf < 2; ++buf) {
-                const int c = c0 + buf;
-                if (c >= total || !ok) break;
-                if (c + 1 < total) load(buf ^ 1, c + 1);
-                if (c % 4 == 0) ask(c + kAhead, c + kAhead + 4);
+            for (int half = 0; half < 2; ++half) {
+                ok = warp_wait<32>(sm, empty + 8 * half, turn, 1u << 0);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int abuf = 2 * buf + half;                // (four buffers are two chunks)
-                    ok = warp_wait<32>(sm, empty + 8 * abuf, turn, 1u << 0);
-                    if (!ok) break;
-                    tc_fence_after();
+                for (int g = 0; g < 2; ++g) {
+                    // 32 values: word g of each quarter of them
+                    uint32_t v[16];
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        // 32 values: word g of each quarter of them
-                        uint32_t v[16];
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t w = half ? (g ? code[q].w : code[q].z) : (g ? code[q].y : code[q].x);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint4 w4 = code[buf][q];
-                            const uint32_t w = half ? (g ? w4.w : w4.z) : (g ? w4.y : w4.x);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[4 * q + i] = decode_pair(w, i, mask, base);
-                        }
-                        st_16(lane_base + abuf * 32 + 16 * g, v);
+                        for (int i = 0; i < 4; ++i) v[4 * q + i] = decode_pair(w, i, mask, base);
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(a_full + 8 * abuf);
+                    st_16(a_at + half * 32 + 16 * g, v);
                 }
+                if (half == 1 && c + 2 < total) load(c + 2);        // the other four warps decode meanwhile
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(a_full + 8 * half);
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < kFirstFold) {
         regs_down<kRegsIssue>();
-        if (warp == 4) {
+        if (warp == kDecodeWarps) {
             // ---- issue: one thread issues, the warp stays together ----
             const uint32_t issue = elect_one();
-            const uint32_t idesc = idesc_bf16(128, cols), bufs = 1u << dshift;
+            const uint32_t idesc = idesc_bf16(128, cols);
             const uint32_t x_full = smem_u32(sm.x_full), a_full = smem_u32(sm.a_full), empty = smem_u32(sm.empty);
             const uint32_t d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
             const uint64_t x_desc = desc_sw128(smem_u32(sm.x));
             // (tensor memory is this CTA's as a whole, so its columns count from 0)
-            uint32_t turn = 0, buf = 0, d_turn = 1, d = 0;
+            uint32_t turn = 0, set = 0, d_turn = 1;
             bool ok = true;
             for (int c0 = 0; c0 < total && ok; c0 += 2, turn ^= 1) {
 #pragma unroll
@@ -368,21 +365,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                     ok = ok && wait_alive(sm, a_full + 8 * ring, turn, 1u << 2);
 #pragma unroll
                     for (int sub = 0; sub < kSubs; ++sub) {
-                        if (start) ok = ok && wait_alive(sm, d_empty + 8 * buf, d_turn, 1u << 3);
+                        // group e of the chunk, place `in` of its set
+                        const int e = GROUP == 128 ? 0 : ring % 2 * kSubs + sub, in = e & (per_set - 1);
+                        if (start && in == 0) ok = ok && wait_alive(sm, d_empty + 8 * set, d_turn, 1u << 3);
                         if (!ok) break;
                         tc_fence_after();
+                        const uint32_t d = set * kCols + in * dcols;
 #pragma unroll
                         for (int i = sub * kEach; i < (sub + 1) * kEach; ++i)
                             mma_bf16_ts(issue, d, kTmemA + 32 * ring + 8 * i, x_desc + (ring * (kHalfBytes >> 4) + 2 * i), idesc,
                                         !(start && i == sub * kEach));
-                        if (end) {
-                            commit_if(issue, d_full + 8 * buf);
-                            d += dcols;
-                            if (++buf == bufs) {
-                                buf = 0;
-                                d = 0;
-                                d_turn ^= 1;
-                            }
+                        if (end && in == per_set - 1) {
+                            commit_if(issue, d_full + 8 * set);
+                            d_turn ^= set;
+                            set ^= 1;
                         }
                     }
                     if (ok) commit_if(issue, empty + 8 * ring);
@@ -392,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             commit_if(issue, smem_u32(&sm.drain));
             if (!mbar_wait(smem_u32(&sm.drain), 0) && issue) atomicOr(&lost_waits, 1u << 4);
             __syncwarp();
-        } else if (warp == 5) {
+        } else if (warp == kDecodeWarps + 1) {
             // ---- copies of x: one thread ----
             if (lane == 0) {
                 int c = 0;
@@ -409,28 +405,29 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                     if (!mbar_wait(smem_u32(&sm.x_full[j % kStages]), (j / kStages) & 1)) atomicOr(&lost_waits, 1u << 6);
             }
             __syncwarp();
-        } else if (warp == 6 && MINS) {
+        } else if (warp == kDecodeWarps + 2 && MINS) {
             // ---- copies of the sums ----
-            const float *src = args.sums + static_cast<int64_t>(chunk0) * kPer * args.sums_ld + row0;
-            int g = 0;
-            for (; g < groups; ++g) {
-                const int slot = g % kSums;
-                if (!warp_wait<64>(sm, smem_u32(&sm.s_empty[slot]), ((g / kSums) & 1) ^ 1, 1u << 9)) break;
-                if (lane == 0) {
+            if (lane == 0) {
+                const float *src = args.sums + static_cast<int64_t>(chunk0) * kPer * args.sums_ld + row0;
+                int c = 0;
+                for (; c < total; ++c) {
+                    const int slot = c % kSums;
+                    if (!wait_alive<64>(sm, smem_u32(&sm.s_empty[slot]), ((c / kSums) & 1) ^ 1, 1u << 9)) break;
                     const uint32_t bar = smem_u32(&sm.s_full[slot]);
-                    mbar_arrive_expect_tx(bar, cols * 4);
-                    bulk_copy_g2s(smem_u32(sm.sums[slot]), src + g * args.sums_ld, cols * 4, bar);
+                    mbar_arrive_expect_tx(bar, kPer * cols * 4);
+                    for (int e = 0; e < kPer; ++e)
+                        bulk_copy_g2s(smem_u32(sm.sums[slot][e]), src + (static_cast<int64_t>(c) * kPer + e) * args.sums_ld, cols * 4, bar);
                 }
-                __syncwarp();
+                for (int j = max(c - kSums, 0); j < c; ++j)
+                    if (!mbar_wait(smem_u32(&sm.s_full[j % kSums]), (j / kSums) & 1)) atomicOr(&lost_waits, 1u << 6);
             }
-            for (int j = max(g - kSums, 0); j < g; ++j)
-                if (!mbar_wait(smem_u32(&sm.s_full[j % kSums]), (j / kSums) & 1)) atomicOr(&lost_waits, 1u << 6);
+            __syncwarp();
         }
         __syncwarp();
     } else {
         // ---- fold: a lane is a weight row, a warp has a third of the rows of x ----
         regs_up<kRegsFold>();
-        const int third = (warp - 8) / 4, team = teams > 1 ? third : 0;
+        const int third = (warp - kFirstFold) / 4, team = teams > 1 ? third : 0;
         const int col0 = teams > 1 ? 0 : third * kFoldCols, mine = min(max(cols - col0, 0), kFoldCols);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
         const int64_t sat = (block0 * 8 + (lane & 7)) * (2 * kPer) + ((lane >> 3) & 1) * kPer;
@@ -442,17 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         load_scales<kPer>(next, ssrc);
         if (MINS) load_scales<kPer>(mnext, msrc);
         bool ok = true;
-        int group = 0, turn = 0;
-        uint32_t buf = 0, d_turn = 0, d_at = lane_base;
-        const uint32_t bufs = 1u << dshift, d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
-        auto step = [&] {
-            d_at += dcols;
-            if (++buf == bufs) {
-                buf = 0;
-                d_at = lane_base;
-                d_turn ^= 1;
-            }
-        };
+        int next_team = 0, slot = 0;
+        uint32_t set = 0, d_turn = 0, s_turn = 0;
+        const uint32_t d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
 #pragma unroll 1
         for (int c = 0; c < total && ok; ++c) {
 #pragma unroll
@@ -464,52 +453,56 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 load_scales<kPer>(next, ssrc + static_cast<int64_t>(c + 1) * (16 * kPer));
                 if (MINS) load_scales<kPer>(mnext, msrc + static_cast<int64_t>(c + 1) * (16 * kPer));
             }
+            if (MINS) ok = warp_wait<20>(sm, smem_u32(&sm.s_full[slot]), s_turn, 1u << 7);
 #pragma unroll
-            for (int e = 0; e < kPer; ++e, ++group) {
-                if (teams > 1) {
-                    const bool others = turn != team;
-                    turn = turn == 2 ? 0 : turn + 1;
-                    if (others) {
-                        step();
-                        continue;
-                    }
+            for (int e = 0; e < kPer; ++e) {
+                const int in = e & (per_set - 1);
+                if (in == 0) {
+                    ok = ok && warp_wait<20>(sm, d_full + 8 * set, d_turn, 1u << 8);
+                    if (!ok) break;
+                    tc_fence_after();
                 }
-                const float s = scale_at(sc, e);
-                const uint64_t s2 = pack2(s, s);
-                float m = 0.0f;
-                if (MINS) m = __fmaf_rn(8.0f, s, -scale_at(mn, e));
-                const uint64_t m2 = pack2(m, m);
-                const int slot = group % kSums;
-                ok = warp_wait(sm, d_full + 8 * buf, d_turn, 1u << 8) &&
-                     (!MINS || warp_wait(sm, smem_u32(&sm.s_full[slot]), (group / kSums) & 1, 1u << 7));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t d = d_at;
+                if (teams == 1 || next_team == team) {
+                    const float s = scale_at(sc, e);
+                    const uint64_t s2 = pack2(s, s);
+                    float m = 0.0f;
+                    if (MINS) m = __fmaf_rn(8.0f, s, -scale_at(mn, e));
+                    const uint64_t m2 = pack2(m, m);
+                    const uint32_t d = lane_base + set * kCols + in * dcols;
+                    const uint32_t sums = smem_u32(sm.sums[slot][e]) + col0 * 4;
 #pragma unroll
-                for (int q = 0; q < kFoldCols / 16; ++q) {
-                    if (16 * q >= mine) break;
-                    uint64_t x[8];
-                    ld_16(d + 16 * q, x);
+                    for (int q = 0; q < kFoldCols / 16; ++q) {
+                        if (16 * q >= mine) break;
+                        uint64_t x[8];
+                        ld_16(d + 16 * q, x);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[8 * q + i] = fma2(x[i], s2, acc[8 * q + i]);
-                    if (MINS) {
-                        const uint32_t at = smem_u32(sm.sums[slot]) + (col0 + 16 * q) * 4;
+                        for (int i = 0; i < 8; ++i) acc[8 * q + i] = fma2(x[i], s2, acc[8 * q + i]);
+                        if (MINS) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint64_t x0, x1;
-                            lds128(at + 16 * i, x0, x1);
-                            acc[8 * q + 2 * i] = fma2(x0, m2, acc[8 * q + 2 * i]);
-                            acc[8 * q + 2 * i + 1] = fma2(x1, m2, acc[8 * q + 2 * i + 1]);
+                            for (int i = 0; i < 4; ++i) {
+                                uint64_t x0, x1;
+                                lds128(sums + 64 * q + 16 * i, x0, x1);
+                                acc[8 * q + 2 * i] = fma2(x0, m2, acc[8 * q + 2 * i]);
+                                acc[8 * q + 2 * i + 1] = fma2(x1, m2, acc[8 * q + 2 * i + 1]);
+                            }
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(d_empty + 8 * buf);
-                    if (MINS) mbar_arrive(smem_u32(&sm.s_empty[slot]));
+                next_team = next_team == 2 ? 0 : next_team + 1;
+                if (in == per_set - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(d_empty + 8 * set);
+                    d_turn ^= set;
+                    set ^= 1;
                 }
-                step();
+            }
+            if (MINS) {
+                if (lane == 0 && ok) mbar_arrive(smem_u32(&sm.s_empty[slot]));
+                if (++slot == kSums) {
+                    slot = 0;
+                    s_turn ^= 1;
+                }
             }
         }
         const int local = 32 * quarter + lane;                      // row of the tile
@@ -523,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             else named_barrier(1, 32 * kFoldWarps);
             const int o0 = rank * kOut / args.split, width = (rank + 1) * kOut / args.split - o0;
             const uint32_t base = smem_u32(sm.part);
-            for (int o = tid - 256; o < rows * width; o += 32 * kFoldWarps) {
+            for (int o = tid - 32 * kFirstFold; o < rows * width; o += 32 * kFoldWarps) {
                 const int r = o / width, e = o0 + o - r * width;
                 const int64_t out = static_cast<int64_t>(ntile) * kOut + e;
                 if (out >= p.n) continue;
@@ -569,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             }
         }
     }
-    if (warp < 8 && args.split > 1) {
+    if (warp < kFirstFold && args.split > 1) {
         cluster_sync();
         cluster_sync();
     }
@@ -577,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4) tmem_dealloc(tmem, 512);
+    if (warp == kDecodeWarps) tmem_dealloc(tmem, 512);
 }
 
 // Sums of x over the groups, [k / group][ld], a thread each (rows from m on: zero).
