@@ -3,19 +3,20 @@
 //
 //   y[r][i] = sum over the groups g of  s_ig * sum_{j in g} (c_ij - 8) x_rj  [+ (8 s_ig - b_ig) * sum_{j in g} x_rj]
 //
-// A warp takes chunks of 16 weight rows x 128 values (1 KB of codes, two 16-byte loads per lane).
-// A word's nibbles become bf16 in place: (w >> 4 i) & 0x000f000f | 0x4300'4300 is the pair 128 + c,
-// and minus 136 it is c - 8, exactly.  They are the A operand (16 x 16) of
-// mma.m16n8k16, up to 8 rows of x the B operand; products are exact in fp32, a group's sum is the
+// A warp takes chunks of two strips of 16 weight rows x 128 values (2 KB of codes, four 16-byte loads per lane;
+// gate/up: a strip of each).  A word's nibbles become bf16 in place: (w >> 4 i) & 0x000f000f | 0x43004300 is
+// the pair 128 + c, and minus 136 it is c - 8, exactly.  They are the A operand (16 x 16) of
+// mma.m16n8k16, 8 rows of x the B operand; products are exact in fp32, a group's sum is the
 // accumulator, and the fold by scales is done in fp32 on the accumulators, where the lane has the same
 // two weight rows.  x lies in shared memory in the order of the B operand, one 16-byte load per
-// two instructions.
+// four instructions.
 //
-// The chunks of a CTA's strips form one contiguous run, of which each warp has an even
-// share, whatever strips it begins and ends in; a warp that leaves a strip stores its sums, and
-// the CTA adds the parts of a strip in ascending order of k.  Where x does not fit into one
-// CTA's shared memory, a cluster's CTAs have a range of k each and the parts are read across the
-// cluster.  Neither depends on the number of rows up to 8, so a row's bits do not either.
+// The chunks of a CTA's units (pairs of strips, or single strips where there are few) form one run, of
+// which each warp has an even share, whatever units it begins and ends in.  A unit that one warp has alone it
+// stores by itself; of the others (two per warp at most) it leaves its sums in shared memory, and they are added up
+// in ascending order of k at the end.  Where x does not fit into one CTA's shared memory, a cluster's CTAs have a
+// range of k each, and the parts are read across the cluster, a batch of units at a time.  Neither depends on
+// the number of rows up to 8, so a row's bits do not either.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -28,17 +29,19 @@
 namespace tq {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kBatch = 32;                      // strips between two reductions
-constexpr int kSlots = kBatch + kWarps;         // parts of strips in a batch: strip + warp is unique
-constexpr int kDepth = 4;                       // chunks in flight per warp
-
-// Chunks of k per CTA: what x, its group sums and the parts leave room for in 227 KB.
-template <int NT>
-constexpr int max_chunks() {
-    return (227 * 1024 - kSlots * NT * 512) / (NT * (2048 + 128));
-}
+// NT: groups of 8 rows of x in a pass.  RS: strips of a unit.  SPLIT: k is split over a cluster.
+template <int NT, int RS, bool SPLIT>
+struct Shape {
+    static constexpr int kWarps = NT == 1 ? 16 : 12;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kDepth = (NT == 1 ? 4 : 6) / RS;       // chunks in flight per warp
+    static constexpr int kBatch = NT == 1 ? 32 : 8;             // units between two reductions over a cluster
+    static constexpr int kSlots = SPLIT ? kBatch + kWarps : 2 * kWarps;     // parts of units
+    static constexpr int kSlotBytes = RS * NT * 512;
+    static constexpr int kChunkBytes = NT * 2048;               // of x
+    // Chunks of k per CTA: what x, its group sums and the parts leave room for in 227 KB.
+    static constexpr int kMaxChunks = (227 * 1024 - kSlots * kSlotBytes) / (kChunkBytes + NT * 8 * 4 * 4);
+};
 
 struct StreamArgs {
     Q4Product p;
@@ -84,9 +87,9 @@ __device__ __forceinline__ float scale_at(const Scales<PER> &s, int half, int p)
 }
 
 // Pair i of a word's codes as bf16 c - 8.
-__device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    uint32_t d;
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i, uint32_t mask, uint32_t base) {
+    uint32_t v, d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w >> (4 * i)), "r"(mask), "r"(base));
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x43084308u));
     return d;
 }
@@ -108,152 +111,236 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile("{ .reg .u32 a; mapa.shared::cluster.u32 a, %1, %2; ld.shared::cluster.f32 %0, [a]; }"
-                 : "=f"(v)
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("{ .reg .u32 a; mapa.shared::cluster.u32 a, %4, %5; ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a]; }"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                  : "r"(addr), "r"(rank)
                  : "memory");
     return v;
 }
 
-// The warp that has item i of `total` dealt evenly to kWarps warps.
-__device__ __forceinline__ int share_begin(int w, int total) { return static_cast<int>(static_cast<int64_t>(w) * total / kWarps); }
-__device__ __forceinline__ int share_of(int i, int total) { return (kWarps * (i + 1) - 1) / total; }
+// Items dealt evenly to W warps: where warp w's share begins, and the warp that has item i.
+template <int W>
+__device__ __forceinline__ int share_begin(int w, int total) { return static_cast<int>(static_cast<int64_t>(w) * total / W); }
+template <int W>
+__device__ __forceinline__ int share_of(int i, int total) { return (W * (i + 1) - 1) / total; }
 
-// NT: groups of 8 rows.  PER: scale groups per chunk.  MATS: 1, or gate and up, whose strips alternate.
-template <int NT, int PER, bool MINS, int MATS>
-__global__ void __launch_bounds__(kThreads, 1) q4_stream_kernel(const StreamArgs a) {
+// PER: scale groups per chunk.
+template <int NT, int RS, int PER, bool MINS, bool GATEUP, bool SPLIT>
+__global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_kernel(const StreamArgs a) {
+    using S = Shape<NT, RS, SPLIT>;
+    static_assert(RS == 2 || !GATEUP);
     extern __shared__ __align__(16) uint8_t smem[];
     const Q4Product &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunks = p.k >> 7;
-    const int rank = a.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int first = rank * chunks / a.cluster, mine = (rank + 1) * chunks / a.cluster - first;
-    float4 *slots = reinterpret_cast<float4 *>(smem);                       // [kSlots][NT][32]
-    uint4 *xs = reinterpret_cast<uint4 *>(slots + kSlots * NT * 32);        // [chunk][4][rows][4]
-    float *sums = reinterpret_cast<float *>(xs + mine * 16 * a.rows);       // [chunk][PER][rows]
+    const int cluster = SPLIT ? a.cluster : 1, rank = SPLIT ? static_cast<int>(cluster_rank()) : 0;
+    const int first = rank * chunks / cluster, mine = (rank + 1) * chunks / cluster - first;
+    float4 *slots = reinterpret_cast<float4 *>(smem);                       // [kSlots][RS][NT][32]
+    uint4 *xs = reinterpret_cast<uint4 *>(smem + S::kSlots * S::kSlotBytes);        // [chunk][4][8 NT rows][4]
+    float *sums = reinterpret_cast<float *>(smem + S::kSlots * S::kSlotBytes + mine * S::kChunkBytes);  // [chunk][PER][8 NT]
 
-    const int clusters = gridDim.x / a.cluster, me = blockIdx.x / a.cluster;
-    const int64_t strips = q4_strips(p.n);
-    const int64_t from = MATS * (me * strips / clusters), to = MATS * ((me + 1) * strips / clusters);
+    const int clusters = gridDim.x / cluster, me = blockIdx.x / cluster;
+    const int64_t strips = q4_strips(p.n), units = GATEUP ? strips : (strips + RS - 1) / RS;
+    const int64_t from = me * units / clusters, to = (me + 1) * units / clusters;
 
     pdl_launch_dependents();
     pdl_wait();
 
+    uint4 code[S::kDepth][RS][2];                       // [strip][rows r, r + 8]
+    Scales<PER> sc[S::kDepth][RS], mn[MINS ? S::kDepth : 1][RS];
+    const uint8_t *cp[RS];
+    const uint16_t *sp[RS], *mp[RS];
+    int64_t batch = from;
+    int count, begin, end, lunit, lchunk;               // units of the batch, this warp's share; what is loaded next
+    auto point = [&] {
+#pragma unroll
+        for (int h = 0; h < RS; ++h) {
+            // (an odd last strip stands in for its pair, whose results go nowhere)
+            const int64_t strip = GATEUP ? batch + lunit : min(RS * (batch + lunit) + h, strips - 1);
+            const int64_t block = strip * chunks + first + lchunk;
+            const int mat = GATEUP ? h : 0;
+            cp[h] = p.codes[mat] + block * kQ4ChunkBytes + lane * 16;
+            sp[h] = p.scales[mat] + (block * 8 + (lane >> 2)) * (2 * PER);
+            if constexpr (MINS) mp[h] = p.mins[mat] + (block * 8 + (lane >> 2)) * (2 * PER);
+        }
+    };
+    auto load = [&](int j) {
+#pragma unroll
+        for (int h = 0; h < RS; ++h) {
+            code[j][h][0] = load_codes(cp[h]);
+            code[j][h][1] = load_codes(cp[h] + 512);
+            sc[j][h] = load_scales<PER>(sp[h]);
+            if constexpr (MINS) mn[j][h] = load_scales<PER>(mp[h]);
+            cp[h] += kQ4ChunkBytes;
+            sp[h] += 16 * PER;
+            if constexpr (MINS) mp[h] += 16 * PER;
+        }
+        if (++lchunk == mine) {
+            lchunk = 0;
+            ++lunit;
+            point();
+        }
+    };
+    // This warp's share of the batch (without a cluster, of all units), and its first loads: they are on
+    // their way while x is laid out.
+    auto open = [&] {
+        count = static_cast<int>(SPLIT ? min(static_cast<int64_t>(S::kBatch), to - batch) : to - batch);
+        begin = share_begin<S::kWarps>(warp, count * mine);
+        end = share_begin<S::kWarps>(warp + 1, count * mine);
+        lunit = begin / mine;
+        lchunk = begin - lunit * mine;
+        point();
+#pragma unroll
+        for (int j = 0; j < S::kDepth; ++j)
+            if (begin + j < end) load(j);
+    };
+    open();
+
     // x, in the order in which lanes read it: 16 bytes are 8 values, chunk = piece / 16,
     // group of 32 = piece / 4 % 4, lane of the quad = piece % 4
-    for (int i = tid; i < mine * 16 * a.rows; i += kThreads) {
+    for (int i = tid; i < mine * 16 * a.rows; i += S::kThreads) {
         const int row = i / (mine * 16), piece = i - row * (mine * 16);
         const uint4 v = *reinterpret_cast<const uint4 *>(p.x + (static_cast<int64_t>(a.row0 + row) * p.k + (first * 16 + piece) * 8));
-        xs[((piece >> 2) * a.rows + row) * 4 + (piece & 3)] = v;
+        xs[((piece >> 2) * (8 * NT) + row) * 4 + (piece & 3)] = v;
     }
     if constexpr (MINS) {
         __syncthreads();
         constexpr int kPieces = 16 / PER;               // of a group
-        for (int i = tid; i < mine * PER * a.rows; i += kThreads) {
+        for (int i = tid; i < mine * PER * a.rows; i += S::kThreads) {
             const int row = i % a.rows, g = i / a.rows;
             float s = 0.0f;
             for (int j = 0; j < kPieces; ++j) {
                 const int piece = g * kPieces + j;
-                const uint4 v = xs[((piece >> 2) * a.rows + row) * 4 + (piece & 3)];
+                const uint4 v = xs[((piece >> 2) * (8 * NT) + row) * 4 + (piece & 3)];
                 const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s += __uint_as_float(u[e] << 16) + __uint_as_float(u[e] & 0xffff0000u);
             }
-            sums[i] = s;
+            sums[g * (8 * NT) + row] = s;
         }
     }
     __syncthreads();
 
-    int col[NT];                                        // row of x of this lane's B operand; any one behind the last
+    // rows of x of this lane's B operand, and of its accumulators: any one behind the last
+    const uint4 *xl[NT];
+    int r0[NT], r1[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) col[t] = min(8 * t + (lane >> 2), a.rows - 1);
+    for (int t = 0; t < NT; ++t) {
+        xl[t] = xs + min(8 * t + (lane >> 2), a.rows - 1) * 4 + (lane & 3);
+        r0[t] = min(8 * t + 2 * (lane & 3), a.rows - 1);
+        r1[t] = min(8 * t + 2 * (lane & 3) + 1, a.rows - 1);
+    }
+    uint32_t mask = 0x000f000fu, base = 0x43004300u;
+    asm volatile("" : "+r"(mask), "+r"(base));          // in registers: two constants do not fit one instruction
 
-    for (int64_t batch = from; batch < to; batch += kBatch) {
-        const int count = static_cast<int>(min(static_cast<int64_t>(kBatch), to - batch));
-        const int total = count * mine;
-        const int begin = share_begin(warp, total), end = share_begin(warp + 1, total);
-
-        uint4 lo[kDepth], hi[kDepth];
-        Scales<PER> sc[kDepth], mn[MINS ? kDepth : 1];
-        int lunit = begin / mine, lchunk = begin - lunit * mine;            // what is loaded next
-        auto load = [&](int j) {
-            const int64_t unit = batch + lunit;
-            const int mat = MATS == 2 ? static_cast<int>(unit & 1) : 0;
-            const int64_t block = (MATS == 2 ? unit >> 1 : unit) * chunks + first + lchunk;
-            const uint8_t *c = p.codes[mat] + block * kQ4ChunkBytes + lane * 16;
-            lo[j] = load_codes(c);
-            hi[j] = load_codes(c + 512);
-            const int64_t at = (block * 8 + (lane >> 2)) * (2 * PER);
-            sc[j] = load_scales<PER>(p.scales[mat] + at);
-            if constexpr (MINS) mn[j] = load_scales<PER>(p.mins[mat] + at);
-            if (++lchunk == mine) {
-                lchunk = 0;
-                ++lunit;
-            }
-        };
+    // A float4 of a unit (strip h, rows of x 8 t and on, lane) is two weight rows, r and r + 8, by two rows of x.
+    auto store = [&](int64_t u, int f, float4 v, float4 up) {
+        const int t = f / 32 % NT, h = f / 32 / NT, e = f % 32 >> 2, row = 8 * t + 2 * (f & 3);
+        const int64_t out = (u * (GATEUP ? 1 : RS) + h) * kQ4Strip + e;
+        const float g[4] = {v.x, v.y, v.z, v.w}, w[4] = {up.x, up.y, up.z, up.w};
 #pragma unroll
-        for (int j = 0; j < kDepth; ++j)
-            if (begin + j < end) load(j);
+        for (int i = 0; i < 4; ++i) {
+            if (row + (i & 1) >= a.rows || out + 8 * (i >> 1) >= p.n) continue;
+            const int64_t at = static_cast<int64_t>(a.row0 + row + (i & 1)) * p.n + out + 8 * (i >> 1);
+            const float y = GATEUP ? __fmul_rn(tq_silu(g[i]), w[i]) : g[i];
+            if (GATEUP || p.y_bf16) static_cast<uint16_t *>(p.y)[at] = f32_to_bf16_bits(y);
+            else static_cast<float *>(p.y)[at] = y;
+        }
+    };
+    constexpr int kAll = RS * NT * 32, kEach = GATEUP ? NT * 32 : kAll;     // float4 of a unit, and with outputs
+    auto plus = [](float4 v, float4 q) { return make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w); };
 
-        float acc[NT][4] = {};
+    while (batch < to) {
+        float acc[RS][NT][4] = {};
         int unit = begin / mine, chunk = begin - unit * mine;
-        for (int i = begin; i < end; i += kDepth) {
+        for (int i = begin; i < end; i += S::kDepth) {
 #pragma unroll
-            for (int j = 0; j < kDepth; ++j) {
+            for (int j = 0; j < S::kDepth; ++j) {
                 if (i + j >= end) break;
-                const uint32_t wl[4] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w}, wh[4] = {hi[j].x, hi[j].y, hi[j].z, hi[j].w};
-                float c[NT][4];
+                const int xo = chunk * (S::kChunkBytes / 16);
+                float c[RS][NT][4];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    if (g % (4 / PER) == 0)
+                    const bool fresh = g % (4 / PER) == 0;
+                    uint4 b[NT];
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) c[t][0] = c[t][1] = c[t][2] = c[t][3] = 0.0f;
-                    uint32_t al[4], ah[4];
+                    for (int t = 0; t < NT; ++t) b[t] = xl[t][xo + g * (8 * NT * 4)];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        al[e] = decode_pair(wl[g], e);
-                        ah[e] = decode_pair(wh[g], e);
-                    }
+                    for (int h = 0; h < RS; ++h) {
+                        const uint4 lo = code[j][h][0], hi = code[j][h][1];
+                        const uint32_t wl = g == 0 ? lo.x : g == 1 ? lo.y : g == 2 ? lo.z : lo.w;
+                        const uint32_t wh = g == 0 ? hi.x : g == 1 ? hi.y : g == 2 ? hi.z : hi.w;
+                        uint32_t al[4], ah[4];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const uint4 b = xs[((chunk * 4 + g) * a.rows + col[t]) * 4 + (lane & 3)];
-                        mma_bf16(c[t], al[0], ah[0], al[1], ah[1], b.x, b.y);
-                        mma_bf16(c[t], al[2], ah[2], al[3], ah[3], b.z, b.w);
+                        for (int e = 0; e < 4; ++e) {
+                            al[e] = decode_pair(wl, e, mask, base);
+                            ah[e] = decode_pair(wh, e, mask, base);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            if (fresh) c[h][t][0] = c[h][t][1] = c[h][t][2] = c[h][t][3] = 0.0f;
+                            mma_bf16(c[h][t], al[0], ah[0], al[1], ah[1], b[t].x, b[t].y);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma_bf16(c[h][t], al[2], ah[2], al[3], ah[3], b[t].z, b[t].w);
                     }
                     if (g % (4 / PER) == 4 / PER - 1) {
                         const int q = g / (4 / PER);
-                        const float s0 = scale_at<PER>(sc[j], 0, q), s1 = scale_at<PER>(sc[j], 1, q);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            acc[t][0] = __fmaf_rn(s0, c[t][0], acc[t][0]);
-                            acc[t][1] = __fmaf_rn(s0, c[t][1], acc[t][1]);
-                            acc[t][2] = __fmaf_rn(s1, c[t][2], acc[t][2]);
-                            acc[t][3] = __fmaf_rn(s1, c[t][3], acc[t][3]);
-                        }
-                        if constexpr (MINS) {
-                            const float b0 = __fmaf_rn(8.0f, s0, -scale_at<PER>(mn[j], 0, q));
-                            const float b1 = __fmaf_rn(8.0f, s1, -scale_at<PER>(mn[j], 1, q));
-                            const float *row = sums + (chunk * PER + q) * a.rows;
+                        for (int h = 0; h < RS; ++h) {
+                            const float s0 = scale_at<PER>(sc[j][h], 0, q), s1 = scale_at<PER>(sc[j][h], 1, q);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                const int r0 = min(8 * t + 2 * (lane & 3), a.rows - 1), r1 = min(8 * t + 2 * (lane & 3) + 1, a.rows - 1);
-                                const float x0 = row[r0], x1 = row[r1];
-                                acc[t][0] = __fmaf_rn(b0, x0, acc[t][0]);
-                                acc[t][1] = __fmaf_rn(b0, x1, acc[t][1]);
-                                acc[t][2] = __fmaf_rn(b1, x0, acc[t][2]);
-                                acc[t][3] = __fmaf_rn(b1, x1, acc[t][3]);
+                                acc[h][t][0] = __fmaf_rn(s0, c[h][t][0], acc[h][t][0]);
+                                acc[h][t][1] = __fmaf_rn(s0, c[h][t][1], acc[h][t][1]);
+                                acc[h][t][2] = __fmaf_rn(s1, c[h][t][2], acc[h][t][2]);
+                                acc[h][t][3] = __fmaf_rn(s1, c[h][t][3], acc[h][t][3]);
+                            }
+                            if constexpr (MINS) {
+                                const float b0 = __fmaf_rn(8.0f, s0, -scale_at<PER>(mn[j][h], 0, q));
+                                const float b1 = __fmaf_rn(8.0f, s1, -scale_at<PER>(mn[j][h], 1, q));
+                                const float *row = sums + (chunk * PER + q) * (8 * NT);
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) {
+                                    const float x0 = row[r0[t]], x1 = row[r1[t]];
+                                    acc[h][t][0] = __fmaf_rn(b0, x0, acc[h][t][0]);
+                                    acc[h][t][1] = __fmaf_rn(b0, x1, acc[h][t][1]);
+                                    acc[h][t][2] = __fmaf_rn(b1, x0, acc[h][t][2]);
+                                    acc[h][t][3] = __fmaf_rn(b1, x1, acc[h][t][3]);
+                                }
                             }
                         }
                     }
                 }
-                if (i + j + kDepth < end) load(j);
+                if (i + j + S::kDepth < end) load(j);
                 if (++chunk == mine || i + j + 1 == end) {
+                    const float4 v0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float4 part[RS][NT];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        slots[((unit + warp) * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-                        acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+                    for (int h = 0; h < RS; ++h)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            part[h][t] = make_float4(acc[h][t][0], acc[h][t][1], acc[h][t][2], acc[h][t][3]);
+                            acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.0f;
+                        }
+                    if (!SPLIT && chunk == mine && unit * mine >= begin) {          // all of the unit is this warp's
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            if constexpr (GATEUP) {
+                                store(batch + unit, t * 32 + lane, part[0][t], part[1][t]);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < RS; ++h) store(batch + unit, (h * NT + t) * 32 + lane, part[h][t], v0);
+                            }
+                        }
+                    } else {
+                        const int slot = SPLIT ? unit + warp : 2 * warp + (unit * mine >= begin);
+#pragma unroll
+                        for (int h = 0; h < RS; ++h)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) slots[slot * kAll + (h * NT + t) * 32 + lane] = part[h][t];
                     }
                     if (chunk == mine) {
                         chunk = 0;
@@ -262,56 +349,84 @@ __global__ void __launch_bounds__(kThreads, 1) q4_stream_kernel(const StreamArgs
                 }
             }
         }
-        if (a.cluster > 1) cluster_sync();
-        else __syncthreads();
-
-        // add up the parts, k ascending; a cluster's CTAs deal the strips to one another
-        const uint32_t base = smem_u32(slots);
-        auto value = [&](int u, int e, int row) {       // strip u of the batch, weight row e
-            const uint32_t in = ((row >> 3) * 32 + (e & 7) * 4 + ((row & 7) >> 1)) * 16 + ((e >> 3) * 2 + (row & 1)) * 4;
-            float v = 0.0f;
-            for (int r = 0; r < a.cluster; ++r) {
-                const int its = (r + 1) * chunks / a.cluster - r * chunks / a.cluster, all = count * its;
-                const int w1 = share_of(u * its + its - 1, all);
-                for (int w = share_of(u * its, all); w <= w1; ++w) {
-                    if (share_begin(w, all) == share_begin(w + 1, all)) continue;
-                    const uint32_t at = base + (u + w) * (NT * 512) + in;
-                    v += a.cluster > 1 ? ld_cluster_f32(at, r) : *reinterpret_cast<const float *>(smem + (at - base));
-                }
+        const int total = count * mine;
+        __syncthreads();
+        // a CTA's own parts of a unit, k ascending
+        auto own_sum = [&](int u, int f) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int w1 = share_of<S::kWarps>(u * mine + mine - 1, total);
+            for (int w = share_of<S::kWarps>(u * mine, total); w <= w1; ++w) {
+                const int w_begin = share_begin<S::kWarps>(w, total);
+                if (w_begin == share_begin<S::kWarps>(w + 1, total)) continue;
+                v = plus(v, slots[(SPLIT ? u + w : 2 * w + (u * mine >= w_begin)) * kAll + f]);
             }
             return v;
         };
-        const int groups = count / MATS;                // strips, or pairs of them
-        const int own = (groups - rank + a.cluster - 1) / a.cluster;
-        for (int i = tid; i < own * 16 * a.rows; i += kThreads) {
-            const int e = i & 15, row = (i >> 4) % a.rows, u = ((i >> 4) / a.rows) * a.cluster + rank;
-            const int64_t out = (batch / MATS + u) * kQ4Strip + e;
-            if (out >= p.n) continue;
-            const int64_t at = static_cast<int64_t>(a.row0 + row) * p.n + out;
-            float v = value(u * MATS, e, row);
-            if constexpr (MATS == 2) v = __fmul_rn(tq_silu(v), value(u * 2 + 1, e, row));
-            if (MATS == 2 || p.y_bf16) static_cast<uint16_t *>(p.y)[at] = f32_to_bf16_bits(v);
-            else static_cast<float *>(p.y)[at] = v;
+        if constexpr (!SPLIT) {
+            // the unit that begins before warp w's share and goes on in it, if no warp before has it, too
+            for (int i = tid; i < (S::kWarps - 1) * kEach; i += S::kThreads) {
+                const int w = 1 + i / kEach, f = i % kEach;
+                const int at = share_begin<S::kWarps>(w, total), u = at / mine;
+                if (at == total || at % mine == 0) continue;
+                const int before = share_begin<S::kWarps>(w - 1, total);
+                if (before % mine != 0 && before / mine == u) continue;
+                const float4 v = own_sum(u, f);
+                store(batch + u, f, v, GATEUP ? own_sum(u, NT * 32 + f) : v);
+            }
+            return;
+        } else {
+            // (a unit's sum goes where its first part was: only the thread that adds it up reads that)
+            for (int i = tid; i < count * kAll; i += S::kThreads) {
+                const int u = i / kAll, f = i % kAll;
+                const float4 v = own_sum(u, f);
+                slots[(u + share_of<S::kWarps>(u * mine, total)) * kAll + f] = v;
+            }
+            cluster_sync();
+            // the units dealt to one another
+            auto all_sum = [&](int u, int f) {
+                float4 q[8], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < cluster) {
+                        const int its = (r + 1) * chunks / cluster - r * chunks / cluster;
+                        q[r] = ld_cluster(smem_u32(slots + (u + share_of<S::kWarps>(u * its, count * its)) * kAll + f), r);
+                    }
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < cluster) v = plus(v, q[r]);
+                return v;
+            };
+            const int own = (count - rank + cluster - 1) / cluster;
+            for (int i = tid; i < own * kEach; i += S::kThreads) {
+                const int u = i / kEach * cluster + rank, f = i % kEach;
+                const float4 v = all_sum(u, f);
+                store(batch + u, f, v, GATEUP ? all_sum(u, NT * 32 + f) : v);
+            }
+            cluster_sync();
+            batch += S::kBatch;
+            if (batch < to) open();
         }
-        if (a.cluster > 1) cluster_sync();
-        else __syncthreads();
     }
 }
 
-template <int NT, int PER, bool MINS, int MATS>
-cudaError_t launch(const StreamArgs &a, int sms, cudaStream_t stream) {
+template <int NT, int RS, int PER, bool MINS, bool GATEUP, bool SPLIT>
+cudaError_t launch(StreamArgs &a, int sms, cudaStream_t stream) {
+    using S = Shape<NT, RS, SPLIT>;
+    const int chunks = a.p.k / 128;
+    if constexpr (!SPLIT)
+        if (chunks > S::kMaxChunks) return launch<NT, RS, PER, MINS, GATEUP, true>(a, sms, stream);
     static SmemLimit limit;
-    cudaError_t e = limit.raise(q4_stream_kernel<NT, PER, MINS, MATS>, 227 * 1024);
+    cudaError_t e = limit.raise(q4_stream_kernel<NT, RS, PER, MINS, GATEUP, SPLIT>, 227 * 1024);
     if (e != cudaSuccess) return e;
-    const int chunks = a.p.k / 128, mine = (chunks + a.cluster - 1) / a.cluster;
-    const size_t smem = kSlots * NT * 512 + static_cast<size_t>(mine) * a.rows * (256 + (MINS ? PER * 4 : 0));
-    const int64_t strips = q4_strips(a.p.n);
-    const int most = sms / a.cluster;
-    const int clusters = static_cast<int>(strips < most ? strips : most);
+    const int64_t strips = q4_strips(a.p.n), units = GATEUP ? strips : (strips + RS - 1) / RS;
+    a.cluster = SPLIT ? (chunks + S::kMaxChunks - 1) / S::kMaxChunks : 1;
+    const int64_t most = sms / a.cluster;
+    const int clusters = static_cast<int>(units < most ? units : most);
+    const int mine = (chunks + a.cluster - 1) / a.cluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * a.cluster);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSlots * S::kSlotBytes + static_cast<size_t>(mine) * (S::kChunkBytes + (MINS ? NT * 8 * PER * 4 : 0));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -320,20 +435,23 @@ cudaError_t launch(const StreamArgs &a, int sms, cudaStream_t stream) {
     attr[1].val.clusterDim.x = a.cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, q4_stream_kernel<NT, PER, MINS, MATS>, a);
+    cfg.numAttrs = SPLIT ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, q4_stream_kernel<NT, RS, PER, MINS, GATEUP, SPLIT>, a);
 }
 
 template <int NT, int PER>
-cudaError_t pick(const StreamArgs &a, int sms, cudaStream_t stream) {
+cudaError_t pick(StreamArgs &a, int sms, cudaStream_t stream) {
     const bool mins = a.p.mins[0] != nullptr;
-    if (a.p.mats == 1) return mins ? launch<NT, PER, true, 1>(a, sms, stream) : launch<NT, PER, false, 1>(a, sms, stream);
-    return mins ? launch<NT, PER, true, 2>(a, sms, stream) : launch<NT, PER, false, 2>(a, sms, stream);
+    if (a.p.mats == 2) return mins ? launch<NT, 2, PER, true, true, false>(a, sms, stream) : launch<NT, 2, PER, false, true, false>(a, sms, stream);
+    // a strip per unit where pairs are too few to come out even
+    if constexpr (NT == 1)
+        if (q4_strips(a.p.n) < 8 * sms)
+            return mins ? launch<1, 1, PER, true, false, false>(a, sms, stream) : launch<1, 1, PER, false, false, false>(a, sms, stream);
+    return mins ? launch<NT, 2, PER, true, false, false>(a, sms, stream) : launch<NT, 2, PER, false, false, false>(a, sms, stream);
 }
 
 template <int NT>
 cudaError_t pass(StreamArgs &a, int sms, cudaStream_t stream) {
-    a.cluster = (a.p.k / 128 + max_chunks<NT>() - 1) / max_chunks<NT>();
     return a.p.group == 128 ? pick<NT, 1>(a, sms, stream) : a.p.group == 64 ? pick<NT, 2>(a, sms, stream) : pick<NT, 4>(a, sms, stream);
 }
 
