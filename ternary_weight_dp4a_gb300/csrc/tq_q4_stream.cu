@@ -101,6 +101,30 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The first of a sum: from zero.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -223,15 +247,11 @@ __global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_k
     }
     __syncthreads();
 
-    // rows of x of this lane's B operand, and of its accumulators: any one behind the last
+    // rows of x of this lane's B operand: any one behind the last
     const uint4 *xl[NT];
-    int r0[NT], r1[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        xl[t] = xs + min(8 * t + (lane >> 2), a.rows - 1) * 4 + (lane & 3);
-        r0[t] = min(8 * t + 2 * (lane & 3), a.rows - 1);
-        r1[t] = min(8 * t + 2 * (lane & 3) + 1, a.rows - 1);
-    }
+    for (int t = 0; t < NT; ++t) xl[t] = xs + min(8 * t + (lane >> 2), a.rows - 1) * 4 + (lane & 3);
+    const uint64_t *xsum = reinterpret_cast<const uint64_t *>(sums) + (lane & 3);       // of its accumulators' two
     uint32_t mask = 0x000f000fu, base = 0x43004300u;
     asm volatile("" : "+r"(mask), "+r"(base));          // in registers: two constants do not fit one instruction
 
@@ -253,7 +273,7 @@ __global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_k
     auto plus = [](float4 v, float4 q) { return make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w); };
 
     while (batch < to) {
-        float acc[RS][NT][4] = {};
+        uint64_t acc[RS][NT][2] = {};                   // weight rows r and r + 8, two rows of x each
         int unit = begin / mine, chunk = begin - unit * mine;
         for (int i = begin; i < end; i += S::kDepth) {
 #pragma unroll
@@ -280,35 +300,35 @@ __global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_k
                         }
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            if (fresh) c[h][t][0] = c[h][t][1] = c[h][t][2] = c[h][t][3] = 0.0f;
-                            mma_bf16(c[h][t], al[0], ah[0], al[1], ah[1], b[t].x, b[t].y);
+                            if (fresh) mma_bf16_first(c[h][t], al[0], ah[0], al[1], ah[1], b[t].x, b[t].y);
+                            else mma_bf16(c[h][t], al[0], ah[0], al[1], ah[1], b[t].x, b[t].y);
                         }
 #pragma unroll
                         for (int t = 0; t < NT; ++t) mma_bf16(c[h][t], al[2], ah[2], al[3], ah[3], b[t].z, b[t].w);
                     }
                     if (g % (4 / PER) == 4 / PER - 1) {
                         const int q = g / (4 / PER);
+                        uint64_t x2[NT];
+                        if constexpr (MINS)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) x2[t] = xsum[(chunk * PER + q) * (4 * NT) + 4 * t];
 #pragma unroll
                         for (int h = 0; h < RS; ++h) {
                             const float s0 = scale_at<PER>(sc[j][h], 0, q), s1 = scale_at<PER>(sc[j][h], 1, q);
+                            const uint64_t s00 = pack2(s0, s0), s11 = pack2(s1, s1);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                acc[h][t][0] = __fmaf_rn(s0, c[h][t][0], acc[h][t][0]);
-                                acc[h][t][1] = __fmaf_rn(s0, c[h][t][1], acc[h][t][1]);
-                                acc[h][t][2] = __fmaf_rn(s1, c[h][t][2], acc[h][t][2]);
-                                acc[h][t][3] = __fmaf_rn(s1, c[h][t][3], acc[h][t][3]);
+                                acc[h][t][0] = fma2(s00, pack2(c[h][t][0], c[h][t][1]), acc[h][t][0]);
+                                acc[h][t][1] = fma2(s11, pack2(c[h][t][2], c[h][t][3]), acc[h][t][1]);
                             }
                             if constexpr (MINS) {
                                 const float b0 = __fmaf_rn(8.0f, s0, -scale_at<PER>(mn[j][h], 0, q));
                                 const float b1 = __fmaf_rn(8.0f, s1, -scale_at<PER>(mn[j][h], 1, q));
-                                const float *row = sums + (chunk * PER + q) * (8 * NT);
+                                const uint64_t b00 = pack2(b0, b0), b11 = pack2(b1, b1);
 #pragma unroll
                                 for (int t = 0; t < NT; ++t) {
-                                    const float x0 = row[r0[t]], x1 = row[r1[t]];
-                                    acc[h][t][0] = __fmaf_rn(b0, x0, acc[h][t][0]);
-                                    acc[h][t][1] = __fmaf_rn(b0, x1, acc[h][t][1]);
-                                    acc[h][t][2] = __fmaf_rn(b1, x0, acc[h][t][2]);
-                                    acc[h][t][3] = __fmaf_rn(b1, x1, acc[h][t][3]);
+                                    acc[h][t][0] = fma2(b00, x2[t], acc[h][t][0]);
+                                    acc[h][t][1] = fma2(b11, x2[t], acc[h][t][1]);
                                 }
                             }
                         }
@@ -322,8 +342,9 @@ __global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_k
                     for (int h = 0; h < RS; ++h)
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            part[h][t] = make_float4(acc[h][t][0], acc[h][t][1], acc[h][t][2], acc[h][t][3]);
-                            acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.0f;
+                            const float2 lo = unpack2(acc[h][t][0]), hi = unpack2(acc[h][t][1]);
+                            part[h][t] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                            acc[h][t][0] = acc[h][t][1] = 0;
                         }
                     if (!SPLIT && chunk == mine && unit * mine >= begin) {          // all of the unit is this warp's
 #pragma unroll
