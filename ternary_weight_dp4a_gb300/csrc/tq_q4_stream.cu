@@ -431,17 +431,22 @@ __global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_k
 }
 
 template <int NT, int RS, int PER, bool MINS, bool GATEUP, bool SPLIT>
-cudaError_t launch(StreamArgs &a, int sms, cudaStream_t stream) {
+cudaError_t launch(StreamArgs &a, int dev, int sms, cudaStream_t stream) {
     using S = Shape<NT, RS, SPLIT>;
     const int chunks = a.p.k / 128;
     if constexpr (!SPLIT)
-        if (chunks > S::kMaxChunks) return launch<NT, RS, PER, MINS, GATEUP, true>(a, sms, stream);
+        if (chunks > S::kMaxChunks) return launch<NT, RS, PER, MINS, GATEUP, true>(a, dev, sms, stream);
     static SmemLimit limit;
     cudaError_t e = limit.raise(q4_stream_kernel<NT, RS, PER, MINS, GATEUP, SPLIT>, 227 * 1024);
     if (e != cudaSuccess) return e;
     const int64_t strips = q4_strips(a.p.n), units = GATEUP ? strips : (strips + RS - 1) / RS;
     a.cluster = SPLIT ? (chunks + S::kMaxChunks - 1) / S::kMaxChunks : 1;
-    const int64_t most = sms / a.cluster;
+    int most = sms;
+    if constexpr (SPLIT) {
+        static ClusterLimit cluster_limit;
+        e = cluster_limit.most(q4_stream_kernel<NT, RS, PER, MINS, GATEUP, SPLIT>, dev, a.cluster, S::kThreads, 227 * 1024, sms, &most);
+        if (e != cudaSuccess) return e;
+    }
     const int clusters = static_cast<int>(units < most ? units : most);
     const int mine = (chunks + a.cluster - 1) / a.cluster;
     cudaLaunchConfig_t cfg = {};
@@ -461,19 +466,19 @@ cudaError_t launch(StreamArgs &a, int sms, cudaStream_t stream) {
 }
 
 template <int NT, int PER>
-cudaError_t pick(StreamArgs &a, int sms, cudaStream_t stream) {
+cudaError_t pick(StreamArgs &a, int dev, int sms, cudaStream_t stream) {
     const bool mins = a.p.mins[0] != nullptr;
-    if (a.p.mats == 2) return mins ? launch<NT, 2, PER, true, true, false>(a, sms, stream) : launch<NT, 2, PER, false, true, false>(a, sms, stream);
+    if (a.p.mats == 2) return mins ? launch<NT, 2, PER, true, true, false>(a, dev, sms, stream) : launch<NT, 2, PER, false, true, false>(a, dev, sms, stream);
     // a strip per unit where pairs are too few to come out even
     if constexpr (NT == 1)
         if (q4_strips(a.p.n) < 8 * sms)
-            return mins ? launch<1, 1, PER, true, false, false>(a, sms, stream) : launch<1, 1, PER, false, false, false>(a, sms, stream);
-    return mins ? launch<NT, 2, PER, true, false, false>(a, sms, stream) : launch<NT, 2, PER, false, false, false>(a, sms, stream);
+            return mins ? launch<1, 1, PER, true, false, false>(a, dev, sms, stream) : launch<1, 1, PER, false, false, false>(a, dev, sms, stream);
+    return mins ? launch<NT, 2, PER, true, false, false>(a, dev, sms, stream) : launch<NT, 2, PER, false, false, false>(a, dev, sms, stream);
 }
 
 template <int NT>
-cudaError_t pass(StreamArgs &a, int sms, cudaStream_t stream) {
-    return a.p.group == 128 ? pick<NT, 1>(a, sms, stream) : a.p.group == 64 ? pick<NT, 2>(a, sms, stream) : pick<NT, 4>(a, sms, stream);
+cudaError_t pass(StreamArgs &a, int dev, int sms, cudaStream_t stream) {
+    return a.p.group == 128 ? pick<NT, 1>(a, dev, sms, stream) : a.p.group == 64 ? pick<NT, 2>(a, dev, sms, stream) : pick<NT, 4>(a, dev, sms, stream);
 }
 
 }  // namespace
@@ -487,7 +492,7 @@ cudaError_t q4_stream_launch(const Q4Product &p, cudaStream_t stream) {
     a.p = p;
     for (a.row0 = 0; a.row0 < p.m; a.row0 += 16) {
         a.rows = p.m - a.row0 < 16 ? p.m - a.row0 : 16;
-        e = a.rows > 8 ? pass<2>(a, sms, stream) : pass<1>(a, sms, stream);
+        e = a.rows > 8 ? pass<2>(a, dev, sms, stream) : pass<1>(a, dev, sms, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

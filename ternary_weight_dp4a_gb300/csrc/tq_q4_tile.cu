@@ -512,6 +512,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < kFoldCols; ++i)
                 if (i < mine) sm.part[(teams > 1 ? team * kFoldCols : col0) + i][local] = half2of(acc[i >> 1], i & 1);
+            if (teams > 1) {
+                named_barrier(1, 32 * kFoldWarps);
+                for (int o = tid - 32 * kFirstFold; o < rows * 128; o += 32 * kFoldWarps) {
+                    float *at = &sm.part[o >> 7][o & 127];
+                    *at = *at + at[kFoldCols * kPartLd] + at[2 * kFoldCols * kPartLd];
+                }
+            }
             if (args.split > 1) cluster_sync();
             else named_barrier(1, 32 * kFoldWarps);
             const int o0 = rank * kOut / args.split, width = (rank + 1) * kOut / args.split - o0;
@@ -522,12 +529,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 if (out >= p.n) continue;
                 // gate/up: output e of the tile is lane 32 (e / 16) + e % 16, its up 16 lanes on
                 const uint32_t at = base + static_cast<uint32_t>(r * kPartLd + (GATEUP ? (e >> 4) * 32 + (e & 15) : e)) * 4;
-                float v = 0.0f, u = 0.0f;
-                for (int s = 0; s < args.split; ++s)
-                    for (int j = 0; j < teams; ++j) {
-                        const uint32_t of = at + j * (kFoldCols * kPartLd * 4);
-                        v += ld_part(of, s, args.split);
-                        if (GATEUP) u += ld_part(of + 64, s, args.split);
+                float vs[8], us[8], v = 0.0f, u = 0.0f;
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < args.split) {
+                        vs[s] = ld_part(at, s, args.split);
+                        if (GATEUP) us[s] = ld_part(at + 64, s, args.split);
+                    }
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < args.split) {
+                        v += vs[s];
+                        if (GATEUP) u += us[s];
                     }
                 const int64_t to = static_cast<int64_t>(row0 + r) * p.n + out;
                 if (GATEUP) v = __fmul_rn(tq_silu(v), u);
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(256) q4_sums_kernel(const uint16_t *x, int m, 
 }
 
 template <int GROUP, bool MINS, bool GATEUP>
-cudaError_t launch(TileArgs &a, int sms, cudaStream_t stream) {
+cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     constexpr size_t smem = sizeof(TileSmem) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static SmemLimit limit;
@@ -602,8 +615,15 @@ cudaError_t launch(TileArgs &a, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int64_t tiles = (q4_strips(a.p.n) + (GATEUP ? 3 : 7)) / (GATEUP ? 4 : 8) * a.row_tiles;
     const int chunks = a.p.k / 128;
+    // CTAs along k: as many as run at once with at least two chunks each
+    static ClusterLimit cluster_limit;
     a.split = 1;
-    while (a.split < 8 && tiles * (a.split + 1) <= sms && chunks >= 2 * (a.split + 1)) ++a.split;
+    for (int more = 2; more <= 8 && tiles * more <= sms && chunks >= 2 * more; ++more) {
+        int most = 0;
+        e = cluster_limit.most(q4_tile_kernel<GROUP, MINS, GATEUP>, dev, more, kThreads, smem, sms, &most);
+        if (e != cudaSuccess) return e;
+        if (tiles <= most) a.split = more;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
     cfg.blockDim = dim3(kThreads);
@@ -621,10 +641,10 @@ cudaError_t launch(TileArgs &a, int sms, cudaStream_t stream) {
 }
 
 template <int GROUP>
-cudaError_t pick(TileArgs &a, int sms, cudaStream_t stream) {
+cudaError_t pick(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     const bool mins = a.p.mins[0] != nullptr;
-    if (a.p.mats == 1) return mins ? launch<GROUP, true, false>(a, sms, stream) : launch<GROUP, false, false>(a, sms, stream);
-    return mins ? launch<GROUP, true, true>(a, sms, stream) : launch<GROUP, false, true>(a, sms, stream);
+    if (a.p.mats == 1) return mins ? launch<GROUP, true, false>(a, dev, sms, stream) : launch<GROUP, false, false>(a, dev, sms, stream);
+    return mins ? launch<GROUP, true, true>(a, dev, sms, stream) : launch<GROUP, false, true>(a, dev, sms, stream);
 }
 
 }  // namespace
@@ -654,7 +674,7 @@ cudaError_t q4_tile_launch(const Q4Product &p, float *sums, cudaStream_t stream)
     e = make_tmap_2d(&a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, static_cast<uint64_t>(p.k), static_cast<uint64_t>(p.m),
                      static_cast<uint64_t>(p.k) * 2, 64, static_cast<uint32_t>(a.rows), CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    return p.group == 128 ? pick<128>(a, sms, stream) : p.group == 64 ? pick<64>(a, sms, stream) : pick<32>(a, sms, stream);
+    return p.group == 128 ? pick<128>(a, dev, sms, stream) : p.group == 64 ? pick<64>(a, dev, sms, stream) : pick<32>(a, dev, sms, stream);
 }
 
 }  // namespace tq
