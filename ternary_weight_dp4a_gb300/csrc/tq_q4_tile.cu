@@ -32,8 +32,8 @@ namespace {
 
 constexpr int kCols = 192;                      // most rows of x per tile
 constexpr int kABufs = 4;                       // of decoded weights: 64 values of k, 32 columns of tensor memory each
-constexpr int kStages = 2;                      // of x in shared memory: 128 values each, in two halves
-constexpr int kSums = 3;                        // chunks' sums of x in shared memory
+constexpr int kStages = 4;                      // of x in shared memory: 128 values each, in two halves
+constexpr int kMaxSets = 3;                     // of accumulators
 constexpr int kFoldWarps = 12;
 constexpr int kFoldCols = kCols / (kFoldWarps / 4);
 constexpr int kDecodeWarps = 8;
@@ -54,9 +54,9 @@ struct __align__(1024) TileSmem {
         uint8_t x[kStages][2][kHalfBytes];
         float part[kCols][kPartLd];             // this CTA's sums, when a tile is split along k
     };
-    float sums[kSums][4][kCols];                // of a chunk's groups
-    uint64_t x_full[kStages], a_full[kABufs], empty[kABufs], d_full[2], d_empty[2];
-    uint64_t s_full[kSums], s_empty[kSums], drain;
+    float sums[kMaxSets][4][kCols];             // of x over a set's groups
+    uint64_t x_full[kStages], x_empty[kStages], a_full[kABufs], a_empty[kABufs], d_full[kMaxSets], d_empty[kMaxSets];
+    uint64_t s_full[kMaxSets], s_empty[kMaxSets], drain;
     uint32_t tmem;
     uint32_t dead;                              // a bounded wait ran out
 };
@@ -230,7 +230,8 @@ __device__ __forceinline__ void load_scales(uint32_t (&v)[(PER + 1) / 2], const 
 }
 template <int N>
 __device__ __forceinline__ float scale_at(const uint32_t (&v)[N], int e) {
-    return f16_bits_to_f32(static_cast<uint16_t>(e & 1 ? v[e >> 1] >> 16 : v[e >> 1] & 0xffffu));
+    const uint32_t w = N == 2 && e >= 2 ? v[N - 1] : v[0];
+    return f16_bits_to_f32(static_cast<uint16_t>(e & 1 ? w >> 16 : w & 0xffffu));
 }
 
 template <int GROUP, bool MINS, bool GATEUP>
@@ -248,30 +249,31 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     const int rows = min(args.rows, p.m - row0), cols = (rows + 15) / 16 * 16;      // (args.rows: a multiple of 16)
     const int chunk0 = rank * chunks / args.split, chunk1 = (rank + 1) * chunks / args.split;
     const int total = chunk1 - chunk0;                              // chunks of this CTA
-    // Accumulators change hands as sets, one set being added to while the fold has the other: all groups
-    // of a chunk where they fit into half of the 384 columns, else half of them, or one.  A hand-over costs some 300
-    // cycles on either side.  Up to 64 rows of x, each third of the fold's warps takes all columns of every third group.
-    const int dcols = (cols + 31) / 32 * 32;
-    const int per_set = kPer * dcols <= kCols ? kPer : kPer == 4 && 2 * dcols <= kCols ? 2 : 1;
-    const int teams = cols <= kFoldCols ? 3 : 1;
+    // Accumulators change hands as sets of some of a chunk's groups, one set being added to while the fold has others; a
+    // hand-over costs some 300 cycles on either side.  Up to 64 rows of x there are three sets of 128
+    // columns, each folded by a third of the warps; else two of 192, all warps having a third of the columns.
+    const int dcols = (cols + 31) / 32 * 32, teams = cols <= kFoldCols ? 3 : 1;
+    const int sets = teams == 3 ? 3 : 2, set_cols = 2 * kCols / sets;
+    const int per_set = kPer * dcols <= set_cols ? kPer : kPer == 4 && 2 * dcols <= set_cols ? 2 : 1;
 
     if (warp == kDecodeWarps) {
         tmem_alloc(smem_u32(&sm.tmem), 512);
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sm.x_full[i]), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm.x_full[i]), 1);
+            mbar_init(smem_u32(&sm.x_empty[i]), 1);
+        }
         for (int i = 0; i < kABufs; ++i) {
             mbar_init(smem_u32(&sm.a_full[i]), 4);
-            mbar_init(smem_u32(&sm.empty[i]), 1);
+            mbar_init(smem_u32(&sm.a_empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kMaxSets; ++i) {
             mbar_init(smem_u32(&sm.d_full[i]), 1);
-            mbar_init(smem_u32(&sm.d_empty[i]), kFoldWarps);
-        }
-        for (int i = 0; i < kSums; ++i) {
+            mbar_init(smem_u32(&sm.d_empty[i]), kFoldWarps / teams);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.s_empty[i]), kFoldWarps);
+            mbar_init(smem_u32(&sm.s_empty[i]), kFoldWarps / teams);
         }
         mbar_init(smem_u32(&sm.drain), 1);
         sm.dead = 0;
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         const int odd = warp >> 2;                                  // which chunks
         const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64;
         const uint32_t a_at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemA + odd * 64;
-        const uint32_t empty = smem_u32(sm.empty) + odd * 16, a_full = smem_u32(sm.a_full) + odd * 16;
+        const uint32_t empty = smem_u32(sm.a_empty) + odd * 16, a_full = smem_u32(sm.a_full) + odd * 16;
         uint32_t mask = 0x000f000fu, base = 0x43004300u;
         asm volatile("" : "+r"(mask), "+r"(base));                  // in registers: two constants do not fit one instruction
         uint4 code[4];
@@ -349,11 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             // ---- issue: one thread issues, the warp stays together ----
             const uint32_t issue = elect_one();
             const uint32_t idesc = idesc_bf16(128, cols);
-            const uint32_t x_full = smem_u32(sm.x_full), a_full = smem_u32(sm.a_full), empty = smem_u32(sm.empty);
+            const uint32_t x_full = smem_u32(sm.x_full), x_empty = smem_u32(sm.x_empty);
+            const uint32_t a_full = smem_u32(sm.a_full), a_empty = smem_u32(sm.a_empty);
             const uint32_t d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
             const uint64_t x_desc = desc_sw128(smem_u32(sm.x));
             // (tensor memory is this CTA's as a whole, so its columns count from 0)
-            uint32_t turn = 0, set = 0, d_turn = 1;
+            uint32_t turn = 0, set = 0, d_turn = 1, d_set = 0, x_at = 0, x_turn = 0;
+            uint64_t x_set = x_desc;
             bool ok = true;
             for (int c0 = 0; c0 < total && ok; c0 += 2, turn ^= 1) {
 #pragma unroll
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                     if (c0 + ring / 2 >= total || !ok) break;
                     constexpr int kSubs = GROUP == 32 ? 2 : 1, kEach = 4 / kSubs;
                     const bool start = GROUP < 128 || ring % 2 == 0, end = GROUP < 128 || ring % 2 == 1;
-                    if (ring % 2 == 0) ok = wait_alive(sm, x_full + 4 * ring, turn, 1u << 1);
+                    if (ring % 2 == 0) ok = wait_alive(sm, x_full + 8 * x_at, x_turn, 1u << 1);
                     ok = ok && wait_alive(sm, a_full + 8 * ring, turn, 1u << 2);
 #pragma unroll
                     for (int sub = 0; sub < kSubs; ++sub) {
@@ -370,18 +374,31 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                         if (start && in == 0) ok = ok && wait_alive(sm, d_empty + 8 * set, d_turn, 1u << 3);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t d = set * kCols + in * dcols;
+                        const uint32_t d = d_set + in * dcols;
 #pragma unroll
                         for (int i = sub * kEach; i < (sub + 1) * kEach; ++i)
-                            mma_bf16_ts(issue, d, kTmemA + 32 * ring + 8 * i, x_desc + (ring * (kHalfBytes >> 4) + 2 * i), idesc,
+                            mma_bf16_ts(issue, d, kTmemA + 32 * ring + 8 * i, x_set + (ring % 2 * (kHalfBytes >> 4) + 2 * i), idesc,
                                         !(start && i == sub * kEach));
                         if (end && in == per_set - 1) {
                             commit_if(issue, d_full + 8 * set);
-                            d_turn ^= set;
-                            set ^= 1;
+                            d_set += set_cols;
+                            if (++set == sets) {
+                                set = d_set = 0;
+                                d_turn ^= 1;
+                            }
                         }
                     }
-                    if (ok) commit_if(issue, empty + 8 * ring);
+                    if (!ok) break;
+                    commit_if(issue, a_empty + 8 * ring);
+                    if (ring % 2 == 1) {
+                        commit_if(issue, x_empty + 8 * x_at);
+                        x_set += 2 * kHalfBytes >> 4;
+                        if (++x_at == kStages) {
+                            x_at = 0;
+                            x_set = x_desc;
+                            x_turn ^= 1;
+                        }
+                    }
                 }
             }
             __syncwarp();
@@ -393,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             if (lane == 0) {
                 int c = 0;
                 for (; c < total; ++c) {
-                    const int ring = c % kStages;                   // free with the second of its buffers of weights
-                    if (!wait_alive<32>(sm, smem_u32(&sm.empty[2 * ring + 1]), ((c / kStages) & 1) ^ 1, 1u << 5)) break;
+                    const int ring = c % kStages;
+                    if (!wait_alive<32>(sm, smem_u32(&sm.x_empty[ring]), ((c / kStages) & 1) ^ 1, 1u << 5)) break;
                     const uint32_t bar = smem_u32(&sm.x_full[ring]);
                     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(args.rows) * 256);
                     load_box(smem_u32(sm.x[ring][0]), &args.x, (chunk0 + c) * 128, row0, bar);
@@ -409,17 +426,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             // ---- copies of the sums ----
             if (lane == 0) {
                 const float *src = args.sums + static_cast<int64_t>(chunk0) * kPer * args.sums_ld + row0;
-                int c = 0;
-                for (; c < total; ++c) {
-                    const int slot = c % kSums;
-                    if (!wait_alive<64>(sm, smem_u32(&sm.s_empty[slot]), ((c / kSums) & 1) ^ 1, 1u << 9)) break;
-                    const uint32_t bar = smem_u32(&sm.s_full[slot]);
-                    mbar_arrive_expect_tx(bar, kPer * cols * 4);
-                    for (int e = 0; e < kPer; ++e)
-                        bulk_copy_g2s(smem_u32(sm.sums[slot][e]), src + (static_cast<int64_t>(c) * kPer + e) * args.sums_ld, cols * 4, bar);
+                int set = 0, turn = 1, g = 0;
+                for (; g < total * kPer; g += per_set) {
+                    if (!wait_alive<64>(sm, smem_u32(&sm.s_empty[set]), turn, 1u << 9)) break;
+                    const uint32_t bar = smem_u32(&sm.s_full[set]);
+                    mbar_arrive_expect_tx(bar, per_set * cols * 4);
+                    for (int e = 0; e < per_set; ++e)
+                        bulk_copy_g2s(smem_u32(sm.sums[set][e]), src + static_cast<int64_t>(g + e) * args.sums_ld, cols * 4, bar);
+                    if (++set == sets) {
+                        set = 0;
+                        turn ^= 1;
+                    }
                 }
-                for (int j = max(c - kSums, 0); j < c; ++j)
-                    if (!mbar_wait(smem_u32(&sm.s_full[j % kSums]), (j / kSums) & 1)) atomicOr(&lost_waits, 1u << 6);
+                for (int j = max(g / per_set - sets, 0); j < g / per_set; ++j)
+                    if (!mbar_wait(smem_u32(&sm.s_full[j % sets]), (j / sets) & 1)) atomicOr(&lost_waits, 1u << 6);
             }
             __syncwarp();
         }
@@ -435,74 +455,70 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         uint64_t acc[kFoldCols / 2];
 #pragma unroll
         for (int i = 0; i < kFoldCols / 2; ++i) acc[i] = 0;
-        uint32_t sc[(kPer + 1) / 2], next[(kPer + 1) / 2], mn[(kPer + 1) / 2], mnext[(kPer + 1) / 2];
-        load_scales<kPer>(next, ssrc);
-        if (MINS) load_scales<kPer>(mnext, msrc);
-        bool ok = true;
-        int next_team = 0, slot = 0;
-        uint32_t set = 0, d_turn = 0, s_turn = 0;
+        constexpr int kWords = (kPer + 1) / 2;
+        uint32_t sc[kWords], next[kWords], mn[kWords], mnext[kWords];
+        const int per_chunk = kPer / per_set, all = total * per_chunk;          // sets
         const uint32_t d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
+        const uint32_t s_full = smem_u32(sm.s_full), s_empty = smem_u32(sm.s_empty);
+        auto ahead = [&](int i) {                                   // the scales of set i's chunk
+            if (i >= all) return;
+            const int64_t at = static_cast<int64_t>(i / per_chunk) * (16 * kPer);
+            load_scales<kPer>(next, ssrc + at);
+            if (MINS) load_scales<kPer>(mnext, msrc + at);
+        };
+        ahead(team);
+        uint32_t set = team, turn = 0;
 #pragma unroll 1
-        for (int c = 0; c < total && ok; ++c) {
+        for (int i = team; i < all; i += teams) {
 #pragma unroll
-            for (int i = 0; i < (kPer + 1) / 2; ++i) {
-                sc[i] = next[i];
-                if (MINS) mn[i] = mnext[i];
+            for (int j = 0; j < kWords; ++j) {
+                sc[j] = next[j];
+                if (MINS) mn[j] = mnext[j];
             }
-            if (c + 1 < total) {
-                load_scales<kPer>(next, ssrc + static_cast<int64_t>(c + 1) * (16 * kPer));
-                if (MINS) load_scales<kPer>(mnext, msrc + static_cast<int64_t>(c + 1) * (16 * kPer));
-            }
-            if (MINS) ok = warp_wait<20>(sm, smem_u32(&sm.s_full[slot]), s_turn, 1u << 7);
+            ahead(i + teams);
+            if (!warp_wait<20>(sm, d_full + 8 * set, turn, 1u << 8)) break;
+            if (MINS)
+                if (!warp_wait<20>(sm, s_full + 8 * set, turn, 1u << 7)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int in = 0; in < per_set; ++in) {
+                const int e = i % per_chunk * per_set + in;
+                const float s = scale_at(sc, e);
+                const uint64_t s2 = pack2(s, s);
+                float m = 0.0f;
+                if (MINS) m = __fmaf_rn(8.0f, s, -scale_at(mn, e));
+                const uint64_t m2 = pack2(m, m);
+                const uint32_t d = lane_base + set * set_cols + in * dcols;
+                const uint32_t sums = smem_u32(sm.sums[set][in]) + col0 * 4;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const int in = e & (per_set - 1);
-                if (in == 0) {
-                    ok = ok && warp_wait<20>(sm, d_full + 8 * set, d_turn, 1u << 8);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                if (teams == 1 || next_team == team) {
-                    const float s = scale_at(sc, e);
-                    const uint64_t s2 = pack2(s, s);
-                    float m = 0.0f;
-                    if (MINS) m = __fmaf_rn(8.0f, s, -scale_at(mn, e));
-                    const uint64_t m2 = pack2(m, m);
-                    const uint32_t d = lane_base + set * kCols + in * dcols;
-                    const uint32_t sums = smem_u32(sm.sums[slot][e]) + col0 * 4;
+                for (int q = 0; q < kFoldCols / 16; ++q) {
+                    if (16 * q >= mine) break;
+                    uint64_t x[8];
+                    ld_16(d + 16 * q, x);
 #pragma unroll
-                    for (int q = 0; q < kFoldCols / 16; ++q) {
-                        if (16 * q >= mine) break;
-                        uint64_t x[8];
-                        ld_16(d + 16 * q, x);
+                    for (int j = 0; j < 8; ++j) acc[8 * q + j] = fma2(x[j], s2, acc[8 * q + j]);
+                    if (MINS) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[8 * q + i] = fma2(x[i], s2, acc[8 * q + i]);
-                        if (MINS) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint64_t x0, x1;
-                                lds128(sums + 64 * q + 16 * i, x0, x1);
-                                acc[8 * q + 2 * i] = fma2(x0, m2, acc[8 * q + 2 * i]);
-                                acc[8 * q + 2 * i + 1] = fma2(x1, m2, acc[8 * q + 2 * i + 1]);
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            uint64_t x0, x1;
+                            lds128(sums + 64 * q + 16 * j, x0, x1);
+                            acc[8 * q + 2 * j] = fma2(x0, m2, acc[8 * q + 2 * j]);
+                            acc[8 * q + 2 * j + 1] = fma2(x1, m2, acc[8 * q + 2 * j + 1]);
                         }
                     }
                 }
-                next_team = next_team == 2 ? 0 : next_team + 1;
-                if (in == per_set - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(d_empty + 8 * set);
-                    d_turn ^= set;
-                    set ^= 1;
-                }
             }
-            if (MINS) {
-                if (lane == 0 && ok) mbar_arrive(smem_u32(&sm.s_empty[slot]));
-                if (++slot == kSums) {
-                    slot = 0;
-                    s_turn ^= 1;
-                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(d_empty + 8 * set);
+                if (MINS) mbar_arrive(s_empty + 8 * set);
+            }
+            if (teams == 3) {                                       // (set i % 3 is the team's own)
+                turn ^= 1;
+            } else if (++set == sets) {
+                set = 0;
+                turn ^= 1;
             }
         }
         const int local = 32 * quarter + lane;                      // row of the tile
