@@ -457,12 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         for (int i = 0; i < kFoldCols / 2; ++i) acc[i] = 0;
         constexpr int kWords = (kPer + 1) / 2;
         uint32_t sc[kWords], next[kWords], mn[kWords], mnext[kWords];
-        const int per_chunk = kPer / per_set, all = total * per_chunk;          // sets
+        const int shift = kPer / per_set >> 1, all = total << shift;           // sets (1, 2 or 4 of a chunk)
         const uint32_t d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
         const uint32_t s_full = smem_u32(sm.s_full), s_empty = smem_u32(sm.s_empty);
         auto ahead = [&](int i) {                                   // the scales of set i's chunk
             if (i >= all) return;
-            const int64_t at = static_cast<int64_t>(i / per_chunk) * (16 * kPer);
+            const int64_t at = static_cast<int64_t>(i >> shift) * (16 * kPer);
             load_scales<kPer>(next, ssrc + at);
             if (MINS) load_scales<kPer>(mnext, msrc + at);
         };
@@ -476,13 +476,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 if (MINS) mn[j] = mnext[j];
             }
             ahead(i + teams);
-            if (!warp_wait<20>(sm, d_full + 8 * set, turn, 1u << 8)) break;
-            if (MINS)
-                if (!warp_wait<20>(sm, s_full + 8 * set, turn, 1u << 7)) break;
+            const bool sums_lane = MINS && (lane & 1);              // both waits at once
+            if (!warp_wait<20>(sm, (sums_lane ? s_full : d_full) + 8 * set, turn, sums_lane ? 1u << 7 : 1u << 8)) break;
             tc_fence_after();
 #pragma unroll 1
             for (int in = 0; in < per_set; ++in) {
-                const int e = i % per_chunk * per_set + in;
+                const int e = (i & ((1 << shift) - 1)) * per_set + in;
                 const float s = scale_at(sc, e);
                 const uint64_t s2 = pack2(s, s);
                 float m = 0.0f;
