@@ -25,6 +25,7 @@
 // cut is found by a radix search over the key's bytes, which takes any input.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "tq.h"
@@ -49,7 +50,6 @@ constexpr float kNats = 24.0f;                  // the histogram's range of ln(w
 constexpr float kSlack = 5e-4f;                 // of the estimated sums
 constexpr int kOneBits = 42;                    // the largest weight is 2^42: a sum of 2^20 stays below 2^63
 constexpr int kPart = 16384;                    // entries per CTA from which a cluster grows
-constexpr int kMostPart = 51200;                // entries that fit into shared memory
 constexpr float kColdest = 1.5777218104420236e-30f;     // 2^-99: below, as 0
 
 typedef unsigned long long u64;
@@ -149,26 +149,25 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 __device__ __forceinline__ u64 entry_of(uint32_t key, int i) { return static_cast<u64>(key) << 32 | ~static_cast<uint32_t>(i); }
 __device__ __forceinline__ int index_of(u64 entry) { return static_cast<int>(~static_cast<uint32_t>(entry)); }
 
-// One row's weights.  Logits are halved so that no difference overflows.
+// One row's weights.  Logits are halved so that no difference overflows.  An infinite temperature has factor 0.
 struct Weights {
-    float half_max, ch, cl;
-    bool equal;                                 // infinite temperature
+    float half_max, ch, cl, least;
 
     __device__ __forceinline__ void set(float largest, float t) {
         half_max = 0.5f * largest;
-        equal = t > 3.4028234663852886e38f;
         const double c = 2.0 * 1.4426950408889634074 / static_cast<double>(t);
         ch = static_cast<float>(c);
         cl = static_cast<float>(c - static_cast<double>(ch));
+        least = -64.0f / ch;                    // below, the weight is 0
     }
 
+    // (-infinity: 0; its NaNs end in the conversion to a whole number, which makes them 0.)
     __device__ __forceinline__ u64 of(float logit, const uint32_t *exp2) const {
-        if (equal) return 1ull << kOneBits;
         const float l = 0.5f * logit, b = -half_max;
-        const float d = __fadd_rn(l, b);
-        const float bp = __fsub_rn(d, l);
-        const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(d, bp)), __fsub_rn(b, bp));
-        if (__fmul_rn(d, ch) < -64.0f) return 0;
+        const float e = __fadd_rn(l, b);
+        const float bp = __fsub_rn(e, l);
+        const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(e, bp)), __fsub_rn(b, bp));
+        const float d = fmaxf(e, least);
         const float t = __fmaf_rn(d, ch, 393216.0f);                       // 1.5 * 2^18: a multiple of 1/32
         const float whole = __fsub_rn(t, 393216.0f);
         float r = __fmaf_rn(d, ch, -whole);
@@ -182,8 +181,7 @@ struct Weights {
         const uint32_t m = exp2[at & 31];
         const uint32_t w = m + static_cast<uint32_t>(__mulhi(static_cast<int>(m >> 1), __float2int_rn(q * 137438953472.0f)) >> 4);
         // w * 2^(floor(at / 32) - 31), scaled by 2^42 and rounded
-        const int down = -(at >> 5);
-        return ((static_cast<u64>(w) << (kOneBits - 31 + 1) >> min(down, 63)) + 1) >> 1;
+        return ((static_cast<u64>(w) << (kOneBits - 31 + 1) >> min(-(at >> 5), 63)) + 1) >> 1;
     }
 };
 
@@ -222,25 +220,35 @@ __device__ __forceinline__ u64 block_exclusive(u64 v, u64 *scratch) {
     return before;
 }
 
-// A part of a row that a warp has.
+// A range of a row's indices.
 struct Segment {
     int from, to;
 };
 
-// CTA r's part of a row, and warp w's segment of it.
-__device__ __forceinline__ Segment segment(int vocab, int cluster, int r, int w) {
-    const int part = (vocab + cluster - 1) / cluster;
-    const int from = min(r * part, vocab), to = min(from + part, vocab);
-    const int len = ((to - from + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int at = min(from + w * len, to);
-    return {at, min(at + len, to)};
-}
+// How a row is dealt out.  Four neighbouring entries at an address that is a multiple of their size are a
+// vector; places count entries from the first vector's beginning, so index = place - lead.  A CTA has `part` places,
+// a warp `len` of them, whole rounds of 32 vectors.
+struct Deal {
+    int vocab, lead, part, len;
+
+    __device__ __forceinline__ Deal(const void *row, int size, int vocab_, int cluster) : vocab(vocab_) {
+        lead = static_cast<int>(reinterpret_cast<uintptr_t>(row) / size % 4);
+        part = ((vocab + lead + cluster - 1) / cluster + 3) / 4 * 4;
+        len = ((part + kWarps - 1) / kWarps + 127) / 128 * 128;
+    }
+    // The indices of CTA r's warp w.
+    __device__ __forceinline__ Segment segment(int r, int w) const {
+        const int from = r * part + w * len, to = min(from + len, (r + 1) * part);
+        return {min(max(from - lead, 0), vocab), min(max(to - lead, 0), vocab)};
+    }
+};
+constexpr int kHeldMost = 200 * 1024 / 4;       // entries in shared memory
 
 template <bool BF16>
 struct Row {
     const void *logits;
     const float *held;                          // this CTA's part in shared memory, or nullptr
-    int first;                                  // of this CTA's part
+    Deal deal;
     Segment seg;                                // this warp's
     int rank, cluster;
     Shared &sm;
@@ -249,7 +257,43 @@ struct Row {
         if constexpr (BF16) return clean<true>(bf16_bits_to_f32(static_cast<const uint16_t *>(logits)[i]));
         else return clean<false>(static_cast<const float *>(logits)[i]);
     }
-    __device__ __forceinline__ float at(int i) const { return held != nullptr ? held[i - first] : read(i); }
+    __device__ __forceinline__ int index(int offset) const { return rank * deal.part + offset - deal.lead; }
+    __device__ __forceinline__ float at(int i) const { return held != nullptr ? held[i + deal.lead - rank * deal.part] : read(i); }
+    // The four entries from this CTA's place `offset` on, -infinity outside of the part or the row.
+    __device__ __forceinline__ float4 fetch(int offset) const {
+        const int i = index(offset);
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (offset >= deal.part) return v;
+        if (i >= 0 && i + 4 <= deal.vocab) {
+            if constexpr (BF16) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(logits) + i);
+                v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                                __uint_as_float(u.y & 0xffff0000u));
+            } else {
+                v = *reinterpret_cast<const float4 *>(static_cast<const float *>(logits) + i);
+            }
+            v.x = clean<BF16>(v.x);
+            v.y = clean<BF16>(v.y);
+            v.z = clean<BF16>(v.z);
+            v.w = clean<BF16>(v.w);
+        } else {
+            if (i >= 0 && i < deal.vocab) v.x = read(i);
+            if (i + 1 >= 0 && i + 1 < deal.vocab) v.y = read(i + 1);
+            if (i + 2 >= 0 && i + 2 < deal.vocab) v.z = read(i + 2);
+            if (i + 3 >= 0 && i + 3 < deal.vocab) v.w = read(i + 3);
+        }
+        return v;
+    }
+    // visit(the four entries, index of the first) for all of this warp's.
+    template <typename Visit>
+    __device__ __forceinline__ void all(Visit visit) const {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        for (int o = warp * deal.len + 4 * lane; o < (warp + 1) * deal.len; o += 128) {
+            const float4 v = held != nullptr ? *reinterpret_cast<const float4 *>(held + o) : fetch(o);
+            const float l[4] = {v.x, v.y, v.z, v.w};
+            visit(l, index(o));
+        }
+    }
 
     // Sum over the cluster of each thread's v.  base: the sum of the CTAs before; warp sums stay in sm.warp_sum.
     __device__ u64 total(u64 v, u64 *base) const {
@@ -336,15 +380,25 @@ struct Row {
         sync_all(cluster);
     }
 
-    // List this warp's entry if `take` (all lanes call).  The count goes on past the list's end.
-    __device__ __forceinline__ void list(bool take, float l, int i) const {
-        const unsigned who = __ballot_sync(0xffffffffu, take);
-        if (who == 0) return;
-        const int lane = threadIdx.x & 31;
+    // List those of a lane's four entries whose bit is set (all lanes call).  The count goes on past the list's end.
+    __device__ __forceinline__ void list(unsigned take, const float (&l)[4], int i) const {
+        if (!__any_sync(0xffffffffu, take != 0)) return;
+        const int lane = threadIdx.x & 31, mine = __popc(take);
+        int before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += u;
+        }
         uint32_t n = 0;
-        if (lane == 0) n = atomicAdd(&sm.listed, __popc(who));
-        n = __shfl_sync(0xffffffffu, n, 0) + __popc(who & ((1u << lane) - 1));
-        if (take && n < kLocal) sm.local[n] = entry_of(key_of(l), i);
+        if (lane == 31) n = atomicAdd(&sm.listed, before);
+        n = __shfl_sync(0xffffffffu, n, 31) + before - mine;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (take >> j & 1) {
+                if (n < kLocal) sm.local[n] = entry_of(key_of(l[j]), i + j);
+                ++n;
+            }
     }
 
     // Entries listed in all CTAs; more than kList if they do not fit (all CTAs agree).
@@ -417,7 +471,7 @@ __device__ __forceinline__ u64 draw_target(float u, u64 sum) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t dynamic[];
     __shared__ Shared sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -436,8 +490,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     pdl_launch_dependents();
     pdl_wait();
 
-    Row<BF16> v{static_cast<const uint8_t *>(a.logits) + static_cast<int64_t>(row) * a.vocab * (BF16 ? 2 : 4), nullptr,
-                segment(a.vocab, a.cluster, rank, 0).from, segment(a.vocab, a.cluster, rank, warp), rank, a.cluster, sm};
+    const void *logits = static_cast<const uint8_t *>(a.logits) + static_cast<int64_t>(row) * a.vocab * (BF16 ? 2 : 4);
+    const Deal deal(logits, BF16 ? 2 : 4, a.vocab, a.cluster);
+    Row<BF16> v{logits, nullptr, deal, deal.segment(rank, warp), rank, a.cluster, sm};
     const float t = a.temperature != nullptr ? a.temperature[row] : 1.0f;
     const int k = a.top_k != nullptr ? a.top_k[row] : 0;
     const float p = a.top_p != nullptr ? a.top_p[row] : 1.0f, floor = a.min_p != nullptr ? a.min_p[row] : 0.0f;
@@ -447,15 +502,19 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     float *held = reinterpret_cast<float *>(dynamic);
     float top = -INFINITY, least = INFINITY;
     int where = 0;
-#pragma unroll 8
-    for (int i = v.seg.from + lane; i < v.seg.to; i += 32) {
-        const float l = v.read(i);
-        if (a.resident) held[i - v.first] = l;
-        if (l > top) {
-            top = l;
-            where = i;
+#pragma unroll 4
+    for (int o = warp * deal.len + 4 * lane; o < (warp + 1) * deal.len; o += 128) {
+        const float4 f = v.fetch(o);
+        if (a.resident) *reinterpret_cast<float4 *>(held + o) = f;
+        const float l[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (l[j] > top) {
+                top = l[j];
+                where = v.index(o) + j;
+            }
+            if (l[j] > -INFINITY) least = fminf(least, l[j]);
         }
-        if (l > -INFINITY) least = fminf(least, l);
     }
     if (a.resident) v.held = held;
     u64 best = top > -INFINITY ? entry_of(key_of(top), where) : 0;
@@ -479,7 +538,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         // a key that at least k of the threads' maxima reach
         uint32_t lo = 0, hi = static_cast<uint32_t>(sm.best >> 32);
         const uint32_t mine = top > -INFINITY ? key_of(top) : 0;
-        for (int i = 0; i < 24 && lo < hi; ++i) {
+        for (int i = 0; i < 18 && lo < hi; ++i) {
             const uint32_t mid = lo + (hi - lo + 1) / 2;
             if (__syncthreads_count(mine >= mid) >= k) lo = mid;
             else hi = mid - 1;
@@ -507,9 +566,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     Weights w;
     w.set(largest, t);
     auto weight = [&](float l) { return w.of(l, sm.exp2); };
-    Cut cut{-INFINITY, -1};
+    Cut cut{-INFINITY, INT_MIN};
     float lowest = -INFINITY;                   // min-p: entries below go
-    if (floor > 0.0f && !w.equal) {
+    if (floor > 0.0f && t <= 3.4028234663852886e38f) {
         // w >= min_p  <=>  l >= l_max + T ln(min_p)
         const double at = static_cast<double>(largest) + static_cast<double>(t) * log(static_cast<double>(fminf(floor, 1.0f)));
         lowest = fminf(__double2float_ru(at), largest);
@@ -518,10 +577,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
 
     if (small_k) {
         const float from = fmaxf(bound > kKeyNone ? logit_of(bound) : -INFINITY, lowest);
-        for (int i = v.seg.from; i < v.seg.to; i += 32) {
-            const float l = i + lane < v.seg.to ? v.at(i + lane) : -INFINITY;
-            v.list(l >= from && l > -INFINITY, l, i + lane);
-        }
+        const float low = fmaxf(from, -3.4028234663852886e38f);
+        v.all([&](const float(&l)[4], int i) {
+            v.list((l[0] >= low) | (l[1] >= low) << 1 | (l[2] >= low) << 2 | (l[3] >= low) << 3, l, i);
+        });
         sync_all(a.cluster);
         const int n = v.listed();
         if (n <= kList) {
@@ -564,7 +623,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
     if (k > 0 && k < a.vocab) {
         u64 n = 0, base;
-        for (int i = v.seg.from + lane; i < v.seg.to; i += 32) n += v.at(i) > -INFINITY;
+        v.all([&](const float(&l)[4], int) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n += l[j] > -INFINITY;
+        });
         n = v.total(n, &base);
         if (static_cast<u64>(k) < n) v.narrow(cut, k, [](float) { return static_cast<u64>(1); });
         for (int b = tid; b < kBins; b += kThreads) sm.hist[b] = 0;
@@ -577,14 +639,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     if (p < 1.0f) {
         const float range = fminf(kNats * t, largest - least), scale = range > 0.0f ? (kBins - 1) / range : 0.0f;
         const float step = range / t / (kBins - 1);         // of ln(weight), per bin
-        for (int i = v.seg.from + lane; i < v.seg.to; i += 32) {
-            const float l = v.at(i);
-            if (!cut.keeps(l, i)) continue;
-            const float x = fminf((largest - l) * scale, kBins - 1.0f);
-            const int b = static_cast<int>(x);
-            // 1 - (x - b) step is the weight as a share of its bin's upper end, to the second order
-            atomicAdd(&sm.hist[b], 16384u - static_cast<uint32_t>((x - b) * step * 16384.0f));
-        }
+        const float fine = scale * 1048576.0f;
+        const uint32_t slope = static_cast<uint32_t>(step * 16384.0f);
+        v.all([&](const float(&l)[4], int i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (cut.keeps(l[j], i + j)) {
+                    const uint32_t x = static_cast<uint32_t>(fminf((largest - l[j]) * fine, (kBins - 1) * 1048576.0f));
+                    // a share of 1 - (x - bin) step of its bin's upper end is the weight, to the second order
+                    atomicAdd(&sm.hist[x >> 20], 16384u - ((x >> 4 & 0xffffu) * slope >> 16));
+                }
+        });
         sync_all(a.cluster);
         float mass[2];
 #pragma unroll
@@ -620,16 +685,23 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         __syncthreads();
         const int lo = sm.lo, hi = sm.hi;
         u64 bracket = 0;
-        for (int i = v.seg.from; i < v.seg.to; i += 32) {
-            const float l = i + lane < v.seg.to ? v.at(i + lane) : -INFINITY;
-            const bool stays = cut.keeps(l, i + lane) && l > -INFINITY;
-            const int b = stays ? static_cast<int>(fminf((largest - l) * scale, kBins - 1.0f)) : kBins;
-            const u64 value = stays ? weight(l) : 0;
-            mine += value;
-            if (b < lo) above += value;
-            else if (b <= hi) bracket += value;
-            v.list(stays && b >= lo && b <= hi, l, i + lane);
-        }
+        const float first_x = static_cast<float>(lo), last_x = static_cast<float>(hi + 1);
+        v.all([&](const float(&l)[4], int i) {
+            unsigned take = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool stays = cut.keeps(l[j], i + j);
+                const float x = fminf((largest - l[j]) * fine, (kBins - 1) * 1048576.0f) * 9.5367431640625e-7f;
+                const u64 value = stays ? weight(l[j]) : 0;
+                mine += value;
+                if (x < first_x) above += value;
+                else if (stays && x < last_x) {
+                    bracket += value;
+                    take |= 1u << j;
+                }
+            }
+            v.list(take, l, i);
+        });
         const u64 sums[3] = {warp_total(mine), warp_total(above), warp_total(bracket)};
         if (tid == 0) sm.sum_all = sm.sum_above = sm.sum_listed = 0;
         __syncthreads();
@@ -668,15 +740,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
                 s += own[e];
             }
             u64 run = sure + block_exclusive(s, sm.scan);
-            const int part = (a.vocab + a.cluster - 1) / a.cluster;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
                 const int i = tid * kEach + e;
                 if (i < n && run < target) {
-                    const int index = index_of(list[i]), r = index / part;
-                    const Segment whole = segment(a.vocab, a.cluster, r, 0);
-                    const int len = max(whole.to - whole.from, 1);      // of every segment but the last ones
-                    atomicAdd(&sm.buckets[r * kWarps + (index - r * part) / len], own[e]);
+                    const int index = index_of(list[i]), place = index + deal.lead, r = place / deal.part;
+                    atomicAdd(&sm.buckets[r * kWarps + (place - r * deal.part) / deal.len], own[e]);
                     if (run + own[e] >= target) {
                         sm.sum_all = run + own[e];
                         sm.found = index;
@@ -693,10 +762,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
     if (!done) {
         mine = 0;
-        for (int i = v.seg.from + lane; i < v.seg.to; i += 32) {
-            const float l = v.at(i);
-            if (cut.keeps(l, i)) mine += weight(l);
-        }
+        v.all([&](const float(&l)[4], int i) {
+            bool keep[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) keep[j] = cut.keeps(l[j], i + j);
+            if (__any_sync(0xffffffffu, keep[0] | keep[1] | keep[2] | keep[3]))
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mine += keep[j] ? weight(l[j]) : 0;
+        });
         mine = warp_total(mine);
         if (lane == 0) sm.warp_sum[warp] = mine;
         sync_all(a.cluster);
@@ -717,7 +790,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         sm.rest = target - before;
     }
     __syncthreads();
-    const Segment s = segment(a.vocab, a.cluster, sm.bin / kWarps, sm.bin % kWarps);
+    const Segment s = deal.segment(sm.bin / kWarps, sm.bin % kWarps);
     const u64 rest = sm.rest;
     auto kept = [&](int i) -> u64 {
         const float l = v.read(i);
@@ -744,16 +817,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
 template <bool BF16>
 cudaError_t sample_launch(SampleArgs a, int sms, cudaStream_t stream) {
     static SmemLimit limit;
-    cudaError_t e = limit.raise(sample_kernel<BF16>, kMostPart * 4);
+    cudaError_t e = limit.raise(sample_kernel<BF16>, kHeldMost * 4);
     if (e != cudaSuccess) return e;
     a.cluster = 1;
     while (a.cluster < kMaxCluster && (a.vocab > a.cluster * kPart || (a.vocab > a.cluster * 1024 && a.m * a.cluster < sms))) a.cluster *= 2;
-    const int part = (a.vocab + a.cluster - 1) / a.cluster;
-    a.resident = part <= kMostPart;
+    const int part = ((a.vocab + 3 + a.cluster - 1) / a.cluster + 3) / 4 * 4;        // (at most: as Deal)
+    const int held = kWarps * (((part + kWarps - 1) / kWarps + 127) / 128 * 128);
+    a.resident = held <= kHeldMost;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.m) * a.cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = max(a.resident ? static_cast<size_t>(part) * 4 : 0, kList * sizeof(u64));
+    cfg.dynamicSmemBytes = max(a.resident ? static_cast<size_t>(held) * 4 : 0, kList * sizeof(u64));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
