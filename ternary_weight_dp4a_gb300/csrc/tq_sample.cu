@@ -129,6 +129,13 @@ __device__ __forceinline__ void put_peer(int *p, int rank, int cluster, int v) {
     else asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer(p, rank)), "r"(v) : "memory");
 }
 
+// *p += v if `on`, without a branch.
+__device__ __forceinline__ void add_if(bool on, uint32_t p, uint32_t v) {
+    asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q red.shared.add.u32 [%0], %1; }" ::"r"(p), "r"(v),
+                 "r"(static_cast<uint32_t>(on))
+                 : "memory");
+}
+
 // A logit as it counts: NaN is -infinity, +infinity the largest finite number of the type, -0 is +0.
 template <bool BF16>
 __device__ __forceinline__ float clean(float l) {
@@ -632,23 +639,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         for (int b = tid; b < kBins; b += kThreads) sm.hist[b] = 0;
         __syncthreads();
     }
-    if (lowest > cut.logit) cut = Cut{lowest, 0x7fffffff};
+    const bool tied = cut.index != INT_MIN;     // some of the entries at the cut go: below, only the cut itself tells
+    if (lowest > cut.logit) cut = Cut{lowest, INT_MAX};
+    // what stays, where `plain`, is what reaches this
+    const bool plain = !tied || cut.index == INT_MAX;
+    const float low = fmaxf(cut.logit, -3.4028234663852886e38f);
 
     u64 mine = 0, above = 0;                    // weights of all that stay, of those that surely do
     bool done = false;
-    if (p < 1.0f) {
+    if (p < 1.0f && plain) {
         const float range = fminf(kNats * t, largest - least), scale = range > 0.0f ? (kBins - 1) / range : 0.0f;
         const float step = range / t / (kBins - 1);         // of ln(weight), per bin
         const float fine = scale * 1048576.0f;
-        const uint32_t slope = static_cast<uint32_t>(step * 16384.0f);
-        v.all([&](const float(&l)[4], int i) {
+        const uint32_t slope = static_cast<uint32_t>(step * 16384.0f), hist = smem_u32(sm.hist);
+        v.all([&](const float(&l)[4], int) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (cut.keeps(l[j], i + j)) {
-                    const uint32_t x = static_cast<uint32_t>(fminf((largest - l[j]) * fine, (kBins - 1) * 1048576.0f));
-                    // a share of 1 - (x - bin) step of its bin's upper end is the weight, to the second order
-                    atomicAdd(&sm.hist[x >> 20], 16384u - ((x >> 4 & 0xffffu) * slope >> 16));
-                }
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = static_cast<uint32_t>(fminf((largest - l[j]) * fine, (kBins - 1) * 1048576.0f));
+                // a share of 1 - (x - bin) step of its bin's upper end is the weight, to the second order
+                add_if(l[j] >= low, hist + (x >> 18 & ~3u), 16384u - ((x >> 4 & 0xffffu) * slope >> 16));
+            }
         });
         sync_all(a.cluster);
         float mass[2];
@@ -674,28 +684,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             all += s;
             if (o < warp) before += s;
         }
-        const float aim = fmaxf(p, 0.0f) * all, low = aim - kSlack * all, high = aim + kSlack * all;
+        const float aim = fmaxf(p, 0.0f) * all, aim_low = aim - kSlack * all, aim_high = aim + kSlack * all;
         float upto[3] = {before, before + mass[0], before + mass[0] + mass[1]};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             // the first bins to reach the one and the other (sums of neighbours may differ by a rounding: the lowest such bin)
-            if (upto[e + 1] >= low) atomicMin(&sm.lo, 2 * tid + e);
-            if (upto[e + 1] >= high) atomicMin(&sm.hi, 2 * tid + e);
+            if (upto[e + 1] >= aim_low) atomicMin(&sm.lo, 2 * tid + e);
+            if (upto[e + 1] >= aim_high) atomicMin(&sm.hi, 2 * tid + e);
         }
         __syncthreads();
-        const int lo = sm.lo, hi = sm.hi;
+        // the bins as logits (whatever the rounding: what they bracket is looked at below)
+        const float above_this = largest - sm.lo / scale, from_this = fmaxf(largest - (sm.hi + 1) / scale, low);
         u64 bracket = 0;
-        const float first_x = static_cast<float>(lo), last_x = static_cast<float>(hi + 1);
         v.all([&](const float(&l)[4], int i) {
             unsigned take = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool stays = cut.keeps(l[j], i + j);
-                const float x = fminf((largest - l[j]) * fine, (kBins - 1) * 1048576.0f) * 9.5367431640625e-7f;
-                const u64 value = stays ? weight(l[j]) : 0;
+                const u64 value = weight(l[j] >= low ? l[j] : -INFINITY);
                 mine += value;
-                if (x < first_x) above += value;
-                else if (stays && x < last_x) {
+                const bool sure = l[j] > above_this;
+                above += sure ? value : 0;
+                if (l[j] >= from_this && !sure) {
                     bracket += value;
                     take |= 1u << j;
                 }
@@ -759,16 +768,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         } else {
             v.narrow(cut, target, weight);
         }
+    } else if (p < 1.0f) {
+        u64 base;
+        v.all([&](const float(&l)[4], int i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mine += cut.keeps(l[j], i + j) ? weight(l[j]) : 0;
+        });
+        const u64 total = v.total(mine, &base), target = p > 0.0f ? max(scaled(p, total, true), static_cast<u64>(1)) : 1;
+        v.narrow(cut, target, weight);
     }
     if (!done) {
         mine = 0;
         v.all([&](const float(&l)[4], int i) {
-            bool keep[4];
+            if (!__any_sync(0xffffffffu, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= cut.logit)) return;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) keep[j] = cut.keeps(l[j], i + j);
-            if (__any_sync(0xffffffffu, keep[0] | keep[1] | keep[2] | keep[3]))
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mine += keep[j] ? weight(l[j]) : 0;
+            for (int j = 0; j < 4; ++j) mine += weight(cut.keeps(l[j], i + j) ? l[j] : -INFINITY);
         });
         mine = warp_total(mine);
         if (lane == 0) sm.warp_sum[warp] = mine;
