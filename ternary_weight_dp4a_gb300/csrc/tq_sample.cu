@@ -82,8 +82,10 @@ struct Shared {
     u64 scan[kWarps];
     u64 buckets[kMaxCluster * kWarps];
     u64 rest;
+    u64 parts[3][kWarps];
     uint32_t bound, listed, bin, lo, hi;
     float least;
+    double drop;                                // T ln(min_p)
     int found;
     uint32_t exp2[32];
 };
@@ -124,6 +126,13 @@ __device__ __forceinline__ float at_peer(const float *p, int rank, int cluster) 
     return __uint_as_float(at_peer(reinterpret_cast<const uint32_t *>(p), rank, cluster));
 }
 
+// f(r) of every CTA r of the cluster, one lane each (a warp's lanes all call); `none` on the others.
+template <typename T, typename F>
+__device__ __forceinline__ T by_lanes(int cluster, T none, F f) {
+    const int lane = threadIdx.x & 31;
+    return lane < cluster ? f(lane) : none;
+}
+
 __device__ __forceinline__ void put_peer(int *p, int rank, int cluster, int v) {
     if (cluster == 1) *p = v;
     else asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer(p, rank)), "r"(v) : "memory");
@@ -162,9 +171,10 @@ struct Weights {
 
     __device__ __forceinline__ void set(float largest, float t) {
         half_max = 0.5f * largest;
-        const double c = 2.0 * 1.4426950408889634074 / static_cast<double>(t);
-        ch = static_cast<float>(c);
-        cl = static_cast<float>(c - static_cast<double>(ch));
+        // 2 log2(e) / t as a pair: the quotient of the constant's upper part, and of what that leaves
+        const float c = 2.8853900432586670f, rest = 3.8519242e-8f;
+        ch = __fdiv_rn(c, t);
+        cl = t <= 3.4028234663852886e38f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-ch, t, c), rest), t) : 0.0f;
         least = -64.0f / ch;                    // below, the weight is 0
     }
 
@@ -410,44 +420,78 @@ struct Row {
 
     // Entries listed in all CTAs; more than kList if they do not fit (all CTAs agree).
     __device__ int listed() const {
-        int n = 0;
-        for (int r = 0; r < cluster; ++r) {
-            const uint32_t c = at_peer(&sm.listed, r, cluster);
-            n += c > kLocal ? kList + 1 : static_cast<int>(c);
-        }
-        return n;
+        const uint32_t c = by_lanes(cluster, 0u, [&](int r) { return at_peer(&sm.listed, r, cluster); });
+        return static_cast<int>(__reduce_add_sync(0xffffffffu, c > kLocal ? kList + 1 : c));
     }
 
-    // First CTA: all lists one behind the other, filled up with zeros to a power of two (returned).
-    __device__ int collect(u64 *list, int n) const {
-        int at = 0, size = 64;
-        for (int r = 0; r < cluster; ++r) {
-            const int c = static_cast<int>(at_peer(&sm.listed, r, cluster));
-            for (int i = threadIdx.x; i < c; i += kThreads) list[at + i] = at_peer(&sm.local[i], r, cluster);
-            at += c;
+    // First CTA: all lists one behind the other.
+    __device__ void collect(u64 *list, int n) const {
+        const uint32_t c = by_lanes(cluster, 0u, [&](int r) { return at_peer(&sm.listed, r, cluster); });
+        for (int i = threadIdx.x; i < (n + kThreads - 1) / kThreads * kThreads; i += kThreads) {
+            int at = i, rank = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster - 1; ++r) {
+                const int here = static_cast<int>(__shfl_sync(0xffffffffu, c, r));
+                if (rank == r && at >= here) {
+                    at -= here;
+                    ++rank;
+                }
+            }
+            if (i < n) list[i] = at_peer(&sm.local[at], rank, cluster);
         }
-        while (size < n) size *= 2;
-        for (int i = n + threadIdx.x; i < size; i += kThreads) list[i] = 0;
-        return size;
     }
 };
 
-// Sort `size` (a power of two) entries descending.
-__device__ void sort(u64 *list, int size) {
-    for (int k = 2; k <= size; k <<= 1) {
+// Sort n entries descending (at most E per thread; a bitonic network, thread t having entries t, t + kThreads, ..):
+// exchanges within a warp by shuffles, within a thread by registers, others through the list.
+template <int E>
+__device__ void sort_network(u64 *list, int n) {
+    const int tid = threadIdx.x;
+    u64 x[E];
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = e * kThreads + tid < n ? list[e * kThreads + tid] : 0;
+    for (int k = 2; k <= E * kThreads; k <<= 1) {
         for (int j = k >> 1; j > 0; j >>= 1) {
-            __syncthreads();
-            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-                const int a = 2 * t - (t & (j - 1)), b = a + j;
-                const u64 x = list[a], y = list[b];
-                if ((x < y) == ((a & k) == 0)) {
-                    list[a] = y;
-                    list[b] = x;
-                }
+            if (j >= kThreads) {
+                const int step = j / kThreads;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int f = e + 1; f < E; ++f)
+                        if ((e ^ f) == step) {
+                            const bool down = ((e * kThreads + tid) & k) == 0;
+                            const u64 hi = max(x[e], x[f]), lo = min(x[e], x[f]);
+                            x[e] = down ? hi : lo;
+                            x[f] = down ? lo : hi;
+                        }
+                continue;
+            }
+            if (j >= 32) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < E; ++e) list[e * kThreads + tid] = x[e];
+                __syncthreads();
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int i = e * kThreads + tid;
+                const u64 y = j >= 32 ? list[i ^ j] : __shfl_xor_sync(0xffffffffu, x[e], j);
+                const bool first = (i & j) == 0, down = (i & k) == 0;
+                x[e] = first == down ? max(x[e], y) : min(x[e], y);
             }
         }
     }
     __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) list[e * kThreads + tid] = x[e];
+    __syncthreads();
+}
+
+__device__ void sort(u64 *list, int n) {
+    if (n <= kThreads) sort_network<1>(list, n);
+    else if (n <= 2 * kThreads) sort_network<2>(list, n);
+    else sort_network<kList / kThreads>(list, n);
 }
 
 // floor(f * s) for a finite f in 0 .. 1.
@@ -497,6 +541,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     pdl_launch_dependents();
     pdl_wait();
 
+    // (binary64 runs at 1/60 of the rate: one thread's, while the row is on its way)
+    if (tid == kThreads - 1 && a.min_p != nullptr) {
+        const float f = a.min_p[row];
+        if (f > 0.0f) sm.drop = static_cast<double>(a.temperature != nullptr ? a.temperature[row] : 1.0f) * log(static_cast<double>(fminf(f, 1.0f)));
+    }
     const void *logits = static_cast<const uint8_t *>(a.logits) + static_cast<int64_t>(row) * a.vocab * (BF16 ? 2 : 4);
     const Deal deal(logits, BF16 ? 2 : 4, a.vocab, a.cluster);
     Row<BF16> v{logits, nullptr, deal, deal.segment(rank, warp), rank, a.cluster, sm};
@@ -553,14 +602,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (tid == 0) sm.bound = lo;
     }
     sync_all(a.cluster);
-    best = 0;
-    uint32_t bound = 0;
-    least = INFINITY;
-    for (int r = 0; r < a.cluster; ++r) {
-        best = max(best, at_peer(&sm.best, r, a.cluster));
-        least = fminf(least, at_peer(&sm.least, r, a.cluster));
-        if (small_k) bound = max(bound, at_peer(&sm.bound, r, a.cluster));
+    best = by_lanes(a.cluster, static_cast<u64>(0), [&](int r) { return at_peer(&sm.best, r, a.cluster); });
+    least = by_lanes(a.cluster, INFINITY, [&](int r) { return at_peer(&sm.least, r, a.cluster); });
+    uint32_t bound = small_k ? by_lanes(a.cluster, 0u, [&](int r) { return at_peer(&sm.bound, r, a.cluster); }) : 0;
+#pragma unroll
+    for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+        best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+        bound = max(bound, __shfl_xor_sync(0xffffffffu, bound, o));
     }
+    best = __shfl_sync(0xffffffffu, best, 0);
+    least = __shfl_sync(0xffffffffu, least, 0);
+    bound = __shfl_sync(0xffffffffu, bound, 0);
     if (best == 0 || !(t >= kColdest)) {        // no candidate, or the first of the order
         if (rank == 0 && tid == 0) {
             a.ids[row] = best == 0 ? -1 : index_of(best);
@@ -577,8 +630,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     float lowest = -INFINITY;                   // min-p: entries below go
     if (floor > 0.0f && t <= 3.4028234663852886e38f) {
         // w >= min_p  <=>  l >= l_max + T ln(min_p)
-        const double at = static_cast<double>(largest) + static_cast<double>(t) * log(static_cast<double>(fminf(floor, 1.0f)));
-        lowest = fminf(__double2float_ru(at), largest);
+        lowest = fminf(__double2float_ru(static_cast<double>(largest) + sm.drop), largest);
     }
     u64 *list = reinterpret_cast<u64 *>(dynamic);           // in the first CTA, when its part is done with
 
@@ -591,11 +643,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         sync_all(a.cluster);
         const int n = v.listed();
         if (n <= kList) {
-            int size = 0;
-            if (rank == 0) size = v.collect(list, n);
+            if (rank == 0) v.collect(list, n);
             sync_all(a.cluster);
             if (rank != 0) return;
-            sort(list, size);
+            sort(list, n);
             const int stay = min(k, n);
             // weights, in place of the candidates behind the first k (at most kSmallK)
             u64 *ws = list + kSmallK;
@@ -665,9 +716,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int b = 2 * tid + e;
-            u64 n = 0;
-            for (int r = 0; r < a.cluster; ++r) n += at_peer(&sm.hist[b], r, a.cluster);
-            mass[e] = static_cast<float>(n) * __expf(-b * step);
+            uint32_t c[kMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) c[r] = r < a.cluster ? at_peer(&sm.hist[b], r, a.cluster) : 0;
+            float n = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) n += static_cast<float>(c[r]);
+            mass[e] = n * __expf(-b * step);
         }
         // sums over the bins from the largest on, in fp32: estimates
         float in = mass[0] + mass[1];
@@ -712,56 +767,48 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             v.list(take, l, i);
         });
         const u64 sums[3] = {warp_total(mine), warp_total(above), warp_total(bracket)};
-        if (tid == 0) sm.sum_all = sm.sum_above = sm.sum_listed = 0;
-        __syncthreads();
         if (lane == 0) {
             sm.warp_sum[warp] = sums[1];
-            atomicAdd(&sm.sum_all, sums[0]);
-            atomicAdd(&sm.sum_above, sums[1]);
-            atomicAdd(&sm.sum_listed, sums[2]);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) sm.parts[i][warp] = sums[i];
+        }
+        __syncthreads();
+        if (warp < 3) {
+            const u64 sum = warp_total(lane < kWarps ? sm.parts[warp][lane] : 0);
+            if (lane == 0) (warp == 0 ? sm.sum_all : warp == 1 ? sm.sum_above : sm.sum_listed) = sum;
         }
         sync_all(a.cluster);
-        u64 total = 0, sure = 0, listed = 0;
-        for (int r = 0; r < a.cluster; ++r) {
-            total += at_peer(&sm.sum_all, r, a.cluster);
-            sure += at_peer(&sm.sum_above, r, a.cluster);
-            listed += at_peer(&sm.sum_listed, r, a.cluster);
-        }
+        const u64 total = warp_total(by_lanes(a.cluster, static_cast<u64>(0), [&](int r) { return at_peer(&sm.sum_all, r, a.cluster); }));
+        const u64 sure = warp_total(by_lanes(a.cluster, static_cast<u64>(0), [&](int r) { return at_peer(&sm.sum_above, r, a.cluster); }));
+        const u64 listed = warp_total(by_lanes(a.cluster, static_cast<u64>(0), [&](int r) { return at_peer(&sm.sum_listed, r, a.cluster); }));
         const u64 target = p > 0.0f ? max(scaled(p, total, true), static_cast<u64>(1)) : 1;
         const int n = v.listed();
         done = n <= kList && sure < target && target <= sure + listed;
         if (done) {
-            int size = 0;
             if (rank == 0) {
-                size = v.collect(list, n);
+                v.collect(list, n);
                 if (tid < a.cluster * kWarps) sm.buckets[tid] = at_peer(&sm.warp_sum[tid % kWarps], tid / kWarps, a.cluster);
             }
             sync_all(a.cluster);
             if (rank != 0) return;
-            sort(list, size);
+            sort(list, n);
             // the cut: the entry at which the sum reaches the target
-            constexpr int kEach = kList / kThreads;
-            u64 own[kEach], s = 0;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int i = tid * kEach + e;
-                own[e] = i < n ? weight(logit_of(static_cast<uint32_t>(list[i] >> 32))) : 0;
-                s += own[e];
-            }
-            u64 run = sure + block_exclusive(s, sm.scan);
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int i = tid * kEach + e;
-                if (i < n && run < target) {
+            u64 run = sure;
+            for (int i0 = 0; run < target && i0 < n; i0 += kThreads) {
+                const int i = i0 + tid;
+                const u64 own = i < n ? weight(logit_of(static_cast<uint32_t>(list[i] >> 32))) : 0;
+                const u64 before = run + block_exclusive(own, sm.scan);
+                if (i < n && before < target) {
                     const int index = index_of(list[i]), place = index + deal.lead, r = place / deal.part;
-                    atomicAdd(&sm.buckets[r * kWarps + (place - r * deal.part) / deal.len], own[e]);
-                    if (run + own[e] >= target) {
-                        sm.sum_all = run + own[e];
+                    atomicAdd(&sm.buckets[r * kWarps + (place - r * deal.part) / deal.len], own);
+                    if (before + own >= target) {
                         sm.found = index;
                         sm.bound = static_cast<uint32_t>(list[i] >> 32);
                     }
                 }
-                run += own[e];
+                if (tid == kThreads - 1) sm.sum_listed = before + own;
+                __syncthreads();
+                run = sm.sum_listed;
             }
             __syncthreads();
             cut = Cut{logit_of(sm.bound), sm.found};
