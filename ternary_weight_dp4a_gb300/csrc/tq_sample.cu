@@ -83,7 +83,7 @@ struct Shared {
     u64 buckets[kMaxCluster * kWarps];
     u64 rest;
     u64 parts[3][kWarps];
-    uint32_t bound, listed, bin, lo, hi;
+    uint32_t bound[2], listed, bin, lo, hi;
     float least;
     double drop;                                // T ln(min_p)
     int found;
@@ -491,6 +491,7 @@ __device__ void sort_network(u64 *list, int n) {
 __device__ void sort(u64 *list, int n) {
     if (n <= kThreads) sort_network<1>(list, n);
     else if (n <= 2 * kThreads) sort_network<2>(list, n);
+    else if (n <= 4 * kThreads) sort_network<4>(list, n);
     else sort_network<kList / kThreads>(list, n);
 }
 
@@ -591,29 +592,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     const bool small_k = k > 0 && k <= kSmallK;
     if (small_k) {
-        // a key that at least k of the threads' maxima reach
-        uint32_t lo = 0, hi = static_cast<uint32_t>(sm.best >> 32);
-        const uint32_t mine = top > -INFINITY ? key_of(top) : 0;
-        for (int i = 0; i < 18 && lo < hi; ++i) {
-            const uint32_t mid = lo + (hi - lo + 1) / 2;
-            if (__syncthreads_count(mine >= mid) >= k) lo = mid;
-            else hi = mid - 1;
+        // Keys that at least k entries of the row reach: of the threads' maxima, k of this CTA's (warp 0), or
+        // its share of k of each CTA's (warp 1).
+        uint32_t *maxima = reinterpret_cast<uint32_t *>(sm.local);
+        maxima[tid] = top > -INFINITY ? key_of(top) : 0;
+        __syncthreads();
+        if (warp < 2) {
+            const int want = warp == 0 ? k : (k + a.cluster - 1) / a.cluster;
+            uint32_t m[kWarps], lo = 0, hi = static_cast<uint32_t>(sm.best >> 32);
+#pragma unroll
+            for (int j = 0; j < kWarps; ++j) m[j] = maxima[32 * j + lane];
+            for (int i = 0; i < 20 && lo < hi; ++i) {
+                const uint32_t mid = lo + (hi - lo + 1) / 2;
+                int n = 0;
+#pragma unroll
+                for (int j = 0; j < kWarps; ++j) n += m[j] >= mid;
+                if (__reduce_add_sync(0xffffffffu, n) >= want) lo = mid;
+                else hi = mid - 1;
+            }
+            if (lane == 0) sm.bound[warp] = lo;
         }
-        if (tid == 0) sm.bound = lo;
     }
     sync_all(a.cluster);
     best = by_lanes(a.cluster, static_cast<u64>(0), [&](int r) { return at_peer(&sm.best, r, a.cluster); });
     least = by_lanes(a.cluster, INFINITY, [&](int r) { return at_peer(&sm.least, r, a.cluster); });
-    uint32_t bound = small_k ? by_lanes(a.cluster, 0u, [&](int r) { return at_peer(&sm.bound, r, a.cluster); }) : 0;
+    uint32_t bound = small_k ? by_lanes(a.cluster, 0u, [&](int r) { return at_peer(&sm.bound[0], r, a.cluster); }) : 0;
+    uint32_t shares = small_k ? by_lanes(a.cluster, 0xffffffffu, [&](int r) { return at_peer(&sm.bound[1], r, a.cluster); }) : 0;
 #pragma unroll
     for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
         best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
         least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
         bound = max(bound, __shfl_xor_sync(0xffffffffu, bound, o));
+        shares = min(shares, __shfl_xor_sync(0xffffffffu, shares, o));
     }
     best = __shfl_sync(0xffffffffu, best, 0);
     least = __shfl_sync(0xffffffffu, least, 0);
-    bound = __shfl_sync(0xffffffffu, bound, 0);
+    bound = __shfl_sync(0xffffffffu, max(bound, shares), 0);
     if (best == 0 || !(t >= kColdest)) {        // no candidate, or the first of the order
         if (rank == 0 && tid == 0) {
             a.ids[row] = best == 0 ? -1 : index_of(best);
@@ -803,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                     atomicAdd(&sm.buckets[r * kWarps + (place - r * deal.part) / deal.len], own);
                     if (before + own >= target) {
                         sm.found = index;
-                        sm.bound = static_cast<uint32_t>(list[i] >> 32);
+                        sm.bound[0] = static_cast<uint32_t>(list[i] >> 32);
                     }
                 }
                 if (tid == kThreads - 1) sm.sum_listed = before + own;
@@ -811,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 run = sm.sum_listed;
             }
             __syncthreads();
-            cut = Cut{logit_of(sm.bound), sm.found};
+            cut = Cut{logit_of(sm.bound[0]), sm.found};
         } else {
             v.narrow(cut, target, weight);
         }
