@@ -86,9 +86,11 @@ def load_peaks():
 
 
 # host-only sources that cannot change what a kernel does on the device
-HOST_ONLY_SOURCES = ("tq_lifecycle.cu",)
+HOST_ONLY_SOURCES = ("tq_lifecycle.cu", "tq_limits.h")
 # the mixture-of-experts layer's own files: the kernels measured here include none of them
 OTHER_KERNELS_PREFIX = "tq_moe_"
+# and those of the 4-bit products and of sampling
+MORE_KERNELS_PREFIXES = ("tq_q4_", "tq_sample")
 
 
 def source_hash() -> str:
@@ -98,7 +100,7 @@ def source_hash() -> str:
     csrc = os.path.join(ROOT, "ternary_weight_dp4a_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
         if f.endswith((".cu", ".cuh", ".h")) and f not in HOST_ONLY_SOURCES and not f.startswith(
-                OTHER_KERNELS_PREFIX):
+                (OTHER_KERNELS_PREFIX, *MORE_KERNELS_PREFIXES)):
             h.update(open(os.path.join(csrc, f), "rb").read())
     return h.hexdigest()[:16]
 

@@ -4,9 +4,8 @@
 
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "tq.h"
+#include "tq_limits.h"
 #include "tq_moe.h"
 #include "tq_workspace.h"
 
@@ -81,27 +80,6 @@ __device__ __forceinline__ bool load_offsets(const MoeProduct &p, int *offsets) 
     }
     return __syncthreads_or(bad) == 0;
 }
-
-// A kernel's limit of dynamic shared memory.  The limit belongs to the function on a device, not
-// to a launch: each kernel's is raised once per device, under a lock, to the most that any
-// call can ask for, so that no thread's call lowers it under another's launch.
-struct SmemLimit {
-    static constexpr int kMaxDev = 64;
-    std::mutex mu;
-    bool raised[kMaxDev] = {};
-
-    template <typename Kernel>
-    cudaError_t raise(Kernel *kernel, size_t most) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        std::lock_guard<std::mutex> lock(mu);
-        if (dev < kMaxDev && raised[dev]) return cudaSuccess;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
-        if (e == cudaSuccess && dev < kMaxDev) raised[dev] = true;
-        return e;
-    }
-};
 
 // A bounded wait ran out: its bit goes into the error word of the call's workspace, and into the
 // library's own, which outlives a workspace that the caller has not kept.

@@ -3,9 +3,8 @@
 
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "tq.h"
+#include "tq_limits.h"
 #include "tq_q4.h"
 
 namespace tq {
@@ -25,39 +24,6 @@ struct Q4Product {
     int m;
     void *y;                // [m][n]: fp32, or bf16 where y_bf16 (h: bf16)
     bool y_bf16;
-};
-
-// How many clusters of a kernel can run at once, asked for once per device and cluster size: a cluster's CTAs
-// are SMs of one GPC, so it is fewer than the SMs divided by the size (2 x 76 SMs: 72 of two, 48 of three).
-struct ClusterLimit {
-    static constexpr int kMaxDev = 64, kMaxSize = 8;
-    std::mutex mu;
-    int known[kMaxDev][kMaxSize + 1] = {};
-
-    template <typename Kernel>
-    cudaError_t most(Kernel *kernel, int dev, int size, int threads, size_t smem, int sms, int *out) {
-        std::lock_guard<std::mutex> lock(mu);
-        if (dev < kMaxDev && known[dev][size] > 0) {
-            *out = known[dev][size];
-            return cudaSuccess;
-        }
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(sms / size * size));
-        cfg.blockDim = dim3(static_cast<unsigned>(threads));
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = static_cast<unsigned>(size);
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-        if (e != cudaSuccess) return e;
-        *out = n > 0 ? n : 1;
-        if (dev < kMaxDev) known[dev][size] = *out;
-        return cudaSuccess;
-    }
 };
 
 cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const uint16_t *mins, int n, int k, int group,

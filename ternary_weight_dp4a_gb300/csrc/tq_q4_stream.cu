@@ -23,7 +23,6 @@
 
 #include "tq_device.cuh"
 #include "tq_launch.h"
-#include "tq_moe_internal.h"
 #include "tq_q4_internal.h"
 
 namespace tq {

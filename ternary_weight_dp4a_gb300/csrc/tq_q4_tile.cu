@@ -22,7 +22,6 @@
 
 #include "tq_device.cuh"
 #include "tq_launch.h"
-#include "tq_moe_internal.h"
 #include "tq_q4_internal.h"
 #include "tq_tcgen05.cuh"
 #include "tq_tmap.h"

@@ -30,7 +30,7 @@
 
 #include "tq.h"
 #include "tq_device.cuh"
-#include "tq_moe_internal.h"
+#include "tq_limits.h"
 #include "tq_sample.h"
 
 namespace tq {
@@ -41,7 +41,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 1024;                     // of the histogram
+constexpr int kBins = 2 * kThreads;             // of the histogram
 constexpr int kRadix = 256;                     // of the radix search
 constexpr int kLocal = 1024;                    // candidates of one CTA
 constexpr int kList = 4096;                     // candidates of a row, sorted by its first CTA
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     __syncthreads();
     if (tid < kWarps) {
         least = __uint_as_float(static_cast<uint32_t>(sm.scan[tid]));
-        for (int o = kWarps / 2; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffu, least, o));
+        for (int o = kWarps / 2; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(kWarps < 32 ? (1u << kWarps % 32) - 1 : 0xffffffffu, least, o));
         if (tid == 0) sm.least = least;
     }
     const bool small_k = k > 0 && k <= kSmallK;

@@ -141,3 +141,102 @@ def test_binding_refuses_shapes(lib):
             tq.PackedQ4(None, None, None, n, k, group)
     with pytest.raises(ValueError, match="codes"):
         tq.pack_q4(torch.zeros(4, 128, dtype=torch.uint8), torch.ones(4, 1).half())
+
+
+def test_source_hash_leaves_out_these_sources(monkeypatch, tmp_path):
+    """The files of the 4-bit products and of sampling are no part of the step kernel, and none of its files includes one."""
+    import os
+
+    import bench
+    real = os.path.join(bench.ROOT, "ternary_weight_dp4a_gb300", "csrc")
+    others = (bench.OTHER_KERNELS_PREFIX, *bench.MORE_KERNELS_PREFIXES)
+    for name in os.listdir(real):
+        if name.endswith((".cu", ".cuh", ".h")) and not name.startswith(others) and name not in bench.HOST_ONLY_SOURCES:
+            text = open(os.path.join(real, name)).read()
+            assert not any(f'#include "{prefix}' in text for prefix in bench.MORE_KERNELS_PREFIXES), name
+    csrc = tmp_path / "ternary_weight_dp4a_gb300" / "csrc"
+    csrc.mkdir(parents=True)
+    (csrc / "k.cu").write_text("kernel")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    h0 = bench.source_hash()
+    (csrc / "tq_q4_other.cu").write_text("a product")
+    (csrc / "tq_sample.cu").write_text("sampling")
+    assert bench.source_hash() == h0
+
+
+@pytest.fixture
+def allocations(monkeypatch):
+    """Calls that launch nothing, on CPU tensors; the list says of each tensor that they allocate whether it
+    was made under the explicit stream."""
+    import contextlib
+    import types
+
+    import torch
+    made, current = [], []
+
+    @contextlib.contextmanager
+    def under(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    class Library(types.SimpleNamespace):
+        def __getattr__(self, name):
+            return lambda *a: 1 << 16 if name.endswith("_bytes") else 0
+
+    monkeypatch.setattr(tq, "load", lambda: Library())
+    monkeypatch.setattr(tq, "_tensor", lambda *a, **k: 0x1000)
+    monkeypatch.setattr(tq, "_device", lambda: -1)                   # where CPU tensors are
+    monkeypatch.setattr(torch.cuda, "stream", under)
+    for name in ("empty", "zeros"):
+        real = getattr(torch, name)
+
+        def make(*a, real=real, **k):
+            made.append(bool(current) and isinstance(current[-1], Stream))
+            return real(*a, **k)
+
+        monkeypatch.setattr(torch, name, make)
+    return made
+
+
+@pytest.mark.parametrize("call,count", [("pack", 3), ("gemv", 2), ("gateup", 2), ("sample", 2)])
+def test_a_call_allocates_on_its_stream(allocations, call, count):
+    import torch
+    u8, half = torch.full((48 * 128,), 1, dtype=torch.uint8), torch.full((48 * 4,), 1.0).half()
+    w = tq.PackedQ4(u8, half, half, 40, 256, 64)
+    x = torch.full((20, 256), 1.0).bfloat16()
+    calls = {
+        "pack": lambda st: tq.pack_q4(torch.full((40, 256), 1, dtype=torch.uint8), torch.full((40, 4), 1.0).half(),
+                                      torch.full((40, 4), 1.0).half(), stream=st),
+        "gemv": lambda st: tq.q4_gemv(w, x, stream=st),
+        "gateup": lambda st: tq.q4_gateup(w, w, x, stream=st),
+        "sample": lambda st: tq.sample(torch.full((3, 50), 1.0), torch.full((3,), 0.5), stream=st),
+    }
+    allocations.clear()
+    calls[call](Stream())
+    assert len(allocations) == count and all(allocations)
+
+
+def test_weights_can_be_copied_and_pickled(launched):  # noqa: F811
+    import copy
+    import pickle
+
+    import torch
+    w = tq.PackedQ4(Tensor(torch.uint8, 48 * 128), Tensor(torch.float16, 48 * 4), None, 40, 256, 64)
+    for other in (copy.deepcopy(w), copy.copy(w), pickle.loads(pickle.dumps(w))):
+        assert (other.n, other.k, other.group, other.mins) == (40, 256, 64, None) and other.nbytes == w.nbytes
+
+
+def test_what_earlier_work_writes_is_not_read_as_read_only():
+    """These kernels start before the work ahead of them in the stream has ended: nothing of theirs is read through
+    const __restrict__, __ldg or the read-only path."""
+    import glob
+    import os
+    import re
+    seen = 0
+    for path in glob.glob(os.path.join(os.path.dirname(tq.__file__), "csrc", "tq_q4_*.cu")) + \
+            glob.glob(os.path.join(os.path.dirname(tq.__file__), "csrc", "tq_sample.cu")):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        seen += 1
+        assert "__restrict__" not in text and "__ldg" not in text and ".nc" not in text, path
+    assert seen == 5
