@@ -765,10 +765,11 @@ class PackedQ4:
 
 def _q4(device, name: str, w: PackedQ4) -> _Q4:
     """The weights of a call, checked to be on the device where it runs."""
-    for part in (w.codes, w.scales, w.mins):
-        if part is not None and part.get_device() != device:
-            raise ValueError(f"{name}: weights on the current device are needed, got {part.device}")
-    return w.c_struct()
+    codes, scales, mins = w.codes, w.scales, w.mins
+    if codes.get_device() != device or scales.get_device() != device or (mins is not None and mins.get_device() != device):
+        raise ValueError(f"{name}: weights on the current device are needed, got codes on {codes.device}, scales on "
+                         f"{scales.device}" + ("" if mins is None else f", mins on {mins.device}"))
+    return _Q4(codes.data_ptr(), scales.data_ptr(), 0 if mins is None else mins.data_ptr(), w.n, w.k, w.group)
 
 
 def pack_q4(codes, scales, mins=None, stream=None) -> PackedQ4:
@@ -800,12 +801,13 @@ def q4_workspace_bytes(m: int, k: int, group: int) -> int:
     return int(load().tq_q4_workspace_bytes(m, k, group))
 
 
+_NO_SCRATCH = (None, 0, 0)
+
+
 def _q4_scratch(w: PackedQ4, m: int, device, workspace, stream):
-    """(address, size) of the workspace that a product takes: the caller's, or one for this call where it needs one."""
+    """A product's workspace, its address and size: the caller's, or one for this call."""
     import torch
     if workspace is None:
-        if w.mins is None or m <= Q4_STREAM_ROWS:
-            return None, 0, 0
         workspace = _new(stream, torch.empty, q4_workspace_bytes(m, w.k, w.group), dtype=torch.uint8, device=device)
         return workspace, workspace.data_ptr(), workspace.numel()
     return workspace, _tensor(_device(), "workspace", workspace, (torch.uint8,)), workspace.numel()
@@ -821,11 +823,19 @@ def q4_gemv(w: PackedQ4, x, y=None, dtype=None, workspace=None, stream=None):
     if k != w.k:
         raise ValueError(f"x: rows of {w.k} values are needed, got {k}")
     if y is None:
-        y = _new(stream, torch.empty, (m, w.n), dtype=dtype or torch.float32, device=x.device)
-    p_y = _tensor(dev, "y", y, (torch.float32, torch.bfloat16), (m, w.n))
-    held, p_ws, size = _q4_scratch(w, m, x.device, workspace, stream)
-    _check("tq_q4_gemv", load().tq_q4_gemv(_q4(dev, "w", w), p_x, m, p_y, int(y.dtype == torch.bfloat16), p_ws, size,
-                                           _stream(stream)))
+        dtype = dtype or torch.float32
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"dtype: float32 or bfloat16 is needed, got {dtype}")
+        y = _new(stream, torch.empty, (m, w.n), dtype=dtype, device=x.device)
+        p_y = y.data_ptr()
+    else:
+        dtype = y.dtype
+        p_y = _tensor(dev, "y", y, (torch.float32, torch.bfloat16), (m, w.n))
+    held, p_ws, size = _NO_SCRATCH if workspace is None and (m <= Q4_STREAM_ROWS or w.mins is None) else \
+        _q4_scratch(w, m, x.device, workspace, stream)
+    status = load().tq_q4_gemv(_q4(dev, "w", w), p_x, m, p_y, dtype is torch.bfloat16, p_ws, size, _stream(stream))
+    if status:
+        _check("tq_q4_gemv", status)
     return y
 
 
@@ -842,9 +852,11 @@ def q4_gateup(gate: PackedQ4, up: PackedQ4, x, h=None, workspace=None, stream=No
         p_h = h.data_ptr()
     else:
         p_h = _tensor(dev, "h", h, (torch.bfloat16,), (m, gate.n))
-    held, p_ws, size = _q4_scratch(gate, m, x.device, workspace, stream)
-    _check("tq_q4_gateup", load().tq_q4_gateup(_q4(dev, "gate", gate), _q4(dev, "up", up), p_x, m, p_h, p_ws, size,
-                                               _stream(stream)))
+    held, p_ws, size = _NO_SCRATCH if workspace is None and (m <= Q4_STREAM_ROWS or gate.mins is None) else \
+        _q4_scratch(gate, m, x.device, workspace, stream)
+    status = load().tq_q4_gateup(_q4(dev, "gate", gate), _q4(dev, "up", up), p_x, m, p_h, p_ws, size, _stream(stream))
+    if status:
+        _check("tq_q4_gateup", status)
     return h
 
 
@@ -885,8 +897,10 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None
         p_probs = probs.data_ptr()
     else:
         p_probs = _tensor(dev, "probs", probs, (f32,), row)
-    _check("tq_sample", load().tq_sample(p_logits, int(logits.dtype == torch.bfloat16), m, vocab, p_t, p_k, p_p, p_min,
-                                         p_uniform, p_ids, p_probs, _stream(stream)))
+    status = load().tq_sample(p_logits, logits.dtype is torch.bfloat16, m, vocab, p_t, p_k, p_p, p_min, p_uniform, p_ids,
+                              p_probs, _stream(stream))
+    if status:
+        _check("tq_sample", status)
     return ids, probs
 
 
