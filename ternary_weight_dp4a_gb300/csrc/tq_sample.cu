@@ -8,7 +8,7 @@
 //
 // Weights are whole numbers: 2^42 exp((l - l_max) / T), rounded.  Sums of them are exact, so
 // no result depends on how a row is split, and a border (a sum that equals a target in real
-// arithmetic, as with equal logits) is met exactly.  exp is 2^(i/32) from a table of 32 (31-bit mantissas) times 2^r,
+// arithmetic, as with equal logits) is met exactly.  exp is 2^(i/32) from a table of 32 (31 bits) times 2^r,
 // |r| <= 1/64, by its Taylor polynomial; the argument is held as the sum of two
 // fp32 numbers (difference by Knuth's TwoSum; product by fused multiply-add), so that the error is
 // 2^-30 of a weight.  fp32 alone would move one border in some thousand draws; binary64 runs at
@@ -54,11 +54,11 @@ constexpr float kColdest = 1.5777218104420236e-30f;     // 2^-99: below, as 0
 
 typedef unsigned long long u64;
 
-__constant__ uint32_t kExp2[32] = {             // 2^(31 + i/32)
-    0x80000000u, 0x82cd8699u, 0x85aac368u, 0x88980e81u, 0x8b95c1e4u, 0x8ea4398bu, 0x91c3d374u, 0x94f4efa9u,
-    0x9837f052u, 0x9b8d39bau, 0x9ef53261u, 0xa2704303u, 0xa5fed6aau, 0xa9a15ab5u, 0xad583eeau, 0xb123f582u,
-    0xb504f334u, 0xb8fbaf47u, 0xbd08a39fu, 0xc12c4ccau, 0xc5672a11u, 0xc9b9bd86u, 0xce248c15u, 0xd2a81d92u,
-    0xd744fccbu, 0xdbfbb798u, 0xe0ccdeecu, 0xe5b906e7u, 0xeac0c6e8u, 0xefe4b99cu, 0xf5257d15u, 0xfa83b2dbu};
+__constant__ uint32_t kExp2[32] = {             // 2^(30 + i/32)
+    0x40000000u, 0x4166c34cu, 0x42d561b4u, 0x444c0740u, 0x45cae0f2u, 0x47521cc6u, 0x48e1e9bau, 0x4a7a77d4u,
+    0x4c1bf829u, 0x4dc69cddu, 0x4f7a9930u, 0x51382182u, 0x52ff6b55u, 0x54d0ad5au, 0x56ac1f75u, 0x5891fac1u,
+    0x5a82799au, 0x5c7dd7a4u, 0x5e8451d0u, 0x60962665u, 0x62b39509u, 0x64dcdec3u, 0x6712460bu, 0x69540ec9u,
+    0x6ba27e65u, 0x6dfddbccu, 0x70666f76u, 0x72dc8374u, 0x75606374u, 0x77f25cceu, 0x7a92be8bu, 0x7d41d96eu};
 
 struct SampleArgs {
     const void *logits;
@@ -145,15 +145,15 @@ __device__ __forceinline__ void add_if(bool on, uint32_t p, uint32_t v) {
                  : "memory");
 }
 
-// A logit as it counts: NaN is -infinity, +infinity the largest finite number of the type, -0 is +0.
+// A logit as it counts: NaN is -infinity (the larger of it and that), +infinity the largest finite number of the type.
 template <bool BF16>
 __device__ __forceinline__ float clean(float l) {
-    return l != l ? -INFINITY : fminf(l, BF16 ? 3.3895313892515355e38f : 3.4028234663852886e38f) + 0.0f;
+    return fminf(fmaxf(l, -INFINITY), BF16 ? 3.3895313892515355e38f : 3.4028234663852886e38f);
 }
 
-// Ascending in the (clean) logit.
+// Ascending in the (clean) logit; -0 as +0.
 __device__ __forceinline__ uint32_t key_of(float l) {
-    const uint32_t b = __float_as_uint(l);
+    const uint32_t b = __float_as_uint(l + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 constexpr uint32_t kKeyNone = 0x007fffffu;      // of -infinity: no candidate
@@ -164,6 +164,17 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 
 __device__ __forceinline__ u64 entry_of(uint32_t key, int i) { return static_cast<u64>(key) << 32 | ~static_cast<uint32_t>(i); }
 __device__ __forceinline__ int index_of(u64 entry) { return static_cast<int>(~static_cast<uint32_t>(entry)); }
+
+// w / 2^k rounded (k > 0), or w * 2^-k, for w below 2^31 and k from -12 on: shifts by amounts that are negative or above 31
+// give 0 in PTX, so both forms are computed and one of them is 0 (or, at k = 0, both are w).
+__device__ __forceinline__ u64 shifted(uint32_t w, int k) {
+    uint32_t half, down, up, high;
+    asm("shl.b32 %0, %1, %2;" : "=r"(half) : "r"(1u), "r"(k - 1));
+    asm("shr.u32 %0, %1, %2;" : "=r"(down) : "r"(w + half), "r"(k));
+    asm("shl.b32 %0, %1, %2;" : "=r"(up) : "r"(w), "r"(-k));
+    asm("shr.u32 %0, %1, %2;" : "=r"(high) : "r"(w), "r"(32 + k));
+    return static_cast<u64>(high) << 32 | (down | up);
+}
 
 // One row's weights.  Logits are halved so that no difference overflows.  An infinite temperature has factor 0.
 struct Weights {
@@ -196,9 +207,9 @@ struct Weights {
         q = __fmul_rn(r, q);
         const int at = __float_as_int(t) - __float_as_int(393216.0f);      // 32 * (exponent), <= 0
         const uint32_t m = exp2[at & 31];
-        const uint32_t w = m + static_cast<uint32_t>(__mulhi(static_cast<int>(m >> 1), __float2int_rn(q * 137438953472.0f)) >> 4);
-        // w * 2^(floor(at / 32) - 31), scaled by 2^42 and rounded
-        return ((static_cast<u64>(w) << (kOneBits - 31 + 1) >> min(-(at >> 5), 63)) + 1) >> 1;
+        const uint32_t w = m + static_cast<uint32_t>(__mulhi(static_cast<int>(m), __float2int_rn(q * 137438953472.0f)) >> 5);
+        // w * 2^(floor(at / 32) + 12), rounded
+        return shifted(w, -(at >> 5) - (kOneBits - 30));
     }
 };
 
@@ -563,14 +574,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     for (int o = warp * deal.len + 4 * lane; o < (warp + 1) * deal.len; o += 128) {
         const float4 f = v.fetch(o);
         if (a.resident) *reinterpret_cast<float4 *>(held + o) = f;
-        const float l[4] = {f.x, f.y, f.z, f.w};
+        const float most = fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)), fewest = fminf(fminf(f.x, f.y), fminf(f.z, f.w));
+        if (most > top) {
+            top = most;
+            where = v.index(o) + (f.x == most ? 0 : f.y == most ? 1 : f.z == most ? 2 : 3);
+        }
+        if (fewest > -INFINITY) {
+            least = fminf(least, fewest);
+        } else {
+            const float l[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (l[j] > top) {
-                top = l[j];
-                where = v.index(o) + j;
-            }
-            if (l[j] > -INFINITY) least = fminf(least, l[j]);
+            for (int j = 0; j < 4; ++j) least = l[j] > -INFINITY ? fminf(least, l[j]) : least;
         }
     }
     if (a.resident) v.held = held;
