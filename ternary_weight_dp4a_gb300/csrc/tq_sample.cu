@@ -43,13 +43,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2 * kThreads;             // of the histogram
 constexpr int kRadix = 256;                     // of the radix search
-constexpr int kLocal = 1024;                    // candidates of one CTA
 constexpr int kList = 4096;                     // candidates of a row, sorted by its first CTA
+constexpr int local_most(int cluster) { return cluster == 1 ? kList : 2 * kList / cluster; }    // of one CTA
 constexpr int kSmallK = kThreads;               // top_k up to this: by the threads' maxima
 constexpr float kNats = 24.0f;                  // the histogram's range of ln(weight)
-constexpr float kSlack = 5e-4f;                 // of the estimated sums
+constexpr float kSlack = 1e-4f;                 // of the estimated sums (the neglected terms are 1e-4 of each bin, and alike)
 constexpr int kOneBits = 42;                    // the largest weight is 2^42: a sum of 2^20 stays below 2^63
-constexpr int kPart = 16384;                    // entries per CTA from which a cluster grows
 constexpr float kColdest = 1.5777218104420236e-30f;     // 2^-99: below, as 0
 
 typedef unsigned long long u64;
@@ -75,7 +74,6 @@ struct Shared {
         uint32_t hist[kBins];
         u64 radix[kRadix];
     };
-    u64 local[kLocal];                          // candidates: key << 32 | ~index
     u64 warp_sum[kWarps];                       // of the draw's segments
     u64 best;                                   // key << 32 | ~index of the largest
     u64 sum_all, sum_above, sum_listed;
@@ -270,12 +268,13 @@ struct Deal {
         return {min(max(from - lead, 0), vocab), min(max(to - lead, 0), vocab)};
     }
 };
-constexpr int kHeldMost = 200 * 1024 / 4;       // entries in shared memory
+constexpr size_t kMostShared = 200 * 1024;      // dynamic
 
 template <bool BF16>
 struct Row {
     const void *logits;
     const float *held;                          // this CTA's part in shared memory, or nullptr
+    u64 *local;                                 // its candidates: key << 32 | ~index
     Deal deal;
     Segment seg;                                // this warp's
     int rank, cluster;
@@ -424,7 +423,7 @@ struct Row {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (take >> j & 1) {
-                if (n < kLocal) sm.local[n] = entry_of(key_of(l[j]), i + j);
+                if (n < local_most(cluster)) local[n] = entry_of(key_of(l[j]), i + j);
                 ++n;
             }
     }
@@ -432,7 +431,7 @@ struct Row {
     // Entries listed in all CTAs; more than kList if they do not fit (all CTAs agree).
     __device__ int listed() const {
         const uint32_t c = by_lanes(cluster, 0u, [&](int r) { return at_peer(&sm.listed, r, cluster); });
-        return static_cast<int>(__reduce_add_sync(0xffffffffu, c > kLocal ? kList + 1 : c));
+        return static_cast<int>(__reduce_add_sync(0xffffffffu, c > local_most(cluster) ? kList + 1 : c));
     }
 
     // First CTA: all lists one behind the other.
@@ -448,7 +447,7 @@ struct Row {
                     ++rank;
                 }
             }
-            if (i < n) list[i] = at_peer(&sm.local[at], rank, cluster);
+            if (i < n) list[i] = at_peer(&local[at], rank, cluster);
         }
     }
 };
@@ -560,14 +559,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     const void *logits = static_cast<const uint8_t *>(a.logits) + static_cast<int64_t>(row) * a.vocab * (BF16 ? 2 : 4);
     const Deal deal(logits, BF16 ? 2 : 4, a.vocab, a.cluster);
-    Row<BF16> v{logits, nullptr, deal, deal.segment(rank, warp), rank, a.cluster, sm};
+    u64 *local = reinterpret_cast<u64 *>(dynamic);
+    Row<BF16> v{logits, nullptr, local, deal, deal.segment(rank, warp), rank, a.cluster, sm};
     const float t = a.temperature != nullptr ? a.temperature[row] : 1.0f;
     const int k = a.top_k != nullptr ? a.top_k[row] : 0;
     const float p = a.top_p != nullptr ? a.top_p[row] : 1.0f, floor = a.min_p != nullptr ? a.min_p[row] : 0.0f;
     const float u = a.uniform[row];
 
     // the row's part, its largest and smallest
-    float *held = reinterpret_cast<float *>(dynamic);
+    // shared memory: this CTA's candidates | its part of the row, or (in the first CTA, when that is done with) all candidates
+    float *held = reinterpret_cast<float *>(local + local_most(a.cluster));
     float top = -INFINITY, least = INFINITY;
     int where = 0;
 #pragma unroll 4
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (small_k) {
         // Keys that at least k entries of the row reach: of the threads' maxima, k of this CTA's (warp 0), or
         // its share of k of each CTA's (warp 1).
-        uint32_t *maxima = reinterpret_cast<uint32_t *>(sm.local);
+        uint32_t *maxima = reinterpret_cast<uint32_t *>(local);
         maxima[tid] = top > -INFINITY ? key_of(top) : 0;
         __syncthreads();
         if (warp < 2) {
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         // w >= min_p  <=>  l >= l_max + T ln(min_p)
         lowest = fminf(__double2float_ru(static_cast<double>(largest) + sm.drop), largest);
     }
-    u64 *list = reinterpret_cast<u64 *>(dynamic);           // in the first CTA, when its part is done with
+    u64 *list = reinterpret_cast<u64 *>(held);
 
     if (small_k) {
         const float from = fmaxf(bound > kKeyNone ? logit_of(bound) : -INFINITY, lowest);
@@ -906,17 +907,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 template <bool BF16>
 cudaError_t sample_launch(SampleArgs a, int sms, cudaStream_t stream) {
     static SmemLimit limit;
-    cudaError_t e = limit.raise(sample_kernel<BF16>, kHeldMost * 4);
+    cudaError_t e = limit.raise(sample_kernel<BF16>, kMostShared);
     if (e != cudaSuccess) return e;
+    // CTAs per row: as many as run at once, two to an SM (one, where parts get below 4096 entries), and
+    // up to eight.  1, 2, 4 and 8 of them, top-p (us): 131072 entries, 16 rows 137 91 56 51, 64 rows 146 113 83 91, 128 rows
+    // 199 149 154 169, 256 rows 256 232 244 295; 32003 entries, 16 rows 34 26 21 23, 64 rows 35 35 28 46, 256 rows 59 70 88 153;
+    // 4000 entries, 1 row 13 14 15 16, 256 rows 20 37 63 135.
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && (a.vocab > a.cluster * kPart || (a.vocab > a.cluster * 1024 && a.m * a.cluster < sms))) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && a.vocab > a.cluster * 4096 &&
+           static_cast<int64_t>(a.m) * 2 * a.cluster <= (a.vocab > 2 * a.cluster * 4096 ? 2 * sms : sms))
+        a.cluster *= 2;
     const int part = ((a.vocab + 3 + a.cluster - 1) / a.cluster + 3) / 4 * 4;        // (at most: as Deal)
-    const int held = kWarps * (((part + kWarps - 1) / kWarps + 127) / 128 * 128);
-    a.resident = held <= kHeldMost;
+    const size_t held = static_cast<size_t>(kWarps) * (((part + kWarps - 1) / kWarps + 127) / 128 * 128) * 4;
+    const size_t local = local_most(a.cluster) * sizeof(u64);
+    // A part is kept in shared memory where that does not cost the SM its second CTA: else it is read again, from
+    // L2 (131072 entries, top-k, four CTAs per row: 16 rows 20 kept, 24 not; 64 rows 38 kept, 29 not).
+    const int per_sm = static_cast<int64_t>(a.m) * a.cluster > sms ? 2 : 1;
+    a.resident = (held + local) * per_sm <= kMostShared;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.m) * a.cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = max(a.resident ? static_cast<size_t>(held) * 4 : 0, kList * sizeof(u64));
+    cfg.dynamicSmemBytes = local + max(a.resident ? held : 0, kList * sizeof(u64));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
