@@ -28,14 +28,17 @@ struct Q4Product {
 
 cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const uint16_t *mins, int n, int k, int group,
                            uint8_t *out_codes, uint16_t *out_scales, uint16_t *out_mins, cudaStream_t stream);
-// Calls of more rows than this run on the tile kernel.
+// Calls of more rows than this run on the tile kernel.  (us, tile and two passes of the stream kernel at 20 or
+// 32 rows: 5120 x 5120 group 128 12 25, 6145 x 2048 group 64 with minima 13 15, 5120 x 17408 group 32 with
+// minima 43 54; gate/up 2 x 17408 x 5120 group 128 47 59, group 32 with minima 74 72; 131072 x 5120 group 64
+// 188 179, group 32 with minima 271 262: the large ones of small groups lose 5%.)
 constexpr int kQ4StreamRows = 16;
 
 // Workspace of the tile kernel, where there are minima: sums of x over the groups, [k / group][q4_sums_ld(m)].
 constexpr int64_t q4_sums_ld(int64_t m) { return (m + 15) / 16 * 16; }
 constexpr size_t q4_sums_bytes(int64_t m, int64_t k, int64_t group) { return static_cast<size_t>(q4_sums_ld(m) * (k / group) * 4); }
 
-// Any number of rows, 16 per pass over the weights; and 192 per pass.
+// Up to kQ4StreamRows rows, and any number.
 cudaError_t q4_stream_launch(const Q4Product &p, cudaStream_t stream);
 cudaError_t q4_tile_launch(const Q4Product &p, float *sums, cudaStream_t stream);
 // The bits of the bounded waits that have run out on the current device (copied in `stream`).

@@ -44,8 +44,6 @@ struct Shape {
 
 struct StreamArgs {
     Q4Product p;
-    int row0;               // first row of this pass
-    int rows;               // rows of this pass
     int cluster;
 };
 
@@ -223,16 +221,16 @@ __global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_k
 
     // x, in the order in which lanes read it: 16 bytes are 8 values, chunk = piece / 16,
     // group of 32 = piece / 4 % 4, lane of the quad = piece % 4
-    for (int i = tid; i < mine * 16 * a.rows; i += S::kThreads) {
+    for (int i = tid; i < mine * 16 * p.m; i += S::kThreads) {
         const int row = i / (mine * 16), piece = i - row * (mine * 16);
-        const uint4 v = *reinterpret_cast<const uint4 *>(p.x + (static_cast<int64_t>(a.row0 + row) * p.k + (first * 16 + piece) * 8));
+        const uint4 v = *reinterpret_cast<const uint4 *>(p.x + (static_cast<int64_t>(row) * p.k + (first * 16 + piece) * 8));
         xs[((piece >> 2) * (8 * NT) + row) * 4 + (piece & 3)] = v;
     }
     if constexpr (MINS) {
         __syncthreads();
         constexpr int kPieces = 16 / PER;               // of a group
-        for (int i = tid; i < mine * PER * a.rows; i += S::kThreads) {
-            const int row = i % a.rows, g = i / a.rows;
+        for (int i = tid; i < mine * PER * p.m; i += S::kThreads) {
+            const int row = i % p.m, g = i / p.m;
             float s = 0.0f;
             for (int j = 0; j < kPieces; ++j) {
                 const int piece = g * kPieces + j;
@@ -249,7 +247,7 @@ __global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_k
     // rows of x of this lane's B operand: any one behind the last
     const uint4 *xl[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xl[t] = xs + min(8 * t + (lane >> 2), a.rows - 1) * 4 + (lane & 3);
+    for (int t = 0; t < NT; ++t) xl[t] = xs + min(8 * t + (lane >> 2), p.m - 1) * 4 + (lane & 3);
     const uint64_t *xsum = reinterpret_cast<const uint64_t *>(sums) + (lane & 3);       // of its accumulators' two
     uint32_t mask = 0x000f000fu, base = 0x43004300u;
     asm volatile("" : "+r"(mask), "+r"(base));          // in registers: two constants do not fit one instruction
@@ -261,8 +259,8 @@ __global__ void __launch_bounds__(Shape<NT, RS, SPLIT>::kThreads, 1) q4_stream_k
         const float g[4] = {v.x, v.y, v.z, v.w}, w[4] = {up.x, up.y, up.z, up.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (row + (i & 1) >= a.rows || out + 8 * (i >> 1) >= p.n) continue;
-            const int64_t at = static_cast<int64_t>(a.row0 + row + (i & 1)) * p.n + out + 8 * (i >> 1);
+            if (row + (i & 1) >= p.m || out + 8 * (i >> 1) >= p.n) continue;
+            const int64_t at = static_cast<int64_t>(row + (i & 1)) * p.n + out + 8 * (i >> 1);
             const float y = GATEUP ? __fmul_rn(tq_silu(g[i]), w[i]) : g[i];
             if (GATEUP || p.y_bf16) static_cast<uint16_t *>(p.y)[at] = f32_to_bf16_bits(y);
             else static_cast<float *>(p.y)[at] = y;
@@ -476,7 +474,7 @@ cudaError_t pick(StreamArgs &a, int dev, int sms, cudaStream_t stream) {
 }
 
 template <int NT>
-cudaError_t pass(StreamArgs &a, int dev, int sms, cudaStream_t stream) {
+cudaError_t pick(StreamArgs &a, int dev, int sms, cudaStream_t stream) {
     return a.p.group == 128 ? pick<NT, 1>(a, dev, sms, stream) : a.p.group == 64 ? pick<NT, 2>(a, dev, sms, stream) : pick<NT, 4>(a, dev, sms, stream);
 }
 
@@ -489,12 +487,7 @@ cudaError_t q4_stream_launch(const Q4Product &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     StreamArgs a{};
     a.p = p;
-    for (a.row0 = 0; a.row0 < p.m; a.row0 += 16) {
-        a.rows = p.m - a.row0 < 16 ? p.m - a.row0 : 16;
-        e = a.rows > 8 ? pass<2>(a, dev, sms, stream) : pass<1>(a, dev, sms, stream);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    return p.m > 8 ? pick<2>(a, dev, sms, stream) : pick<1>(a, dev, sms, stream);
 }
 
 }  // namespace tq
