@@ -75,7 +75,10 @@ size_t tq_q4_workspace_bytes(int32_t m, int32_t k, int32_t group);
 /* y[r][i] = sum over j of W[i][j] * x[r][j], for m rows x (bf16 bits [m][k],
  * 16-byte aligned), rounded to y_type (tq_dtype) once.  Per group, the sum of
  * (c - 8) * x over exact products is taken in fp32 by matrix instructions, and
- * folded in fp32 as s * sum, plus (8 s - b) * (sum of x) where there are minima.
+ * folded in fp32 as s * sum, plus (8 s - b) * (sum of x) where there are minima;
+ * calls of many rows with groups of 32 or 64 have s in the matrix instructions too,
+ * exactly, as the sum of two bf16.  An infinity or NaN in a row of x, or in a scale
+ * or minimum, makes results that depend on it infinite or NaN, and no others.
  * In calls of up to 8 rows (a packed decode step) each row has the bits that it
  * has alone; with more rows the order of the sums may differ.
  * y: [m][n], aligned to its type; n 1 .. TQ_Q4_MAX_N, k up to TQ_Q4_MAX_K, m 1 ..

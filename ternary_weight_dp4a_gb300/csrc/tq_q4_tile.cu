@@ -14,6 +14,11 @@
 // the copies of x (256) share one 128-byte port: 3000 cycles per 256 rows and 128 values were measured,
 // 1024 per 128 rows here.
 //
+// Groups of 32 or 64 and many rows: a fold per group would take longer than the MMAs (an accumulator's hand-over
+// and 192 columns: 990 cycles per group of 32, whose MMAs take 256).  There the scale goes into the weights, exactly:
+// an fp16 scale is the sum of two bf16 of five bits, and five bits times c - 8 is exact in bf16, so two MMAs
+// instead of one bring s (c - 8) x, and the fold adds up one accumulator per 128 values of k; minima stay with it.
+//
 // Few tiles are split along k over the CTAs of a cluster, which add up their parts through shared memory.
 //
 // Warps: 0-7 decode (four for every other chunk of 128 values), 8 issues MMAs, 9 copies x, 10 its sums,
@@ -233,7 +238,23 @@ __device__ __forceinline__ float scale_at(const uint32_t (&v)[N], int e) {
     return f16_bits_to_f32(static_cast<uint16_t>(e & 1 ? w >> 16 : w & 0xffffu));
 }
 
-template <int GROUP, bool MINS, bool GATEUP>
+// A scale as the sum of two bf16 of five bits each, twice each: times c - 8 either is exact in bf16.  (fp16 has 11
+// bits; what rounding to five leaves is at most half of the fifth's unit, so five bits and a sign.)
+__device__ __forceinline__ void split_scale(float s, uint32_t &hi, uint32_t &lo) {
+    const uint32_t u = __float_as_uint(s);
+    const bool finite = (u & 0x7f800000u) != 0x7f800000u;
+    const uint32_t h = finite ? (u + 0x40000u) & 0xfff80000u : u;
+    const uint32_t l = finite ? __float_as_uint(s - __uint_as_float(h)) : 0u;
+    hi = __byte_perm(h, h, 0x3232);
+    lo = __byte_perm(l, l, 0x3232);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+template <int GROUP, bool MINS, bool GATEUP, bool SCALED>
 __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_constant__ TileArgs args) {
     extern __shared__ uint8_t smem_raw[];
     TileSmem &sm = *reinterpret_cast<TileSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -253,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     // columns, each folded by a third of the warps; else two of 192, all warps having a third of the columns.
     const int dcols = (cols + 31) / 32 * 32, teams = cols <= kFoldCols ? 3 : 1;
     const int sets = teams == 3 ? 3 : 2, set_cols = 2 * kCols / sets;
-    const int per_set = kPer * dcols <= set_cols ? kPer : kPer == 4 && 2 * dcols <= set_cols ? 2 : 1;
+    const int per_set = SCALED || kPer * dcols <= set_cols ? kPer : kPer == 4 && 2 * dcols <= set_cols ? 2 : 1;
 
     if (warp == kDecodeWarps) {
         tmem_alloc(smem_u32(&sm.tmem), 512);
@@ -298,7 +319,58 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     pdl_launch_dependents();
     pdl_wait();
 
-    if (warp < kDecodeWarps) {
+    if (SCALED && warp < kDecodeWarps) {
+        // ---- decode with scales: 32 values' two parts a buffer, two buffers of every chunk for either four warps ----
+        regs_down<kRegsDecode>();
+        const int second = warp >> 2;                               // half of the chunk
+        const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64 + second * 8;
+        const uint16_t *ssrc = p.scales[mat] + (block0 * 8 + (lane & 7)) * (2 * kPer) + ((lane >> 3) & 1) * kPer;
+        const uint32_t a_at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemA + second * 64;
+        const uint32_t empty = smem_u32(sm.a_empty) + second * 16, a_full = smem_u32(sm.a_full) + second * 16;
+        uint32_t mask = 0x000f000fu, base = 0x43004300u;
+        asm volatile("" : "+r"(mask), "+r"(base));
+        uint2 code[4];
+        uint32_t sc[(kPer + 1) / 2];
+        auto load = [&](int c) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                asm volatile("ld.global.v2.u32 {%0,%1}, [%2];"
+                             : "=r"(code[q].x), "=r"(code[q].y)
+                             : "l"(src + static_cast<int64_t>(c) * kQ4ChunkBytes + q * 16));
+            load_scales<kPer>(sc, ssrc + static_cast<int64_t>(c) * (16 * kPer));
+        };
+        load(0);
+        bool ok = true;
+        uint32_t turn = 1;
+        for (int c = 0; c < total && ok; ++c, turn ^= 1) {
+            if (second == 0 && c % 4 == 0) ask(c + kAhead, c + kAhead + 4);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                ok = warp_wait<32>(sm, empty + 8 * g, turn, 1u << 0);
+                if (!ok) break;
+                tc_fence_after();
+                // (group 64: one scale of the pair for each half of the chunk; 32: one of its half's pair for each buffer)
+                const uint32_t two = kPer == 4 && second ? sc[(kPer - 1) / 2] : sc[0];
+                uint32_t hi, lo;
+                split_scale(f16_bits_to_f32(static_cast<uint16_t>((kPer == 4 ? g : second) ? two >> 16 : two & 0xffffu)), hi, lo);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t v[16];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[4 * q + i] = mul_bf16x2(decode_pair(g ? code[q].y : code[q].x, i, mask, base), part ? lo : hi);
+                    st_16(a_at + 32 * g + 16 * part, v);
+                }
+                if (g == 1 && c + 1 < total) load(c + 1);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(a_full + 8 * g);
+            }
+        }
+    } else if (warp < kDecodeWarps) {
         // ---- decode: a lane's 128 codes of a chunk are 64 bytes, two halves of them one buffer each ----
         regs_down<kRegsDecode>();
         const int odd = warp >> 2;                                  // which chunks
@@ -358,7 +430,37 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             uint32_t turn = 0, set = 0, d_turn = 1, d_set = 0, x_at = 0, x_turn = 0;
             uint64_t x_set = x_desc;
             bool ok = true;
-            for (int c0 = 0; c0 < total && ok; c0 += 2, turn ^= 1) {
+            if constexpr (SCALED) {
+                for (int c = 0; c < total && ok; ++c, turn ^= 1) {
+                    ok = wait_alive(sm, x_full + 8 * x_at, x_turn, 1u << 1) && wait_alive(sm, d_empty + 8 * set, d_turn, 1u << 3);
+#pragma unroll
+                    for (int ring = 0; ring < kABufs; ++ring) {
+                        ok = ok && wait_alive(sm, a_full + 8 * ring, turn, 1u << 2);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)                 // (both parts: the same values of x)
+                            mma_bf16_ts(issue, d_set, kTmemA + 32 * ring + 8 * i,
+                                        x_set + (ring / 2 * (kHalfBytes >> 4) + 4 * (ring % 2) + 2 * (i % 2)), idesc, ring + i > 0);
+                        commit_if(issue, a_empty + 8 * ring);
+                    }
+                    if (!ok) break;
+                    commit_if(issue, d_full + 8 * set);
+                    d_set += set_cols;
+                    if (++set == sets) {
+                        set = d_set = 0;
+                        d_turn ^= 1;
+                    }
+                    commit_if(issue, x_empty + 8 * x_at);
+                    x_set += 2 * kHalfBytes >> 4;
+                    if (++x_at == kStages) {
+                        x_at = 0;
+                        x_set = x_desc;
+                        x_turn ^= 1;
+                    }
+                }
+            }
+            for (int c0 = 0; !SCALED && c0 < total && ok; c0 += 2, turn ^= 1) {
 #pragma unroll
                 for (int ring = 0; ring < kABufs; ++ring) {
                     if (c0 + ring / 2 >= total || !ok) break;
@@ -478,8 +580,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             const bool sums_lane = MINS && (lane & 1);              // both waits at once
             if (!warp_wait<20>(sm, (sums_lane ? s_full : d_full) + 8 * set, turn, sums_lane ? 1u << 7 : 1u << 8)) break;
             tc_fence_after();
+            if (SCALED) {
+                const uint32_t d = lane_base + set * set_cols;
+                const uint64_t one = pack2(1.0f, 1.0f);
+#pragma unroll
+                for (int q = 0; q < kFoldCols / 16; ++q) {
+                    if (16 * q >= mine) break;
+                    uint64_t x[8];
+                    ld_16(d + 16 * q, x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[8 * q + j] = fma2(x[j], one, acc[8 * q + j]);
+                }
+            }
 #pragma unroll 1
-            for (int in = 0; in < per_set; ++in) {
+            for (int in = 0; in < (SCALED && !MINS ? 0 : per_set); ++in) {
                 const int e = (i & ((1 << shift) - 1)) * per_set + in;
                 const float s = scale_at(sc, e);
                 const uint64_t s2 = pack2(s, s);
@@ -491,10 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
 #pragma unroll
                 for (int q = 0; q < kFoldCols / 16; ++q) {
                     if (16 * q >= mine) break;
-                    uint64_t x[8];
-                    ld_16(d + 16 * q, x);
+                    if (!SCALED) {
+                        uint64_t x[8];
+                        ld_16(d + 16 * q, x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[8 * q + j] = fma2(x[j], s2, acc[8 * q + j]);
+                        for (int j = 0; j < 8; ++j) acc[8 * q + j] = fma2(x[j], s2, acc[8 * q + j]);
+                    }
                     if (MINS) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -620,12 +736,12 @@ __global__ void __launch_bounds__(256) q4_sums_kernel(const uint16_t *x, int m, 
     sums[g * ld + row] = s;
 }
 
-template <int GROUP, bool MINS, bool GATEUP>
+template <int GROUP, bool MINS, bool GATEUP, bool SCALED>
 cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     constexpr size_t smem = sizeof(TileSmem) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static SmemLimit limit;
-    cudaError_t e = limit.raise(q4_tile_kernel<GROUP, MINS, GATEUP>, smem);
+    cudaError_t e = limit.raise(q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (q4_strips(a.p.n) + (GATEUP ? 3 : 7)) / (GATEUP ? 4 : 8) * a.row_tiles;
     const int chunks = a.p.k / 128;
@@ -634,7 +750,7 @@ cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     a.split = 1;
     for (int more = 2; more <= 8 && tiles * more <= sms && chunks >= 2 * more; ++more) {
         int most = 0;
-        e = cluster_limit.most(q4_tile_kernel<GROUP, MINS, GATEUP>, dev, more, kThreads, smem, sms, &most);
+        e = cluster_limit.most(q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, dev, more, kThreads, smem, sms, &most);
         if (e != cudaSuccess) return e;
         if (tiles <= most) a.split = more;
     }
@@ -651,14 +767,27 @@ cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, q4_tile_kernel<GROUP, MINS, GATEUP>, a);
+    return cudaLaunchKernelEx(&cfg, q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, a);
+}
+
+template <int GROUP, bool MINS, bool GATEUP>
+cudaError_t pick(TileArgs &a, int dev, int sms, cudaStream_t stream) {
+    // Scales in the weights cost twice the MMAs, whatever the rows; folds of small groups cost by the column, and with
+    // minima more.  (us, folded and scaled: 131072 x 5120, group 32 64 rows 260 376, 80 rows 415 359, 192 rows
+    // 646 379; with minima 32 rows 294 349, 64 rows 437 390, 192 rows 947 648; group 64 128 rows 328 333, 160 rows
+    // 341 342, 192 rows 358 352, with minima 64 rows 285 360, 80 rows 386 369, 192 rows 556 454; gate/up
+    // 2 x 17408 x 5120, 512 rows: 594 298, with minima 735 508; group 64 343 285, with minima 436 361.)
+    constexpr int kFolded = GROUP == 32 ? (MINS ? 48 : 64) : MINS ? 64 : 128;
+    if constexpr (GROUP < 128)
+        if (a.rows > kFolded) return launch<GROUP, MINS, GATEUP, true>(a, dev, sms, stream);
+    return launch<GROUP, MINS, GATEUP, false>(a, dev, sms, stream);
 }
 
 template <int GROUP>
 cudaError_t pick(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     const bool mins = a.p.mins[0] != nullptr;
-    if (a.p.mats == 1) return mins ? launch<GROUP, true, false>(a, dev, sms, stream) : launch<GROUP, false, false>(a, dev, sms, stream);
-    return mins ? launch<GROUP, true, true>(a, dev, sms, stream) : launch<GROUP, false, true>(a, dev, sms, stream);
+    if (a.p.mats == 1) return mins ? pick<GROUP, true, false>(a, dev, sms, stream) : pick<GROUP, false, false>(a, dev, sms, stream);
+    return mins ? pick<GROUP, true, true>(a, dev, sms, stream) : pick<GROUP, false, true>(a, dev, sms, stream);
 }
 
 }  // namespace

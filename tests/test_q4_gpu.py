@@ -182,6 +182,58 @@ def test_infinities_and_nan_stay_in_their_rows(tq, m):
     assert not got[row].isfinite().any() and torch.equal(got[keep], clean[keep])
 
 
+@pytest.mark.parametrize("mins", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_scales_of_every_size(tq, group, mins):
+    """fp16 scales and minima of every exponent and either sign, subnormal ones and zeros among them; and NaN, infinities."""
+    import torch
+    n, k = 150, 384
+    g = torch.Generator(device="cuda")
+    g.manual_seed(group + mins)
+    codes = torch.randint(0, 16, (n, k), generator=g, device="cuda", dtype=torch.uint8)
+
+    def halves():
+        bits = torch.randint(0, 1 << 16, (n, k // group), generator=g, device="cuda", dtype=torch.int32)
+        bits = torch.where((bits & 0x7c00) == 0x7c00, bits & 0x83ff, bits)          # no exponent of NaN: subnormal
+        return bits.to(torch.int16).view(torch.float16)
+    s, b = halves(), halves() if mins else None
+    w = tq.pack_q4(codes, s, b)
+    sd = s.double().repeat_interleave(group, 1)
+    bd = 8 * sd if b is None else b.double().repeat_interleave(group, 1)
+    special = s.clone()
+    special[20, 1], special[30, 0], special[140, 2] = float("inf"), float("nan"), float("-inf")
+    odd = tq.pack_q4(codes, special, b)
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[[20, 30, 140]] = False
+    for m in (1, 9, 17, 64, 100, 192):
+        x = _x(m, k, m)
+        xd = x.double()
+        want = xd @ (sd * codes.double() - bd).T
+        size = xd.abs() @ (sd * (codes.double() - 8)).abs().T
+        if mins:
+            size += xd.abs() @ (8 * sd - bd).abs().T
+        # as Matrix.product; with scales in the matrix instructions, 128 values are 16 additions of up to 33/32 of it
+        tol = (34 * 2.0 ** -23 + (128 * mins + 2 * k // group + 25) * 2.0 ** -24) * size
+        clean = tq.q4_gemv(w, x)
+        _check(clean, want, tol)
+        got = tq.q4_gemv(odd, x)
+        assert torch.equal(got[:, keep], clean[:, keep]) and not got[:, ~keep].isfinite().any()
+
+
+@pytest.mark.parametrize("m", [64, 80, 192])
+@pytest.mark.parametrize("group", [32, 64])
+def test_infinities_and_nan_in_wide_calls(tq, group, m):
+    import torch
+    w = Matrix(tq, 40, 512, group, True, 5)
+    x = _x(m, 512, 1)
+    clean = tq.q4_gemv(w.dev, x)
+    keep = torch.arange(m, device="cuda") != 33
+    for bad in ("nan", "inf", "-inf"):
+        x[33, 100] = float(bad)
+        got = tq.q4_gemv(w.dev, x)
+        assert torch.equal(got[keep], clean[keep]) and not got[33].isfinite().any()
+
+
 def test_offsets_past_32_bits(tq):
     """Packed codes and unpacked ones of more than 2^31 and 2^32 bytes."""
     import torch
