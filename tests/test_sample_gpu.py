@@ -184,6 +184,34 @@ def test_rows_do_not_depend_on_each_other(tq):
             assert i.item() == ids[r].item() and q.item() == probs[r].item()
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("vocab", [4097, 9000, 20_000, 40_001, 70_001, 131_072])
+def test_a_row_is_the_same_in_any_batch(tq, vocab, dtype):
+    """Batches of other sizes give a row more or fewer CTAs, and its parts are kept or read again."""
+    import torch
+    rng = np.random.default_rng(vocab)
+    most = 320
+    logits = _logits(most, vocab, 2.5, dtype, 9)
+    logits[::16] = logits[::16].round()                                     # many equal
+    logits[3::16] = 1.0
+    logits[5::16, ::2] = -INF
+    logits[7::16, 1000:] = torch.finfo(logits.dtype).min
+    logits[9::16, 100] = float("nan")
+    logits[11::16] *= 1e-3
+    on = lambda v, d=torch.float32: torch.as_tensor(v, dtype=d, device="cuda")  # noqa: E731
+    u = on(rng.random(most, dtype=np.float32))
+    t = on(rng.uniform(0.3, 1.5, most) * (rng.integers(0, 12, most) > 0))
+    k = on(rng.integers(0, 700, most) * (rng.integers(0, 3, most) > 0), torch.int32)
+    p = on(np.where(rng.integers(0, 3, most) > 0, rng.uniform(0.05, 1, most), 1.0))
+    f = on(rng.uniform(0, 0.1, most) * (rng.integers(0, 2, most) > 0))
+    for settings in ({}, {"temperature": t}, {"top_k": k}, {"top_p": p}, {"min_p": f}, {"temperature": t, "top_k": k, "top_p": p, "min_p": f}):
+        few = [tq.sample(logits[i:i + 4], u[i:i + 4], **{n: v[i:i + 4] for n, v in settings.items()}) for i in range(0, most, 4)]
+        ids, probs = (torch.cat(v) for v in zip(*few))
+        for m in (20, 50, 76, 100, 160, most):
+            got = tq.sample(logits[:m], u[:m], **{n: v[:m] for n, v in settings.items()})
+            assert torch.equal(got[0], ids[:m]) and torch.equal(got[1], probs[:m]), (m, list(settings))
+
+
 def test_shares_are_the_probabilities(tq):
     """Evenly spaced numbers draw every token as often as its probability says, within one."""
     import torch
