@@ -32,8 +32,8 @@ extern "C" {
  * ids[r] = i; probs[r] (may be NULL) = w_i / (the sum of what stayed).  A row
  * without candidates has -1 and 0.
  * Per-row settings, each [m] or NULL for none of it:
- *   temperature fp32: 0, negative or NaN: the first of the order, with
- *     probability 1 (the row's other settings are not looked at); NULL: 1;
+ *   temperature fp32: below 2^-99 (0, negative) or NaN: the first of the order,
+ *     with probability 1 (the row's other settings are not looked at); NULL: 1;
  *     +infinity: equal weights
  *   top_k int32: <= 0 or more than there are: all
  *   top_p fp32: >= 1 or NaN: all; <= 0: the first

@@ -49,10 +49,6 @@ __global__ void __launch_bounds__(256) q4_pack_scales_kernel(const uint16_t *sca
     if (mins != nullptr) out_mins[w] = row < n ? mins[from] : 0;
 }
 
-// Launched behind the packing kernels without programmatic serialisation: it starts when they have
-// ended and their writes are visible, so that no later kernel overlaps them.
-__global__ void q4_pack_end_kernel() {}
-
 }  // namespace
 
 cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const uint16_t *mins, int n, int k, int group,
@@ -66,9 +62,6 @@ cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const u
     const int64_t entries = blocks * 16 * per;
     q4_pack_scales_kernel<<<static_cast<unsigned>((entries + 255) / 256), 256, 0, stream>>>(
         scales, mins, n, k / group, per, entries, out_scales, out_mins);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    q4_pack_end_kernel<<<1, 1, 0, stream>>>();
     return cudaGetLastError();
 }
 

@@ -17,9 +17,10 @@
 // A cluster of CTAs has a row, a part of it in each CTA's shared memory; the first CTA finishes.
 //   top_k <= 512: the top_k-th largest of a CTA's threads' maxima bounds the cut from below, so a few
 //     times top_k entries at most are candidates; the first CTA sorts them and does the rest on them.
-//   top_p: a histogram of the weights over 1024 bins, even in the logit, brackets the cut to about 0.1%
+//   top_p: a histogram of the weights over 1024 bins, even in the logit, brackets the cut to a bin and 0.02%
 //     of the sum; one pass then adds up the exact weights above the bracket and lists its entries,
-//     and the first CTA sorts those.
+//     and the first CTA sorts those.  (A bin counts in whole numbers and may pass 2^32 where a CTA has more than
+//     2^18 entries: the bracket is checked against the exact sums, and one that misses takes the radix search.)
 //   the draw: every warp's segment has its sum, the first CTA finds the segment and reads it again.
 // Where candidates do not fit their list (thousands of equal logits, or a top_k beyond), the
 // cut is found by a radix search over the key's bytes, which takes any input.
@@ -27,6 +28,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "tq.h"
 #include "tq_device.cuh"
@@ -286,23 +288,31 @@ struct Row {
     }
     __device__ __forceinline__ int index(int offset) const { return rank * deal.part + offset - deal.lead; }
     __device__ __forceinline__ float at(int i) const { return held != nullptr ? held[i + deal.lead - rank * deal.part] : read(i); }
+    // A vector's bits, as loaded: where all of it is in the part and the row.
+    using Bits = std::conditional_t<BF16, uint2, float4>;
+    __device__ __forceinline__ bool whole(int offset) const {
+        const int i = index(offset);
+        return offset < deal.part && i >= 0 && i + 4 <= deal.vocab;
+    }
+    __device__ __forceinline__ Bits bits(int offset) const {
+        if constexpr (BF16) return *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(logits) + index(offset));
+        else return *reinterpret_cast<const float4 *>(static_cast<const float *>(logits) + index(offset));
+    }
+    static __device__ __forceinline__ float4 values(const Bits &u) {
+        float4 v;
+        if constexpr (BF16)
+            v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                            __uint_as_float(u.y & 0xffff0000u));
+        else v = u;
+        return make_float4(clean<BF16>(v.x), clean<BF16>(v.y), clean<BF16>(v.z), clean<BF16>(v.w));
+    }
     // The four entries from this CTA's place `offset` on, -infinity outside of the part or the row.
     __device__ __forceinline__ float4 fetch(int offset) const {
         const int i = index(offset);
         float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (offset >= deal.part) return v;
-        if (i >= 0 && i + 4 <= deal.vocab) {
-            if constexpr (BF16) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(logits) + i);
-                v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                                __uint_as_float(u.y & 0xffff0000u));
-            } else {
-                v = *reinterpret_cast<const float4 *>(static_cast<const float *>(logits) + i);
-            }
-            v.x = clean<BF16>(v.x);
-            v.y = clean<BF16>(v.y);
-            v.z = clean<BF16>(v.z);
-            v.w = clean<BF16>(v.w);
+        if (whole(offset)) {
+            v = values(bits(offset));
         } else {
             if (i >= 0 && i < deal.vocab) v.x = read(i);
             if (i + 1 >= 0 && i + 1 < deal.vocab) v.y = read(i + 1);
@@ -315,8 +325,16 @@ struct Row {
     template <typename Visit>
     __device__ __forceinline__ void all(Visit visit) const {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        for (int o = warp * deal.len + 4 * lane; o < (warp + 1) * deal.len; o += 128) {
-            const float4 v = held != nullptr ? *reinterpret_cast<const float4 *>(held + o) : fetch(o);
+        const int end = (warp + 1) * deal.len;
+        int o = warp * deal.len + 4 * lane;
+        // One CTA per row reads it again with a load a vector ahead of its use (256 rows of 131072, top-p 225 us to
+        // 204).  Parts of a row that are read again come from L2, and gain nothing (64 rows 67, 73).
+        Bits next{};
+        const bool ahead = held == nullptr && cluster == 1;
+        if (ahead && whole(o)) next = bits(o);
+        for (; o < end; o += 128) {
+            const float4 v = held != nullptr ? *reinterpret_cast<const float4 *>(held + o) : ahead && whole(o) ? values(next) : fetch(o);
+            if (ahead && o + 128 < end && whole(o + 128)) next = bits(o + 128);
             const float l[4] = {v.x, v.y, v.z, v.w};
             visit(l, index(o));
         }
@@ -524,7 +542,6 @@ __device__ __forceinline__ u64 scaled(float f, u64 s, bool up) {
     }
     return v + (up && rest);
 }
-
 
 // The target of the draw: the first index whose sum exceeds it is drawn.
 __device__ __forceinline__ u64 draw_target(float u, u64 sum) {

@@ -266,6 +266,25 @@ def test_streams_and_graphs(tq):
     assert torch.equal(i, want[1][0]) and torch.equal(q, want[1][1])
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_the_largest_vocabulary(tq, dtype):
+    """One CTA has all of a row, in bins that pass 32 bits where the row is flat; few rows have eight."""
+    import torch
+    m, vocab = 160, 1 << 20
+    logits = _logits(m, vocab, 1.0, dtype, 4)
+    logits[::4] = 2.0
+    logits[1::4] *= 4
+    logits[2::4, 5:] = -2.0
+    u = torch.rand((m,), device="cuda")
+    for settings in ({}, {"top_p": 0.8}, {"top_k": 300}, {"top_k": 700_000, "top_p": 0.5, "min_p": 0.01}):
+        on = {n: torch.full((m,), v, device="cuda", dtype=torch.int32 if n == "top_k" else torch.float32) for n, v in settings.items()}
+        ids, probs = tq.sample(logits, u, **on)
+        for r in (0, 4, 80):
+            i, q = tq.sample(logits[r:r + 4], u[r:r + 4], **{n: v[r:r + 4] for n, v in on.items()})
+            assert torch.equal(i, ids[r:r + 4]) and torch.equal(q, probs[r:r + 4])
+        check(tq, logits[:4], u[:4].cpu().numpy(), **{n: v[:4].cpu().numpy() for n, v in on.items()})
+
+
 def test_many_rows(tq):
     """More rows than CTAs that fit at once, and offsets past 32 bits."""
     import torch
