@@ -17,6 +17,11 @@
 // in ascending order of k at the end.  Where x does not fit into one CTA's shared memory, a cluster's CTAs have a
 // range of k each, and the parts are read across the cluster, a batch of units at a time.  Neither depends on
 // the number of rows up to 8, so a row's bits do not either.
+//
+// What bounds it.  One row, large matrices, group 128: memory (131072 x 5120 64 us, 5.4 TB/s; gate and up 17408 x 5120
+// 22 us, of which 4 before the first weights).  Small groups and more rows: instructions (a word is 20 for
+// 8 weights, a group's fold 8 more per 8 rows of x, minima as many again; 13 rows, gate and up 17408 x 5120, group
+// 32 with minima 45 us, 2.5 TB/s).  Small matrices: latency (5120 x 5120 6.3 us).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -33,7 +38,9 @@ template <int NT, int RS, bool SPLIT>
 struct Shape {
     static constexpr int kWarps = NT == 1 ? 16 : 12;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kDepth = (NT == 1 ? 4 : 6) / RS;       // chunks in flight per warp
+    // Chunks in flight per warp.  (Of two strips, two of them, for 16 warps; 12 warps have registers for three.  12
+    // warps for up to 8 rows, or bulk prefetches into L2 ahead of the loads, are not faster.)
+    static constexpr int kDepth = (NT == 1 ? 4 : 6) / RS;
     static constexpr int kBatch = NT == 1 ? 32 : 8;             // units between two reductions over a cluster
     static constexpr int kSlots = SPLIT ? kBatch + kWarps : 2 * kWarps;     // parts of units
     static constexpr int kSlotBytes = RS * NT * 512;
@@ -466,7 +473,8 @@ template <int NT, int PER>
 cudaError_t pick(StreamArgs &a, int dev, int sms, cudaStream_t stream) {
     const bool mins = a.p.mins[0] != nullptr;
     if (a.p.mats == 2) return mins ? launch<NT, 2, PER, true, true, false>(a, dev, sms, stream) : launch<NT, 2, PER, false, true, false>(a, dev, sms, stream);
-    // a strip per unit where pairs are too few to come out even
+    // a strip per unit where pairs are too few to come out even (one row: 5120 x 5120 6.3 us, with pairs 8.1; 131072 x
+    // 5120 67, with pairs 64)
     if constexpr (NT == 1)
         if (q4_strips(a.p.n) < 8 * sms)
             return mins ? launch<1, 1, PER, true, false, false>(a, dev, sms, stream) : launch<1, 1, PER, false, false, false>(a, dev, sms, stream);

@@ -11,13 +11,18 @@
 // Why the weights are A: an MMA with A in tensor memory takes 128 cycles for K = 16 at any N up to 224, and shared
 // memory then carries x alone.  With the weights as B, in shared memory, an MMA brings 256 weight rows to 128
 // rows of x in 182 cycles, but the decoded weights' stores (512 cycles per 128 values of k), the MMAs' reads (768) and
-// the copies of x (256) share one 128-byte port: 3000 cycles per 256 rows and 128 values were measured,
-// 1024 per 128 rows here.
+// the copies of x (256) share one 128-byte port: 3000 cycles per 256 rows and 128 values were measured, 1500 for
+// 128 rows; here it is 1300, 1024 of them MMAs.
 //
 // Groups of 32 or 64 and many rows: a fold per group would take longer than the MMAs (an accumulator's hand-over
 // and 192 columns: 990 cycles per group of 32, whose MMAs take 256).  There the scale goes into the weights, exactly:
 // an fp16 scale is the sum of two bf16 of five bits, and five bits times c - 8 is exact in bf16, so two MMAs
 // instead of one bring s (c - 8) x, and the fold adds up one accumulator per 128 values of k; minima stay with it.
+//
+// What bounds it (gate and up 17408 x 5120, 512 rows): group 128 188 us, 970 TFLOP/s: the MMAs' 128 cycles, whatever
+// N is, and 176 of 192 columns in use (512 = 3 x 176 - 16).  Groups of 32 298 us: the same MMAs twice.  With
+// minima 262 and 508: the fold reads every group's sums of x from shared memory, 64 of them in every lane, at 128
+// bytes per cycle.  Up to 64 rows: the MMAs too (131072 x 5120 by 32 rows 188 us at group 128, 215 at 32).
 //
 // Few tiles are split along k over the CTAs of a cluster, which add up their parts through shared memory.
 //

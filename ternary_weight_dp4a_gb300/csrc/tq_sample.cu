@@ -272,7 +272,8 @@ struct Deal {
 };
 constexpr size_t kMostShared = 200 * 1024;      // dynamic
 
-template <bool BF16>
+// AGAIN: one CTA has the row and reads it again in every pass.
+template <bool BF16, bool AGAIN>
 struct Row {
     const void *logits;
     const float *held;                          // this CTA's part in shared memory, or nullptr
@@ -327,14 +328,18 @@ struct Row {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const int end = (warp + 1) * deal.len;
         int o = warp * deal.len + 4 * lane;
-        // One CTA per row reads it again with a load a vector ahead of its use (256 rows of 131072, top-p 225 us to
-        // 204).  Parts of a row that are read again come from L2, and gain nothing (64 rows 67, 73).
+        // One CTA loads a vector ahead of its use (256 rows of 131072, top-p 225 us to 204).  Parts of a row that are
+        // read again come from L2, and gain nothing (64 rows 67, 73).
         Bits next{};
-        const bool ahead = held == nullptr && cluster == 1;
-        if (ahead && whole(o)) next = bits(o);
+        if (AGAIN && whole(o)) next = bits(o);
         for (; o < end; o += 128) {
-            const float4 v = held != nullptr ? *reinterpret_cast<const float4 *>(held + o) : ahead && whole(o) ? values(next) : fetch(o);
-            if (ahead && o + 128 < end && whole(o + 128)) next = bits(o + 128);
+            float4 v;
+            if constexpr (AGAIN) {
+                v = whole(o) ? values(next) : fetch(o);
+                if (o + 128 < end && whole(o + 128)) next = bits(o + 128);
+            } else {
+                v = held != nullptr ? *reinterpret_cast<const float4 *>(held + o) : fetch(o);
+            }
             const float l[4] = {v.x, v.y, v.z, v.w};
             visit(l, index(o));
         }
@@ -549,7 +554,7 @@ __device__ __forceinline__ u64 draw_target(float u, u64 sum) {
     return min(scaled(u, sum, false), sum - 1);
 }
 
-template <bool BF16>
+template <bool BF16, bool AGAIN>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t dynamic[];
     __shared__ Shared sm;
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const void *logits = static_cast<const uint8_t *>(a.logits) + static_cast<int64_t>(row) * a.vocab * (BF16 ? 2 : 4);
     const Deal deal(logits, BF16 ? 2 : 4, a.vocab, a.cluster);
     u64 *local = reinterpret_cast<u64 *>(dynamic);
-    Row<BF16> v{logits, nullptr, local, deal, deal.segment(rank, warp), rank, a.cluster, sm};
+    Row<BF16, AGAIN> v{logits, nullptr, local, deal, deal.segment(rank, warp), rank, a.cluster, sm};
     const float t = a.temperature != nullptr ? a.temperature[row] : 1.0f;
     const int k = a.top_k != nullptr ? a.top_k[row] : 0;
     const float p = a.top_p != nullptr ? a.top_p[row] : 1.0f, floor = a.min_p != nullptr ? a.min_p[row] : 0.0f;
@@ -921,11 +926,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
 }
 
+template <bool BF16, bool AGAIN>
+cudaError_t sample_launch(const SampleArgs &a, size_t smem, cudaStream_t stream) {
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(sample_kernel<BF16, AGAIN>, kMostShared);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.m) * a.cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, AGAIN>, a);
+}
+
 template <bool BF16>
 cudaError_t sample_launch(SampleArgs a, int sms, cudaStream_t stream) {
-    static SmemLimit limit;
-    cudaError_t e = limit.raise(sample_kernel<BF16>, kMostShared);
-    if (e != cudaSuccess) return e;
     // CTAs per row: as many as run at once, two to an SM (one, where parts get below 4096 entries), and
     // up to eight.  1, 2, 4 and 8 of them, top-p (us): 131072 entries, 16 rows 137 91 56 51, 64 rows 146 113 83 91, 128 rows
     // 199 149 154 169, 256 rows 256 232 244 295; 32003 entries, 16 rows 34 26 21 23, 64 rows 35 35 28 46, 256 rows 59 70 88 153;
@@ -941,20 +964,8 @@ cudaError_t sample_launch(SampleArgs a, int sms, cudaStream_t stream) {
     // L2 (131072 entries, top-k, four CTAs per row: 16 rows 20 kept, 24 not; 64 rows 38 kept, 29 not).
     const int per_sm = static_cast<int64_t>(a.m) * a.cluster > sms ? 2 : 1;
     a.resident = (held + local) * per_sm <= kMostShared;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.m) * a.cluster);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = local + max(a.resident ? held : 0, kList * sizeof(u64));
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<BF16>, a);
+    const size_t smem = local + max(a.resident ? held : 0, kList * sizeof(u64));
+    return a.cluster == 1 && !a.resident ? sample_launch<BF16, true>(a, smem, stream) : sample_launch<BF16, false>(a, smem, stream);
 }
 
 cudaError_t sample_launch(const SampleArgs &a, bool bf16, cudaStream_t stream) {
