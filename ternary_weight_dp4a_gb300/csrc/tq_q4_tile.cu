@@ -19,8 +19,8 @@
 // an fp16 scale is the sum of two bf16 of five bits, and five bits times c - 8 is exact in bf16, so two MMAs
 // instead of one bring s (c - 8) x, and the fold adds up one accumulator per 128 values of k; minima stay with it.
 //
-// What bounds it (gate and up 17408 x 5120, 512 rows): group 128 188 us, 970 TFLOP/s: the MMAs' 128 cycles, whatever
-// N is, and 176 of 192 columns in use (512 = 3 x 176 - 16).  Groups of 32 298 us: the same MMAs twice.  With
+// What bounds it (gate and up 17408 x 5120, 512 rows): group 128 187 us, 976 TFLOP/s: the MMAs' 128 cycles, whatever
+// N is, with 176 columns (512 rows are three tiles of 171).  Groups of 32 295 us: the same MMAs twice.  With
 // minima 262 and 508: the fold reads every group's sums of x from shared memory, 64 of them in every lane, at 128
 // bytes per cycle.  Up to 64 rows: the MMAs too (131072 x 5120 by 32 rows 188 us at group 128, 215 at 32).
 //
@@ -77,6 +77,7 @@ struct TileArgs {
     int64_t sums_ld;
     int row_tiles, rows;                        // rows of x per tile
     int split;                                  // CTAs along k
+    int first;                                  // tile of this launch
 };
 
 constexpr uint32_t idesc_bf16(int m, int n) {
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int chunks = p.k >> 7;
-    const int rank = blockIdx.x % args.split, tile = blockIdx.x / args.split;
+    const int rank = blockIdx.x % args.split, tile = args.first + blockIdx.x / args.split;
     const int row0 = tile % args.row_tiles * args.rows, ntile = tile / args.row_tiles;
     const int rows = min(args.rows, p.m - row0), cols = (rows + 15) / 16 * 16;      // (args.rows: a multiple of 16)
     const int chunk0 = rank * chunks / args.split, chunk1 = (rank + 1) * chunks / args.split;
@@ -748,31 +749,44 @@ cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     static SmemLimit limit;
     cudaError_t e = limit.raise(q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (q4_strips(a.p.n) + (GATEUP ? 3 : 7)) / (GATEUP ? 4 : 8) * a.row_tiles;
+    const int tiles = static_cast<int>((q4_strips(a.p.n) + (GATEUP ? 3 : 7)) / (GATEUP ? 4 : 8) * a.row_tiles);
     const int chunks = a.p.k / 128;
-    // CTAs along k: as many as run at once with at least two chunks each
+    // `count` tiles from a.first on, each split along k over as many CTAs as run at once with at least two chunks each.
     static ClusterLimit cluster_limit;
-    a.split = 1;
-    for (int more = 2; more <= 8 && tiles * more <= sms && chunks >= 2 * more; ++more) {
-        int most = 0;
-        e = cluster_limit.most(q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, dev, more, kThreads, smem, sms, &most);
+    auto some = [&](int count) {
+        a.split = 1;
+        for (int more = 2; more <= 8 && count * more <= sms && chunks >= 2 * more; ++more) {
+            int most = 0;
+            const cudaError_t e = cluster_limit.most(q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, dev, more, kThreads, smem, sms, &most);
+            if (e != cudaSuccess) return e;
+            if (count <= most) a.split = more;
+        }
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(count) * a.split);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = a.split;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = a.split > 1 ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, a);
+    };
+    // A last round of up to half the SMs' tiles is a launch of its own, split along k; it waits for the rounds before.
+    // (us, one launch and two: gate/up of 64 rows, 160 tiles, 5120 51 37, 2048 32 26, 1024 25 21; 32 x 20480 x 1024
+    // group 128 with minima 25 22; 64 x 28672 x 4096, 224 tiles 46 40; gate/up of 512 rows, 816 tiles, 5120 190 187.)
+    const int rest = tiles % sms;
+    if (tiles > sms && rest > 0 && 2 * rest <= sms && chunks >= 8) {
+        e = some(tiles - rest);
         if (e != cudaSuccess) return e;
-        if (tiles <= most) a.split = more;
+        a.first = tiles - rest;
+        return some(rest);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, a);
+    return some(tiles);
 }
 
 template <int GROUP, bool MINS, bool GATEUP>

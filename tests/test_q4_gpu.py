@@ -110,6 +110,24 @@ def test_many_rows(tq, m):
     assert torch.equal(tq.q4_gemv(w.dev, x), tq.q4_gemv(w.dev, x))          # the same every time
 
 
+@pytest.mark.parametrize("n,k,group,mins", [(20_001, 1024, 64, True), (19_500, 2048, 32, False), (28_700, 1152, 128, True), (19_456, 1024, 32, True)])
+def test_more_tiles_than_run_at_once(tq, n, k, group, mins):
+    """The last round's tiles are split along k; sizes with 5, 1, 73 and no tiles in it."""
+    w = Matrix(tq, n, k, group, mins, 7)
+    for m in (17, 100):
+        x = _x(m, k, m)
+        want, tol = w.product(x)
+        _check(tq.q4_gemv(w.dev, x), want, tol)
+    half = n // 2
+    gate, up = Matrix(tq, half, k, group, mins, 8), Matrix(tq, half, k, group, mins, 9)
+    x = _x(40, k, 3)
+    g, tg = gate.product(x)
+    u, tu = up.product(x)
+    s = g * g.sigmoid()
+    tol = 1.1 * tg * (u.abs() + tu) + s.abs() * tu + 2.0 ** -20 * (s * u).abs()     # as test_gateup
+    _check(tq.q4_gateup(gate.dev, up.dev, x), s * u, tol + 2.0 ** -8 * ((s * u).abs() + tol) + 1e-37)
+
+
 def test_packed_layout(tq):
     """include/tq_q4.h's formulas, value by value."""
     n, k, group = 21, 256, 64
