@@ -39,7 +39,7 @@ extern "C" {
  *   top_p fp32: >= 1 or NaN: all; <= 0: the first
  *   min_p fp32: <= 0 or NaN: all; > 1 counts as 1
  * uniform: fp32 [m], in [0, 1); NaN or below 0 counts as 0, and from 1 on the last
- * index that stayed is drawn.
+ * index that stayed with a weight above 0 is drawn (below 2^-43 it rounds to 0).
  * Weights are whole multiples of 2^-42 with a relative error of about 2^-30, and
  * sums of them are exact: the result does not depend on how a row is split over
  * threads, and differs from that of real arithmetic only where a sum comes
