@@ -53,8 +53,11 @@ constexpr uint32_t kTmemA = 2 * kCols;
 constexpr int kAhead = 16;                      // chunks of codes in L2 ahead of the decode
 constexpr int kPartLd = 128 + 4;                // floats per row of x of a part
 
-// register shares (launched with 80 per thread): 128 x (2 x 56 + 32 + 3 x 112) = 768 x 80
-constexpr int kRegsDecode = 56, kRegsIssue = 32, kRegsFold = 112;
+// register shares (launched with 80 per thread): 128 x (2 x 56 + 32 + 3 x 112) = 768 x 80; with scaled weights and no
+// minima 2 x 72 + 32 + 3 x 96, less (512 rows, group 32 254 us, with the shares of the others 292)
+constexpr int kRegsIssue = 32;
+constexpr int regs_decode(bool scaled, bool mins) { return scaled && !mins ? 72 : 56; }
+constexpr int regs_fold(bool scaled, bool mins) { return scaled && !mins ? 96 : 112; }
 
 __device__ unsigned lost_waits;                 // bits of all waits that have run out on this device
 
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
 
     if (SCALED && warp < kDecodeWarps) {
         // ---- decode with scales: 32 values' two parts a buffer, two buffers of every chunk for either four warps ----
-        regs_down<kRegsDecode>();
+        regs_down<regs_decode(SCALED, MINS)>();
         const int second = warp >> 2;                               // half of the chunk
         const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64 + second * 8;
         const uint16_t *ssrc = p.scales[mat] + (block0 * 8 + (lane & 7)) * (2 * kPer) + ((lane >> 3) & 1) * kPer;
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         }
     } else if (warp < kDecodeWarps) {
         // ---- decode: a lane's 128 codes of a chunk are 64 bytes, two halves of them one buffer each ----
-        regs_down<kRegsDecode>();
+        regs_down<regs_decode(SCALED, MINS)>();
         const int odd = warp >> 2;                                  // which chunks
         const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64;
         const uint32_t a_at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemA + odd * 64;
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         __syncwarp();
     } else {
         // ---- fold: a lane is a weight row, a warp has a third of the rows of x ----
-        regs_up<kRegsFold>();
+        regs_up<regs_fold(SCALED, MINS)>();
         const int third = (warp - kFirstFold) / 4, team = teams > 1 ? third : 0;
         const int col0 = teams > 1 ? 0 : third * kFoldCols, mine = min(max(cols - col0, 0), kFoldCols);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
