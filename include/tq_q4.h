@@ -67,7 +67,7 @@ tq_status tq_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint16_
                      uint16_t *packed_mins, tq_stream_t stream);
 
 /* Bytes of the workspace that a product of m rows with a matrix that has minima
- * takes (the sums of x over the groups); 0 where none is needed, up to 16 rows,
+ * takes (the sums of x over the groups, or their parts); 0 where none is needed, up to 16 rows,
  * and for sizes out of range.  256-byte aligned, any contents, reusable after every
  * call, not shared by calls that may overlap.  Matrices without minima need none. */
 size_t tq_q4_workspace_bytes(int32_t m, int32_t k, int32_t group);
@@ -77,7 +77,8 @@ size_t tq_q4_workspace_bytes(int32_t m, int32_t k, int32_t group);
  * (c - 8) * x over exact products is taken in fp32 by matrix instructions, and
  * folded in fp32 as s * sum, plus (8 s - b) * (sum of x) where there are minima;
  * calls of many rows with groups of 32 or 64 have s in the matrix instructions too,
- * exactly, as the sum of two bf16.  An infinity or NaN in a row of x, or in a scale
+ * exactly, as the sum of two bf16, and (8 s - b) * (sum of x) as products of bf16
+ * parts, to 2^-24.  An infinity or NaN in a row of x, or in a scale
  * or minimum, makes results that depend on it infinite or NaN, and no others.
  * In calls of up to 8 rows (a packed decode step) each row has the bits that it
  * has alone; with more rows the order of the sums may differ.
@@ -103,7 +104,8 @@ tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const u
  *   bit 1  the matrix instructions waited for x    bit 2  for decoded weights
  *   bit 3  for a free accumulator                  bit 4  at exit
  *   bit 6  the copies of x in flight at exit
- *   bit 7  the fold waited for the sums of x        bit 8  for an accumulator
+ *   bit 7  the fold, or the matrix instructions, waited for the sums of x
+ *   bit 8  the fold waited for an accumulator
  *   bit 9  the copies of the sums waited for a free place */
 tq_status tq_q4_read_error_word(uint32_t *value, tq_stream_t stream);
 

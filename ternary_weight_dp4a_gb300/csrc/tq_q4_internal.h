@@ -34,9 +34,31 @@ cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const u
 // 188 179, group 32 with minima 271 262: the large ones of small groups lose 5%.)
 constexpr int kQ4StreamRows = 16;
 
-// Workspace of the tile kernel, where there are minima: sums of x over the groups, [k / group][q4_sums_ld(m)].
+// Rows of x of a tile, a multiple of 16: even shares of `most` at most.
+constexpr int kQ4TileCols = 192, kQ4ScaledCols = 176;       // (with scaled weights and minima)
+constexpr int q4_tile_rows(int m, int most) {
+    const int tiles = (m + most - 1) / most;
+    return ((m + tiles - 1) / tiles + 15) / 16 * 16;
+}
+
+// Whether the tile kernel has the scales in the weights.  That costs twice the MMAs, whatever the rows; folds of small
+// groups cost by the column, and with minima more.  (us, folded and scaled.  131072 x 5120: group 32 64 rows 259 296, 80
+// rows 415 274, 192 rows 644 326; with minima 32 rows 297 294, 48 rows 401 308, 160 rows 888 331; group 64 96 rows 255
+// 273, 112 rows 320 275; with minima 64 rows 284 306, 80 rows 385 289, 160 rows 517 316, 192 rows, which are
+// two tiles then, 550 576.  Gate/up 2 x 17408 x 5120, 512 rows: group 32 559 257, with minima 693 283; group 64 326 254,
+// with minima 414 284.)
+constexpr bool q4_scaled(int m, int group, bool mins) {
+    const int rows = q4_tile_rows(m, kQ4TileCols);
+    return group == 32 ? rows > (mins ? 32 : 64) : group == 64 && rows > (mins ? 64 : 96);
+}
+
+// Workspace of the tile kernel, where there are minima: sums of x over the groups, [k / group][q4_sums_ld(m)], or
+// with scaled weights their parts, 32 bf16 for every row and 128 values.
 constexpr int64_t q4_sums_ld(int64_t m) { return (m + 15) / 16 * 16; }
-constexpr size_t q4_sums_bytes(int64_t m, int64_t k, int64_t group) { return static_cast<size_t>(q4_sums_ld(m) * (k / group) * 4); }
+constexpr size_t q4_sums_bytes(int64_t m, int64_t k, int64_t group) {
+    return static_cast<size_t>(q4_scaled(static_cast<int>(m), static_cast<int>(group), true) ? m * (k / 128) * 64
+                                                                                            : q4_sums_ld(m) * (k / group) * 4);
+}
 
 // Up to kQ4StreamRows rows, and any number.
 cudaError_t q4_stream_launch(const Q4Product &p, cudaStream_t stream);

@@ -17,12 +17,15 @@
 // Groups of 32 or 64 and many rows: a fold per group would take longer than the MMAs (an accumulator's hand-over
 // and 192 columns: 990 cycles per group of 32, whose MMAs take 256).  There the scale goes into the weights, exactly:
 // an fp16 scale is the sum of two bf16 of five bits, and five bits times c - 8 is exact in bf16, so two MMAs
-// instead of one bring s (c - 8) x, and the fold adds up one accumulator per 128 values of k; minima stay with it.
+// instead of one bring s (c - 8) x, and the fold adds up one accumulator per 128 values of k.  Minima are then a product
+// of their own in the tensor core: (8 s - b) (sum of x) of the chunk's groups, both factors in three bf16 and six
+// of the nine products, 6 values of k per group in one or two MMAs more.
 //
 // What bounds it (gate and up 17408 x 5120, 512 rows): group 128 187 us, 976 TFLOP/s: the MMAs' 128 cycles, whatever
-// N is, with 176 columns (512 rows are three tiles of 171).  Groups of 32 295 us: the same MMAs twice.  With
-// minima 262 and 508: the fold reads every group's sums of x from shared memory, 64 of them in every lane, at 128
-// bytes per cycle.  Up to 64 rows: the MMAs too (131072 x 5120 by 32 rows 188 us at group 128, 215 at 32).
+// N is, with 176 columns (512 rows are three tiles of 171).  Groups of 32 254 us: the same MMAs twice, 96% of
+// the time; with minima 281, two more of 18.  Group 128 with minima 262: the fold reads every group's sums of x
+// from shared memory, 64 of them in every lane, at 128 bytes per cycle.  Up to 64 rows: the MMAs too (131072 x 5120
+// by 32 rows 188 us at group 128, 215 at 32).
 //
 // Few tiles are split along k over the CTAs of a cluster, which add up their parts through shared memory.
 //
@@ -39,7 +42,7 @@
 namespace tq {
 namespace {
 
-constexpr int kCols = 192;                      // most rows of x per tile
+constexpr int kCols = kQ4TileCols;              // most rows of x per tile
 constexpr int kABufs = 4;                       // of decoded weights: 64 values of k, 32 columns of tensor memory each
 constexpr int kStages = 4;                      // of x in shared memory: 128 values each, in two halves
 constexpr int kMaxSets = 3;                     // of accumulators
@@ -50,14 +53,13 @@ constexpr int kFirstFold = kDecodeWarps + 4;
 constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
 constexpr uint32_t kHalfBytes = kCols * 128;     // of a stage: 64 values
 constexpr uint32_t kTmemA = 2 * kCols;
+constexpr uint32_t kTmemMins = kQ4ScaledCols;   // 16 columns behind either accumulator's, where scaled weights have minima
 constexpr int kAhead = 16;                      // chunks of codes in L2 ahead of the decode
 constexpr int kPartLd = 128 + 4;                // floats per row of x of a part
 
-// register shares (launched with 80 per thread): 128 x (2 x 56 + 32 + 3 x 112) = 768 x 80; with scaled weights and no
-// minima 2 x 72 + 32 + 3 x 96, less (512 rows, group 32 254 us, with the shares of the others 292)
-constexpr int kRegsIssue = 32;
-constexpr int regs_decode(bool scaled, bool mins) { return scaled && !mins ? 72 : 56; }
-constexpr int regs_fold(bool scaled, bool mins) { return scaled && !mins ? 96 : 112; }
+// Register shares (launched with 80 per thread): 128 x (2 x 56 + 32 + 3 x 112) = 768 x 80; with scaled weights 2 x 72
+// + 32 + 3 x 96, less (512 rows, group 32 254 us, with the others' shares 292).
+constexpr int kRegsDecode = 56, kRegsIssue = 32, kRegsFold = 112, kRegsScaledDecode = 72, kRegsScaledFold = 96;
 
 __device__ unsigned lost_waits;                 // bits of all waits that have run out on this device
 
@@ -66,9 +68,12 @@ struct __align__(1024) TileSmem {
         uint8_t x[kStages][2][kHalfBytes];
         float part[kCols][kPartLd];             // this CTA's sums, when a tile is split along k
     };
-    float sums[kMaxSets][4][kCols];             // of x over a set's groups
+    union {
+        float sums[kMaxSets][4][kCols];         // of x over a set's groups
+        uint8_t parts[2][kCols * 64];           // or, with scaled weights, their parts: a chunk's 32 per row
+    };
     uint64_t x_full[kStages], x_empty[kStages], a_full[kABufs], a_empty[kABufs], d_full[kMaxSets], d_empty[kMaxSets];
-    uint64_t s_full[kMaxSets], s_empty[kMaxSets], drain;
+    uint64_t s_full[kMaxSets], s_empty[kMaxSets], p_full[2], p_empty[2], m_full[2], drain;
     uint32_t tmem;
     uint32_t dead;                              // a bounded wait ran out
 };
@@ -76,6 +81,7 @@ struct __align__(1024) TileSmem {
 struct TileArgs {
     Q4Product p;
     CUtensorMap x;                              // [m][k] bf16, boxes of a tile's rows x 64 values
+    CUtensorMap parts;                          // [m][k / 128 * 32] bf16, boxes of a tile's rows x 32
     const float *sums;                          // [k / group][sums_ld]: sums of x over the groups, where there are minima
     int64_t sums_ld;
     int row_tiles, rows;                        // rows of x per tile
@@ -117,6 +123,16 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
     d |= static_cast<uint64_t>(1024 >> 4) << 32;
     d |= 1ull << 46;
     d |= 2ull << 61;
+    return d;
+}
+
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr) {
+    // the same with rows of 64 bytes: atoms of 512
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
+    d |= 1ull << 16;
+    d |= static_cast<uint64_t>(512 >> 4) << 32;
+    d |= 1ull << 46;
+    d |= 4ull << 61;
     return d;
 }
 
@@ -263,6 +279,32 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// The sum of x over a group and 8 s - b, each as three bf16 (24 bits), and six of their products: all but 2^-25 of
+// the whole one.
+__device__ __forceinline__ void split_parts(float v, uint32_t (&p)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        p[i] = f32_to_bf16_bits(v);
+        v -= __uint_as_float(p[i] << 16);
+    }
+}
+// Of the weights: 1 1, 2 1, 2 3.
+__device__ __forceinline__ void weight_parts(float v, uint32_t (&w)[3]) {
+    uint32_t p[3];
+    split_parts(v, p);
+    w[0] = p[0] | p[0] << 16;
+    w[1] = p[1] | p[0] << 16;
+    w[2] = p[1] | p[2] << 16;
+}
+// Of x: 1 2, 1 3, 2 1.
+__device__ __forceinline__ void sum_parts(float v, uint32_t (&w)[3]) {
+    uint32_t p[3];
+    split_parts(v, p);
+    w[0] = p[0] | p[1] << 16;
+    w[1] = p[0] | p[2] << 16;
+    w[2] = p[1] | p[0] << 16;
+}
+
 template <int GROUP, bool MINS, bool GATEUP, bool SCALED>
 __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_constant__ TileArgs args) {
     extern __shared__ uint8_t smem_raw[];
@@ -282,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     // hand-over costs some 300 cycles on either side.  Up to 64 rows of x there are three sets of 128
     // columns, each folded by a third of the warps; else two of 192, all warps having a third of the columns.
     const int dcols = (cols + 31) / 32 * 32, teams = cols <= kFoldCols ? 3 : 1;
-    const int sets = teams == 3 ? 3 : 2, set_cols = 2 * kCols / sets;
+    const int sets = teams == 3 ? 3 : 2, set_cols = SCALED && MINS && teams == 3 ? 96 : 2 * kCols / sets;
     const int per_set = SCALED || kPer * dcols <= set_cols ? kPer : kPer == 4 && 2 * dcols <= set_cols ? 2 : 1;
 
     if (warp == kDecodeWarps) {
@@ -303,6 +345,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             mbar_init(smem_u32(&sm.d_empty[i]), kFoldWarps / teams);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
             mbar_init(smem_u32(&sm.s_empty[i]), kFoldWarps / teams);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.p_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_empty[i]), 1);
+            mbar_init(smem_u32(&sm.m_full[i]), 4);
         }
         mbar_init(smem_u32(&sm.drain), 1);
         sm.dead = 0;
@@ -330,36 +377,48 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
 
     if (SCALED && warp < kDecodeWarps) {
         // ---- decode with scales: 32 values' two parts a buffer, two buffers of every chunk for either four warps ----
-        regs_down<regs_decode(SCALED, MINS)>();
+        regs_down<SCALED ? kRegsScaledDecode : kRegsDecode>();
         const int second = warp >> 2;                               // half of the chunk
         const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64 + second * 8;
         const uint16_t *ssrc = p.scales[mat] + (block0 * 8 + (lane & 7)) * (2 * kPer) + ((lane >> 3) & 1) * kPer;
-        const uint32_t a_at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemA + second * 64;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16), a_at = lanes + kTmemA + second * 64;
         const uint32_t empty = smem_u32(sm.a_empty) + second * 16, a_full = smem_u32(sm.a_full) + second * 16;
         uint32_t mask = 0x000f000fu, base = 0x43004300u;
         asm volatile("" : "+r"(mask), "+r"(base));
+        const uint16_t *msrc = MINS ? p.mins[mat] + (ssrc - p.scales[mat]) : nullptr;
+        constexpr int kWords = (kPer + 1) / 2;
         uint2 code[4];
-        uint32_t sc[(kPer + 1) / 2];
+        uint32_t sc[kWords], mn[kWords], sc_next[kWords], mn_next[kWords];
         auto load = [&](int c) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 asm volatile("ld.global.v2.u32 {%0,%1}, [%2];"
                              : "=r"(code[q].x), "=r"(code[q].y)
                              : "l"(src + static_cast<int64_t>(c) * kQ4ChunkBytes + q * 16));
-            load_scales<kPer>(sc, ssrc + static_cast<int64_t>(c) * (16 * kPer));
+        };
+        auto load_row = [&](int c) {
+            load_scales<kPer>(sc_next, ssrc + static_cast<int64_t>(c) * (16 * kPer));
+            if (MINS) load_scales<kPer>(mn_next, msrc + static_cast<int64_t>(c) * (16 * kPer));
         };
         load(0);
+        load_row(0);
         bool ok = true;
         uint32_t turn = 1;
         for (int c = 0; c < total && ok; ++c, turn ^= 1) {
             if (second == 0 && c % 4 == 0) ask(c + kAhead, c + kAhead + 4);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                sc[i] = sc_next[i];
+                if (MINS) mn[i] = mn_next[i];
+            }
+            if (c + 1 < total) load_row(c + 1);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 ok = warp_wait<32>(sm, empty + 8 * g, turn, 1u << 0);
                 if (!ok) break;
                 tc_fence_after();
                 // (group 64: one scale of the pair for each half of the chunk; 32: one of its half's pair for each buffer)
-                const uint32_t two = kPer == 4 && second ? sc[(kPer - 1) / 2] : sc[0];
+                const uint32_t two = kPer == 4 && second ? sc[kWords - 1] : sc[0];
                 uint32_t hi, lo;
                 split_scale(f16_bits_to_f32(static_cast<uint16_t>((kPer == 4 ? g : second) ? two >> 16 : two & 0xffffu)), hi, lo);
 #pragma unroll
@@ -378,10 +437,35 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(a_full + 8 * g);
             }
+            if constexpr (MINS) {
+                // the minima: every other chunk's for either four warps
+                if (!ok) break;
+                if (second == (c & 1)) {
+                    ok = warp_wait<32>(sm, smem_u32(&sm.p_empty[second]), (c >> 1 & 1) ^ 1, 1u << 0);
+                    if (!ok) break;
+                    uint32_t extra[16];
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) {
+                        uint32_t w[3];
+                        weight_parts(__fmaf_rn(8.0f, scale_at(sc, e), -scale_at(mn, e)), w);
+                        extra[3 * e] = w[0];
+                        extra[3 * e + 1] = w[1];
+                        extra[3 * e + 2] = w[2];
+                    }
+#pragma unroll
+                    for (int i = 3 * kPer; i < 16; ++i) extra[i] = 0;
+                    tc_fence_after();
+                    st_16(lanes + kTmemMins + second * kCols, extra);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.m_full[second]));
+                }
+            }
         }
     } else if (warp < kDecodeWarps) {
         // ---- decode: a lane's 128 codes of a chunk are 64 bytes, two halves of them one buffer each ----
-        regs_down<regs_decode(SCALED, MINS)>();
+        regs_down<SCALED ? kRegsScaledDecode : kRegsDecode>();
         const int odd = warp >> 2;                                  // which chunks
         const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64;
         const uint32_t a_at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemA + odd * 64;
@@ -440,6 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             uint64_t x_set = x_desc;
             bool ok = true;
             if constexpr (SCALED) {
+                const uint32_t p_full = smem_u32(sm.p_full), p_empty = smem_u32(sm.p_empty), m_full = smem_u32(sm.m_full);
+                const uint64_t p_desc = desc_sw64(smem_u32(sm.parts));
                 for (int c = 0; c < total && ok; ++c, turn ^= 1) {
                     ok = wait_alive(sm, x_full + 8 * x_at, x_turn, 1u << 1) && wait_alive(sm, d_empty + 8 * set, d_turn, 1u << 3);
 #pragma unroll
@@ -454,6 +540,17 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                         commit_if(issue, a_empty + 8 * ring);
                     }
                     if (!ok) break;
+                    if constexpr (MINS) {
+                        // the minima: 6 values per group, 24 or 12 of 32
+                        const uint32_t at = c & 1, phase = c >> 1 & 1;
+                        ok = wait_alive(sm, p_full + 8 * at, phase, 1u << 7) && wait_alive(sm, m_full + 8 * at, phase, 1u << 2);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < kPer / 2; ++i)
+                            mma_bf16_ts(issue, d_set, kTmemMins + at * kCols + 8 * i, p_desc + (at * (kCols * 64 >> 4) + 2 * i), idesc, 1);
+                        commit_if(issue, p_empty + 8 * at);
+                    }
                     commit_if(issue, d_full + 8 * set);
                     d_set += set_cols;
                     if (++set == sets) {
@@ -533,8 +630,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             }
             __syncwarp();
         } else if (warp == kDecodeWarps + 2 && MINS) {
-            // ---- copies of the sums ----
-            if (lane == 0) {
+            // ---- copies of the sums, or of their parts ----
+            if (SCALED && lane == 0) {
+                int c = 0;
+                for (; c < total; ++c) {
+                    if (!wait_alive<64>(sm, smem_u32(&sm.p_empty[c & 1]), (c >> 1 & 1) ^ 1, 1u << 9)) break;
+                    const uint32_t bar = smem_u32(&sm.p_full[c & 1]);
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(args.rows) * 64);
+                    load_box(smem_u32(sm.parts[c & 1]), &args.parts, (chunk0 + c) * 32, row0, bar);
+                }
+                for (int j = max(c - 2, 0); j < c; ++j)
+                    if (!mbar_wait(smem_u32(&sm.p_full[j & 1]), j >> 1 & 1)) atomicOr(&lost_waits, 1u << 6);
+            } else if (lane == 0) {
                 const float *src = args.sums + static_cast<int64_t>(chunk0) * kPer * args.sums_ld + row0;
                 int set = 0, turn = 1, g = 0;
                 for (; g < total * kPer; g += per_set) {
@@ -556,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         __syncwarp();
     } else {
         // ---- fold: a lane is a weight row, a warp has a third of the rows of x ----
-        regs_up<regs_fold(SCALED, MINS)>();
+        regs_up<SCALED ? kRegsScaledFold : kRegsFold>();
         const int third = (warp - kFirstFold) / 4, team = teams > 1 ? third : 0;
         const int col0 = teams > 1 ? 0 : third * kFoldCols, mine = min(max(cols - col0, 0), kFoldCols);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
@@ -571,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         const uint32_t d_full = smem_u32(sm.d_full), d_empty = smem_u32(sm.d_empty);
         const uint32_t s_full = smem_u32(sm.s_full), s_empty = smem_u32(sm.s_empty);
         auto ahead = [&](int i) {                                   // the scales of set i's chunk
-            if (i >= all) return;
+            if (SCALED || i >= all) return;
             const int64_t at = static_cast<int64_t>(i >> shift) * (16 * kPer);
             load_scales<kPer>(next, ssrc + at);
             if (MINS) load_scales<kPer>(mnext, msrc + at);
@@ -586,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 if (MINS) mn[j] = mnext[j];
             }
             ahead(i + teams);
-            const bool sums_lane = MINS && (lane & 1);              // both waits at once
+            const bool sums_lane = MINS && !SCALED && (lane & 1);              // both waits at once
             if (!warp_wait<20>(sm, (sums_lane ? s_full : d_full) + 8 * set, turn, sums_lane ? 1u << 7 : 1u << 8)) break;
             tc_fence_after();
             if (SCALED) {
@@ -602,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                 }
             }
 #pragma unroll 1
-            for (int in = 0; in < (SCALED && !MINS ? 0 : per_set); ++in) {
+            for (int in = 0; in < (SCALED ? 0 : per_set); ++in) {
                 const int e = (i & ((1 << shift) - 1)) * per_set + in;
                 const float s = scale_at(sc, e);
                 const uint64_t s2 = pack2(s, s);
@@ -614,12 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
 #pragma unroll
                 for (int q = 0; q < kFoldCols / 16; ++q) {
                     if (16 * q >= mine) break;
-                    if (!SCALED) {
-                        uint64_t x[8];
-                        ld_16(d + 16 * q, x);
+                    uint64_t x[8];
+                    ld_16(d + 16 * q, x);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[8 * q + j] = fma2(x[j], s2, acc[8 * q + j]);
-                    }
+                    for (int j = 0; j < 8; ++j) acc[8 * q + j] = fma2(x[j], s2, acc[8 * q + j]);
                     if (MINS) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -635,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(d_empty + 8 * set);
-                if (MINS) mbar_arrive(s_empty + 8 * set);
+                if (MINS && !SCALED) mbar_arrive(s_empty + 8 * set);
             }
             if (teams == 3) {                                       // (set i % 3 is the team's own)
                 turn ^= 1;
@@ -725,8 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     if (warp == kDecodeWarps) tmem_dealloc(tmem, 512);
 }
 
-// Sums of x over the groups, [k / group][ld], a thread each (rows from m on: zero).
-__global__ void __launch_bounds__(256) q4_sums_kernel(const uint16_t *x, int m, int k, int group, int64_t ld, float *sums) {
+// Sums of x over the groups, a thread each: [k / group][ld] (rows from m on: zero), or with `parts` their six parts,
+// [m][k / 128][32] (behind the last: zero).
+__global__ void __launch_bounds__(256) q4_sums_kernel(const uint16_t *x, int m, int k, int group, int64_t ld, float *sums, uint32_t *parts) {
     pdl_launch_dependents();
     pdl_wait();
     const int per_row = k / group;
@@ -742,7 +848,17 @@ __global__ void __launch_bounds__(256) q4_sums_kernel(const uint16_t *x, int m, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) s += __uint_as_float(u[e] << 16) + __uint_as_float(u[e] & 0xffff0000u);
         }
-    sums[g * ld + row] = s;
+    if (parts == nullptr) {
+        sums[g * ld + row] = s;
+    } else if (row < m) {
+        const int per = 128 / group, e = g % per;
+        uint32_t w[3];
+        sum_parts(s, w);
+        uint32_t *out = parts + (row * (k / 128) + g / per) * 16;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) out[3 * e + i] = w[i];
+        for (int i = 3 * per + e; i < 16; i += per) out[i] = 0;
+    }
 }
 
 template <int GROUP, bool MINS, bool GATEUP, bool SCALED>
@@ -794,14 +910,8 @@ cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
 
 template <int GROUP, bool MINS, bool GATEUP>
 cudaError_t pick(TileArgs &a, int dev, int sms, cudaStream_t stream) {
-    // Scales in the weights cost twice the MMAs, whatever the rows; folds of small groups cost by the column, and with
-    // minima more.  (us, folded and scaled: 131072 x 5120, group 32 64 rows 260 376, 80 rows 415 359, 192 rows
-    // 646 379; with minima 32 rows 294 349, 64 rows 437 390, 192 rows 947 648; group 64 128 rows 328 333, 160 rows
-    // 341 342, 192 rows 358 352, with minima 64 rows 285 360, 80 rows 386 369, 192 rows 556 454; gate/up
-    // 2 x 17408 x 5120, 512 rows: 594 298, with minima 735 508; group 64 343 285, with minima 436 361.)
-    constexpr int kFolded = GROUP == 32 ? (MINS ? 48 : 64) : MINS ? 64 : 128;
     if constexpr (GROUP < 128)
-        if (a.rows > kFolded) return launch<GROUP, MINS, GATEUP, true>(a, dev, sms, stream);
+        if (q4_scaled(a.p.m, GROUP, MINS)) return launch<GROUP, MINS, GATEUP, true>(a, dev, sms, stream);
     return launch<GROUP, MINS, GATEUP, false>(a, dev, sms, stream);
 }
 
@@ -825,15 +935,19 @@ cudaError_t q4_tile_launch(const Q4Product &p, float *sums, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     TileArgs a{};
     a.p = p;
-    a.row_tiles = (p.m + kCols - 1) / kCols;
-    a.rows = ((p.m + a.row_tiles - 1) / a.row_tiles + 15) / 16 * 16;
+    const bool scaled = q4_scaled(p.m, p.group, p.mins[0] != nullptr);
+    a.rows = q4_tile_rows(p.m, scaled && p.mins[0] != nullptr ? kQ4ScaledCols : kCols);
     a.row_tiles = (p.m + a.rows - 1) / a.rows;
     if (p.mins[0] != nullptr) {
+        uint32_t *parts = scaled ? reinterpret_cast<uint32_t *>(sums) : nullptr;
         a.sums = sums;
         a.sums_ld = q4_sums_ld(p.m);
         const int64_t entries = a.sums_ld * (p.k / p.group);
         e = launch_pdl(q4_sums_kernel, dim3(static_cast<unsigned>((entries + 255) / 256)), dim3(256), 0, stream, p.x, p.m, p.k,
-                       p.group, a.sums_ld, sums);
+                       p.group, a.sums_ld, sums, parts);
+        if (e == cudaSuccess && parts != nullptr)
+            e = make_tmap_2d(&a.parts, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, parts, static_cast<uint64_t>(p.k) / 4, static_cast<uint64_t>(p.m),
+                             static_cast<uint64_t>(p.k) / 2, 32, static_cast<uint32_t>(a.rows), CU_TENSOR_MAP_SWIZZLE_64B);
         if (e != cudaSuccess) return e;
     }
     e = make_tmap_2d(&a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, static_cast<uint64_t>(p.k), static_cast<uint64_t>(p.m),
