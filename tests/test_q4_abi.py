@@ -240,3 +240,11 @@ def test_what_earlier_work_writes_is_not_read_as_read_only():
         seen += 1
         assert "__restrict__" not in text and "__ldg" not in text and ".nc" not in text, path
     assert seen == 5
+
+
+def test_workspace_of_the_most_rows_does_for_fewer(lib):
+    for group in (32, 64, 128):
+        sizes = [lib.tq_q4_workspace_bytes(m, 1024, group) for m in range(1, 1200)]
+        assert sizes == sorted(sizes) and sizes[15] == 0 and sizes[16] > 0
+    # parts of the sums: 32 bf16 for every row and 128 values; sums: fp32 for every group and 16 rows at a time
+    assert lib.tq_q4_workspace_bytes(512, 1024, 32) == 512 * 8 * 64 and lib.tq_q4_workspace_bytes(100, 1024, 128) == 112 * 8 * 4
