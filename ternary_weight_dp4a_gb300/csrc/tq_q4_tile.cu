@@ -12,7 +12,7 @@
 // memory then carries x alone.  With the weights as B, in shared memory, an MMA brings 256 weight rows to 128
 // rows of x in 182 cycles, but the decoded weights' stores (512 cycles per 128 values of k), the MMAs' reads (768) and
 // the copies of x (256) share one 128-byte port: 3000 cycles per 256 rows and 128 values were measured, 1500 for
-// 128 rows; here it is 1300, 1024 of them MMAs.
+// 128 rows; here it is 1200, 1024 of them MMAs.
 //
 // Groups of 32 or 64 and many rows: a fold per group would take longer than the MMAs (an accumulator's hand-over
 // and 192 columns: 990 cycles per group of 32, whose MMAs take 256).  There the scale goes into the weights, exactly:
@@ -21,11 +21,11 @@
 // of their own in the tensor core: (8 s - b) (sum of x) of the chunk's groups, both factors in three bf16 and six
 // of the nine products, 6 values of k per group in one or two MMAs more.
 //
-// What bounds it (gate and up 17408 x 5120, 512 rows): group 128 187 us, 976 TFLOP/s: the MMAs' 128 cycles, whatever
+// What bounds it (gate and up 17408 x 5120, 512 rows): group 128 176 us, 1040 TFLOP/s: the MMAs' 128 cycles, whatever
 // N is, with 176 columns (512 rows are three tiles of 171).  Groups of 32 254 us: the same MMAs twice, 96% of
-// the time; with minima 281, two more of 18.  Group 128 with minima 262: the fold reads every group's sums of x
+// the time; with minima 281, two more of 18.  Group 128 with minima 234: the fold reads every group's sums of x
 // from shared memory, 64 of them in every lane, at 128 bytes per cycle.  Up to 64 rows: the MMAs too (131072 x 5120
-// by 32 rows 188 us at group 128, 215 at 32).
+// by 32 rows 164 us at group 128, 212 at 32).
 //
 // Few tiles are split along k over the CTAs of a cluster, which add up their parts through shared memory.
 //
@@ -57,9 +57,13 @@ constexpr uint32_t kTmemMins = kQ4ScaledCols;   // 16 columns behind either accu
 constexpr int kAhead = 16;                      // chunks of codes in L2 ahead of the decode
 constexpr int kPartLd = 128 + 4;                // floats per row of x of a part
 
-// Register shares (launched with 80 per thread): 128 x (2 x 56 + 32 + 3 x 112) = 768 x 80; with scaled weights 2 x 72
-// + 32 + 3 x 96, less (512 rows, group 32 254 us, with the others' shares 292).
-constexpr int kRegsDecode = 56, kRegsIssue = 32, kRegsFold = 112, kRegsScaledDecode = 72, kRegsScaledFold = 96;
+// Register shares (launched with 80 per thread): 128 x (2 x 64 + 32 + 3 x 104) and 128 x (2 x 72 + 32 + 3 x 96) are less
+// than 768 x 80.  `light`: the fold has one scale per chunk or none.  (us, 56 and 112, 64 and 104, 72 and 96: gate/up of
+// 512 rows, scaled 292 - 254; group 128 186 177 176, with minima 252 234 272; 32 x 131072 x 5120 group 128 164 170 164,
+// group 32 216 212 227; 64 rows, group 64 with minima 285 268 283.)
+constexpr int kRegsIssue = 32;
+constexpr int regs_decode(bool light) { return light ? 72 : 64; }
+constexpr int regs_fold(bool light) { return light ? 96 : 104; }
 
 __device__ unsigned lost_waits;                 // bits of all waits that have run out on this device
 
@@ -312,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     const Q4Product &p = args.p;
     constexpr int kPer = 128 / GROUP;                               // groups per chunk
     constexpr int kOut = GATEUP ? 64 : 128;                         // outputs per tile
+    constexpr bool kLight = SCALED || (GROUP == 128 && !MINS);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int chunks = p.k >> 7;
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
 
     if (SCALED && warp < kDecodeWarps) {
         // ---- decode with scales: 32 values' two parts a buffer, two buffers of every chunk for either four warps ----
-        regs_down<SCALED ? kRegsScaledDecode : kRegsDecode>();
+        regs_down<regs_decode(kLight)>();
         const int second = warp >> 2;                               // half of the chunk
         const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64 + second * 8;
         const uint16_t *ssrc = p.scales[mat] + (block0 * 8 + (lane & 7)) * (2 * kPer) + ((lane >> 3) & 1) * kPer;
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         }
     } else if (warp < kDecodeWarps) {
         // ---- decode: a lane's 128 codes of a chunk are 64 bytes, two halves of them one buffer each ----
-        regs_down<SCALED ? kRegsScaledDecode : kRegsDecode>();
+        regs_down<regs_decode(kLight)>();
         const int odd = warp >> 2;                                  // which chunks
         const uint8_t *src = p.codes[mat] + block0 * kQ4ChunkBytes + ((lane >> 3) & 1) * 512 + (lane & 7) * 64;
         const uint32_t a_at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemA + odd * 64;
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         __syncwarp();
     } else {
         // ---- fold: a lane is a weight row, a warp has a third of the rows of x ----
-        regs_up<SCALED ? kRegsScaledFold : kRegsFold>();
+        regs_up<regs_fold(kLight)>();
         const int third = (warp - kFirstFold) / 4, team = teams > 1 ? third : 0;
         const int col0 = teams > 1 ? 0 : third * kFoldCols, mine = min(max(cols - col0, 0), kFoldCols);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
