@@ -30,8 +30,8 @@ cudaError_t q4_pack_launch(const uint8_t *codes, const uint16_t *scales, const u
                            uint8_t *out_codes, uint16_t *out_scales, uint16_t *out_mins, cudaStream_t stream);
 // Calls of more rows than this run on the tile kernel.  (us, tile and two passes of the stream kernel at 20 or
 // 32 rows: 5120 x 5120 group 128 12 25, 6145 x 2048 group 64 with minima 13 15, 5120 x 17408 group 32 with
-// minima 43 54; gate/up 2 x 17408 x 5120 group 128 47 59, group 32 with minima 74 72; 131072 x 5120 group 64
-// 188 179, group 32 with minima 271 262: the large ones of small groups lose 5%.)
+// minima 47 54; gate/up 2 x 17408 x 5120 group 128 46 59, group 32 with minima 83 72; 131072 x 5120 group 64
+// 185 179, group 32 with minima 297 262: large ones of small groups with minima lose 13%.)
 constexpr int kQ4StreamRows = 16;
 
 // Rows of x of a tile, a multiple of 16: even shares of `most` at most.
