@@ -210,10 +210,13 @@ __device__ __forceinline__ bool wait_alive(TileSmem &sm, uint32_t bar, uint32_t 
     wait_slow<SLEEP>(sm, bar, parity, bit);
     return *reinterpret_cast<volatile uint32_t *>(&sm.dead) == 0;
 }
-// The same for a whole warp: one answer.
+// The same for a whole warp: one answer.  Lanes may wait for different barriers; what any of them announces is there for
+// all lanes behind __syncwarp, which orders memory between them (a vote does not).
 template <int SLEEP = 0>
 __device__ __forceinline__ bool warp_wait(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned bit) {
-    return __all_sync(0xffffffffu, wait_alive<SLEEP>(sm, bar, parity, bit));
+    const bool ok = __all_sync(0xffffffffu, wait_alive<SLEEP>(sm, bar, parity, bit));
+    __syncwarp();
+    return ok;
 }
 
 __device__ __forceinline__ void cluster_sync() {
