@@ -212,7 +212,8 @@ __device__ __forceinline__ void warp_wait(TileSmem &sm, uint32_t bar, uint32_t p
     if (!mbar_try_wait(bar, parity)) wait_slow<SLEEP>(sm, bar, parity, err, bit);
     __syncwarp();
 }
-// The same, and whether the CTA is still alive (one answer for the whole warp).
+// The same, and whether the CTA is still alive (one answer for the whole warp).  Lanes may wait for different barriers:
+// __syncwarp orders memory between them, which a vote does not.
 template <int SLEEP = 0>
 __device__ __forceinline__ bool warp_wait_alive(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned *err, unsigned bit) {
     bool ok = mbar_try_wait(bar, parity);
@@ -220,7 +221,9 @@ __device__ __forceinline__ bool warp_wait_alive(TileSmem &sm, uint32_t bar, uint
         wait_slow<SLEEP>(sm, bar, parity, err, bit);
         ok = *reinterpret_cast<volatile uint32_t *>(&sm.dead) == 0;
     }
-    return __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();
+    return ok;
 }
 
 template <int FMT, bool GATEUP>

@@ -24,3 +24,11 @@ def test_a_wait_of_the_4_bit_tile_kernel_orders_memory_between_the_lanes():
     assert [name for name, _ in waits] == ["warp_wait"]
     for name, body in waits:
         assert "__syncwarp();" in body[body.index("__all_sync"):], name
+
+
+def test_a_wait_of_the_expert_tile_kernel_orders_memory_between_the_lanes():
+    """Its issuing warp waits for weights, activations and an accumulator on a lane each, and one lane then reads all."""
+    waits = _waits(CSRC + "tq_moe_tile.cu")
+    assert [name for name, _ in waits] == ["warp_wait_alive"]
+    for name, body in waits:
+        assert "__syncwarp();" in body[body.index("__all_sync"):], name
