@@ -97,8 +97,9 @@ tq_status tq_q4_gateup(const tq_q4_weight *gate, const tq_q4_weight *up, const u
 
 /* The bits of the bounded waits that have run out in any tq_q4_* call of this
  * process on the current device since the library was loaded (calls of more than
- * 16 rows have such waits; each takes about half a second before it sets its bit,
- * and the call's outputs are then not valid).  Synchronises the stream.  TQ_OK, or
+ * 16 rows have such waits; one runs out after about half a second.  The call then
+ * ends, whatever its size, within a second or two more, and its outputs are not
+ * valid; later calls are not concerned).  Synchronises the stream.  TQ_OK, or
  * TQ_ERR_TIMEOUT if a bit is set:
  *   bit 0  the decoders waited for a free stage    bit 5  the copies of x
  *   bit 1  the matrix instructions waited for x    bit 2  for decoded weights

@@ -66,6 +66,10 @@ constexpr int regs_decode(bool light) { return light ? 72 : 64; }
 constexpr int regs_fold(bool light) { return light ? 96 : 104; }
 
 __device__ unsigned lost_waits;                 // bits of all waits that have run out on this device
+// The launch that the last of them was in.  CTAs of it that start later copy nothing and give up at their first
+// wait, so that the launch ends whatever its size.  (A graph's replays are one launch by this number: the first CTA
+// clears it, and only CTAs that cannot run beside the first look.)
+__device__ unsigned long long lost_grid = ~0ull;
 
 struct __align__(1024) TileSmem {
     union {
@@ -91,6 +95,7 @@ struct TileArgs {
     int row_tiles, rows;                        // rows of x per tile
     int split;                                  // CTAs along k
     int first;                                  // tile of this launch
+    int at_once;                                // CTAs that can run at the same time
 };
 
 constexpr uint32_t idesc_bf16(int m, int n) {
@@ -184,7 +189,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 __device__ __forceinline__ float half2of(uint64_t v, int j) { return __uint_as_float(static_cast<uint32_t>(j ? v >> 32 : v)); }
 
-// A bounded wait.  One that runs out sets `dead` and the error word; every later
+__device__ __forceinline__ unsigned long long grid_id() {
+    unsigned long long g;
+    asm volatile("mov.u64 %0, %%gridid;" : "=l"(g));
+    return g;
+}
+
+// A bounded wait.  One that runs out sets `dead`, the error word and the launch's; every later
 // wait of the CTA then gives up at once, so that all roles come to their end.
 template <int SLEEP>
 __device__ __forceinline__ void wait_slow(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned bit) {
@@ -199,6 +210,7 @@ __device__ __forceinline__ void wait_slow(TileSmem &sm, uint32_t bar, uint32_t p
         if (clock64() - t0 > kWaitBudgetCycles) {
             *reinterpret_cast<volatile uint32_t *>(&sm.dead) = 1;
             atomicOr(&lost_waits, bit);
+            atomicExch(&lost_grid, grid_id());
             return;
         }
     }
@@ -217,6 +229,15 @@ __device__ __forceinline__ bool warp_wait(TileSmem &sm, uint32_t bar, uint32_t p
     const bool ok = __all_sync(0xffffffffu, wait_alive<SLEEP>(sm, bar, parity, bit));
     __syncwarp();
     return ok;
+}
+
+// A wait for a copy in flight at the CTA's end, bounded from t0 on: all of its copies together have the time of one.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, long long t0) {
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > kWaitBudgetCycles) {
+            atomicOr(&lost_waits, 1u << 6);
+            return;
+        }
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -335,6 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     const int sets = teams == 3 ? 3 : 2, set_cols = SCALED && MINS && teams == 3 ? 96 : 2 * kCols / sets;
     const int per_set = SCALED || kPer * dcols <= set_cols ? kPer : kPer == 4 && 2 * dcols <= set_cols ? 2 : 1;
 
+    // (asked for here, so that the answer is there when the copies begin)
+    unsigned long long lost = ~0ull;
+    if (static_cast<int>(blockIdx.x) >= args.at_once && (warp == kDecodeWarps + 1 || warp == kDecodeWarps + 2))
+        lost = *const_cast<volatile unsigned long long *>(&lost_grid);
     if (warp == kDecodeWarps) {
         tmem_alloc(smem_u32(&sm.tmem), 512);
         tmem_relinquish();
@@ -519,6 +544,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
         }
     } else if (warp < kFirstFold) {
         regs_down<kRegsIssue>();
+        const bool give_up = lost != ~0ull && lost == grid_id();
+        if (give_up) *reinterpret_cast<volatile uint32_t *>(&sm.dead) = 1;
+        const int copied = give_up ? 0 : total;                     // chunks
         if (warp == kDecodeWarps) {
             // ---- issue: one thread issues, the warp stays together ----
             const uint32_t issue = elect_one();
@@ -624,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
             // ---- copies of x: one thread ----
             if (lane == 0) {
                 int c = 0;
-                for (; c < total; ++c) {
+                for (; c < copied; ++c) {
                     const int ring = c % kStages;
                     if (!wait_alive<32>(sm, smem_u32(&sm.x_empty[ring]), ((c / kStages) & 1) ^ 1, 1u << 5)) break;
                     const uint32_t bar = smem_u32(&sm.x_full[ring]);
@@ -633,26 +661,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                     load_box(smem_u32(sm.x[ring][1]), &args.x, (chunk0 + c) * 128 + 64, row0, bar);
                 }
                 // none of this CTA's copies may be in flight when it leaves
-                for (int j = max(c - kStages, 0); j < c; ++j)
-                    if (!mbar_wait(smem_u32(&sm.x_full[j % kStages]), (j / kStages) & 1)) atomicOr(&lost_waits, 1u << 6);
+                const long long t0 = clock64();
+                for (int j = max(c - kStages, 0); j < c; ++j) drain_wait(smem_u32(&sm.x_full[j % kStages]), (j / kStages) & 1, t0);
             }
             __syncwarp();
         } else if (warp == kDecodeWarps + 2 && MINS) {
             // ---- copies of the sums, or of their parts ----
             if (SCALED && lane == 0) {
                 int c = 0;
-                for (; c < total; ++c) {
+                for (; c < copied; ++c) {
                     if (!wait_alive<64>(sm, smem_u32(&sm.p_empty[c & 1]), (c >> 1 & 1) ^ 1, 1u << 9)) break;
                     const uint32_t bar = smem_u32(&sm.p_full[c & 1]);
                     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(args.rows) * 64);
                     load_box(smem_u32(sm.parts[c & 1]), &args.parts, (chunk0 + c) * 32, row0, bar);
                 }
-                for (int j = max(c - 2, 0); j < c; ++j)
-                    if (!mbar_wait(smem_u32(&sm.p_full[j & 1]), j >> 1 & 1)) atomicOr(&lost_waits, 1u << 6);
+                const long long t0 = clock64();
+                for (int j = max(c - 2, 0); j < c; ++j) drain_wait(smem_u32(&sm.p_full[j & 1]), j >> 1 & 1, t0);
             } else if (lane == 0) {
                 const float *src = args.sums + static_cast<int64_t>(chunk0) * kPer * args.sums_ld + row0;
                 int set = 0, turn = 1, g = 0;
-                for (; g < total * kPer; g += per_set) {
+                for (; g < copied * kPer; g += per_set) {
                     if (!wait_alive<64>(sm, smem_u32(&sm.s_empty[set]), turn, 1u << 9)) break;
                     const uint32_t bar = smem_u32(&sm.s_full[set]);
                     mbar_arrive_expect_tx(bar, per_set * cols * 4);
@@ -663,9 +691,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
                         turn ^= 1;
                     }
                 }
-                for (int j = max(g / per_set - sets, 0); j < g / per_set; ++j)
-                    if (!mbar_wait(smem_u32(&sm.s_full[j % sets]), (j / sets) & 1)) atomicOr(&lost_waits, 1u << 6);
+                const long long t0 = clock64();
+                for (int j = max(g / per_set - sets, 0); j < g / per_set; ++j) drain_wait(smem_u32(&sm.s_full[j % sets]), (j / sets) & 1, t0);
             }
+            __syncwarp();
+        } else if (warp == kFirstFold - 1) {
+            if (blockIdx.x == 0 && lane == 0) atomicCAS(&lost_grid, grid_id(), ~0ull);
             __syncwarp();
         }
         __syncwarp();
@@ -878,6 +909,7 @@ cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int tiles = static_cast<int>((q4_strips(a.p.n) + (GATEUP ? 3 : 7)) / (GATEUP ? 4 : 8) * a.row_tiles);
     const int chunks = a.p.k / 128;
+    a.at_once = sms;
     // `count` tiles from a.first on, each split along k over as many CTAs as run at once with at least two chunks each.
     static ClusterLimit cluster_limit;
     auto some = [&](int count) {
