@@ -307,8 +307,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
-// The sum of x over a group and 8 s - b, each as three bf16 (24 bits), and six of their products: all but 2^-25 of
-// the whole one.
+// The sum of x over a group and 8 s - b, each as three bf16 (24 bits), and six of their products: all but 2^-24 of
+// the whole one (the second part is up to 2^-8 of the first's unit, the third 2^-17: 2 * 2^-8 * 2^-17).
 __device__ __forceinline__ void split_parts(float v, uint32_t (&p)[3]) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
