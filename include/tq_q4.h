@@ -79,7 +79,10 @@ size_t tq_q4_workspace_bytes(int32_t m, int32_t k, int32_t group);
  * calls of many rows with groups of 32 or 64 have s in the matrix instructions too,
  * exactly, as the sum of two bf16, and (8 s - b) * (sum of x) as products of bf16
  * parts, to 2^-24.  An infinity or NaN in a row of x, or in a scale
- * or minimum, makes results that depend on it infinite or NaN, and no others.
+ * or minimum, makes results that depend on it infinite or NaN, and no others
+ * do.  So may sums that leave fp32's range on the way: a group's sums of (c - 8) * x
+ * and of x stay in it for |x| up to 2^117; what is added up of them is
+ * s * (c - 8) * x, and (8 s - b) * x where there are minima.
  * In calls of up to 8 rows (a packed decode step) each row has the bits that it
  * has alone; with more rows the order of the sums may differ.
  * y: [m][n], aligned to its type; n 1 .. TQ_Q4_MAX_N, k up to TQ_Q4_MAX_K, m 1 ..
