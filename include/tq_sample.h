@@ -40,10 +40,13 @@ extern "C" {
  *   min_p fp32: <= 0 or NaN: all; > 1 counts as 1
  * uniform: fp32 [m], in [0, 1); NaN or below 0 counts as 0, and from 1 on the last
  * index that stayed with a weight above 0 is drawn (below 2^-43 it rounds to 0).
- * Weights are whole multiples of 2^-42 with a relative error of about 2^-30, and
- * sums of them are exact: the result does not depend on how a row is split over
- * threads, and differs from that of real arithmetic only where a sum comes
- * that near to a border.  A row's results do not depend on the other rows.
+ * Weights are whole multiples of 2^-42, each off by up to 2^-43 and about 2^-30 of
+ * itself, and sums of them are exact: the result does not depend on how a row is split
+ * over threads.  A sum of n weights is off by up to n * 2^-43 and 2^-30 of itself (2^-23 of
+ * it where all of the largest vocabulary is a tail of weights near 2^-42), and the result
+ * differs from that of real arithmetic only where a sum comes that near to a border;
+ * a probability is off by what its weight and the sum are, and by its rounding.  A row's
+ * results do not depend on the other rows.
  * logits aligned to their type; the other arrays 4-byte aligned;
  * 1 <= vocab <= TQ_SAMPLE_MAX_VOCAB, 1 <= m <= TQ_SAMPLE_MAX_ROWS. */
 tq_status tq_sample(const void *logits, int32_t logits_type, int32_t m, int32_t vocab,

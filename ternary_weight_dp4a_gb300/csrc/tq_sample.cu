@@ -11,8 +11,8 @@
 // arithmetic, as with equal logits) is met exactly.  exp is 2^(i/32) from a table of 32 (31 bits) times 2^r,
 // |r| <= 1/64, by its Taylor polynomial; the argument is held as the sum of two
 // fp32 numbers (difference by Knuth's TwoSum; product by fused multiply-add), so that the error is
-// 2^-30 of a weight.  fp32 alone would move one border in some thousand draws; binary64 runs at
-// 1/60 of the rate here.
+// 2^-30 of a weight and half a unit, 2^-43 (over a flat tail of 2^20 weights of a unit or so, 2^-23 of the sum).  fp32 alone
+// would move one border in some thousand draws; binary64 runs at 1/60 of the rate here.
 //
 // A cluster of CTAs has a row, a part of it in each CTA's shared memory; the first CTA finishes.
 //   top_k <= 512: the top_k-th largest of a CTA's threads' maxima bounds the cut from below, so a few
