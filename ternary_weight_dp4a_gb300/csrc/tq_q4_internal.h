@@ -44,16 +44,25 @@ constexpr int q4_tile_rows(int m, int most) {
 // Whether the tile kernel has the scales in the weights.  That costs twice the MMAs, whatever the rows; folds of small
 // groups cost by the column, and with minima more.  (us, folded and scaled.  131072 x 5120: group 32 64 rows 259 296, 80
 // rows 415 274, 192 rows 644 326; with minima 32 rows 297 294, 48 rows 401 308, 160 rows 888 331; group 64 96 rows 255
-// 273, 112 rows 320 275; with minima 64 rows 284 306, 80 rows 385 289, 160 rows 517 316, 192 rows, which are
-// two tiles then, 550 576.  Gate/up 2 x 17408 x 5120, 512 rows: group 32 559 257, with minima 693 283; group 64 326 254,
-// with minima 414 284.)
+// 273, 112 rows 320 275; with minima 64 rows 284 306, 80 rows 385 289, 160 rows 478 321, 176 rows 491 335.  Gate/up 2 x
+// 17408 x 5120, 512 rows: group 32 559 257, with minima 693 283; group 64 326 254, with minima 414 284.)
 constexpr bool q4_scaled(int m, int group, bool mins) {
     const int rows = q4_tile_rows(m, kQ4TileCols);
     return group == 32 ? rows > (mins ? 32 : 64) : group == 64 && rows > (mins ? 64 : 96);
 }
 
+// The same for a call whose weights make `tiles` tiles.  With minima 177 to 192 rows are one folded tile and two scaled ones:
+// groups of 64 are folded there, unless all scaled tiles run at once anyhow.  (us, folded and scaled, 177 rows and
+// 192: 131072 x 5120 504 564, 505 565; gate/up 2 x 17408 x 5120 156 182, 157 183; 2 x 4096 x 2048, 64 tiles, 35 31, 36 33.
+// Groups of 32, 131072 x 5120: 952 565, 954 565.  353 to 384 rows are two and three: 961 841, 294 262.)
+constexpr bool q4_scaled_call(int m, int group, bool mins, int64_t tiles, int sms) {
+    const bool two = mins && m > kQ4ScaledCols && m <= kQ4TileCols;
+    return q4_scaled(m, group, mins) && !(two && group == 64 && 2 * tiles > sms);
+}
+
 // Workspace of the tile kernel, where there are minima: sums of x over the groups, [k / group][q4_sums_ld(m)], or
-// with scaled weights their parts, 32 bf16 for every row and 128 values.
+// with scaled weights their parts, 32 bf16 for every row and 128 values.  (The parts are the larger, and it is their size
+// where a call may take either.)
 constexpr int64_t q4_sums_ld(int64_t m) { return (m + 15) / 16 * 16; }
 constexpr size_t q4_sums_bytes(int64_t m, int64_t k, int64_t group) {
     return static_cast<size_t>(q4_scaled(static_cast<int>(m), static_cast<int>(group), true) ? m * (k / 128) * 64

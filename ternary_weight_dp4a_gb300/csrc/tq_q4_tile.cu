@@ -92,7 +92,9 @@ struct TileArgs {
     CUtensorMap parts;                          // [m][k / 128 * 32] bf16, boxes of a tile's rows x 32
     const float *sums;                          // [k / group][sums_ld]: sums of x over the groups, where there are minima
     int64_t sums_ld;
+    int tiles;                                  // of the weights
     int row_tiles, rows;                        // rows of x per tile
+    bool scaled;
     int split;                                  // CTAs along k
     int first;                                  // tile of this launch
     int at_once;                                // CTAs that can run at the same time
@@ -907,7 +909,7 @@ cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     static SmemLimit limit;
     cudaError_t e = limit.raise(q4_tile_kernel<GROUP, MINS, GATEUP, SCALED>, smem);
     if (e != cudaSuccess) return e;
-    const int tiles = static_cast<int>((q4_strips(a.p.n) + (GATEUP ? 3 : 7)) / (GATEUP ? 4 : 8) * a.row_tiles);
+    const int tiles = a.tiles * a.row_tiles;
     const int chunks = a.p.k / 128;
     a.at_once = sms;
     // `count` tiles from a.first on, each split along k over as many CTAs as run at once with at least two chunks each.
@@ -951,7 +953,7 @@ cudaError_t launch(TileArgs &a, int dev, int sms, cudaStream_t stream) {
 template <int GROUP, bool MINS, bool GATEUP>
 cudaError_t pick(TileArgs &a, int dev, int sms, cudaStream_t stream) {
     if constexpr (GROUP < 128)
-        if (q4_scaled(a.p.m, GROUP, MINS)) return launch<GROUP, MINS, GATEUP, true>(a, dev, sms, stream);
+        if (a.scaled) return launch<GROUP, MINS, GATEUP, true>(a, dev, sms, stream);
     return launch<GROUP, MINS, GATEUP, false>(a, dev, sms, stream);
 }
 
@@ -975,11 +977,13 @@ cudaError_t q4_tile_launch(const Q4Product &p, float *sums, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     TileArgs a{};
     a.p = p;
-    const bool scaled = q4_scaled(p.m, p.group, p.mins[0] != nullptr);
-    a.rows = q4_tile_rows(p.m, scaled && p.mins[0] != nullptr ? kQ4ScaledCols : kCols);
+    const int per = p.mats == 2 ? 4 : 8;        // strips of each matrix in a tile
+    a.tiles = static_cast<int>((q4_strips(p.n) + per - 1) / per);
+    a.scaled = q4_scaled_call(p.m, p.group, p.mins[0] != nullptr, a.tiles, sms);
+    a.rows = q4_tile_rows(p.m, a.scaled && p.mins[0] != nullptr ? kQ4ScaledCols : kCols);
     a.row_tiles = (p.m + a.rows - 1) / a.rows;
     if (p.mins[0] != nullptr) {
-        uint32_t *parts = scaled ? reinterpret_cast<uint32_t *>(sums) : nullptr;
+        uint32_t *parts = a.scaled ? reinterpret_cast<uint32_t *>(sums) : nullptr;
         a.sums = sums;
         a.sums_ld = q4_sums_ld(p.m);
         const int64_t entries = a.sums_ld * (p.k / p.group);

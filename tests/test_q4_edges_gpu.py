@@ -24,7 +24,7 @@ def product(w, x):
 
 @pytest.mark.parametrize("mins", [False, True])
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("n,k", [(131, 640), (1000, 2048)])
+@pytest.mark.parametrize("n,k", [(131, 640), (1000, 2048), (20_001, 256)])
 def test_rows_at_the_ends_of_a_tile(tq, n, k, group, mins):  # noqa: F811
     import torch
     w, up = Matrix(tq, n, k, group, mins, 11), Matrix(tq, n, k, group, mins, 12)
