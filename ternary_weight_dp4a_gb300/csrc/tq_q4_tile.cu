@@ -197,7 +197,7 @@ __device__ __forceinline__ unsigned long long grid_id() {
     return g;
 }
 
-// A bounded wait.  One that runs out sets `dead`, the error word and the launch's; every later
+// A bounded wait.  One that runs out sets `dead` and the error word; every later
 // wait of the CTA then gives up at once, so that all roles come to their end.
 template <int SLEEP>
 __device__ __forceinline__ void wait_slow(TileSmem &sm, uint32_t bar, uint32_t parity, unsigned bit) {
@@ -212,7 +212,6 @@ __device__ __forceinline__ void wait_slow(TileSmem &sm, uint32_t bar, uint32_t p
         if (clock64() - t0 > kWaitBudgetCycles) {
             *reinterpret_cast<volatile uint32_t *>(&sm.dead) = 1;
             atomicOr(&lost_waits, bit);
-            atomicExch(&lost_grid, grid_id());
             return;
         }
     }
@@ -869,6 +868,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     if (warp == kDecodeWarps) tmem_dealloc(tmem, 512);
+    // (here, before a later CTA has its place: in the waits it took the fold of small groups 4% more time)
+    if (tid == 0 && sm.dead) atomicExch(&lost_grid, grid_id());
 }
 
 // Sums of x over the groups, a thread each: [k / group][ld] (rows from m on: zero), or with `parts` their six parts,
