@@ -16,6 +16,10 @@
  *   W[i][j] = s * c - b        with minima
  * group is 32, 64 or 128; k is a multiple of 128.  Activations are bf16 and are
  * not rotated or quantised.
+ * (Q4_K is the form with minima in groups of 32, but its scales and minima are an
+ * fp16 number of eight groups times a 6-bit one of the group, up to 17 bits.  Here each
+ * is one fp16 number: the caller rounds that product, by up to 2^-11 of it, or half a
+ * unit of fp16's smallest exponent, 2^-25.)
  *
  * Packed layout (tq_q4_pack writes it; rows are padded to a multiple of 16 with
  * zero weights).  Row i is row r = i % 16 of strip t = i / 16, value j is in
