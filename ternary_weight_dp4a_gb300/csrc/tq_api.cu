@@ -139,10 +139,9 @@ int pass_rows(int m, int r0, int per) { return m - r0 < per ? m - r0 : per; }
 
 // ---- engine choice -----------------------------------------------------------
 // TQ_ENGINE_AUTO takes the dp4a kernel: measured on GB300 it is the faster of
-// the two at every row count (a tcgen05.mma of M = 128, K = 32 costs ~145
-// cycles whatever N is, so the tensor-core kernel cannot stream the weights
-// faster than ~30 us per 71 MB FFN layer, and its pipeline's latencies add
-// to that), and the tensor-core kernel only where the dp4a kernel's plan
+// the two at every row count (the latencies of the tensor-core kernel's decode
+// and fold, with its tensor pipe 1.4% busy at 8 rows, take longer than the
+// dp4a products), and the tensor-core kernel only where the dp4a kernel's plan
 // does not fit.  The tensor-core kernel's plan for a pass of min(m, 8) rows
 // decides for the whole call (a smaller last pass needs less).  Returns TQ_OK
 // with *tc set, or an error (TQ_ERR_UNSUPPORTED when the tensor-core engine

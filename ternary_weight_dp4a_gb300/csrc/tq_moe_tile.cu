@@ -12,10 +12,10 @@
 //   acc = fma(d, scale_w * scale_a, acc),
 // in registers, blocks in ascending order: the stream kernel's bits.
 //
-// What bounds it.  With A in tensor memory an MMA of M = 128, K = 32 takes 128 cycles
-// for every N <= 224 (measured; 140 at N = 256, and 173 with A in shared memory): 1024
-// cycles for a block.  Every block's accumulator has to leave tensor memory and be folded
-// meanwhile, and the hand-over (commit, wait, read, release) has its latency on each side:
+// What bounds it.  With A in tensor memory an MMA of M = 128, K = 32 takes N / 2 cycles (measured; and 51
+// at least, issued by one thread in a branch, as here): 768 cycles for a block of 192 columns.  Every
+// block's accumulator has to leave tensor memory and be folded meanwhile, and the hand-over (commit,
+// wait, read, release) has its latency on each side:
 // a block takes about 2000 cycles, and that is the bound, not the tensor core, nor memory.
 // Two accumulators of 192 columns leave room for four blocks of A, and a third of them for
 // each of three warps to a quarter of the lanes (two of 224: two blocks of A, two warps;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         // quarter and every fourth column from t on (shape 16x128b, register pairs are
         // rows i and i + 8), so a column's scale serves eight lanes and four rows.  With
         // a row and all columns per lane (32x32b) every scale is read in all 32 lanes, 530 of
-        // the 1024 cycles that a block's MMAs take, from the shared memory that also feeds
+        // the 768 cycles that a block's MMAs take, from the shared memory that also feeds
         // the MMAs (896): the fold of a block then took 1200 cycles.
         const int quarter = warp & 3, part = (warp - 8) >> 2, i = lane >> 2, t = lane & 3;
         int group = 0;                              // groups of scales since the start

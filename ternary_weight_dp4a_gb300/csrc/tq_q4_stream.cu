@@ -21,7 +21,10 @@
 // What bounds it.  One row, large matrices, group 128: memory (131072 x 5120 64 us, 5.4 TB/s; gate and up 17408 x 5120
 // 22 us, of which 4 before the first weights).  Small groups and more rows: instructions (a word is 20 for
 // 8 weights, a group's fold 8 more per 8 rows of x, minima as many again; 13 rows, gate and up 17408 x 5120, group
-// 32 with minima 45 us, 2.5 TB/s).  Small matrices: latency (5120 x 5120 6.3 us).
+// 32 with minima 45 us, 2.5 TB/s).  Small matrices: latency (5120 x 5120 6.3 us).  Split k: the same, and the registers
+// that its indices take (20 of the 30 instances spill; 8 x 5120 x 17408, group 32 with minima, 60 bytes of stores and
+// 68 of loads, 22 us; up to 504 and 292 for gate/up in groups of 64 with minima.  13 rows, gate and up 28672 x 8192: group 128
+// 84 us, 2.8 TB/s, group 32 with minima 109).
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -8,23 +8,25 @@
 // while the tensor core works on the next group.  A lane is a weight row, so its scales are the thread's own
 // and never leave its registers.  The sums of x come from a kernel of their own, through a workspace.
 //
-// Why the weights are A: an MMA with A in tensor memory takes 128 cycles for K = 16 at any N up to 224, and shared
-// memory then carries x alone.  With the weights as B, in shared memory, an MMA brings 256 weight rows to 128
-// rows of x in 182 cycles, but the decoded weights' stores (512 cycles per 128 values of k), the MMAs' reads (768) and
+// Why the weights are A: with A in tensor memory an MMA takes N / 2 cycles for K = 16 from N = 32 on, and shared
+// memory carries x alone.  With the weights as B, in shared memory, the decoded weights' stores (512 cycles per
+// 128 values of k), the MMAs' reads (768) and
 // the copies of x (256) share one 128-byte port: 3000 cycles per 256 rows and 128 values were measured, 1500 for
-// 128 rows; here it is 1200, 1024 of them MMAs.
+// 128 rows; here it is 1170, 704 of them MMAs (176 columns).
 //
 // Groups of 32 or 64 and many rows: a fold per group would take longer than the MMAs (an accumulator's hand-over
-// and 192 columns: 990 cycles per group of 32, whose MMAs take 256).  There the scale goes into the weights, exactly:
+// and 192 columns: 990 cycles per group of 32, whose MMAs take 192).  There the scale goes into the weights, exactly:
 // an fp16 scale is the sum of two bf16 of five bits, and five bits times c - 8 is exact in bf16, so two MMAs
 // instead of one bring s (c - 8) x, and the fold adds up one accumulator per 128 values of k.  Minima are then a product
 // of their own in the tensor core: (8 s - b) (sum of x) of the chunk's groups, both factors in three bf16 and six
 // of the nine products, 6 values of k per group in one or two MMAs more.
 //
-// What bounds it (gate and up 17408 x 5120, 512 rows): group 128 176 us, 1040 TFLOP/s: the MMAs' 128 cycles, whatever
-// N is, with 176 columns (512 rows are three tiles of 171).  Groups of 32 254 us: the same MMAs twice, 96% of
-// the time; with minima 281, two more of 18.  Group 128 with minima 234: the fold reads every group's sums of x
-// from shared memory, 64 of them in every lane, at 128 bytes per cycle.  Up to 64 rows: the MMAs too (131072 x 5120
+// What bounds it (gate and up 17408 x 5120, 512 rows; cycles per 128 values of k by clocks around the waits).  Group
+// 128 175 us, 1040 TFLOP/s: 1170 cycles of the issuing warp, 704 of them the MMAs' (176 columns: 512 rows are three
+// tiles of 171), the others the latencies of its waits and commits one behind the other.  Groups of 32 256 us: the MMAs
+// twice, 1408 of 1800; with minima 288, two more of 18.  Group 128 with minima 235: the fold reads every group's sums
+// of x from shared memory, 64 of them in every lane, at 128 bytes per cycle.  Up to 64 rows: the issuing warp's
+// latencies alone, 1020 to 1330 cycles with 128 to 256 of MMAs, while decode and fold wait (131072 x 5120
 // by 32 rows 164 us at group 128, 212 at 32).
 //
 // Few tiles are split along k over the CTAs of a cluster, which add up their parts through shared memory.
